@@ -71,7 +71,9 @@ typedef enum {
                           than the device has: a green context, MPS limits) */
 } sv_status;
 
-typedef enum { SV_BF16 = 0, SV_FP32 = 1 } sv_dtype;
+/* Logits are SV_BF16 or SV_FP32; the key/value cache calls take SV_FP16 too
+   (each call says which). */
+typedef enum { SV_BF16 = 0, SV_FP32 = 1, SV_FP16 = 2 } sv_dtype;
 
 typedef enum {
   /* SpecInfer multi-step speculative sampling: child c is tested against
@@ -101,6 +103,8 @@ typedef enum {
 #define SV_DERR_CHECK 0x40     /* an internal bounds or alignment check failed (debug
                                   builds, -DSV_CHECKS, only): a library bug, never the
                                   data; the access it guarded was skipped */
+#define SV_DERR_PAGE 0x80      /* a page id outside [0, num_pages) in a page table entry
+                                  that the call needs */
 
 /* Limits of this implementation. */
 #define SV_MAX_K 32        /* drafts per chain */
@@ -109,6 +113,8 @@ typedef enum {
 #define SV_MAX_TOPK 64     /* top-k filter size */
 #define SV_MAX_TREE_NODES 64 /* nodes per tree (N) and draft rows (M) */
 #define SV_MAX_TREE_B 1024  /* requests per tree call */
+#define SV_MAX_KV_T 65536   /* tokens a request adds to the cache in one call */
+#define SV_MAX_KV_HEADS 256 /* key/value heads, and query heads */
 
 /*
  * Chain verification, one request per b ([L17] sec. 2.4 Algorithm 1).
@@ -291,6 +297,145 @@ sv_status sv_tree_mask(const sv_tree_mask_args* args, void* workspace, size_t ws
  */
 sv_status sv_row_stats(const sv_chain_args* args, float* alpha, float* expected,
                        void* workspace, size_t ws_bytes, sv_stream_t stream);
+
+/* ---- Key/value cache in 8 bits (no counterpart on the pages beyond the
+ * truncation index: [S14] "step", [DVP] II.2, [L17] sec. 4.3) ----
+ *
+ * The target model's forward pass over a round reads the keys and values of
+ * every earlier token; accept_len and accepted_nodes say which of the
+ * round's own tokens stay.  These calls hold that cache, write a round's
+ * tokens into it, attend to it, and read tokens back.
+ *
+ * Layout.  The cache is paged: page p holds page_size tokens of every
+ * key/value head, k and v apart, as e4m3 codes (1 sign, 4 exponent, 3
+ * mantissa bits; largest value 448, no infinity) in blocks [page_size][D]:
+ *   code of token i, channel d, head h of page p:
+ *     k[p * page_stride + h * head_stride + i * D + d]
+ * and one scale for each page and head, again k and v apart:
+ *     value = code * k_scale[p * Hkv + h].
+ * A scale is a power of two, 2^e with -48 <= e <= 48: the largest value of
+ * a page and head decides e (below), so codes lose no more than e4m3's own
+ * rounding, and changing a page's scale moves codes by whole exponents.
+ * Token position i of request b lives in page page_table[b * slots + i /
+ * page_size]; entries a call does not need are not read and may hold
+ * anything.  Several requests may name one page as long as no call writes
+ * into it.
+ */
+typedef struct {
+  int32_t num_pages, page_size;  /* page_size: 16, 32, 64 or 128 */
+  int32_t Hkv, D;                /* D: 64 or 128 */
+  void *k, *v;                   /* codes, 16-byte aligned */
+  int64_t page_stride;           /* bytes between pages, a multiple of 16 */
+  int64_t head_stride;           /* bytes between heads, a multiple of 16, >= page_size * D */
+  float *k_scale, *v_scale;      /* [num_pages][Hkv] */
+  const int32_t* page_table;     /* [B][slots] */
+  int32_t slots;
+} sv_kv_cache;
+
+/*
+ * Write the keys and values of a round's tokens: token t < n = num_new[b]
+ * of request b goes to position kv_len[b] + t.
+ *
+ * For every page and head that gets tokens, k and v apart:
+ *   a = the largest finite |x| of the new tokens in the page,
+ *   e = the smallest integer with a <= 448 * 2^e, kept within [-48, 48]
+ *       (-48 when a == 0);
+ *   if the page holds tokens below kv_len[b], which stay, e is raised to
+ *   the page's present e where that is larger; where it is smaller the
+ *   codes of the tokens that stay are rounded again at the new scale;
+ *   code = x / 2^e to the nearest e4m3 value, ties to even, saturated at
+ *   448 (so +-inf becomes +-448 * 2^e); NaN stays NaN.
+ * A page without tokens that stay starts anew: tokens of an earlier round
+ * that were rejected leave no trace in its scale.  Codes past the last
+ * token written are not touched.
+ *
+ * NaN or inf in the new values records SV_DERR_NONFINITE; kv_len < 0,
+ * num_new outside [0, T] or a length past slots * page_size records
+ * SV_DERR_ARG and the request is not written; a page id outside
+ * [0, num_pages) records SV_DERR_PAGE and that page is not written.  Only
+ * the workspace's error word is used (SV_MIN_WORKSPACE_BYTES).
+ */
+typedef struct {
+  sv_kv_cache cache;
+  int32_t B, T;              /* 0 <= B <= SV_MAX_B, 1 <= T <= SV_MAX_KV_T */
+  sv_dtype dtype;            /* SV_BF16, SV_FP16 or SV_FP32 */
+  const void* k_new;         /* [B][T][Hkv][D], D contiguous */
+  const void* v_new;
+  int64_t k_batch_stride, k_token_stride, k_head_stride; /* elements */
+  int64_t v_batch_stride, v_token_stride, v_head_stride;
+  const int32_t* kv_len;     /* [B] tokens the request holds before the call */
+  const int32_t* num_new;    /* [B] in [0, T], or NULL (= T) */
+} sv_kv_write_args;
+
+sv_status sv_kv_write(const sv_kv_write_args* args, void* workspace, size_t ws_bytes,
+                      sv_stream_t stream);
+
+/*
+ * Read tokens back: row t < n = num[b] of request b is the value (code *
+ * scale, rounded to dtype) at position start[b] + (rows ? rows[b][t] : t);
+ * rows t >= n are zero.  With start = kv_len and rows = the accepted nodes
+ * of a tree this is the accepted path; written again at kv_len + 1 it
+ * becomes contiguous (read and write give back the same codes unless a
+ * page's scale drops values below its smallest step).
+ *
+ * num outside [0, T] records SV_DERR_ARG (all rows zero), a position
+ * outside [0, slots * page_size) SV_DERR_ARG and a page id outside
+ * [0, num_pages) SV_DERR_PAGE (that row is zero).
+ */
+typedef struct {
+  sv_kv_cache cache;
+  int32_t B, T;
+  sv_dtype dtype;            /* of k_out and v_out: SV_BF16, SV_FP16 or SV_FP32 */
+  void *k_out, *v_out;       /* [B][T][Hkv][D], D contiguous */
+  int64_t out_batch_stride, out_token_stride, out_head_stride; /* elements, of both */
+  const int32_t* start;      /* [B], or NULL (= 0) */
+  const int32_t* num;        /* [B] in [0, T], or NULL (= T) */
+  const int32_t* rows;       /* [B][T], or NULL (row t is token t) */
+} sv_kv_read_args;
+
+sv_status sv_kv_read(const sv_kv_read_args* args, void* workspace, size_t ws_bytes,
+                     sv_stream_t stream);
+
+/*
+ * Attention of a round's queries over the cache, after sv_kv_write put the
+ * round's own keys and values there.  Query token t < n = num_new[b] of
+ * request b, query head j (key/value head j / (Hq / Hkv)):
+ *   x_i = scale * sum_d q[d] * key_i[d]         over the positions i it sees,
+ *   out = sum_i exp(x_i) value_i / sum_i exp(x_i),
+ *   lse = log sum_i exp(x_i).
+ * It sees every position i < kv_len[b] and, of the round's own tokens
+ * (position kv_len[b] + s, s < n): s <= t when mask is NULL (a chain of
+ * drafts, or a chunk of a prompt), else those whose bit s of mask row t is
+ * set (sv_tree_mask's rows: a node's ancestors and itself; T <= 64).  A row
+ * that sees nothing, and every row t >= n, is 0 with lse = -inf.  What a
+ * row does not see does not reach it, NaN and stale codes included.
+ * Products and sums are taken in 32 bits; the queries enter the products
+ * as they are, the weights exp(x_i - max) rounded to 11 bits (fp16).
+ *
+ * kv_len < 0, num_new outside [0, T] or a length past slots * page_size
+ * records SV_DERR_ARG (all rows of the request as if n were 0); a page id
+ * outside [0, num_pages) records SV_DERR_PAGE and no row sees that page.
+ */
+typedef struct {
+  sv_kv_cache cache;
+  int32_t B, T, Hq;          /* Hq: a multiple of Hkv, <= SV_MAX_KV_HEADS */
+  sv_dtype dtype;            /* of q and out: SV_BF16 or SV_FP16 */
+  const void* q;             /* [B][T][Hq][D], D contiguous */
+  int64_t q_batch_stride, q_token_stride, q_head_stride; /* elements */
+  void* out;                 /* [B][T][Hq][D] contiguous */
+  float* lse;                /* optional [B][T][Hq] */
+  const int32_t* kv_len;     /* [B] tokens before the round */
+  const int32_t* num_new;    /* [B] in [0, T], or NULL (= T) */
+  const uint32_t* mask;      /* [B][T][words], or NULL (causal) */
+  int32_t words;             /* 32-bit words of a mask row, >= (T + 31) / 32 */
+  float scale;
+} sv_kv_attention_args;
+
+/* Workspace bytes an attention call needs (0 on invalid sizes). */
+size_t sv_kv_attention_workspace_bytes(int32_t B, int32_t T, int32_t Hq, int32_t Hkv, int32_t D);
+
+sv_status sv_kv_attention(const sv_kv_attention_args* args, void* workspace, size_t ws_bytes,
+                          sv_stream_t stream);
 
 /* Synchronise `stream`, read and clear the workspace error word.
    *device_flags receives the SV_DERR_* bits (may be NULL).  Returns SV_OK,

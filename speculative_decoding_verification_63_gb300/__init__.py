@@ -22,7 +22,8 @@ from ._binding import (  # noqa: F401
     sv_verify_chain, sv_verify_tree, sv_version, sv_workspace_init,
     SV_NOALLOC_SCRATCH_BYTES, sv_noalloc_get_error, sv_verify_chain_noalloc,
     SV_TREE_MSS, SV_TREE_MSS_NOREPLACE, SV_TREE_NAIVE, TREE_MODES, SV_MIN_WORKSPACE_BYTES,
-    sv_tree_mask, sv_row_stats)
+    sv_tree_mask, sv_row_stats, SV_FP16, SV_DERR_PAGE, SV_MAX_KV_HEADS, SV_MAX_KV_T,
+    sv_kv_attention, sv_kv_attention_workspace_bytes, sv_kv_read, sv_kv_write)
 from ._build import build_library  # noqa: F401
 
 _ws_lock = threading.Lock()
@@ -150,6 +151,82 @@ def row_stats(target_logits, draft_logits, temperature, num_drafts=None, top_k=N
     sv_row_stats(target_logits, draft_logits, temperature, out["alpha"], out["expected"], ws,
                  num_drafts=num_drafts, top_k=top_k, max_top_k=max_top_k)
     return out
+
+
+def kv_cache(num_pages: int, page_size: int, num_heads: int, head_dim: int,
+             device=None) -> dict:
+    """An empty 8-bit key/value cache: e4m3 codes k, v [num_pages][num_heads]
+    [page_size][head_dim] and power-of-two scales k_scale, v_scale
+    [num_pages][num_heads] (device tensors).  Which pages a request holds is
+    the caller's page table [B][slots] int32 (slot i: tokens i * page_size ..)."""
+    dev = torch.device(device if device is not None else "cuda")
+    shape = (num_pages, num_heads, page_size, head_dim)
+    return dict(k=torch.zeros(shape, dtype=torch.uint8, device=dev).view(torch.float8_e4m3fn),
+                v=torch.zeros(shape, dtype=torch.uint8, device=dev).view(torch.float8_e4m3fn),
+                k_scale=torch.ones(shape[:2], dtype=torch.float32, device=dev),
+                v_scale=torch.ones(shape[:2], dtype=torch.float32, device=dev))
+
+
+def kv_write(cache: dict, page_table, kv_len, k_new, v_new, num_new=None,
+             ws: torch.Tensor | None = None) -> None:
+    """Quantise a round's keys and values k_new, v_new [B][T][heads][D] (bf16,
+    fp16 or fp32) into the cache: token t < num_new[b] goes to position
+    kv_len[b] + t of request b."""
+    if ws is None:
+        ws = workspace(SV_MIN_WORKSPACE_BYTES, k_new.device, "kv")
+    sv_kv_write(cache, page_table, kv_len, k_new, v_new, ws, num_new=num_new)
+
+
+def kv_read(cache: dict, page_table, start, num, T: int, rows=None, dtype=torch.bfloat16,
+            ws: torch.Tensor | None = None) -> dict:
+    """Read tokens back as values: row t < num[b] is position start[b] + t, or
+    start[b] + rows[b][t]; later rows are zero.  Returns k and v
+    [B][T][heads][D] (device tensors)."""
+    pages, H, P, D = cache["k"].shape
+    B, dev = page_table.shape[0], page_table.device
+    out = dict(k=torch.empty((B, T, H, D), dtype=dtype, device=dev),
+               v=torch.empty((B, T, H, D), dtype=dtype, device=dev))
+    if ws is None:
+        ws = workspace(SV_MIN_WORKSPACE_BYTES, dev, "kv")
+    sv_kv_read(cache, page_table, start, num, out["k"], out["v"], ws, rows=rows)
+    return out
+
+
+def kv_attention(q, cache: dict, page_table, kv_len, num_new=None, mask=None,
+                 scale: float | None = None, with_lse: bool = False,
+                 ws: torch.Tensor | None = None) -> dict:
+    """Attention of a round's queries q [B][T][heads][D] (bf16 or fp16) over
+    the cache, which holds kv_len[b] earlier tokens and the round's own (see
+    kv_write): causal among the round's tokens, or by the rows of a tree mask
+    [B][T][words] (tree_mask).  scale defaults to 1 / sqrt(D).  Returns out
+    [B][T][heads][D] and, when with_lse, lse [B][T][heads] (device tensors)."""
+    B, T, Hq, D = q.shape
+    out = dict(out=torch.empty((B, T, Hq, D), dtype=q.dtype, device=q.device))
+    if with_lse:
+        out["lse"] = torch.empty((B, T, Hq), dtype=torch.float32, device=q.device)
+    if ws is None:
+        need = sv_kv_attention_workspace_bytes(B, T, Hq, cache["k"].shape[1], D)
+        if need == 0:
+            raise SpecVerifyError(SV_EINVAL, "kv_attention (sizes)")
+        ws = workspace(need, q.device, "kv_attention")
+    sv_kv_attention(q, cache, page_table, kv_len, out["out"], ws,
+                    scale=D ** -0.5 if scale is None else scale, num_new=num_new, mask=mask,
+                    lse=out.get("lse"))
+    return out
+
+
+def kv_commit(cache: dict, page_table, kv_len, accept_len, accepted_nodes,
+              ws: torch.Tensor | None = None) -> None:
+    """Keep a tree round's accepted path: the tokens of accepted_nodes[b][0 ..
+    accept_len[b]) (verify_tree's results), which kv_write put at kv_len[b] +
+    node, move to kv_len[b] + 1 .. behind the root.  The request then holds
+    kv_len + 1 + accept_len tokens.  (A chain round needs nothing moved: it
+    holds kv_len + 1 + accept_len tokens as it is.)"""
+    T = accepted_nodes.shape[1]
+    if T == 0:
+        return
+    path = kv_read(cache, page_table, kv_len, accept_len, T, rows=accepted_nodes, ws=ws)
+    kv_write(cache, page_table, kv_len + 1, path["k"], path["v"], num_new=accept_len, ws=ws)
 
 
 def check_device_errors(ws: torch.Tensor) -> None:

@@ -15,19 +15,22 @@ import torch
 from ._build import LIBRARY
 
 SV_OK, SV_EINVAL, SV_ECUDA, SV_ETIMEOUT, SV_EDATA, SV_EWORKSPACE, SV_EUNSUPPORTED, SV_ECORESIDENT = range(8)
-SV_BF16, SV_FP32 = 0, 1
+SV_BF16, SV_FP32, SV_FP16 = 0, 1, 2
 SV_TREE_MSS, SV_TREE_MSS_NOREPLACE, SV_TREE_NAIVE = 0, 1, 2
 TREE_MODES = {"mss": SV_TREE_MSS, "noreplace": SV_TREE_MSS_NOREPLACE, "naive": SV_TREE_NAIVE}
 SV_DERR_TOKEN, SV_DERR_NONFINITE, SV_DERR_MASS = 0x01, 0x02, 0x04
 SV_DERR_TREE, SV_DERR_TIMEOUT, SV_DERR_ARG = 0x08, 0x10, 0x20
 SV_DERR_CHECK = 0x40
+SV_DERR_PAGE = 0x80
 SV_MAX_K, SV_MAX_B, SV_MAX_V, SV_MAX_TOPK = 32, 1024, 1 << 20, 64
 SV_MAX_TREE_NODES, SV_MAX_TREE_B = 64, 1024
+SV_MAX_KV_T, SV_MAX_KV_HEADS = 65536, 256
 
 # every symbol include/specverify.h declares
 EXPORTS = ("sv_chain_workspace_bytes", "sv_tree_workspace_bytes", "sv_workspace_init",
            "sv_verify_chain", "sv_verify_tree", "sv_get_error", "sv_selftest_wait_timeout",
            "sv_verify_chain_noalloc", "sv_noalloc_get_error", "sv_tree_mask", "sv_row_stats",
+           "sv_kv_write", "sv_kv_read", "sv_kv_attention_workspace_bytes", "sv_kv_attention",
            "sv_status_string", "sv_version")
 SV_MIN_WORKSPACE_BYTES = 8192
 SV_NOALLOC_SCRATCH_BYTES = 8 << 20
@@ -61,6 +64,34 @@ class SvTreeArgs(ctypes.Structure):
 class SvTreeMaskArgs(ctypes.Structure):
     _fields_ = [("B", _i32), ("N", _i32), ("words", _i32), ("parent", _P), ("num_nodes", _P),
                 ("mask", _P), ("depth", _P)]
+
+
+class SvKvCache(ctypes.Structure):
+    _fields_ = [("num_pages", _i32), ("page_size", _i32), ("Hkv", _i32), ("D", _i32),
+                ("k", _P), ("v", _P), ("page_stride", _i64), ("head_stride", _i64),
+                ("k_scale", _P), ("v_scale", _P), ("page_table", _P), ("slots", _i32)]
+
+
+class SvKvWriteArgs(ctypes.Structure):
+    _fields_ = [("cache", SvKvCache), ("B", _i32), ("T", _i32), ("dtype", _i32),
+                ("k_new", _P), ("v_new", _P),
+                ("k_batch_stride", _i64), ("k_token_stride", _i64), ("k_head_stride", _i64),
+                ("v_batch_stride", _i64), ("v_token_stride", _i64), ("v_head_stride", _i64),
+                ("kv_len", _P), ("num_new", _P)]
+
+
+class SvKvReadArgs(ctypes.Structure):
+    _fields_ = [("cache", SvKvCache), ("B", _i32), ("T", _i32), ("dtype", _i32),
+                ("k_out", _P), ("v_out", _P),
+                ("out_batch_stride", _i64), ("out_token_stride", _i64), ("out_head_stride", _i64),
+                ("start", _P), ("num", _P), ("rows", _P)]
+
+
+class SvKvAttentionArgs(ctypes.Structure):
+    _fields_ = [("cache", SvKvCache), ("B", _i32), ("T", _i32), ("Hq", _i32), ("dtype", _i32),
+                ("q", _P), ("q_batch_stride", _i64), ("q_token_stride", _i64),
+                ("q_head_stride", _i64), ("out", _P), ("lse", _P), ("kv_len", _P),
+                ("num_new", _P), ("mask", _P), ("words", _i32), ("scale", ctypes.c_float)]
 
 
 class SpecVerifyError(RuntimeError):
@@ -110,6 +141,12 @@ def lib(path: str | None = None):
     h.sv_tree_mask.restype = ctypes.c_int
     h.sv_row_stats.argtypes = [ctypes.POINTER(SvChainArgs), _P, _P, _P, ctypes.c_size_t, _P]
     h.sv_row_stats.restype = ctypes.c_int
+    for f, args in [("sv_kv_write", SvKvWriteArgs), ("sv_kv_read", SvKvReadArgs),
+                    ("sv_kv_attention", SvKvAttentionArgs)]:
+        getattr(h, f).argtypes = [ctypes.POINTER(args), _P, ctypes.c_size_t, _P]
+        getattr(h, f).restype = ctypes.c_int
+    h.sv_kv_attention_workspace_bytes.argtypes = [_i32, _i32, _i32, _i32, _i32]
+    h.sv_kv_attention_workspace_bytes.restype = ctypes.c_size_t
     h.sv_status_string.argtypes = [ctypes.c_int]
     h.sv_status_string.restype = ctypes.c_char_p
     h.sv_version.argtypes = []
@@ -398,3 +435,124 @@ def sv_row_stats(target_logits, draft_logits, temperature, alpha, expected, work
                             workspace.numel() * workspace.element_size(), _stream(stream))
     if st != SV_OK:
         raise SpecVerifyError(st, "sv_row_stats")
+
+
+# ------------------------------------------------- 8-bit key/value cache
+
+_KV_DTYPES = {torch.bfloat16: SV_BF16, torch.float32: SV_FP32, torch.float16: SV_FP16}
+
+
+def _kv_cache(c: SvKvCache, cache: dict, page_table, B: int) -> None:
+    """Fill an sv_kv_cache from the cache's tensors (k, v [pages][Hkv][P][D]
+    e4m3, k_scale, v_scale [pages][Hkv] fp32) and the page table [B][slots]."""
+    k, v, ks, vs = cache["k"], cache["v"], cache["k_scale"], cache["v_scale"]
+    if k.dtype != torch.float8_e4m3fn or k.dim() != 4:
+        raise ValueError(f"cache k: expected float8_e4m3fn [pages][heads][page][D], got {k.dtype} "
+                         f"{tuple(k.shape)}")
+    pages, H, P, D = k.shape
+    st = k.stride()
+    if v.dtype != k.dtype or v.shape != k.shape or v.stride() != st:
+        raise ValueError("cache v: expected k's dtype, shape and strides")
+    if st[3] != 1 or st[2] != D:
+        raise ValueError("cache: the tokens of a page and head must be contiguous")
+    _check(ks, torch.float32, (pages, H), "k_scale")
+    _check(vs, torch.float32, (pages, H), "v_scale")
+    if page_table.dtype != torch.int32 or page_table.dim() != 2 or page_table.shape[0] != B \
+            or not page_table.is_contiguous():
+        raise ValueError(f"page_table: expected contiguous int32 [{B}][slots]")
+    c.num_pages, c.page_size, c.Hkv, c.D = pages, P, H, D
+    c.k, c.v = _ptr(k), _ptr(v)
+    c.page_stride = st[0] if pages > 1 else 0
+    c.head_stride = st[1] if H > 1 else P * D
+    c.k_scale, c.v_scale, c.page_table = _ptr(ks), _ptr(vs), _ptr(page_table)
+    c.slots = page_table.shape[1]
+
+
+def _rows4(t, shape, what: str):
+    """The (batch, token, head) strides of a [B][T][heads][D] tensor with
+    contiguous D."""
+    if tuple(t.shape) != shape or t.stride(3) != 1:
+        raise ValueError(f"{what}: expected {shape} with contiguous rows, got {tuple(t.shape)}")
+    if t.dtype not in _KV_DTYPES:
+        raise ValueError(f"{what}: expected bfloat16, float16 or float32, got {t.dtype}")
+    return t.stride()[:3]
+
+
+def sv_kv_write(cache: dict, page_table, kv_len, k_new, v_new, workspace, num_new=None,
+                stream=None) -> None:
+    """Enqueue sv_kv_write: quantise k_new, v_new [B][T][Hkv][D] into the
+    cache at positions kv_len[b] .. of each request."""
+    B, T, H, D = k_new.shape
+    a = SvKvWriteArgs()
+    _kv_cache(a.cache, cache, page_table, B)
+    shape = (B, T, a.cache.Hkv, a.cache.D)
+    a.k_batch_stride, a.k_token_stride, a.k_head_stride = _rows4(k_new, shape, "k_new")
+    a.v_batch_stride, a.v_token_stride, a.v_head_stride = _rows4(v_new, shape, "v_new")
+    if v_new.dtype != k_new.dtype:
+        raise ValueError("v_new: expected k_new's dtype")
+    _check(kv_len, torch.int32, (B,), "kv_len")
+    _check(num_new, torch.int32, (B,), "num_new")
+    a.B, a.T, a.dtype = B, T, _KV_DTYPES[k_new.dtype]
+    a.k_new, a.v_new = _ptr(k_new), _ptr(v_new)
+    a.kv_len, a.num_new = _ptr(kv_len), _ptr(num_new)
+    st = lib().sv_kv_write(ctypes.byref(a), _ptr(workspace),
+                           workspace.numel() * workspace.element_size(), _stream(stream))
+    if st != SV_OK:
+        raise SpecVerifyError(st, "sv_kv_write")
+
+
+def sv_kv_read(cache: dict, page_table, start, num, k_out, v_out, workspace, rows=None,
+               stream=None) -> None:
+    """Enqueue sv_kv_read: the values at positions start[b] + t, or start[b]
+    + rows[b][t], into k_out, v_out [B][T][Hkv][D] (rows t >= num[b] zero)."""
+    B, T, H, D = k_out.shape
+    a = SvKvReadArgs()
+    _kv_cache(a.cache, cache, page_table, B)
+    shape = (B, T, a.cache.Hkv, a.cache.D)
+    strides = _rows4(k_out, shape, "k_out")
+    if _rows4(v_out, shape, "v_out") != strides or v_out.dtype != k_out.dtype:
+        raise ValueError("v_out: expected k_out's dtype and strides")
+    a.out_batch_stride, a.out_token_stride, a.out_head_stride = strides
+    _check(start, torch.int32, (B,), "start")
+    _check(num, torch.int32, (B,), "num")
+    _check(rows, torch.int32, (B, T), "rows")
+    a.B, a.T, a.dtype = B, T, _KV_DTYPES[k_out.dtype]
+    a.k_out, a.v_out = _ptr(k_out), _ptr(v_out)
+    a.start, a.num, a.rows = _ptr(start), _ptr(num), _ptr(rows)
+    st = lib().sv_kv_read(ctypes.byref(a), _ptr(workspace),
+                          workspace.numel() * workspace.element_size(), _stream(stream))
+    if st != SV_OK:
+        raise SpecVerifyError(st, "sv_kv_read")
+
+
+def sv_kv_attention_workspace_bytes(B: int, T: int, Hq: int, Hkv: int, D: int) -> int:
+    return lib().sv_kv_attention_workspace_bytes(B, T, Hq, Hkv, D)
+
+
+def sv_kv_attention(q, cache: dict, page_table, kv_len, out, workspace, scale: float,
+                    num_new=None, mask=None, lse=None, stream=None) -> None:
+    """Enqueue sv_kv_attention: q [B][T][Hq][D] over the cache into out (the
+    same shape, contiguous) and, optionally, lse [B][T][Hq] fp32."""
+    B, T, Hq, D = q.shape
+    a = SvKvAttentionArgs()
+    _kv_cache(a.cache, cache, page_table, B)
+    if D != a.cache.D or q.dtype == torch.float32:
+        raise ValueError(f"q: expected bfloat16 or float16 [B][T][Hq][{a.cache.D}], got {q.dtype} "
+                         f"{tuple(q.shape)}")
+    a.q_batch_stride, a.q_token_stride, a.q_head_stride = _rows4(q, (B, T, Hq, D), "q")
+    _check(out, q.dtype, (B, T, Hq, D), "out")
+    _check(lse, torch.float32, (B, T, Hq), "lse")
+    _check(kv_len, torch.int32, (B,), "kv_len")
+    _check(num_new, torch.int32, (B,), "num_new")
+    if mask is not None:
+        if mask.dim() != 3:
+            raise ValueError("mask: expected [B][T][words]")
+        _check(mask, torch.int32, (B, T, mask.shape[2]), "mask")
+        a.mask, a.words = _ptr(mask), mask.shape[2]
+    a.B, a.T, a.Hq, a.dtype = B, T, Hq, _KV_DTYPES[q.dtype]
+    a.q, a.out, a.lse = _ptr(q), _ptr(out), _ptr(lse)
+    a.kv_len, a.num_new, a.scale = _ptr(kv_len), _ptr(num_new), scale
+    st = lib().sv_kv_attention(ctypes.byref(a), _ptr(workspace),
+                               workspace.numel() * workspace.element_size(), _stream(stream))
+    if st != SV_OK:
+        raise SpecVerifyError(st, "sv_kv_attention")

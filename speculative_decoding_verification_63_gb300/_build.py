@@ -1,6 +1,7 @@
 """Build of libspecverify.so with nvcc for sm_103a (GB300), in-tree."""
 from __future__ import annotations
 
+import concurrent.futures
 import os
 import shutil
 import subprocess
@@ -39,8 +40,8 @@ def compile_flags(nvtx: bool = False, extra_flags=(), checks: bool = False) -> l
 
 def build_library(force: bool = False, verbose: bool = False, extra_flags=(),
                   nvtx: bool | None = None, checks: bool = False) -> str:
-    """Compile csrc/specverify.cu into libspecverify.so (one translation
-    unit, -O3, IEEE division and sqrt, no fast-math).  nvtx (default: the
+    """Compile csrc/*.cu into libspecverify.so (the units side by side, -O3,
+    IEEE division and sqrt, no fast-math).  nvtx (default: the
     environment variable SV_NVTX=1) builds the traced variant; a change of
     flags forces a rebuild.  checks builds the debug library,
     libspecverify_checks.so, instead."""
@@ -55,12 +56,24 @@ def build_library(force: bool = False, verbose: bool = False, extra_flags=(),
             and os.path.getmtime(out) >= newest):
         return out
     tmp = out + f".tmp{os.getpid()}"
-    cmd = [nvcc(), *flags, "-o", tmp, os.path.join(CSRC, "specverify.cu")]
+    units = [p for p in sources() if p.endswith(".cu")]
+    objects = [f"{tmp}.{i}.o" for i in range(len(units))]
+    extra = ["-Xptxas=-v"] if verbose else []
+    cmds = [[nvcc(), *extra, *(f for f in flags if f != "-shared"), "-c", "-o", o, u]
+            for u, o in zip(units, objects)]
     if verbose:
-        cmd.insert(1, "-Xptxas=-v")
-        print(" ".join(cmd))
-    subprocess.run(cmd, check=True)
-    os.replace(tmp, out)
+        for cmd in cmds:
+            print(" ".join(cmd))
+    try:
+        with concurrent.futures.ThreadPoolExecutor(len(cmds)) as ex:
+            for f in [ex.submit(subprocess.run, cmd, check=True) for cmd in cmds]:
+                f.result()
+        subprocess.run([nvcc(), *flags, "-o", tmp, *objects], check=True)
+        os.replace(tmp, out)
+    finally:
+        for o in objects:
+            if os.path.exists(o):
+                os.remove(o)
     with open(stamp, "w") as f:
         f.write(" ".join(flags))
     return out

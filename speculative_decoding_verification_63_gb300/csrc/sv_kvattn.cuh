@@ -1,0 +1,682 @@
+// sv_kvattn.cuh -- attention of a round's queries over the paged 8-bit
+// key/value cache.
+//
+//   out = sum_i exp(x_i) v_i / sum_i exp(x_i),  x_i = scale * q . k_i
+//
+// in one pass over the cache with a running reference in place of the
+// maximum.  Codes become halves exactly, so a product q . code is exact in
+// the 32-bit accumulators up to their own rounding; the page scales 2^ek and
+// 2^ev are applied to x and to the weights:
+//   w_i = 2^(x_i log2(e) + ev_i - ref),  O = sum_i w_i code_i,
+//   Z = sum_i w_i 2^-ev_i,               out = O / Z.
+// Folding ev into the exponent costs nothing and keeps the weights of pages
+// with different scales comparable in 16 bits.  The weights are rounded to
+// halves (relative 2^-11) for the second product; Z sums them unrounded.
+// The reference follows the running maximum only when that has risen more
+// than kRefSlack above it, so the rescaling of O is rare; the weights are
+// shifted up by kRefShift, which keeps them within the halves' range
+// (2^(kRefShift + kRefSlack) = 2^15) and moves the halves' underflow to
+// 2^-32 of the reference.
+//
+// Work.  A unit is 16 query rows (round tokens x heads of one group) of one
+// request and key/value head; its blocks are 64 positions each.  The blocks
+// of all units in a row are cut into equal parts, one for each CTA, so ragged
+// lengths balance and a single long request spreads over the whole GPU.  A
+// unit cut between CTAs leaves partial (ref, Z, O) in the workspace; the CTA
+// that arrives last joins them in order (the result does not depend on which
+// CTA that is) and zeroes what it read.
+#pragma once
+
+#include "sv_kvcache.cuh"
+
+namespace sv {
+
+constexpr int kKaRows = 16;           // query rows of a unit: one m16 tile
+constexpr int kKaBlock = 64;          // positions of a block
+constexpr int kKaStages = 5;
+constexpr int kKaWarps = 4;           // consumer warps
+constexpr int kKaThreads = kKaWarps * 32 + 32;
+constexpr int kKaCtasPerSm = 2;
+constexpr int kKaMaxCtas = 2 * 160;   // tickets and partials are sized for this many
+constexpr int kKaMinBlocks = 4;       // blocks below which a CTA is not worth starting
+constexpr float kRefShift = 8.f, kRefSlack = 7.f;
+
+struct KvAttnProblem {
+  KvCache c;
+  int B, T, Hq, G;  // G = Hq / Hkv
+  const void* q;
+  long long q_batch, q_token, q_head;
+  bool q_vec;  // 8-byte loads of four queries
+  void* out;
+  float* lse;
+  const int *kv_len, *num_new;
+  const unsigned* mask;
+  int words;
+  float scale_log2;  // scale * log2(e)
+  unsigned* tickets;
+  float* partials;
+  int* err;
+};
+
+// A CTA's partial result: 4 floats of statistics a lane, then O.
+template <int D>
+constexpr int kKaPartialFloats = 32 * (4 + D / 2);
+
+template <int D>
+struct KaShared {
+  unsigned char k[kKaStages][kKaBlock * D];
+  unsigned char v[kKaStages][kKaBlock * D];
+  float merge[2][kKaPartialFloats<D>];
+  // cumulated block counts of the requests
+  long long prefix[SV_MAX_B + 1];
+  long long scan[8];
+  float k_scale[kKaStages][kKaBlock / 16];  // < 0: no such page
+  float v_scale[kKaStages][kKaBlock / 16];
+  uint64_t full[kKaStages], empty[kKaStages];
+  int dead;       // a wait ran out
+  unsigned last;  // this CTA joins the unit
+};
+
+struct KaLen {
+  int len, n;  // tokens before the round, round tokens (0 when invalid)
+};
+__device__ __forceinline__ KaLen ka_len(const KvAttnProblem& a, int b, bool* bad) {
+  KaLen r;
+  r.len = a.kv_len[b];
+  r.n = a.num_new ? a.num_new[b] : a.T;
+  if (r.len < 0 || r.n < 0 || r.n > a.T ||
+      static_cast<long long>(r.len) + r.n > static_cast<long long>(a.c.slots) * a.c.page_size) {
+    *bad = true;
+    r.len = r.n = 0;
+  }
+  return r;
+}
+
+// A position in the list of all blocks: request, unit of the request
+// (key/value head major, row tile minor) and block of the unit.
+struct KaCursor {
+  int b, unit, blk;
+  int len, n, tiles, nblk;  // of request b
+  __device__ __forceinline__ void load(const KvAttnProblem& a) {
+    bool bad = false;
+    const KaLen l = ka_len(a, b, &bad);
+    len = l.len;
+    n = l.n;
+    tiles = (n * a.G + kKaRows - 1) / kKaRows;
+    nblk = (len + n + kKaBlock - 1) / kKaBlock;
+  }
+  __device__ __forceinline__ void seek(const KvAttnProblem& a, const long long* prefix,
+                                       long long at) {
+    int lo = 0, hi = a.B;  // the last b with prefix[b] <= at
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) / 2;
+      if (prefix[mid] <= at) lo = mid; else hi = mid;
+    }
+    b = lo;
+    load(a);
+    const long long in = at - prefix[b];
+    unit = static_cast<int>(in / nblk);
+    blk = static_cast<int>(in - static_cast<long long>(unit) * nblk);
+  }
+  // to the next unit (requests without units are skipped)
+  __device__ __forceinline__ void next_unit(const KvAttnProblem& a) {
+    blk = 0;
+    if (++unit < a.c.Hkv * tiles) return;
+    unit = 0;
+    do {
+      if (++b >= a.B) return;
+      load(a);
+    } while (n == 0);
+  }
+};
+
+__device__ __forceinline__ void ka_mma(float (&d)[4], const unsigned (&a)[4], unsigned b0,
+                                       unsigned b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+      "{%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ unsigned half2_of(float lo, float hi) {
+  const __half2 h = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const unsigned*>(&h);
+}
+
+__device__ __forceinline__ float quad_max(float x) {
+  x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 1));
+  return fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 2));
+}
+__device__ __forceinline__ float quad_sum(float x) {
+  x += __shfl_xor_sync(0xffffffffu, x, 1);
+  return x + __shfl_xor_sync(0xffffffffu, x, 2);
+}
+
+// A wait that records its expiry once and lets the CTA run on without
+// waiting (every barrier of the block is still met).
+__device__ __forceinline__ void ka_wait(uint64_t* bar, uint32_t parity, int* dead, int* err) {
+  if (mbar_try_wait(bar, parity)) return;
+  if (*static_cast<volatile int*>(dead)) return;
+  if (!mbar_wait_bounded(bar, parity, 1000000000ull)) {
+    *static_cast<volatile int*>(dead) = 1;
+    record_error(err, SV_DERR_TIMEOUT);
+  }
+}
+
+__device__ __forceinline__ void mbar_expect_tx(uint64_t* bar, uint32_t bytes) {
+  asm volatile("mbarrier.expect_tx.relaxed.cta.shared::cta.b64 [%0], %1;" ::"r"(smem_u32(bar)),
+               "r"(bytes)
+               : "memory");
+}
+
+// The statistics and accumulators of a warp: rows g and g + 8 of the tile
+// (g = lane / 4); O[j] holds, for column pair 2t, 2t+1 (t = lane % 4) of the
+// j-th n8 tile, channels (2t) D/8 + j and (2t+1) D/8 + j.
+template <int D>
+struct KaAcc {
+  float ref[2], z[2];
+  float o[D / 8][4];
+  __device__ __forceinline__ void clear() {
+    ref[0] = ref[1] = kNegInf;
+    z[0] = z[1] = 0.f;
+#pragma unroll
+    for (int j = 0; j < D / 8; ++j) o[j][0] = o[j][1] = o[j][2] = o[j][3] = 0.f;
+  }
+  // join with another partial (its statistics given, its O read through get)
+  template <class Get>
+  __device__ __forceinline__ void join(float r0, float r1, float z0, float z1, Get get) {
+    const float n0 = fmaxf(ref[0], r0), n1 = fmaxf(ref[1], r1);
+    const float a0 = ref[0] == kNegInf ? 0.f : exp2f(ref[0] - n0);
+    const float a1 = ref[1] == kNegInf ? 0.f : exp2f(ref[1] - n1);
+    const float b0 = r0 == kNegInf ? 0.f : exp2f(r0 - n0);
+    const float b1 = r1 == kNegInf ? 0.f : exp2f(r1 - n1);
+    ref[0] = n0;
+    ref[1] = n1;
+    z[0] = z[0] * a0 + z0 * b0;
+    z[1] = z[1] * a1 + z1 * b1;
+#pragma unroll
+    for (int j = 0; j < D / 8; ++j) {
+      o[j][0] = o[j][0] * a0 + get(4 * j) * b0;
+      o[j][1] = o[j][1] * a0 + get(4 * j + 1) * b0;
+      o[j][2] = o[j][2] * a1 + get(4 * j + 2) * b1;
+      o[j][3] = o[j][3] * a1 + get(4 * j + 3) * b1;
+    }
+  }
+  // p[i * 32 + lane]: every access of a warp is one line
+  __device__ __forceinline__ void store(float* p, int lane) const {
+    p[lane] = ref[0];
+    p[32 + lane] = ref[1];
+    p[64 + lane] = z[0];
+    p[96 + lane] = z[1];
+#pragma unroll
+    for (int j = 0; j < D / 8; ++j)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) p[(4 + 4 * j + i) * 32 + lane] = o[j][i];
+  }
+};
+
+template <class T>
+__device__ __forceinline__ float2 ka_two(const T* p);
+template <>
+__device__ __forceinline__ float2 ka_two(const __half* p) {
+  return make_float2(__half2float(p[0]), __half2float(p[1]));
+}
+template <>
+__device__ __forceinline__ float2 ka_two(const __nv_bfloat16* p) {
+  return make_float2(__bfloat162float(p[0]), __bfloat162float(p[1]));
+}
+
+template <int D, class T>
+__global__ void __launch_bounds__(kKaThreads, kKaCtasPerSm) kv_attn_kernel(const KvAttnProblem a) {
+  extern __shared__ __align__(128) unsigned char ka_smem[];
+  KaShared<D>& sh = *reinterpret_cast<KaShared<D>*>(ka_smem);
+  const int tid = static_cast<int>(threadIdx.x), warp = tid >> 5, lane = tid & 31;
+  const int grid = static_cast<int>(gridDim.x), cta = static_cast<int>(blockIdx.x);
+  if (tid == 0) {
+    for (int s = 0; s < kKaStages; ++s) {
+      mbar_init(&sh.full[s], 32);
+      mbar_init(&sh.empty[s], kKaWarps / 2);
+    }
+    sh.dead = 0;
+    fence_mbar_init();
+  }
+  grid_dependency_wait();
+
+  // cumulated block counts, and the rows of the round that hold no token
+  long long total = 0;
+  for (int base = 0; base < a.B; base += kKaThreads) {
+    const int b = base + tid;
+    long long mine = 0;
+    if (b < a.B) {
+      bool bad = false;
+      const KaLen l = ka_len(a, b, &bad);
+      if (bad && cta == 0) record_error(a.err, SV_DERR_ARG);
+      mine = static_cast<long long>(a.c.Hkv) * ((l.n * a.G + kKaRows - 1) / kKaRows) *
+             ((static_cast<long long>(l.len) + l.n + kKaBlock - 1) / kKaBlock);
+    }
+    long long x = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long y = __shfl_up_sync(0xffffffffu, x, o);
+      if (lane >= o) x += y;
+    }
+    __syncthreads();
+    if (lane == 31) sh.scan[warp] = x;
+    __syncthreads();
+    long long before = total;
+    for (int w = 0; w < kKaThreads / 32; ++w) {
+      if (w < warp) before += sh.scan[w];
+      total += sh.scan[w];
+    }
+    if (b < a.B) sh.prefix[b] = before + x - mine;
+  }
+  if (tid == 0) sh.prefix[a.B] = total;
+  __syncthreads();
+
+  for (int b = cta; b < a.B; b += grid) {
+    bool bad = false;
+    const KaLen l = ka_len(a, b, &bad);
+    const long long row0 = (static_cast<long long>(b) * a.T + l.n) * a.Hq;
+    const long long rows = static_cast<long long>(a.T - l.n) * a.Hq;
+    uint4* o = reinterpret_cast<uint4*>(static_cast<T*>(a.out) + row0 * D);
+    for (long long i = tid; i < rows * (D / 8); i += kKaThreads) o[i] = make_uint4(0, 0, 0, 0);
+    if (a.lse)
+      for (long long i = tid; i < rows; i += kKaThreads) a.lse[row0 + i] = kNegInf;
+  }
+
+  // this CTA's part of the blocks
+  const long long parts =
+      max(1ll, min(static_cast<long long>(grid), total / kKaMinBlocks));
+  if (cta >= parts) return;
+  const long long w0 = total * cta / parts, w1 = total * (cta + 1) / parts;
+  if (w0 >= w1) return;
+
+  if (warp == kKaWarps) {
+    // ------------------------------------------------------------ producer
+    // Lane l < 8 owns copy l of a block: 16 positions of keys (l < 4) or
+    // values; its page id is looked up one block ahead.
+    const uint64_t pol = policy_evict_first();
+    KaCursor cur;
+    cur.seek(a, sh.prefix, w0);
+    const int sub = lane & 3;
+    const bool is_v = lane >= 4;
+    auto page_of = [&](const KaCursor& c) -> int {
+      const int pos = c.blk * kKaBlock + sub * 16;
+      if (lane >= 8 || c.b >= a.B || pos >= c.len + c.n) return -2;
+      return a.c.page_table[static_cast<long long>(c.b) * a.c.slots + (pos >> a.c.page_shift)];
+    };
+    int page = page_of(cur);
+    long long i = 0;
+    for (long long w = w0; w < w1; ++w, ++i) {
+      const int s = static_cast<int>(i % kKaStages);
+      const uint32_t round = static_cast<uint32_t>(i / kKaStages);
+      if (round > 0) ka_wait(&sh.empty[s], (round - 1) & 1, &sh.dead, a.err);
+      __syncwarp();
+      if (__any_sync(0xffffffffu, *static_cast<volatile int*>(&sh.dead))) {
+        // let the consumers' waits end
+        mbar_arrive(&sh.full[s]);
+        continue;
+      }
+      const int h = cur.unit / cur.tiles;
+      const int pos = cur.blk * kKaBlock + sub * 16;
+      const bool there = page >= 0 && page < a.c.num_pages;
+      if (page != -2 && !there) record_error(a.err, SV_DERR_PAGE);
+      float sc = -1.f;
+      if (there) {
+        const unsigned char* src = (is_v ? a.c.v : a.c.k) + page * a.c.page_stride +
+                                   h * a.c.head_stride + (pos & (a.c.page_size - 1)) * D;
+        mbar_expect_tx(&sh.full[s], 16 * D);
+        bulk_copy_g2s_hint((is_v ? sh.v[s] : sh.k[s]) + sub * 16 * D, src, 16 * D, &sh.full[s],
+                           pol);
+        sc = (is_v ? a.c.v_scale : a.c.k_scale)[static_cast<long long>(page) * a.c.Hkv + h];
+      }
+      if (++cur.blk == cur.nblk) cur.next_unit(a);
+      page = w + 1 < w1 ? page_of(cur) : -2;
+      if (lane < 8) (is_v ? sh.v_scale[s] : sh.k_scale[s])[sub] = sc;
+      mbar_arrive(&sh.full[s]);
+    }
+    // copies of the last stages must land before the block ends
+    for (long long j = max(0ll, i - kKaStages); j < i; ++j)
+      if (!mbar_wait_bounded(&sh.full[j % kKaStages],
+                             static_cast<uint32_t>(j / kKaStages) & 1, 1000000000ull))
+        record_error(a.err, SV_DERR_TIMEOUT);
+    return;
+  }
+
+  // ------------------------------------------------------------- consumers
+  const int g = lane >> 2, t = lane & 3;
+  const int pair = warp >> 1, half = warp & 1;  // pairs take alternate blocks, warps a half each
+  constexpr int KS = D / 16;
+  KaCursor cur;
+  cur.seek(a, sh.prefix, w0);
+  long long w = w0;
+  while (w < w1) {
+    const int h = cur.unit / cur.tiles, tile = cur.unit % cur.tiles;
+    const int blk0 = cur.blk;
+    const int blk1 = static_cast<int>(min(static_cast<long long>(cur.nblk), blk0 + (w1 - w)));
+    const int L = cur.len + cur.n;
+
+    // the unit's queries as fragments: bf16 rows are scaled by a power of two
+    // into the halves' range
+    unsigned qf[KS][4];
+    float c2[2];  // log2(e) * scale * 2^(the row's exponent)
+    int rt[2];    // round token of the row (T: none)
+    {
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        const int row = tile * kKaRows + g + 8 * r;
+        const bool ok = row < cur.n * a.G;
+        rt[r] = ok ? row / a.G : a.T;
+        const T* p = static_cast<const T*>(a.q) + cur.b * a.q_batch +
+                     (ok ? row / a.G : 0) * a.q_token + (h * a.G + (ok ? row % a.G : 0)) * a.q_head +
+                     t * (D / 4);
+        float f[D / 4];
+        float m = 0.f;
+#pragma unroll
+        for (int i = 0; i < D / 4; i += 4) {
+          alignas(8) T e[4];
+          if (a.q_vec) {
+            *reinterpret_cast<uint2*>(e) = ok ? *reinterpret_cast<const uint2*>(p + i)
+                                              : make_uint2(0, 0);
+          } else {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) e[j] = ok ? p[i + j] : from_float<T>(0.f);
+          }
+          const float2 x = ka_two(e), y = ka_two(e + 2);
+          f[i] = x.x;
+          f[i + 1] = x.y;
+          f[i + 2] = y.x;
+          f[i + 3] = y.y;
+        }
+        int ex = 0;
+        if (sizeof(T) == 2 && !__is_same(T, __half)) {
+#pragma unroll
+          for (int i = 0; i < D / 4; ++i) m = fmaxf(m, fabsf(f[i]));
+          m = quad_max(m);
+          // the row's largest value lands in [2^14, 2^15)
+          ex = min(max(static_cast<int>(__float_as_uint(m) >> 23) - 127 - 14, -100), 100);
+          const float k = pow2f(-ex);
+#pragma unroll
+          for (int i = 0; i < D / 4; ++i) f[i] *= k;
+        }
+        c2[r] = a.scale_log2 * pow2f(ex);
+#pragma unroll
+        for (int i = 0; i < KS; ++i) {
+          qf[i][r] = half2_of(f[4 * i], f[4 * i + 1]);
+          qf[i][2 + r] = half2_of(f[4 * i + 2], f[4 * i + 3]);
+        }
+      }
+    }
+
+    KaAcc<D> acc;
+    acc.clear();
+    for (int blk = blk0; blk < blk1; ++blk) {
+      const long long i = w - w0 + (blk - blk0);
+      if ((i & 1) != pair) continue;
+      const int s = static_cast<int>(i % kKaStages);
+      ka_wait(&sh.full[s], static_cast<uint32_t>(i / kKaStages) & 1, &sh.dead, a.err);
+      const int pos0 = blk * kKaBlock + half * 32;
+
+      float x[4][4];
+#pragma unroll
+      for (int nt = 0; nt < 4; ++nt) {
+        x[nt][0] = x[nt][1] = x[nt][2] = x[nt][3] = 0.f;
+        const unsigned char* kp = sh.k[s] + (half * 32 + nt * 8 + g) * D + t * (D / 4);
+#pragma unroll
+        for (int c = 0; c < D / 64; ++c) {
+          const uint4 kw = *reinterpret_cast<const uint4*>(kp + 16 * c);
+          const unsigned ww[4] = {kw.x, kw.y, kw.z, kw.w};
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            ka_mma(x[nt], qf[4 * c + j], half2_lo(ww[j]), half2_hi(ww[j]));
+        }
+      }
+      float kse[2], vse[2];
+      float zin[2];  // 2^-ev
+      bool edge = pos0 + 32 > cur.len;
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        const float ks = sh.k_scale[s][half * 2 + u], vs = sh.v_scale[s][half * 2 + u];
+        edge |= ks < 0.f;
+        kse[u] = pow2f(scale_exp(ks));
+        const int ev = scale_exp(vs);
+        vse[u] = static_cast<float>(ev);
+        zin[u] = pow2f(-ev);
+      }
+#pragma unroll
+      for (int nt = 0; nt < 4; ++nt)
+#pragma unroll
+        for (int i4 = 0; i4 < 4; ++i4)
+          x[nt][i4] = fmaf(x[nt][i4], c2[i4 >> 1] * kse[nt >> 1], vse[nt >> 1]);
+
+      uint32_t seen[2] = {0xffffffffu, 0xffffffffu};  // bit nt * 2 + column of the thread's 8
+      if (edge) {
+        // positions at or past the round: what each row sees of them
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+          uint32_t m = 0;
+          for (int nt = 0; nt < 4; ++nt)
+            for (int c = 0; c < 2; ++c) {
+              const int pos = pos0 + nt * 8 + 2 * t + c;
+              const int j = pos - cur.len;
+              bool see = pos < L && rt[r] < a.T && sh.k_scale[s][half * 2 + (nt >> 1)] >= 0.f;
+              if (j >= 0 && see)
+                see = a.mask == nullptr
+                          ? j <= rt[r]
+                          : (a.mask[(static_cast<long long>(cur.b) * a.T + rt[r]) * a.words +
+                                    (j >> 5)] >> (j & 31)) & 1;
+              m |= static_cast<uint32_t>(see) << (nt * 2 + c);
+            }
+          seen[r] = m;
+        }
+#pragma unroll
+        for (int nt = 0; nt < 4; ++nt)
+#pragma unroll
+          for (int i4 = 0; i4 < 4; ++i4)
+            if (!(seen[i4 >> 1] >> (nt * 2 + (i4 & 1)) & 1)) x[nt][i4] = kNegInf;
+      }
+
+      float mx[2];
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        float m = kNegInf;
+#pragma unroll
+        for (int nt = 0; nt < 4; ++nt) m = fmaxf(m, fmaxf(x[nt][2 * r], x[nt][2 * r + 1]));
+        mx[r] = quad_max(m);
+      }
+      const bool rise = mx[0] > acc.ref[0] + kRefSlack || mx[1] > acc.ref[1] + kRefSlack;
+      if (__any_sync(0xffffffffu, rise)) {
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+          if (mx[r] > acc.ref[r] + kRefSlack) {
+            const float f = acc.ref[r] == kNegInf ? 0.f : fast_exp2(acc.ref[r] - mx[r]);
+            acc.ref[r] = mx[r];
+            acc.z[r] *= f;
+#pragma unroll
+            for (int j = 0; j < D / 8; ++j) {
+              acc.o[j][2 * r] *= f;
+              acc.o[j][2 * r + 1] *= f;
+            }
+          }
+        }
+      }
+      const float base[2] = {acc.ref[0] == kNegInf ? 0.f : acc.ref[0] - kRefShift,
+                             acc.ref[1] == kNegInf ? 0.f : acc.ref[1] - kRefShift};
+      unsigned pf[2][4];
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        float sum[2] = {0.f, 0.f};
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+          float* xx = x[2 * u + q];
+#pragma unroll
+          for (int i4 = 0; i4 < 4; ++i4) {
+            xx[i4] = fast_exp2(xx[i4] - base[i4 >> 1]);
+            sum[i4 >> 1] += xx[i4];
+          }
+          pf[u][2 * q] = half2_of(xx[0], xx[1]);
+          pf[u][2 * q + 1] = half2_of(xx[2], xx[3]);
+        }
+        acc.z[0] = fmaf(sum[0], zin[u], acc.z[0]);
+        acc.z[1] = fmaf(sum[1], zin[u], acc.z[1]);
+      }
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        // four tokens of the thread: 2t, 2t+1, 2t+8, 2t+9 of the 16
+        constexpr int VW = D / 32;  // words of a token's channels g D/8 ..
+        unsigned vw[4][VW];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const int tok = half * 32 + u * 16 + 2 * t + (k & 1) + (k >> 1) * 8;
+          const unsigned char* vp = sh.v[s] + tok * D + g * (D / 8);
+          if (D == 128) {
+            const uint4 r = *reinterpret_cast<const uint4*>(vp);
+            vw[k][0] = r.x;
+            vw[k][1] = r.y;
+            vw[k][VW - 2] = r.z;
+            vw[k][VW - 1] = r.w;
+          } else {
+            const uint2 r = *reinterpret_cast<const uint2*>(vp);
+            vw[k][0] = r.x;
+            vw[k][1] = r.y;
+          }
+        }
+        if (edge) {
+          // Codes nobody wrote, and NaN in places a row does not see, must
+          // not meet a zero weight: 0 * NaN is NaN.  NaN codes leave the
+          // product and are put into the rows that see them.
+          bool nan = false;
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const int tok = half * 32 + u * 16 + 2 * t + (k & 1) + (k >> 1) * 8;
+            const bool there = blk * kKaBlock + tok < L && sh.k_scale[s][half * 2 + u] >= 0.f;
+#pragma unroll
+            for (int j = 0; j < VW; ++j) {
+              if (!there) vw[k][j] = 0u;
+              const unsigned m = vw[k][j] & 0x7f7f7f7fu;
+              // bytes equal to 0x7f
+              const unsigned is = (m + 0x01010101u) & 0x80808080u;
+              nan |= is != 0u;
+              vw[k][j] &= ~((is >> 7) * 0xffu);
+            }
+          }
+          if (__any_sync(0xffffffffu, nan)) {
+            for (int tok = 0; tok < 16; ++tok) {
+              const int pos = pos0 + u * 16 + tok;
+              if (pos >= L || sh.k_scale[s][half * 2 + u] < 0.f) break;
+              // the lane of this row that holds column tok, and its bit
+              const int src = (lane & ~3) | ((tok & 7) >> 1);
+              const int bit = (2 * u + (tok >> 3)) * 2 + (tok & 1);
+              const bool s0 = __shfl_sync(0xffffffffu, seen[0], src) >> bit & 1;
+              const bool s1 = __shfl_sync(0xffffffffu, seen[1], src) >> bit & 1;
+              const unsigned char* vr = sh.v[s] + (half * 32 + u * 16 + tok) * D;
+#pragma unroll
+              for (int j = 0; j < D / 8; ++j)
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                  if ((vr[(2 * t + c) * (D / 8) + j] & 0x7f) == 0x7f) {
+                    if (s0) acc.o[j][c] = __int_as_float(0x7fc00000);
+                    if (s1) acc.o[j][2 + c] = __int_as_float(0x7fc00000);
+                  }
+                }
+            }
+          }
+        }
+#pragma unroll
+        for (int j = 0; j < VW; ++j) {
+          const unsigned a0 = __byte_perm(vw[0][j], vw[1][j], 0x5140);
+          const unsigned a1 = __byte_perm(vw[2][j], vw[3][j], 0x5140);
+          const unsigned b0 = __byte_perm(vw[0][j], vw[1][j], 0x7362);
+          const unsigned b1 = __byte_perm(vw[2][j], vw[3][j], 0x7362);
+          ka_mma(acc.o[4 * j], pf[u], half2_lo(a0), half2_lo(a1));
+          ka_mma(acc.o[4 * j + 1], pf[u], half2_hi(a0), half2_hi(a1));
+          ka_mma(acc.o[4 * j + 2], pf[u], half2_lo(b0), half2_lo(b1));
+          ka_mma(acc.o[4 * j + 3], pf[u], half2_hi(b0), half2_hi(b1));
+        }
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sh.empty[s]);
+    }
+
+    // join the four warps: 1 -> 0 and 3 -> 2, then 2 -> 0
+    acc.z[0] = quad_sum(acc.z[0]);
+    acc.z[1] = quad_sum(acc.z[1]);
+    auto join_smem = [&](const float* p) {
+      acc.join(p[lane], p[32 + lane], p[64 + lane], p[96 + lane],
+               [&](int i) { return p[(4 + i) * 32 + lane]; });
+    };
+    named_sync(1, kKaWarps * 32);  // the buffers are free
+    if (warp & 1) acc.store(sh.merge[warp >> 1], lane);
+    named_sync(1, kKaWarps * 32);
+    if (!(warp & 1)) join_smem(sh.merge[warp >> 1]);
+    named_sync(1, kKaWarps * 32);
+    if (warp == 2) acc.store(sh.merge[0], lane);
+    named_sync(1, kKaWarps * 32);
+    if (warp == 0) join_smem(sh.merge[0]);
+
+    const bool starts = blk0 == 0, ends = blk1 == cur.nblk;
+    bool write = true;
+    if (!(starts && ends)) {
+      // the unit is cut: CTAs first .. last hold a part of it
+      const long long u0 = sh.prefix[cur.b] + static_cast<long long>(cur.unit) * cur.nblk;
+      const int first = static_cast<int>(((u0 + 1) * parts - 1) / total);
+      const int last = static_cast<int>(((u0 + cur.nblk) * parts - 1) / total);
+      constexpr int PF = kKaPartialFloats<D>;
+      if (warp == 0) {
+        // a part that begins inside the unit is its CTA's first
+        acc.store(a.partials + (2ll * cta + (starts ? 1 : 0)) * PF, lane);
+        __threadfence();
+        __syncwarp();
+        if (lane == 0)
+          sh.last = atomic_add_acq_rel(&a.tickets[first], 1u) ==
+                    static_cast<unsigned>(last - first);
+        __syncwarp();
+        write = sh.last != 0;
+        if (write) {
+          __threadfence();
+          acc.clear();
+          for (int c = first; c <= last; ++c) {
+            float* p = a.partials + (2ll * c + (c == first ? 1 : 0)) * PF;
+            acc.join(__ldcg(p + lane), __ldcg(p + 32 + lane), __ldcg(p + 64 + lane),
+                     __ldcg(p + 96 + lane), [&](int i) { return __ldcg(p + (4 + i) * 32 + lane); });
+            for (int i = lane; i < PF; i += 32) p[i] = 0.f;
+          }
+          if (lane == 0) a.tickets[first] = 0u;
+        }
+      }
+    }
+    if (warp == 0 && write) {
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        if (rt[r] < a.T) {
+          const int row = tile * kKaRows + g + 8 * r;
+          const long long orow =
+              (static_cast<long long>(cur.b) * a.T + rt[r]) * a.Hq + h * a.G + row % a.G;
+          const bool any = !(acc.z[r] == 0.f);  // true for NaN
+          const float inv = any ? 1.f / acc.z[r] : 0.f;
+          T* o = static_cast<T*>(a.out) + orow * D;
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            alignas(16) T e[D / 8];
+#pragma unroll
+            for (int j = 0; j < D / 8; ++j)
+              e[j] = from_float<T>(any ? acc.o[j][2 * r + c] * inv : 0.f);
+#pragma unroll
+            for (int j = 0; j < D / 64; ++j)
+              reinterpret_cast<uint4*>(o + (2 * t + c) * (D / 8))[j] =
+                  reinterpret_cast<const uint4*>(e)[j];
+          }
+          if (a.lse && t == 0)
+            a.lse[orow] = any ? (log2f(acc.z[r]) + acc.ref[r] - kRefShift) * 0.69314718055994531f
+                              : kNegInf;
+        }
+      }
+    }
+    w += blk1 - blk0;
+    cur.blk = blk1;
+    if (cur.blk == cur.nblk) cur.next_unit(a);
+  }
+}
+
+}  // namespace sv

@@ -1,0 +1,360 @@
+// sv_kvcache.cuh -- the paged 8-bit key/value cache: its device view, e4m3
+// conversions, and the kernels that write a round's tokens into it and read
+// tokens back.
+//
+// A page holds page_size tokens of every head, keys and values apart, as
+// e4m3 codes with one power-of-two scale 2^e for each (page, head).  Powers
+// of two make three things exact: x / 2^e, the change of a page's scale
+// (codes move by whole exponents; only values that fall among the
+// subnormals are rounded again), and the bound a <= 448 * 2^e, which is a
+// comparison of a's exponent and mantissa bits.  A scale of arbitrary size
+// would gain nothing: e4m3's relative step does not depend on it.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include "sv_rowpass.cuh"
+
+namespace sv {
+
+constexpr int kKvExpLo = -48, kKvExpHi = 48;
+constexpr int kKvThreads = 256;
+
+struct KvCache {
+  unsigned char *k, *v;
+  long long page_stride, head_stride;  // bytes
+  float *k_scale, *v_scale;
+  const int* page_table;
+  int num_pages, page_size, page_shift, Hkv, D, slots;
+};
+
+// 2^e for e in [-126, 127].
+__device__ __forceinline__ float pow2f(int e) { return __int_as_float((e + 127) << 23); }
+
+// The exponent of a stored scale (a power of two in range, whatever the bits).
+__device__ __forceinline__ int scale_exp(float s) {
+  const int e = static_cast<int>((__float_as_uint(s) >> 23) & 255u) - 127;
+  return min(max(e, kKvExpLo), kKvExpHi);
+}
+
+// The smallest e with a <= 448 * 2^e, within the range of the scales:
+// 448 = 1.75 * 2^8, so e = exponent(a) - 8, and one more when a's mantissa
+// exceeds 1.75.
+__device__ __forceinline__ int needed_exp(float a) {
+  const unsigned u = __float_as_uint(a);
+  const int e = static_cast<int>(u >> 23) - 127 - 8 + ((u & 0x7fffffu) > 0x600000u ? 1 : 0);
+  return min(max(e, kKvExpLo), kKvExpHi);
+}
+
+// Two floats to two e4m3 codes (first in the low byte): nearest, ties to
+// even, saturated at 448; NaN becomes the NaN code.
+__device__ __forceinline__ unsigned e4m3x2(float lo, float hi) {
+  unsigned short r;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+__device__ __forceinline__ unsigned e4m3x4(float a, float b, float c, float d) {
+  return e4m3x2(a, b) | (e4m3x2(c, d) << 16);
+}
+
+// Two e4m3 codes to two halves (exact).
+__device__ __forceinline__ unsigned half2_of_e4m3x2(unsigned short c) {
+  unsigned r;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"(c));
+  return r;
+}
+__device__ __forceinline__ unsigned half2_lo(unsigned w) {
+  return half2_of_e4m3x2(static_cast<unsigned short>(w));
+}
+__device__ __forceinline__ unsigned half2_hi(unsigned w) {
+  return half2_of_e4m3x2(static_cast<unsigned short>(w >> 16));
+}
+
+__device__ __forceinline__ float2 float2_of_half2(unsigned w) {
+  return __half22float2(*reinterpret_cast<const __half2*>(&w));
+}
+
+// Sixteen consecutive values of type T, as loaded: 32 bytes of a 16-bit
+// type, 64 of fp32.  Element loads where the address is not 16-byte aligned.
+template <class T>
+struct Raw16 {
+  uint4 w[sizeof(T)];
+};
+
+template <class T>
+__device__ __forceinline__ void load16(Raw16<T>& r, const T* p, bool vec) {
+  if (vec) {
+#pragma unroll
+    for (int i = 0; i < static_cast<int>(sizeof(T)); ++i)
+      r.w[i] = __ldg(reinterpret_cast<const uint4*>(p) + i);
+  } else {
+    T* e = reinterpret_cast<T*>(r.w);
+#pragma unroll
+    for (int i = 0; i < 16; ++i) e[i] = p[i];
+  }
+}
+
+template <class T>
+__device__ __forceinline__ float elem16(const Raw16<T>& r, int i);
+template <>
+__device__ __forceinline__ float elem16(const Raw16<float>& r, int i) {
+  return reinterpret_cast<const float*>(r.w)[i];
+}
+template <>
+__device__ __forceinline__ float elem16(const Raw16<__nv_bfloat16>& r, int i) {
+  const unsigned w = reinterpret_cast<const unsigned*>(r.w)[i >> 1];
+  return (i & 1) ? bf16hi(w) : bf16lo(w);
+}
+template <>
+__device__ __forceinline__ float elem16(const Raw16<__half>& r, int i) {
+  return __half2float(reinterpret_cast<const __half*>(r.w)[i]);
+}
+
+// ------------------------------------------------------------------- write
+
+struct KvWriteProblem {
+  KvCache c;
+  int B, T, pages;  // pages a request can touch: ceil(T / page_size) + 1
+  int group;        // threads of one (page, head, side): 32 .. 256
+  bool vec;         // 16-byte loads of the new values
+  const void *k_new, *v_new;
+  long long k_batch, k_token, k_head, v_batch, v_token, v_head;
+  const int *kv_len, *num_new;
+  int* err;
+};
+
+// One thread group per (request, page of the round, side, head): it takes
+// the largest |x| of the page's new tokens, settles the scale, and converts
+// from registers, so each new value is read once and each code written once
+// (bound: HBM; 3 bytes a bf16 value).  A thread holds sixteen-value chunks,
+// CH at a time; a group has a thread for every CH chunks of a full page or,
+// when the round is shorter than a page, of the round, so a page is in
+// registers at once and nothing is read twice.
+template <class T, int CH>
+__global__ void __launch_bounds__(kKvThreads) kv_write_kernel(const KvWriteProblem a) {
+  __shared__ float red[kKvThreads / 32];
+  grid_dependency_wait();
+  const int tid = static_cast<int>(threadIdx.x);
+  const int GT = a.group, gl = tid & (GT - 1);
+  const long long task = static_cast<long long>(blockIdx.x) * (kKvThreads / GT) + tid / GT;
+  const int Hkv = a.c.Hkv, D = a.c.D, P = a.c.page_size;
+  const int h = static_cast<int>(task % Hkv);
+  const int side = static_cast<int>(task / Hkv & 1);
+  const long long bi = task / Hkv / 2;
+  const int i = static_cast<int>(bi % a.pages);
+  const long long b = bi / a.pages;
+
+  int kept = 0, first = 0, count = 0, page = 0, row0 = 0;
+  bool active = b < a.B;
+  if (active) {
+    const int len = a.kv_len[b];
+    const int n = a.num_new ? a.num_new[b] : a.T;
+    const bool ok = len >= 0 && n >= 0 && n <= a.T &&
+                    static_cast<long long>(len) + n <= static_cast<long long>(a.c.slots) * P;
+    active = false;
+    if (!ok) {
+      if (i == 0 && h == 0 && side == 0 && gl == 0) record_error(a.err, SV_DERR_ARG);
+    } else if (n > 0) {
+      const int slot = (len >> a.c.page_shift) + i;
+      const int from = max(len, slot << a.c.page_shift);
+      const long long to =
+          min(static_cast<long long>(len) + n, (static_cast<long long>(slot) + 1) << a.c.page_shift);
+      if (from < to) {
+        page = a.c.page_table[b * a.c.slots + slot];
+        if (page < 0 || page >= a.c.num_pages) {
+          if (h == 0 && side == 0 && gl == 0) record_error(a.err, SV_DERR_PAGE);
+        } else {
+          active = true;
+          kept = i == 0 ? len & (P - 1) : 0;
+          first = from - len;
+          count = static_cast<int>(to - from);
+          row0 = from & (P - 1);
+        }
+      }
+    }
+  }
+
+  const int parts = D / 16;  // chunks of a token: 4 or 8
+  const int pshift = D == 64 ? 2 : 3;
+  const int chunks = active ? count << pshift : 0;
+  const T* src = static_cast<const T*>(side ? a.v_new : a.k_new) +
+                 (side ? b * a.v_batch + h * a.v_head : b * a.k_batch + h * a.k_head);
+  const long long tstride = side ? a.v_token : a.k_token;
+  Raw16<T> x[CH];
+  float amax = 0.f;
+  bool bad = false;
+#pragma unroll
+  for (int j = 0; j < CH; ++j) {
+    const int c = gl + j * GT;
+    if (c < chunks)
+      load16(x[j], src + (first + (c >> pshift)) * tstride + (c & (parts - 1)) * 16, a.vec);
+  }
+#pragma unroll
+  for (int j = 0; j < CH; ++j) {
+    if (gl + j * GT < chunks) {
+#pragma unroll
+      for (int k = 0; k < 16; ++k) {
+        const float m = fabsf(elem16(x[j], k));
+        const bool fin = m < kPosInf;  // false for NaN
+        bad |= !fin;
+        amax = fmaxf(amax, fin ? m : 0.f);
+      }
+    }
+  }
+  if (bad) record_error(a.err, SV_DERR_NONFINITE);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+  float* scale = (side ? a.c.v_scale : a.c.k_scale) + static_cast<long long>(page) * Hkv + h;
+  int before = kKvExpLo;
+  if (active && kept > 0) before = scale_exp(*scale);
+  if ((tid & 31) == 0) red[tid >> 5] = amax;
+  __syncthreads();  // every thread has read the old scale
+  const int w0 = (tid / GT) * (GT / 32);
+  for (int w = 0; w < GT / 32; ++w) amax = fmaxf(amax, red[w0 + w]);
+  if (!active) return;
+  const int e = max(needed_exp(amax), before);
+  const float inv = pow2f(-e);
+  unsigned char* dst = (side ? a.c.v : a.c.k) + page * a.c.page_stride + h * a.c.head_stride;
+#pragma unroll
+  for (int j = 0; j < CH; ++j) {
+    const int c = gl + j * GT;
+    if (c < chunks) {
+      unsigned w[4];
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        w[q] = e4m3x4(elem16(x[j], 4 * q) * inv, elem16(x[j], 4 * q + 1) * inv,
+                      elem16(x[j], 4 * q + 2) * inv, elem16(x[j], 4 * q + 3) * inv);
+      *reinterpret_cast<uint4*>(dst + (row0 + (c >> pshift)) * D + (c & (parts - 1)) * 16) =
+          make_uint4(w[0], w[1], w[2], w[3]);
+    }
+  }
+  if (kept > 0 && e > before) {
+    // the tokens that stay, at the larger scale
+    const float f = pow2f(before - e);
+    for (int c = gl; c < kept << pshift; c += GT) {
+      uint4* p = reinterpret_cast<uint4*>(dst + static_cast<long long>(c) * 16);
+      uint4 v = *p;
+      unsigned* w = reinterpret_cast<unsigned*>(&v);
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const float2 lo = float2_of_half2(half2_lo(w[q])), hi = float2_of_half2(half2_hi(w[q]));
+        w[q] = e4m3x4(lo.x * f, lo.y * f, hi.x * f, hi.y * f);
+      }
+      *p = v;
+    }
+  }
+  if (gl == 0 && (kept == 0 || e > before)) *scale = pow2f(e);
+}
+
+// -------------------------------------------------------------------- read
+
+struct KvReadProblem {
+  KvCache c;
+  int B, T;
+  bool vec;
+  void *k_out, *v_out;
+  long long batch, token, head;
+  const int *start, *num, *rows;
+  int* err;
+};
+
+template <class T>
+__device__ __forceinline__ T from_float(float x);
+template <>
+__device__ __forceinline__ float from_float<float>(float x) { return x; }
+template <>
+__device__ __forceinline__ __nv_bfloat16 from_float<__nv_bfloat16>(float x) {
+  return __float2bfloat16_rn(x);
+}
+template <>
+__device__ __forceinline__ __half from_float<__half>(float x) { return __float2half_rn(x); }
+
+// A thread takes sixteen codes of one token, head and side: 16 bytes in, 32
+// or 64 out (bound: HBM; 3 bytes a bf16 value).  Consecutive threads take a
+// token's channels, then its heads, so the output is written in order; a
+// head's row of a token is one or half a 128-byte line of the cache.
+// kKvReadChunks chunks per thread are loaded together: a chunk's address
+// hangs on the page table, and the loads of several overlap that latency.
+constexpr int kKvReadChunks = 4;
+
+template <class T>
+__global__ void __launch_bounds__(kKvThreads) kv_read_kernel(const KvReadProblem a) {
+  grid_dependency_wait();
+  const int Hkv = a.c.Hkv, D = a.c.D, P = a.c.page_size;
+  const int parts = D / 16;
+  const long long total = static_cast<long long>(a.B) * a.T * Hkv * parts;
+  const long long at0 =
+      static_cast<long long>(blockIdx.x) * (kKvThreads * kKvReadChunks) + threadIdx.x;
+  const int side = static_cast<int>(blockIdx.y);
+  const unsigned char* base = side ? a.c.v : a.c.k;
+  const float* scales = side ? a.c.v_scale : a.c.k_scale;
+  T* out = static_cast<T*>(side ? a.v_out : a.k_out);
+  uint4 code[kKvReadChunks];
+  float s[kKvReadChunks];
+#pragma unroll
+  for (int j = 0; j < kKvReadChunks; ++j) {
+    const long long at = at0 + j * kKvThreads;
+    code[j] = make_uint4(0, 0, 0, 0);
+    s[j] = 0.f;
+    if (at >= total) continue;
+    const int part = static_cast<int>(at) & (parts - 1);
+    const long long th = at / parts;
+    const int h = static_cast<int>(th % Hkv);
+    const long long bt = th / Hkv;
+    const int t = static_cast<int>(bt % a.T);
+    const long long b = bt / a.T;
+    const int n = a.num ? a.num[b] : a.T;
+    const bool report = side == 0 && h == 0 && part == 0;
+    if (n < 0 || n > a.T) {
+      if (report && t == 0) record_error(a.err, SV_DERR_ARG);
+      continue;
+    }
+    if (t >= n) continue;
+    const long long pos = static_cast<long long>(a.start ? a.start[b] : 0) +
+                          (a.rows ? a.rows[b * a.T + t] : t);
+    if (pos < 0 || pos >= static_cast<long long>(a.c.slots) * P) {
+      if (report) record_error(a.err, SV_DERR_ARG);
+      continue;
+    }
+    const int page = a.c.page_table[b * a.c.slots + (pos >> a.c.page_shift)];
+    if (page < 0 || page >= a.c.num_pages) {
+      if (report) record_error(a.err, SV_DERR_PAGE);
+      continue;
+    }
+    code[j] = *reinterpret_cast<const uint4*>(base + page * a.c.page_stride +
+                                              h * a.c.head_stride +
+                                              (pos & (P - 1)) * D + part * 16);
+    s[j] = scales[static_cast<long long>(page) * Hkv + h];
+  }
+#pragma unroll
+  for (int j = 0; j < kKvReadChunks; ++j) {
+    const long long at = at0 + j * kKvThreads;
+    if (at >= total) continue;
+    const int part = static_cast<int>(at) & (parts - 1);
+    const long long th = at / parts;
+    const int h = static_cast<int>(th % Hkv);
+    const long long bt = th / Hkv;
+    T* p = out + bt / a.T * a.batch + bt % a.T * a.token + h * a.head + part * 16;
+    Raw16<T> y;
+    T* e = reinterpret_cast<T*>(y.w);
+    const unsigned* w = reinterpret_cast<const unsigned*>(&code[j]);
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const float2 lo = float2_of_half2(half2_lo(w[q])), hi = float2_of_half2(half2_hi(w[q]));
+      e[4 * q] = from_float<T>(lo.x * s[j]);
+      e[4 * q + 1] = from_float<T>(lo.y * s[j]);
+      e[4 * q + 2] = from_float<T>(hi.x * s[j]);
+      e[4 * q + 3] = from_float<T>(hi.y * s[j]);
+    }
+    if (a.vec) {
+#pragma unroll
+      for (int q = 0; q < static_cast<int>(sizeof(T)); ++q) reinterpret_cast<uint4*>(p)[q] = y.w[q];
+    } else {
+#pragma unroll
+      for (int q = 0; q < 16; ++q) p[q] = e[q];
+    }
+  }
+}
+
+}  // namespace sv
