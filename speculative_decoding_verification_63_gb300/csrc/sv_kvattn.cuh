@@ -92,18 +92,25 @@ __device__ __forceinline__ KaLen ka_len(const KvAttnProblem& a, int b, bool* bad
   return r;
 }
 
+// Blocks of the row tile `tile` (ROWS rows each) of a request: up to the
+// last position its rows can see.
+template <int ROWS, int BLOCK>
+__device__ __forceinline__ int ka_tile_blocks(const KvAttnProblem& a, const KaLen& l, int tile) {
+  const int last = a.mask != nullptr ? l.n - 1 : min(l.n - 1, ((tile + 1) * ROWS - 1) / a.G);
+  return (l.len + last + 1 + BLOCK - 1) / BLOCK;
+}
+
 // A position in the list of all blocks: request, unit of the request
 // (key/value head major, row tile minor) and block of the unit.
+template <int ROWS, int BLOCK>
 struct KaCursor {
-  int b, unit, blk;
-  int len, n, tiles, nblk;  // of request b
+  KaLen l;  // of request b
+  int b, head, tile, tiles, blk, nblk;
+  long long unit0;  // the unit's first block in the list
   __device__ __forceinline__ void load(const KvAttnProblem& a) {
     bool bad = false;
-    const KaLen l = ka_len(a, b, &bad);
-    len = l.len;
-    n = l.n;
-    tiles = (n * a.G + kKaRows - 1) / kKaRows;
-    nblk = (len + n + kKaBlock - 1) / kKaBlock;
+    l = ka_len(a, b, &bad);
+    tiles = (l.n * a.G + ROWS - 1) / ROWS;
   }
   __device__ __forceinline__ void seek(const KvAttnProblem& a, const long long* prefix,
                                        long long at) {
@@ -114,19 +121,160 @@ struct KaCursor {
     }
     b = lo;
     load(a);
-    const long long in = at - prefix[b];
-    unit = static_cast<int>(in / nblk);
-    blk = static_cast<int>(in - static_cast<long long>(unit) * nblk);
+    const long long per_head = (prefix[b + 1] - prefix[b]) / a.c.Hkv;
+    head = static_cast<int>((at - prefix[b]) / per_head);
+    unit0 = prefix[b] + head * per_head;
+    for (tile = 0;; ++tile) {
+      nblk = ka_tile_blocks<ROWS, BLOCK>(a, l, tile);
+      if (at < unit0 + nblk || tile + 1 >= tiles) break;
+      unit0 += nblk;
+    }
+    blk = static_cast<int>(at - unit0);
   }
   // to the next unit (requests without units are skipped)
   __device__ __forceinline__ void next_unit(const KvAttnProblem& a) {
+    unit0 += nblk;
     blk = 0;
-    if (++unit < a.c.Hkv * tiles) return;
-    unit = 0;
-    do {
-      if (++b >= a.B) return;
-      load(a);
-    } while (n == 0);
+    if (++tile >= tiles) {
+      tile = 0;
+      if (++head >= a.c.Hkv) {
+        head = 0;
+        do {
+          if (++b >= a.B) return;
+          load(a);
+        } while (l.n == 0);
+      }
+    }
+    nblk = ka_tile_blocks<ROWS, BLOCK>(a, l, tile);
+  }
+};
+
+// The cumulated block counts of the requests into prefix[0 .. B] (every
+// thread of the block calls this); returns their total.
+template <int ROWS, int BLOCK, int THREADS>
+__device__ __forceinline__ long long ka_prefix(const KvAttnProblem& a, long long* prefix,
+                                               long long* scan, bool report) {
+  const int tid = static_cast<int>(threadIdx.x), warp = tid >> 5, lane = tid & 31;
+  long long total = 0;
+  for (int base = 0; base < a.B; base += THREADS) {
+    const int b = base + tid;
+    long long mine = 0;
+    if (b < a.B) {
+      bool bad = false;
+      const KaLen l = ka_len(a, b, &bad);
+      if (bad && report) record_error(a.err, SV_DERR_ARG);
+      const int tiles = (l.n * a.G + ROWS - 1) / ROWS;
+      for (int tile = 0; tile < tiles; ++tile) mine += ka_tile_blocks<ROWS, BLOCK>(a, l, tile);
+      mine *= a.c.Hkv;
+    }
+    long long x = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long y = __shfl_up_sync(0xffffffffu, x, o);
+      if (lane >= o) x += y;
+    }
+    __syncthreads();
+    if (lane == 31) scan[warp] = x;
+    __syncthreads();
+    long long before = total;
+    for (int w = 0; w < THREADS / 32; ++w) {
+      if (w < warp) before += scan[w];
+      total += scan[w];
+    }
+    if (b < a.B) prefix[b] = before + x - mine;
+  }
+  if (tid == 0) prefix[a.B] = total;
+  __syncthreads();
+  return total;
+}
+
+// Rows of the round that hold no token: 0, lse -inf.
+template <class T, int D, int THREADS>
+__device__ __forceinline__ void ka_clear_rows(const KvAttnProblem& a) {
+  for (int b = static_cast<int>(blockIdx.x); b < a.B; b += static_cast<int>(gridDim.x)) {
+    bool bad = false;
+    const KaLen l = ka_len(a, b, &bad);
+    const long long row0 = (static_cast<long long>(b) * a.T + l.n) * a.Hq;
+    const long long rows = static_cast<long long>(a.T - l.n) * a.Hq;
+    uint4* o = reinterpret_cast<uint4*>(static_cast<T*>(a.out) + row0 * D);
+    for (long long i = threadIdx.x; i < rows * (D / 8); i += THREADS) o[i] = make_uint4(0, 0, 0, 0);
+    if (a.lse)
+      for (long long i = threadIdx.x; i < rows; i += THREADS) a.lse[row0 + i] = kNegInf;
+  }
+}
+
+// CTA c of `parts` holds blocks [total c / parts, total (c + 1) / parts);
+// this is the one that holds block x.
+__device__ __forceinline__ int ka_cta_of(long long x, long long parts, long long total) {
+  return static_cast<int>(((x + 1) * parts - 1) / total);
+}
+
+// What the producer warp knows of the blocks ahead.  A block's page ids hang
+// on the page table, its scales on the page ids: two round trips to memory.
+// Each lane owns one copy (16 positions of keys or of values) of one block of
+// a batch of NB = 32 / (BLOCK / 8) blocks, and the two lookups run two and one
+// batches ahead of the copies, so neither is waited for.
+template <int ROWS, int BLOCK>
+struct KaFeed {
+  static constexpr int kCopies = BLOCK / 8, NB = 32 / kCopies;
+  KaCursor<ROWS, BLOCK> cur;  // the lane's block, two batches ahead
+  int left;                   // blocks from there to the end of the CTA's part
+  int sub, page;              // 16-position piece; its page (-2: none)
+  bool is_v;
+  struct Item {
+    const unsigned char* src;  // null: nothing to copy
+    float scale;               // < 0: no such page
+    int first, tokens, round;  // the block begins a segment; its place
+  };
+  int a_first, a_tokens, a_round, a_head, a_pos;  // of `page`
+
+  __device__ __forceinline__ void advance(const KvAttnProblem& a, int steps) {
+    for (int k = 0; k < steps && left > 0; ++k) {
+      --left;
+      if (++cur.blk == cur.nblk && left > 0) cur.next_unit(a);
+    }
+  }
+  __device__ __forceinline__ void look(const KvAttnProblem& a, bool very_first) {
+    page = -2;
+    if (left > 0) {
+      a_pos = cur.blk * BLOCK + sub * 16;
+      a_head = cur.head;
+      a_first = cur.blk == 0 || very_first;
+      a_tokens = cur.l.len + cur.l.n - cur.blk * BLOCK;
+      a_round = cur.blk * BLOCK - cur.l.len;
+      if (a_pos < cur.l.len + cur.l.n)
+        page = a.c.page_table[static_cast<long long>(cur.b) * a.c.slots +
+                              (a_pos >> a.c.page_shift)];
+      advance(a, NB);
+    }
+  }
+  __device__ __forceinline__ Item resolve(const KvAttnProblem& a) {
+    Item it;
+    it.src = nullptr;
+    it.scale = -1.f;
+    it.first = a_first;
+    it.tokens = a_tokens;
+    it.round = a_round;
+    if (page >= 0 && page < a.c.num_pages) {
+      it.src = (is_v ? a.c.v : a.c.k) + page * a.c.page_stride + a_head * a.c.head_stride +
+               (a_pos & (a.c.page_size - 1)) * a.c.D;
+      it.scale =
+          (is_v ? a.c.v_scale : a.c.k_scale)[static_cast<long long>(page) * a.c.Hkv + a_head];
+    } else if (page != -2) {
+      record_error(a.err, SV_DERR_PAGE);
+    }
+    return it;
+  }
+  // positions the lane at its block of the first batch
+  __device__ __forceinline__ void start(const KvAttnProblem& a, const long long* prefix,
+                                        long long w0, int n, int lane) {
+    cur.seek(a, prefix, w0);
+    left = n;
+    sub = lane % (kCopies / 2);
+    is_v = lane % kCopies >= kCopies / 2;
+    const int mine = lane / kCopies;
+    advance(a, mine);
+    look(a, mine == 0);
   }
 };
 
@@ -216,6 +364,11 @@ struct KaAcc {
   }
 };
 
+template <int N>
+struct KaInt {
+  static constexpr int value = N;
+};
+
 template <class T>
 __device__ __forceinline__ float2 ka_two(const T* p);
 template <>
@@ -235,7 +388,7 @@ __global__ void __launch_bounds__(kKaThreads, kKaCtasPerSm) kv_attn_kernel(const
   const int grid = static_cast<int>(gridDim.x), cta = static_cast<int>(blockIdx.x);
   if (tid == 0) {
     for (int s = 0; s < kKaStages; ++s) {
-      mbar_init(&sh.full[s], 32);
+      mbar_init(&sh.full[s], KaFeed<kKaRows, kKaBlock>::kCopies);
       mbar_init(&sh.empty[s], kKaWarps / 2);
     }
     sh.dead = 0;
@@ -243,47 +396,8 @@ __global__ void __launch_bounds__(kKaThreads, kKaCtasPerSm) kv_attn_kernel(const
   }
   grid_dependency_wait();
 
-  // cumulated block counts, and the rows of the round that hold no token
-  long long total = 0;
-  for (int base = 0; base < a.B; base += kKaThreads) {
-    const int b = base + tid;
-    long long mine = 0;
-    if (b < a.B) {
-      bool bad = false;
-      const KaLen l = ka_len(a, b, &bad);
-      if (bad && cta == 0) record_error(a.err, SV_DERR_ARG);
-      mine = static_cast<long long>(a.c.Hkv) * ((l.n * a.G + kKaRows - 1) / kKaRows) *
-             ((static_cast<long long>(l.len) + l.n + kKaBlock - 1) / kKaBlock);
-    }
-    long long x = mine;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const long long y = __shfl_up_sync(0xffffffffu, x, o);
-      if (lane >= o) x += y;
-    }
-    __syncthreads();
-    if (lane == 31) sh.scan[warp] = x;
-    __syncthreads();
-    long long before = total;
-    for (int w = 0; w < kKaThreads / 32; ++w) {
-      if (w < warp) before += sh.scan[w];
-      total += sh.scan[w];
-    }
-    if (b < a.B) sh.prefix[b] = before + x - mine;
-  }
-  if (tid == 0) sh.prefix[a.B] = total;
-  __syncthreads();
-
-  for (int b = cta; b < a.B; b += grid) {
-    bool bad = false;
-    const KaLen l = ka_len(a, b, &bad);
-    const long long row0 = (static_cast<long long>(b) * a.T + l.n) * a.Hq;
-    const long long rows = static_cast<long long>(a.T - l.n) * a.Hq;
-    uint4* o = reinterpret_cast<uint4*>(static_cast<T*>(a.out) + row0 * D);
-    for (long long i = tid; i < rows * (D / 8); i += kKaThreads) o[i] = make_uint4(0, 0, 0, 0);
-    if (a.lse)
-      for (long long i = tid; i < rows; i += kKaThreads) a.lse[row0 + i] = kNegInf;
-  }
+  const long long total = ka_prefix<kKaRows, kKaBlock, kKaThreads>(a, sh.prefix, sh.scan, cta == 0);
+  ka_clear_rows<T, D, kKaThreads>(a);
 
   // this CTA's part of the blocks
   const long long parts =
@@ -294,50 +408,36 @@ __global__ void __launch_bounds__(kKaThreads, kKaCtasPerSm) kv_attn_kernel(const
 
   if (warp == kKaWarps) {
     // ------------------------------------------------------------ producer
-    // Lane l < 8 owns copy l of a block: 16 positions of keys (l < 4) or
-    // values; its page id is looked up one block ahead.
     const uint64_t pol = policy_evict_first();
-    KaCursor cur;
-    cur.seek(a, sh.prefix, w0);
-    const int sub = lane & 3;
-    const bool is_v = lane >= 4;
-    auto page_of = [&](const KaCursor& c) -> int {
-      const int pos = c.blk * kKaBlock + sub * 16;
-      if (lane >= 8 || c.b >= a.B || pos >= c.len + c.n) return -2;
-      return a.c.page_table[static_cast<long long>(c.b) * a.c.slots + (pos >> a.c.page_shift)];
-    };
-    int page = page_of(cur);
-    long long i = 0;
-    for (long long w = w0; w < w1; ++w, ++i) {
-      const int s = static_cast<int>(i % kKaStages);
-      const uint32_t round = static_cast<uint32_t>(i / kKaStages);
-      if (round > 0) ka_wait(&sh.empty[s], (round - 1) & 1, &sh.dead, a.err);
-      __syncwarp();
-      if (__any_sync(0xffffffffu, *static_cast<volatile int*>(&sh.dead))) {
-        // let the consumers' waits end
-        mbar_arrive(&sh.full[s]);
-        continue;
+    KaFeed<kKaRows, kKaBlock> feed;
+    const int n = static_cast<int>(w1 - w0);
+    feed.start(a, sh.prefix, w0, n, lane);
+    auto item = feed.resolve(a);
+    feed.look(a, false);
+    int i = 0;
+    for (int i0 = 0; i0 < n; i0 += feed.NB) {
+      const auto next = feed.resolve(a);
+      feed.look(a, false);
+      for (int j = 0; j < feed.NB && i < n; ++j, ++i) {
+        const int s = i % kKaStages;
+        if (i >= kKaStages)
+          ka_wait(&sh.empty[s], static_cast<uint32_t>(i / kKaStages - 1) & 1, &sh.dead, a.err);
+        __syncwarp();
+        if (lane / feed.kCopies == j) {
+          if (item.src != nullptr && !*static_cast<volatile int*>(&sh.dead)) {
+            mbar_expect_tx(&sh.full[s], 16 * D);
+            bulk_copy_g2s_hint((feed.is_v ? sh.v[s] : sh.k[s]) + feed.sub * 16 * D, item.src,
+                               16 * D, &sh.full[s], pol);
+          }
+          (feed.is_v ? sh.v_scale[s] : sh.k_scale[s])[feed.sub] = item.scale;
+          mbar_arrive(&sh.full[s]);
+        }
+        __syncwarp();
       }
-      const int h = cur.unit / cur.tiles;
-      const int pos = cur.blk * kKaBlock + sub * 16;
-      const bool there = page >= 0 && page < a.c.num_pages;
-      if (page != -2 && !there) record_error(a.err, SV_DERR_PAGE);
-      float sc = -1.f;
-      if (there) {
-        const unsigned char* src = (is_v ? a.c.v : a.c.k) + page * a.c.page_stride +
-                                   h * a.c.head_stride + (pos & (a.c.page_size - 1)) * D;
-        mbar_expect_tx(&sh.full[s], 16 * D);
-        bulk_copy_g2s_hint((is_v ? sh.v[s] : sh.k[s]) + sub * 16 * D, src, 16 * D, &sh.full[s],
-                           pol);
-        sc = (is_v ? a.c.v_scale : a.c.k_scale)[static_cast<long long>(page) * a.c.Hkv + h];
-      }
-      if (++cur.blk == cur.nblk) cur.next_unit(a);
-      page = w + 1 < w1 ? page_of(cur) : -2;
-      if (lane < 8) (is_v ? sh.v_scale[s] : sh.k_scale[s])[sub] = sc;
-      mbar_arrive(&sh.full[s]);
+      item = next;
     }
     // copies of the last stages must land before the block ends
-    for (long long j = max(0ll, i - kKaStages); j < i; ++j)
+    for (int j = max(0, n - kKaStages); j < n; ++j)
       if (!mbar_wait_bounded(&sh.full[j % kKaStages],
                              static_cast<uint32_t>(j / kKaStages) & 1, 1000000000ull))
         record_error(a.err, SV_DERR_TIMEOUT);
@@ -348,14 +448,14 @@ __global__ void __launch_bounds__(kKaThreads, kKaCtasPerSm) kv_attn_kernel(const
   const int g = lane >> 2, t = lane & 3;
   const int pair = warp >> 1, half = warp & 1;  // pairs take alternate blocks, warps a half each
   constexpr int KS = D / 16;
-  KaCursor cur;
+  KaCursor<kKaRows, kKaBlock> cur;
   cur.seek(a, sh.prefix, w0);
   long long w = w0;
   while (w < w1) {
-    const int h = cur.unit / cur.tiles, tile = cur.unit % cur.tiles;
+    const int h = cur.head, tile = cur.tile;
     const int blk0 = cur.blk;
     const int blk1 = static_cast<int>(min(static_cast<long long>(cur.nblk), blk0 + (w1 - w)));
-    const int L = cur.len + cur.n;
+    const int L = cur.l.len + cur.l.n;
 
     // the unit's queries as fragments: bf16 rows are scaled by a power of two
     // into the halves' range
@@ -366,7 +466,7 @@ __global__ void __launch_bounds__(kKaThreads, kKaCtasPerSm) kv_attn_kernel(const
 #pragma unroll
       for (int r = 0; r < 2; ++r) {
         const int row = tile * kKaRows + g + 8 * r;
-        const bool ok = row < cur.n * a.G;
+        const bool ok = row < cur.l.n * a.G;
         rt[r] = ok ? row / a.G : a.T;
         const T* p = static_cast<const T*>(a.q) + cur.b * a.q_batch +
                      (ok ? row / a.G : 0) * a.q_token + (h * a.G + (ok ? row % a.G : 0)) * a.q_head +
@@ -434,7 +534,7 @@ __global__ void __launch_bounds__(kKaThreads, kKaCtasPerSm) kv_attn_kernel(const
       }
       float kse[2], vse[2];
       float zin[2];  // 2^-ev
-      bool edge = pos0 + 32 > cur.len;
+      bool edge = pos0 + 32 > cur.l.len;
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
         const float ks = sh.k_scale[s][half * 2 + u], vs = sh.v_scale[s][half * 2 + u];
@@ -459,7 +559,7 @@ __global__ void __launch_bounds__(kKaThreads, kKaCtasPerSm) kv_attn_kernel(const
           for (int nt = 0; nt < 4; ++nt)
             for (int c = 0; c < 2; ++c) {
               const int pos = pos0 + nt * 8 + 2 * t + c;
-              const int j = pos - cur.len;
+              const int j = pos - cur.l.len;
               bool see = pos < L && rt[r] < a.T && sh.k_scale[s][half * 2 + (nt >> 1)] >= 0.f;
               if (j >= 0 && see)
                 see = a.mask == nullptr
@@ -616,12 +716,49 @@ __global__ void __launch_bounds__(kKaThreads, kKaCtasPerSm) kv_attn_kernel(const
     if (warp == 0) join_smem(sh.merge[0]);
 
     const bool starts = blk0 == 0, ends = blk1 == cur.nblk;
-    bool write = true;
-    if (!(starts && ends)) {
+    // the rows' results, channels of tiles j0 .. j0 + NJ - 1
+    auto finish = [&](float z0, float z1, float r0, float r1, int j0, auto nj, auto get) {
+      constexpr int NJ = decltype(nj)::value;
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        if (rt[r] < a.T) {
+          const int row = tile * kKaRows + g + 8 * r;
+          const long long orow =
+              (static_cast<long long>(cur.b) * a.T + rt[r]) * a.Hq + h * a.G + row % a.G;
+          const float z = r ? z1 : z0, ref = r ? r1 : r0;
+          const bool any = !(z == 0.f);  // true for NaN
+          const float inv = any ? 1.f / z : 0.f;
+          T* o = static_cast<T*>(a.out) + orow * D + j0;
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            alignas(16) T e[NJ];
+#pragma unroll
+            for (int j = 0; j < NJ; ++j)
+              e[j] = from_float<T>(any ? get(4 * j + 2 * r + c) * inv : 0.f);
+            T* oc = o + (2 * t + c) * (D / 8);
+            if constexpr (NJ % 8 == 0) {
+#pragma unroll
+              for (int j = 0; j < NJ / 8; ++j)
+                reinterpret_cast<uint4*>(oc)[j] = reinterpret_cast<const uint4*>(e)[j];
+            } else if constexpr (NJ == 4) {
+              *reinterpret_cast<uint2*>(oc) = *reinterpret_cast<const uint2*>(e);
+            } else {
+              *reinterpret_cast<unsigned*>(oc) = *reinterpret_cast<const unsigned*>(e);
+            }
+          }
+          if (a.lse && t == 0 && j0 == 0)
+            a.lse[orow] = any ? (log2f(z) + ref - kRefShift) * 0.69314718055994531f : kNegInf;
+        }
+      }
+    };
+    if (starts && ends) {
+      if (warp == 0)
+        finish(acc.z[0], acc.z[1], acc.ref[0], acc.ref[1], 0, KaInt<D / 8>(),
+               [&](int i) { return acc.o[i >> 2][i & 3]; });
+    } else {
       // the unit is cut: CTAs first .. last hold a part of it
-      const long long u0 = sh.prefix[cur.b] + static_cast<long long>(cur.unit) * cur.nblk;
-      const int first = static_cast<int>(((u0 + 1) * parts - 1) / total);
-      const int last = static_cast<int>(((u0 + cur.nblk) * parts - 1) / total);
+      const int first = ka_cta_of(cur.unit0, parts, total);
+      const int last = ka_cta_of(cur.unit0 + cur.nblk - 1, parts, total);
       constexpr int PF = kKaPartialFloats<D>;
       if (warp == 0) {
         // a part that begins inside the unit is its CTA's first
@@ -631,46 +768,47 @@ __global__ void __launch_bounds__(kKaThreads, kKaCtasPerSm) kv_attn_kernel(const
         if (lane == 0)
           sh.last = atomic_add_acq_rel(&a.tickets[first], 1u) ==
                     static_cast<unsigned>(last - first);
-        __syncwarp();
-        write = sh.last != 0;
-        if (write) {
-          __threadfence();
-          acc.clear();
-          for (int c = first; c <= last; ++c) {
-            float* p = a.partials + (2ll * c + (c == first ? 1 : 0)) * PF;
-            acc.join(__ldcg(p + lane), __ldcg(p + 32 + lane), __ldcg(p + 64 + lane),
-                     __ldcg(p + 96 + lane), [&](int i) { return __ldcg(p + (4 + i) * 32 + lane); });
-            for (int i = lane; i < PF; i += 32) p[i] = 0.f;
-          }
-          if (lane == 0) a.tickets[first] = 0u;
-        }
       }
-    }
-    if (warp == 0 && write) {
-#pragma unroll
-      for (int r = 0; r < 2; ++r) {
-        if (rt[r] < a.T) {
-          const int row = tile * kKaRows + g + 8 * r;
-          const long long orow =
-              (static_cast<long long>(cur.b) * a.T + rt[r]) * a.Hq + h * a.G + row % a.G;
-          const bool any = !(acc.z[r] == 0.f);  // true for NaN
-          const float inv = any ? 1.f / acc.z[r] : 0.f;
-          T* o = static_cast<T*>(a.out) + orow * D;
-#pragma unroll
-          for (int c = 0; c < 2; ++c) {
-            alignas(16) T e[D / 8];
-#pragma unroll
-            for (int j = 0; j < D / 8; ++j)
-              e[j] = from_float<T>(any ? acc.o[j][2 * r + c] * inv : 0.f);
-#pragma unroll
-            for (int j = 0; j < D / 64; ++j)
-              reinterpret_cast<uint4*>(o + (2 * t + c) * (D / 8))[j] =
-                  reinterpret_cast<const uint4*>(e)[j];
-          }
-          if (a.lse && t == 0)
-            a.lse[orow] = any ? (log2f(acc.z[r]) + acc.ref[r] - kRefShift) * 0.69314718055994531f
-                              : kNegInf;
+      named_sync(1, kKaWarps * 32);
+      if (sh.last) {
+        // The last to arrive joins the parts in order, each warp a quarter of
+        // the channels, and leaves zeros behind.
+        __threadfence();
+        constexpr int NJ = D / 32;
+        auto part = [&](int c) { return a.partials + (2ll * c + (c == first ? 1 : 0)) * PF; };
+        float m0 = kNegInf, m1 = kNegInf;
+#pragma unroll 8
+        for (int c = first; c <= last; ++c) {
+          m0 = fmaxf(m0, __ldcg(part(c) + lane));
+          m1 = fmaxf(m1, __ldcg(part(c) + 32 + lane));
         }
+        float z0 = 0.f, z1 = 0.f, o[4 * NJ];
+#pragma unroll
+        for (int i = 0; i < 4 * NJ; ++i) o[i] = 0.f;
+#pragma unroll 2
+        for (int c = first; c <= last; ++c) {
+          float* p = part(c);
+          const float r0 = __ldcg(p + lane), r1 = __ldcg(p + 32 + lane);
+          // a part that saw nothing has Z = 0 and O = 0 (or NaN, which stays)
+          const float f0 = r0 == kNegInf ? 1.f : exp2f(r0 - m0);
+          const float f1 = r1 == kNegInf ? 1.f : exp2f(r1 - m1);
+          z0 = fmaf(__ldcg(p + 64 + lane), f0, z0);
+          z1 = fmaf(__ldcg(p + 96 + lane), f1, z1);
+          float* po = p + (4 + 4 * NJ * warp) * 32 + lane;
+#pragma unroll
+          for (int i = 0; i < 4 * NJ; ++i)
+            o[i] = fmaf(__ldcg(po + i * 32), (i & 2) ? f1 : f0, o[i]);
+        }
+        named_sync(1, kKaWarps * 32);  // the statistics have been read
+        for (int c = first; c <= last; ++c) {
+          float* p = part(c);
+          p[warp * 32 + lane] = 0.f;
+          float* po = p + (4 + 4 * NJ * warp) * 32 + lane;
+#pragma unroll
+          for (int i = 0; i < 4 * NJ; ++i) po[i * 32] = 0.f;
+        }
+        if (tid == 0) a.tickets[first] = 0u;
+        finish(z0, z1, m0, m1, NJ * warp, KaInt<NJ>(), [&](int i) { return o[i]; });
       }
     }
     w += blk1 - blk0;
