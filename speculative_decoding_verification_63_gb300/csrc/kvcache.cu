@@ -195,7 +195,7 @@ sv_status sv_kv_write(const sv_kv_write_args* a, void* workspace, size_t ws_byte
   p.c = cache_view(a->cache);
   p.B = a->B;
   p.T = a->T;
-  p.pages = (a->T + p.c.page_size - 1) / p.c.page_size + 1;
+  p.pages = (a->T + p.c.page_size - 2) / p.c.page_size + 1;
   p.k_new = a->k_new;
   p.v_new = a->v_new;
   p.k_batch = a->k_batch_stride;
@@ -215,10 +215,9 @@ sv_status sv_kv_write(const sv_kv_write_args* a, void* workspace, size_t ws_byte
   p.group = 32;
   while (p.group * kCh < chunks) p.group *= 2;
   static_assert(128 * 128 / 16 <= kKvThreads * kCh, "a page fits one block");
-  const int64_t tasks = static_cast<int64_t>(a->B) * p.pages * 2 * p.c.Hkv;
-  const int64_t blocks = (tasks * p.group + kKvThreads - 1) / kKvThreads;
-  if (blocks > 0x7fffffff) return SV_EINVAL;
-  const dim3 grid(static_cast<unsigned>(blocks));
+  const int64_t threads = static_cast<int64_t>(p.pages) * 2 * p.c.Hkv * p.group;
+  const dim3 grid(static_cast<unsigned>((threads + kKvThreads - 1) / kKvThreads),
+                  static_cast<unsigned>(a->B));
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   switch (a->dtype) {
     case SV_BF16: return launch(kv_write_kernel<__nv_bfloat16, kCh>, p, grid, kKvThreads, 0, st);
@@ -259,11 +258,12 @@ sv_status sv_kv_read(const sv_kv_read_args* a, void* workspace, size_t ws_bytes,
   p.num = a->num;
   p.rows = a->rows;
   p.err = error_word(workspace);
-  const int64_t total = static_cast<int64_t>(a->B) * a->T * p.c.Hkv * (p.c.D / 16);
-  const int64_t per = kKvThreads * kKvReadChunks;
-  const int64_t blocks = (total + per - 1) / per;
-  if (blocks > 0x7fffffff) return SV_EINVAL;
-  const dim3 grid(static_cast<unsigned>(blocks), 2);
+  // about 1024 chunks of sixteen values a block
+  const int per = p.c.Hkv * (p.c.D / 16);
+  p.tokens = std::max(1, kKvThreads * kKvReadChunks / per);
+  p.magic = static_cast<unsigned>((1ull << 32) / static_cast<unsigned>(per)) + 1u;
+  const dim3 grid(static_cast<unsigned>((a->T + p.tokens - 1) / p.tokens),
+                  static_cast<unsigned>(a->B), 2);
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   switch (a->dtype) {
     case SV_BF16: return launch(kv_read_kernel<__nv_bfloat16>, p, grid, kKvThreads, 0, st);
@@ -295,6 +295,12 @@ sv_status sv_kv_attention(const sv_kv_attention_args* a, void* workspace, size_t
     return SV_EINVAL;
   if (a->mask != nullptr && (a->T > SV_MAX_TREE_NODES || a->words < (a->T + 31) / 32))
     return SV_EINVAL;
+  // the blocks of all units are counted in 32 bits
+  const int64_t rows = static_cast<int64_t>(a->T) * (a->Hq / a->cache.Hkv);
+  const int64_t positions = static_cast<int64_t>(a->cache.slots) * a->cache.page_size;
+  if (static_cast<double>(a->B) * a->cache.Hkv * ((rows + 15) / 16) *
+          ((positions + kKaBlock - 1) / kKaBlock) >= 2147483648.0)
+    return SV_EINVAL;
   const sv_status wst = workspace_ok(workspace, ws_bytes, need);
   if (wst != SV_OK) return wst;
   Device dev;
@@ -307,6 +313,7 @@ sv_status sv_kv_attention(const sv_kv_attention_args* a, void* workspace, size_t
   p.T = a->T;
   p.Hq = a->Hq;
   p.G = a->Hq / a->cache.Hkv;
+  p.g_magic = static_cast<unsigned>((1ull << 32) / static_cast<unsigned>(p.G)) + 1u;
   p.q = a->q;
   p.q_batch = a->q_batch_stride;
   p.q_token = a->q_token_stride;

@@ -44,6 +44,7 @@ constexpr float kRefShift = 8.f, kRefSlack = 7.f;
 struct KvAttnProblem {
   KvCache c;
   int B, T, Hq, G;  // G = Hq / Hkv
+  unsigned g_magic;  // floor(2^32 / G) + 1
   const void* q;
   long long q_batch, q_token, q_head;
   bool q_vec;  // 8-byte loads of four queries
@@ -68,14 +69,22 @@ struct KaShared {
   unsigned char v[kKaStages][kKaBlock * D];
   float merge[2][kKaPartialFloats<D>];
   // cumulated block counts of the requests
-  long long prefix[SV_MAX_B + 1];
-  long long scan[8];
+  int prefix[SV_MAX_B + 1];
+  int scan[8];
   float k_scale[kKaStages][kKaBlock / 16];  // < 0: no such page
   float v_scale[kKaStages][kKaBlock / 16];
   uint64_t full[kKaStages], empty[kKaStages];
   int dead;       // a wait ran out
   unsigned last;  // this CTA joins the unit
 };
+
+// n / G for a row n < T G < 2^24 of a round (G <= 256: the multiplier's
+// error, below n G / 2^32, cannot reach the next quotient).  Divisions by
+// instruction sequences, 64-bit ones above all, made up most of these
+// kernels' code, and code comes through caches that the stream empties.
+__device__ __forceinline__ int ka_div_g(const KvAttnProblem& a, int n) {
+  return a.G == 1 ? n : static_cast<int>(__umulhi(static_cast<unsigned>(n), a.g_magic));
+}
 
 struct KaLen {
   int len, n;  // tokens before the round, round tokens (0 when invalid)
@@ -96,7 +105,7 @@ __device__ __forceinline__ KaLen ka_len(const KvAttnProblem& a, int b, bool* bad
 // last position its rows can see.
 template <int ROWS, int BLOCK>
 __device__ __forceinline__ int ka_tile_blocks(const KvAttnProblem& a, const KaLen& l, int tile) {
-  const int last = a.mask != nullptr ? l.n - 1 : min(l.n - 1, ((tile + 1) * ROWS - 1) / a.G);
+  const int last = a.mask != nullptr ? l.n - 1 : ka_div_g(a, min((tile + 1) * ROWS, l.n * a.G) - 1);
   return (l.len + last + 1 + BLOCK - 1) / BLOCK;
 }
 
@@ -106,14 +115,13 @@ template <int ROWS, int BLOCK>
 struct KaCursor {
   KaLen l;  // of request b
   int b, head, tile, tiles, blk, nblk;
-  long long unit0;  // the unit's first block in the list
+  int unit0;  // the unit's first block in the list
   __device__ __forceinline__ void load(const KvAttnProblem& a) {
     bool bad = false;
     l = ka_len(a, b, &bad);
     tiles = (l.n * a.G + ROWS - 1) / ROWS;
   }
-  __device__ __forceinline__ void seek(const KvAttnProblem& a, const long long* prefix,
-                                       long long at) {
+  __device__ __forceinline__ void seek(const KvAttnProblem& a, const int* prefix, int at) {
     int lo = 0, hi = a.B;  // the last b with prefix[b] <= at
     while (hi - lo > 1) {
       const int mid = (lo + hi) / 2;
@@ -121,15 +129,16 @@ struct KaCursor {
     }
     b = lo;
     load(a);
-    const long long per_head = (prefix[b + 1] - prefix[b]) / a.c.Hkv;
-    head = static_cast<int>((at - prefix[b]) / per_head);
+    const int per_head = (prefix[b + 1] - prefix[b]) / a.c.Hkv;
+    head = (at - prefix[b]) / per_head;
     unit0 = prefix[b] + head * per_head;
+#pragma unroll 1
     for (tile = 0;; ++tile) {
       nblk = ka_tile_blocks<ROWS, BLOCK>(a, l, tile);
       if (at < unit0 + nblk || tile + 1 >= tiles) break;
       unit0 += nblk;
     }
-    blk = static_cast<int>(at - unit0);
+    blk = at - unit0;
   }
   // to the next unit (requests without units are skipped)
   __device__ __forceinline__ void next_unit(const KvAttnProblem& a) {
@@ -152,31 +161,34 @@ struct KaCursor {
 // The cumulated block counts of the requests into prefix[0 .. B] (every
 // thread of the block calls this); returns their total.
 template <int ROWS, int BLOCK, int THREADS>
-__device__ __forceinline__ long long ka_prefix(const KvAttnProblem& a, long long* prefix,
-                                               long long* scan, bool report) {
+__device__ __forceinline__ int ka_prefix(const KvAttnProblem& a, int* prefix, int* scan,
+                                         bool report) {
   const int tid = static_cast<int>(threadIdx.x), warp = tid >> 5, lane = tid & 31;
-  long long total = 0;
+  int total = 0;
+#pragma unroll 1
   for (int base = 0; base < a.B; base += THREADS) {
     const int b = base + tid;
-    long long mine = 0;
+    int mine = 0;
     if (b < a.B) {
       bool bad = false;
       const KaLen l = ka_len(a, b, &bad);
       if (bad && report) record_error(a.err, SV_DERR_ARG);
       const int tiles = (l.n * a.G + ROWS - 1) / ROWS;
+#pragma unroll 1
       for (int tile = 0; tile < tiles; ++tile) mine += ka_tile_blocks<ROWS, BLOCK>(a, l, tile);
       mine *= a.c.Hkv;
     }
-    long long x = mine;
+    int x = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-      const long long y = __shfl_up_sync(0xffffffffu, x, o);
+      const int y = __shfl_up_sync(0xffffffffu, x, o);
       if (lane >= o) x += y;
     }
     __syncthreads();
     if (lane == 31) scan[warp] = x;
     __syncthreads();
-    long long before = total;
+    int before = total;
+#pragma unroll 1
     for (int w = 0; w < THREADS / 32; ++w) {
       if (w < warp) before += scan[w];
       total += scan[w];
@@ -190,29 +202,40 @@ __device__ __forceinline__ long long ka_prefix(const KvAttnProblem& a, long long
 
 // Rows of the round that hold no token: 0, lse -inf.
 template <class T, int D, int THREADS>
-__device__ __forceinline__ void ka_clear_rows(const KvAttnProblem& a) {
+__device__ __forceinline__ void ka_clear_rows(const KvAttnProblem& a, int thread) {
   for (int b = static_cast<int>(blockIdx.x); b < a.B; b += static_cast<int>(gridDim.x)) {
     bool bad = false;
     const KaLen l = ka_len(a, b, &bad);
     const long long row0 = (static_cast<long long>(b) * a.T + l.n) * a.Hq;
     const long long rows = static_cast<long long>(a.T - l.n) * a.Hq;
     uint4* o = reinterpret_cast<uint4*>(static_cast<T*>(a.out) + row0 * D);
-    for (long long i = threadIdx.x; i < rows * (D / 8); i += THREADS) o[i] = make_uint4(0, 0, 0, 0);
+    for (long long i = thread; i < rows * (D / 8); i += THREADS) o[i] = make_uint4(0, 0, 0, 0);
     if (a.lse)
-      for (long long i = threadIdx.x; i < rows; i += THREADS) a.lse[row0 + i] = kNegInf;
+      for (long long i = thread; i < rows; i += THREADS) a.lse[row0 + i] = kNegInf;
   }
 }
 
-// CTA c of `parts` holds blocks [total c / parts, total (c + 1) / parts);
-// this is the one that holds block x.
-__device__ __forceinline__ int ka_cta_of(long long x, long long parts, long long total) {
-  return static_cast<int>(((x + 1) * parts - 1) / total);
-}
+// The blocks in equal parts: the first `more` of them hold `per` + 1 blocks,
+// the others `per`.  (The calls' sizes keep the number of blocks below 2^31.)
+struct KaParts {
+  int count, per, more;
+  __device__ __forceinline__ KaParts(int total, int most, int least) {
+    count = max(1, min(most, total / least));
+    per = total / count;
+    more = total - per * count;
+  }
+  __device__ __forceinline__ int begin(int c) const { return c * per + min(c, more); }
+  // the part that holds block x
+  __device__ __forceinline__ int of(int x) const {
+    const int cut = more * (per + 1);
+    return x < cut ? x / (per + 1) : more + (x - cut) / per;
+  }
+};
 
 // What the producer warp knows of the blocks ahead.  A block's page ids hang
 // on the page table, its scales on the page ids: two round trips to memory.
-// Each lane owns one copy (16 positions of keys or of values) of one block of
-// a batch of NB = 32 / (BLOCK / 8) blocks, and the two lookups run two and one
+// Each lane owns 16 positions, keys or values, of one block of a batch of
+// NB = 32 / (BLOCK / 8) blocks, and the two lookups run two and one
 // batches ahead of the copies, so neither is waited for.
 template <int ROWS, int BLOCK>
 struct KaFeed {
@@ -223,23 +246,31 @@ struct KaFeed {
   bool is_v;
   struct Item {
     const unsigned char* src;  // null: nothing to copy
+    int bytes;
     float scale;               // < 0: no such page
     int first, tokens, round;  // the block begins a segment; its place
+    int b, head, tile, rows;   // its unit; rows of the request
   };
-  int a_first, a_tokens, a_round, a_head, a_pos;  // of `page`
+  int a_first, a_tokens, a_round, a_b, a_head, a_tile, a_rows, a_pos;  // of `page`
 
   __device__ __forceinline__ void advance(const KvAttnProblem& a, int steps) {
+#pragma unroll 1
     for (int k = 0; k < steps && left > 0; ++k) {
       --left;
       if (++cur.blk == cur.nblk && left > 0) cur.next_unit(a);
     }
   }
-  __device__ __forceinline__ void look(const KvAttnProblem& a, bool very_first) {
+  // the page of the lane's block, and on to the next batch (`first`: the
+  // first batch, whose first block begins a segment)
+  __device__ __forceinline__ void look(const KvAttnProblem& a, bool first) {
     page = -2;
     if (left > 0) {
       a_pos = cur.blk * BLOCK + sub * 16;
+      a_b = cur.b;
       a_head = cur.head;
-      a_first = cur.blk == 0 || very_first;
+      a_tile = cur.tile;
+      a_rows = cur.l.n * a.G;
+      a_first = cur.blk == 0 || (first && threadIdx.x % 32 < kCopies);
       a_tokens = cur.l.len + cur.l.n - cur.blk * BLOCK;
       a_round = cur.blk * BLOCK - cur.l.len;
       if (a_pos < cur.l.len + cur.l.n)
@@ -251,12 +282,22 @@ struct KaFeed {
   __device__ __forceinline__ Item resolve(const KvAttnProblem& a) {
     Item it;
     it.src = nullptr;
+    it.bytes = 0;
     it.scale = -1.f;
     it.first = a_first;
     it.tokens = a_tokens;
     it.round = a_round;
+    it.b = a_b;
+    it.head = a_head;
+    it.tile = a_tile;
+    it.rows = a_rows;
     if (page >= 0 && page < a.c.num_pages) {
-      it.src = (is_v ? a.c.v : a.c.k) + page * a.c.page_stride + a_head * a.c.head_stride +
+      // one copy for all positions of the block in a page (a warp issues a
+      // copy in about 200 clocks, whatever its size)
+      const int run = min(a.c.page_size, BLOCK);
+      it.bytes = run * a.c.D;
+      if ((a_pos & (run - 1)) == 0)
+        it.src = (is_v ? a.c.v : a.c.k) + page * a.c.page_stride + a_head * a.c.head_stride +
                (a_pos & (a.c.page_size - 1)) * a.c.D;
       it.scale =
           (is_v ? a.c.v_scale : a.c.k_scale)[static_cast<long long>(page) * a.c.Hkv + a_head];
@@ -265,16 +306,15 @@ struct KaFeed {
     }
     return it;
   }
-  // positions the lane at its block of the first batch
-  __device__ __forceinline__ void start(const KvAttnProblem& a, const long long* prefix,
-                                        long long w0, int n, int lane) {
+  // positions the lane at its block of the first batch; look() comes next
+  __device__ __forceinline__ void start(const KvAttnProblem& a, const int* prefix, int w0, int n,
+                                        int lane) {
     cur.seek(a, prefix, w0);
     left = n;
     sub = lane % (kCopies / 2);
     is_v = lane % kCopies >= kCopies / 2;
-    const int mine = lane / kCopies;
-    advance(a, mine);
-    look(a, mine == 0);
+    page = -2;
+    advance(a, lane / kCopies);
   }
 };
 
@@ -292,6 +332,12 @@ __device__ __forceinline__ unsigned half2_of(float lo, float hi) {
   return *reinterpret_cast<const unsigned*>(&h);
 }
 
+// Four 16-bit values at an address that is only 2-byte aligned.
+__device__ __noinline__ uint2 ka_load4(const unsigned short* p) {
+  return make_uint2(p[0] | static_cast<unsigned>(p[1]) << 16,
+                    p[2] | static_cast<unsigned>(p[3]) << 16);
+}
+
 __device__ __forceinline__ float quad_max(float x) {
   x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 1));
   return fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 2));
@@ -301,15 +347,24 @@ __device__ __forceinline__ float quad_sum(float x) {
   return x + __shfl_xor_sync(0xffffffffu, x, 2);
 }
 
-// A wait that records its expiry once and lets the CTA run on without
-// waiting (every barrier of the block is still met).
-__device__ __forceinline__ void ka_wait(uint64_t* bar, uint32_t parity, int* dead, int* err) {
-  if (mbar_try_wait(bar, parity)) return;
-  if (*static_cast<volatile int*>(dead)) return;
-  if (!mbar_wait_bounded(bar, parity, 1000000000ull)) {
-    *static_cast<volatile int*>(dead) = 1;
-    record_error(err, SV_DERR_TIMEOUT);
+// A bounded wait (1 s) that records its expiry once and lets the CTA run on
+// without waiting (every barrier of the block is still met).
+__device__ __noinline__ void ka_wait_slow(uint64_t* bar, uint32_t parity, int* dead, int* err) {
+  const uint64_t t0 = globaltimer_ns();
+  while (!*static_cast<volatile int*>(dead)) {
+    for (int k = 0; k < 64; ++k)
+      if (mbar_try_wait(bar, parity)) return;
+    if (globaltimer_ns() - t0 > 1000000000ull) {
+      *static_cast<volatile int*>(dead) = 1;
+      record_error(err, SV_DERR_TIMEOUT);
+    }
   }
+}
+__device__ __forceinline__ void ka_wait(uint64_t* bar, uint32_t parity, int* dead, int* err) {
+#pragma unroll 1
+  for (int k = 0; k < 64; ++k)
+    if (mbar_try_wait(bar, parity)) return;
+  ka_wait_slow(bar, parity, dead, err);
 }
 
 __device__ __forceinline__ void mbar_expect_tx(uint64_t* bar, uint32_t bytes) {
@@ -335,10 +390,10 @@ struct KaAcc {
   template <class Get>
   __device__ __forceinline__ void join(float r0, float r1, float z0, float z1, Get get) {
     const float n0 = fmaxf(ref[0], r0), n1 = fmaxf(ref[1], r1);
-    const float a0 = ref[0] == kNegInf ? 0.f : exp2f(ref[0] - n0);
-    const float a1 = ref[1] == kNegInf ? 0.f : exp2f(ref[1] - n1);
-    const float b0 = r0 == kNegInf ? 0.f : exp2f(r0 - n0);
-    const float b1 = r1 == kNegInf ? 0.f : exp2f(r1 - n1);
+    const float a0 = ref[0] == kNegInf ? 0.f : fast_exp2(ref[0] - n0);
+    const float a1 = ref[1] == kNegInf ? 0.f : fast_exp2(ref[1] - n1);
+    const float b0 = r0 == kNegInf ? 0.f : fast_exp2(r0 - n0);
+    const float b1 = r1 == kNegInf ? 0.f : fast_exp2(r1 - n1);
     ref[0] = n0;
     ref[1] = n1;
     z[0] = z[0] * a0 + z0 * b0;
@@ -396,28 +451,28 @@ __global__ void __launch_bounds__(kKaThreads, kKaCtasPerSm) kv_attn_kernel(const
   }
   grid_dependency_wait();
 
-  const long long total = ka_prefix<kKaRows, kKaBlock, kKaThreads>(a, sh.prefix, sh.scan, cta == 0);
-  ka_clear_rows<T, D, kKaThreads>(a);
+  const int total = ka_prefix<kKaRows, kKaBlock, kKaThreads>(a, sh.prefix, sh.scan, cta == 0);
+  ka_clear_rows<T, D, kKaThreads>(a, tid);
 
   // this CTA's part of the blocks
-  const long long parts =
-      max(1ll, min(static_cast<long long>(grid), total / kKaMinBlocks));
-  if (cta >= parts) return;
-  const long long w0 = total * cta / parts, w1 = total * (cta + 1) / parts;
-  if (w0 >= w1) return;
+  const KaParts parts(total, grid, kKaMinBlocks);
+  if (cta >= parts.count) return;
+  const int w0 = parts.begin(cta), n = parts.begin(cta + 1) - w0;
+  if (n <= 0) return;
 
   if (warp == kKaWarps) {
     // ------------------------------------------------------------ producer
     const uint64_t pol = policy_evict_first();
     KaFeed<kKaRows, kKaBlock> feed;
-    const int n = static_cast<int>(w1 - w0);
     feed.start(a, sh.prefix, w0, n, lane);
-    auto item = feed.resolve(a);
-    feed.look(a, false);
+    typename KaFeed<kKaRows, kKaBlock>::Item item = {}, next = {};
     int i = 0;
-    for (int i0 = 0; i0 < n; i0 += feed.NB) {
-      const auto next = feed.resolve(a);
-      feed.look(a, false);
+#pragma unroll 1
+    for (int i0 = -2 * feed.NB; i0 < n; i0 += feed.NB) {
+      item = next;
+      next = feed.resolve(a);
+      feed.look(a, i0 < -feed.NB);
+      if (i0 < 0) continue;
       for (int j = 0; j < feed.NB && i < n; ++j, ++i) {
         const int s = i % kKaStages;
         if (i >= kKaStages)
@@ -425,16 +480,15 @@ __global__ void __launch_bounds__(kKaThreads, kKaCtasPerSm) kv_attn_kernel(const
         __syncwarp();
         if (lane / feed.kCopies == j) {
           if (item.src != nullptr && !*static_cast<volatile int*>(&sh.dead)) {
-            mbar_expect_tx(&sh.full[s], 16 * D);
+            mbar_expect_tx(&sh.full[s], item.bytes);
             bulk_copy_g2s_hint((feed.is_v ? sh.v[s] : sh.k[s]) + feed.sub * 16 * D, item.src,
-                               16 * D, &sh.full[s], pol);
+                               item.bytes, &sh.full[s], pol);
           }
           (feed.is_v ? sh.v_scale[s] : sh.k_scale[s])[feed.sub] = item.scale;
           mbar_arrive(&sh.full[s]);
         }
         __syncwarp();
       }
-      item = next;
     }
     // copies of the last stages must land before the block ends
     for (int j = max(0, n - kKaStages); j < n; ++j)
@@ -450,11 +504,10 @@ __global__ void __launch_bounds__(kKaThreads, kKaCtasPerSm) kv_attn_kernel(const
   constexpr int KS = D / 16;
   KaCursor<kKaRows, kKaBlock> cur;
   cur.seek(a, sh.prefix, w0);
-  long long w = w0;
-  while (w < w1) {
+  for (int w = 0; w < n;) {
     const int h = cur.head, tile = cur.tile;
     const int blk0 = cur.blk;
-    const int blk1 = static_cast<int>(min(static_cast<long long>(cur.nblk), blk0 + (w1 - w)));
+    const int blk1 = min(cur.nblk, blk0 + n - w);
     const int L = cur.l.len + cur.l.n;
 
     // the unit's queries as fragments: bf16 rows are scaled by a power of two
@@ -467,22 +520,19 @@ __global__ void __launch_bounds__(kKaThreads, kKaCtasPerSm) kv_attn_kernel(const
       for (int r = 0; r < 2; ++r) {
         const int row = tile * kKaRows + g + 8 * r;
         const bool ok = row < cur.l.n * a.G;
-        rt[r] = ok ? row / a.G : a.T;
+        const int tok = ok ? ka_div_g(a, row) : 0, hg = ok ? row - tok * a.G : 0;
+        rt[r] = ok ? tok : a.T;
         const T* p = static_cast<const T*>(a.q) + cur.b * a.q_batch +
-                     (ok ? row / a.G : 0) * a.q_token + (h * a.G + (ok ? row % a.G : 0)) * a.q_head +
-                     t * (D / 4);
+                     tok * a.q_token + (h * a.G + hg) * a.q_head + t * (D / 4);
         float f[D / 4];
         float m = 0.f;
 #pragma unroll
         for (int i = 0; i < D / 4; i += 4) {
-          alignas(8) T e[4];
-          if (a.q_vec) {
-            *reinterpret_cast<uint2*>(e) = ok ? *reinterpret_cast<const uint2*>(p + i)
-                                              : make_uint2(0, 0);
-          } else {
-#pragma unroll
-            for (int j = 0; j < 4; ++j) e[j] = ok ? p[i + j] : from_float<T>(0.f);
-          }
+          uint2 e4 = make_uint2(0, 0);
+          if (ok)
+            e4 = a.q_vec ? *reinterpret_cast<const uint2*>(p + i)
+                         : ka_load4(reinterpret_cast<const unsigned short*>(p + i));
+          const T* e = reinterpret_cast<const T*>(&e4);
           const float2 x = ka_two(e), y = ka_two(e + 2);
           f[i] = x.x;
           f[i + 1] = x.y;
@@ -512,9 +562,9 @@ __global__ void __launch_bounds__(kKaThreads, kKaCtasPerSm) kv_attn_kernel(const
     KaAcc<D> acc;
     acc.clear();
     for (int blk = blk0; blk < blk1; ++blk) {
-      const long long i = w - w0 + (blk - blk0);
+      const int i = w + blk - blk0;
       if ((i & 1) != pair) continue;
-      const int s = static_cast<int>(i % kKaStages);
+      const int s = i % kKaStages;
       ka_wait(&sh.full[s], static_cast<uint32_t>(i / kKaStages) & 1, &sh.dead, a.err);
       const int pos0 = blk * kKaBlock + half * 32;
 
@@ -556,8 +606,9 @@ __global__ void __launch_bounds__(kKaThreads, kKaCtasPerSm) kv_attn_kernel(const
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
           uint32_t m = 0;
-          for (int nt = 0; nt < 4; ++nt)
-            for (int c = 0; c < 2; ++c) {
+#pragma unroll 1
+          for (int e = 0; e < 8; ++e) {
+              const int nt = e >> 1, c = e & 1;
               const int pos = pos0 + nt * 8 + 2 * t + c;
               const int j = pos - cur.l.len;
               bool see = pos < L && rt[r] < a.T && sh.k_scale[s][half * 2 + (nt >> 1)] >= 0.f;
@@ -662,6 +713,7 @@ __global__ void __launch_bounds__(kKaThreads, kKaCtasPerSm) kv_attn_kernel(const
             }
           }
           if (__any_sync(0xffffffffu, nan)) {
+#pragma unroll 1
             for (int tok = 0; tok < 16; ++tok) {
               const int pos = pos0 + u * 16 + tok;
               if (pos >= L || sh.k_scale[s][half * 2 + u] < 0.f) break;
@@ -724,7 +776,7 @@ __global__ void __launch_bounds__(kKaThreads, kKaCtasPerSm) kv_attn_kernel(const
         if (rt[r] < a.T) {
           const int row = tile * kKaRows + g + 8 * r;
           const long long orow =
-              (static_cast<long long>(cur.b) * a.T + rt[r]) * a.Hq + h * a.G + row % a.G;
+              (static_cast<long long>(cur.b) * a.T + rt[r]) * a.Hq + h * a.G + row - rt[r] * a.G;
           const float z = r ? z1 : z0, ref = r ? r1 : r0;
           const bool any = !(z == 0.f);  // true for NaN
           const float inv = any ? 1.f / z : 0.f;
@@ -757,8 +809,7 @@ __global__ void __launch_bounds__(kKaThreads, kKaCtasPerSm) kv_attn_kernel(const
                [&](int i) { return acc.o[i >> 2][i & 3]; });
     } else {
       // the unit is cut: CTAs first .. last hold a part of it
-      const int first = ka_cta_of(cur.unit0, parts, total);
-      const int last = ka_cta_of(cur.unit0 + cur.nblk - 1, parts, total);
+      const int first = parts.of(cur.unit0), last = parts.of(cur.unit0 + cur.nblk - 1);
       constexpr int PF = kKaPartialFloats<D>;
       if (warp == 0) {
         // a part that begins inside the unit is its CTA's first
@@ -790,8 +841,8 @@ __global__ void __launch_bounds__(kKaThreads, kKaCtasPerSm) kv_attn_kernel(const
           float* p = part(c);
           const float r0 = __ldcg(p + lane), r1 = __ldcg(p + 32 + lane);
           // a part that saw nothing has Z = 0 and O = 0 (or NaN, which stays)
-          const float f0 = r0 == kNegInf ? 1.f : exp2f(r0 - m0);
-          const float f1 = r1 == kNegInf ? 1.f : exp2f(r1 - m1);
+          const float f0 = r0 == kNegInf ? 1.f : fast_exp2(r0 - m0);
+          const float f1 = r1 == kNegInf ? 1.f : fast_exp2(r1 - m1);
           z0 = fmaf(__ldcg(p + 64 + lane), f0, z0);
           z1 = fmaf(__ldcg(p + 96 + lane), f1, z1);
           float* po = p + (4 + 4 * NJ * warp) * 32 + lane;

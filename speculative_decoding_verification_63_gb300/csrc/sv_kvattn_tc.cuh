@@ -5,29 +5,34 @@
 //
 // A unit is 128 query rows (one row of tensor memory each), a block 128
 // positions.  One CTA per SM; its warps:
-//   0-7    softmax: thread = query row, so maximum and sum need no shuffles;
-//          warps 0-3 take a block's first 64 positions, 4-7 the others, and
-//          the two threads of a row agree on its reference.
+//   0-7    softmax, two streams of four warps: thread = row of tensor memory,
+//          so maximum and sum need no shuffles.  Stream s takes every second
+//          block and has scores, sums, reference and accumulator of its own:
+//          what one waits for (a block's scores, its weights' way to the
+//          products) the other's work hides.  They join at the unit's end.
 //   8-11   convert key codes to halves, from the raw ring into the layout the
 //   12-15  tensor cores read (128-byte rows, 16-byte pieces swizzled by row
 //          mod 8); 12-15 the same for value codes.  Keys are read along
 //          channels (K-major), values along positions (MN-major).
-//   16     issues S = Q K^T (Q in tensor memory), two blocks ahead at most.
-//   17     allocates tensor memory, issues O += P V (P: the weights as halves,
-//          in the columns of S they came from).
+//   16     issues S_s = Q K^T.
+//   17     allocates tensor memory, issues O_s += P_s V (P_s: the weights as
+//          halves, in the columns of S_s they came from).
 //   18     bulk copies of raw codes, scales, the blocks' descriptions.
-// Q and P stay in tensor memory because shared memory is the busiest unit:
-// a block of 128 channels carries 64 KB of raw codes (written, read), 64 KB
-// of halves written and 64 KB read by the products, 1500 clocks at 128 bytes
-// a clock, against 1024 clocks of products and the 1390 clocks in which HBM
-// delivers those codes to one SM.  Blocks of 64 positions would double the
-// clocks of S: a product of 64 columns takes as long as one of 128 (64
-// clocks, measured).  The loops are kept short: 19 warps in six different
-// loops stall on instruction fetch otherwise (the first version of this
-// kernel, with everything unrolled, took 3200 clocks a 64-position block,
-// 4.7 of 20 stalled warp-cycles an instruction for want of instructions).
+// Shared memory is the busiest unit: a block of 128 channels carries 64 KB of
+// raw codes (written, read), 64 KB of halves written and 96 KB read by the
+// products, 1750 clocks at 128 bytes a clock, against 1024 clocks of products
+// and the 1390 clocks in which HBM delivers those codes to one SM.  Blocks of
+// 64 positions would double the clocks of S: a product of 64 columns takes as
+// long as one of 128 (64 clocks, measured).
 //
-// Tensor memory, 512 columns: S_0 S_1 (128 each), O (D), Q (D / 2).
+// Few rows.  The products take 128 rows at a time whatever they hold, but a
+// warp sees only 32 of them, so units of up to 64 (32) rows are laid down two
+// (four) times: copy c of a row handles the c-th share of each block's
+// positions, with a reference, sum and accumulator of its own and weights of
+// zero elsewhere, and the copies join at the unit's end.  Every warp then has
+// a half (quarter) of the exponentials and all four schedulers take part.
+//
+// Tensor memory, 512 columns: S_0 S_1 (128 each), O_0 O_1 (D each).
 #pragma once
 
 #include "sv_kvattn.cuh"
@@ -36,39 +41,48 @@ namespace sv {
 
 constexpr int kTcRows = 128;
 constexpr int kTcBlock = 128;
-constexpr int kTcSlots = 5;    // raw ring: keys and values of a block in turn
-constexpr int kTcMeta = 8;     // block descriptions (at most five blocks in flight)
+// Raw ring: keys and values of a block in turn, 16 KB each at D = 128.
+constexpr int kTcSlots = 7;
+constexpr int kTcMeta = 8;     // block descriptions (at most seven blocks in flight)
 constexpr int kTcSoftmax = 256, kTcConvert = 128;
 constexpr int kTcThreads = kTcSoftmax + 2 * kTcConvert + 96;
 constexpr int kTcMaxCtas = 160;
 constexpr int kTcMinBlocks = 2;
 
-// A partial result: ref and z of the 128 rows, then O [row][D].
+// A partial result: ref and z of the 128 rows, then O [D][row]: a warp's lanes
+// are rows, so its stores and loads are whole lines.
 template <int D>
 constexpr int kTcPartialFloats = kTcRows * (2 + D);
 
-struct alignas(16) TcMeta {  // scales are read four at a time
-  int first;           // the block begins a segment (a unit, or this CTA's part of one)
-  int tokens;          // positions of the block below the request's length
-  int round;           // the block's first position, from the round's first token
-  int nan;             // a value code of an edge block is NaN (set by the converters)
-  float ks[8];         // 2^ek of its 16-position pieces; < 0: no such page
-  float ev[8], zin[8]; // ev and 2^-ev
+struct alignas(16) TcMeta {
+  int first;     // the block begins a segment (a unit, or this CTA's part of one)
+  int tokens;    // positions of the block below the request's length
+  int round;     // the block's first position, from the round's first token
+  int edge;      // rows may see different positions, or a page is missing
+  float4 s[8];   // of its 16-position pieces: 2^ek (< 0: no such page), ev, 2^-ev
+  int nan;       // a value code of an edge block is NaN (set by the converters)
 };
 
 template <int D>
 struct TcShared {
-  unsigned char kh[2][kTcBlock * D * 2];  // halves, 1024-byte aligned
-  unsigned char vh[2][kTcBlock * D * 2];
+  unsigned char kh[kTcBlock * D * 2];  // halves, 1024-byte aligned
+  unsigned char vh[kTcBlock * D * 2];
+  unsigned char qh[kTcRows * D * 2];
   unsigned char raw[kTcSlots][kTcBlock * D];
-  long long prefix[SV_MAX_B + 1];
-  long long scan[kTcThreads / 32 + 1];
-  unsigned short nanmask[2][kTcBlock][D / 16];
+  union {
+    int prefix[SV_MAX_B + 1];        // until every warp has found its place
+    float join[2][kTcRows][8];       // copies of rows at a unit's end
+  };
+  int scan[kTcThreads / 32 + 1];
+  unsigned short nanmask[kTcBlock][D / 16];
   TcMeta meta[kTcMeta];
-  float exch[2][2][kTcRows];
-  float zsum[2][2][kTcRows];
+  float scratch[2][kTcRows];  // the queries' largest values
+  float ends[2][2][kTcRows];  // references and sums of the streams
+  unsigned long long nanrow[D / 64][kTcRows];  // channels in which a lane's row saw a NaN
+  KaCursor<kTcRows, kTcBlock> cur[8];          // the softmax warps' places
+  int total, nanany;
   uint64_t rawfull[kTcSlots], rawempty[kTcSlots];
-  uint64_t kfull[2], vfull[2], sfull[2], pfull[2], pvdone[2], qfull;
+  uint64_t kfull, vfull, sfull[2], pfull[2], pvdone[2], qfull;
   unsigned tmem;
   int dead;
   unsigned last;
@@ -113,12 +127,22 @@ __device__ __forceinline__ void tc_mma(unsigned d, unsigned a, uint64_t b, unsig
       : "memory");
 }
 
+// D[tmem] (+)= A[smem] B[smem]
+__device__ __forceinline__ void tc_mma_ss(unsigned d, uint64_t a, uint64_t b, unsigned idesc,
+                                          bool accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(static_cast<unsigned>(accumulate))
+      : "memory");
+}
+
 #define SV_R4(x, i) "=r"(x[i]), "=r"(x[i + 1]), "=r"(x[i + 2]), "=r"(x[i + 3])
 #define SV_R16(x, i) SV_R4(x, i), SV_R4(x, i + 4), SV_R4(x, i + 8), SV_R4(x, i + 12)
 #define SV_I4(x, i) "r"(x[i]), "r"(x[i + 1]), "r"(x[i + 2]), "r"(x[i + 3])
 #define SV_I16(x, i) SV_I4(x, i), SV_I4(x, i + 4), SV_I4(x, i + 8), SV_I4(x, i + 12)
 
-// 16 or 32 columns of this thread's tensor-memory row (lane of the warp's
+// 8, 16 or 32 columns of this thread's tensor-memory row (lane of the warp's
 // quarter).  The wait is part of the statement: the registers hold nothing
 // before it.
 __device__ __forceinline__ void tc_ld32(unsigned (&x)[32], unsigned addr) {
@@ -138,11 +162,18 @@ __device__ __forceinline__ void tc_ld16(unsigned (&x)[16], unsigned addr) {
       : "r"(addr)
       : "memory");
 }
-__device__ __forceinline__ void tc_st32(unsigned addr, const unsigned (&x)[32]) {
+__device__ __forceinline__ void tc_ld8(unsigned (&x)[8], unsigned addr) {
   asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,"
-      "%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(addr),
-      SV_I16(x, 0), SV_I16(x, 16)
+      "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : SV_R4(x, 0), SV_R4(x, 4)
+      : "r"(addr)
+      : "memory");
+}
+__device__ __forceinline__ void tc_st8(unsigned addr, const unsigned* x) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(addr),
+      SV_I4(x, 0), SV_I4(x, 4)
       : "memory");
 }
 __device__ __forceinline__ void tc_st16(unsigned addr, const unsigned (&x)[16]) {
@@ -174,158 +205,198 @@ __device__ __forceinline__ void tc_wait(uint64_t* bar, uint32_t parity, int* dea
   __syncwarp();
 }
 
-// Named barrier that also joins a predicate of its threads (or).
-__device__ __forceinline__ bool named_sync_or(uint32_t id, uint32_t count, bool p) {
-  uint32_t r;
-  asm volatile(
-      "{\n\t.reg .pred q, s;\n\tsetp.ne.b32 q, %3, 0;\n\t"
-      "barrier.cta.red.or.pred s, %1, %2, q;\n\tselp.u32 %0, 1, 0, s;\n\t}"
-      : "=r"(r)
-      : "r"(id), "r"(count), "r"(static_cast<uint32_t>(p))
-      : "memory");
-  return r != 0;
-}
-
 // The last CTA to arrive joins a cut unit's parts (CTAs first .. last, in
-// order) and leaves zeros behind.  All softmax threads: a thread owns four
-// channels of every eighth (D = 128) row, eight rows at a time, so the loads
-// of a part are in flight together.  w: 512 floats of shared memory.
+// order, two at a time with their loads in flight together) and leaves zeros
+// behind.  All softmax threads: thread = row, set s the s-th half of the
+// channels, sixteen at a time.
 template <int D, class T>
-__device__ __noinline__ void tc_join(const KvAttnProblem& a, float* w, int first, int last,
-                                     int live, int tile, long long req) {
-  constexpr int PF = kTcPartialFloats<D>;
-  constexpr int LANES = D / 4, RSTEP = kTcSoftmax / LANES, RK = 8;
-  const int tid = static_cast<int>(threadIdx.x);
+__device__ __noinline__ void tc_join(const KvAttnProblem& a, int first, int last, int live,
+                                     int tile, long long req) {
+  constexpr int PF = kTcPartialFloats<D>, N = 16;
+  const int row = static_cast<int>(threadIdx.x) & (kTcRows - 1);
+  const int c0 = (static_cast<int>(threadIdx.x) / kTcRows) * (D / 2);
   auto part = [&](int c) { return a.partials + (2ll * c + (c == first ? 1 : 0)) * PF; };
-  float* const wm = w;              // the rows' common reference
-  float* const wf = w + kTcRows;    // one part's factors (two buffers)
-  if (tid < kTcRows) {
-    float m = kNegInf, z = 0.f;
-    if (tid < live) {
-#pragma unroll 8
-      for (int c = first; c <= last; ++c) m = fmaxf(m, __ldcg(part(c) + tid));
-#pragma unroll 4
-      for (int c = first; c <= last; ++c) {
-        const float r = __ldcg(part(c) + tid);
-        // a part that saw nothing has z = 0 and O = 0 (or NaN, which stays)
-        z = fmaf(__ldcg(part(c) + kTcRows + tid), r == kNegInf ? 1.f : fast_exp2(r - m), z);
-      }
-      const int g = tile * kTcRows + tid;
-      if (a.lse)
-        a.lse[req + static_cast<long long>(g / a.G) * a.Hq + g % a.G] =
-            !(z == 0.f) ? (log2f(z) + m - kRefShift) * 0.69314718055994531f : kNegInf;
-    }
-    wm[tid] = m;
-    wf[2 * kTcRows + tid] = !(z == 0.f) ? 1.f / z : 0.f;
-  }
-  named_sync(1, kTcSoftmax);
-  const int c4 = tid % LANES, r0 = tid / LANES;
+  const int g = tile * kTcRows + row, t = ka_div_g(a, g);
+  const long long orow = req + static_cast<long long>(t) * a.Hq + g - t * a.G;
+  if (row < live) {
 #pragma unroll 1
-  for (int rb = r0; rb < live; rb += RSTEP * RK) {
-    float4 acc[RK];
+    for (int ch = c0; ch < c0 + D / 2; ch += N) {
+      float m = kNegInf, z = 0.f, acc[N];
 #pragma unroll
-    for (int k = 0; k < RK; ++k) acc[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+      for (int j = 0; j < N; ++j) acc[j] = 0.f;
+#pragma unroll 1
+      for (int c = first; c <= last; c += 2) {
+        float* const p = part(c) + row;
+        float* const q = part(min(c + 1, last)) + row;
+        float v[N], w[N];
+        const float r0 = __ldcg(p), z0 = __ldcg(p + kTcRows);
+        float r1 = __ldcg(q), z1 = __ldcg(q + kTcRows);
+#pragma unroll
+        for (int j = 0; j < N; ++j) v[j] = __ldcg(p + (2 + ch + j) * kTcRows);
+#pragma unroll
+        for (int j = 0; j < N; ++j) w[j] = __ldcg(q + (2 + ch + j) * kTcRows);
+        if (c == last) {  // no second one
+          r1 = kNegInf;
+          z1 = 0.f;
+#pragma unroll
+          for (int j = 0; j < N; ++j) w[j] = 0.f;
+        }
+        const float n = fmaxf(m, fmaxf(r0, r1));
+        // a part that saw nothing has z = 0 and O = 0 (or NaN, which stays)
+        const float fm = m == kNegInf ? 1.f : fast_exp2(m - n);
+        const float f0 = r0 == kNegInf ? 1.f : fast_exp2(r0 - n);
+        const float f1 = r1 == kNegInf ? 1.f : fast_exp2(r1 - n);
+        m = n;
+        z = z * fm + z0 * f0 + z1 * f1;
+#pragma unroll
+        for (int j = 0; j < N; ++j) acc[j] = acc[j] * fm + v[j] * f0 + w[j] * f1;
+      }
+      const bool any = !(z == 0.f);
+      const float inv = any ? 1.f / z : 0.f;
+      T* const o = static_cast<T*>(a.out) + orow * D + ch;
+#pragma unroll
+      for (int j = 0; j < N; j += 8) {
+        alignas(16) T e[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) e[k] = from_float<T>(any ? acc[j + k] * inv : 0.f);
+        *reinterpret_cast<uint4*>(o + j) = *reinterpret_cast<const uint4*>(e);
+      }
+      if (a.lse && ch == 0)
+        a.lse[orow] = any ? (log2f(z) + m - kRefShift) * 0.69314718055994531f : kNegInf;
+    }
+  }
+  named_sync(1, kTcSoftmax);  // everything has been read
+  if (row < live) {
 #pragma unroll 1
     for (int c = first; c <= last; ++c) {
-      float* p = part(c);
-#pragma unroll
-      for (int k = 0; k < RK; ++k) {
-        const int r = rb + k * RSTEP;
-        if (r < live) {
-          float4* q = reinterpret_cast<float4*>(p + 2 * kTcRows + r * D) + c4;
-          const float4 v = __ldcg(q);
-          const float rc = __ldcg(p + r);
-          const float f = rc == kNegInf ? 1.f : fast_exp2(rc - wm[r]);
-          acc[k].x = fmaf(v.x, f, acc[k].x);
-          acc[k].y = fmaf(v.y, f, acc[k].y);
-          acc[k].z = fmaf(v.z, f, acc[k].z);
-          acc[k].w = fmaf(v.w, f, acc[k].w);
-          *q = make_float4(0.f, 0.f, 0.f, 0.f);
-        }
-      }
-    }
-#pragma unroll
-    for (int k = 0; k < RK; ++k) {
-      const int r = rb + k * RSTEP;
-      if (r < live) {
-        const int g = tile * kTcRows + r;
-        const float i = wf[2 * kTcRows + r];
-        alignas(8) T e[4] = {from_float<T>(i != 0.f ? acc[k].x * i : 0.f),
-                             from_float<T>(i != 0.f ? acc[k].y * i : 0.f),
-                             from_float<T>(i != 0.f ? acc[k].z * i : 0.f),
-                             from_float<T>(i != 0.f ? acc[k].w * i : 0.f)};
-        *reinterpret_cast<uint2*>(static_cast<T*>(a.out) +
-                                  (req + static_cast<long long>(g / a.G) * a.Hq + g % a.G) * D +
-                                  c4 * 4) = *reinterpret_cast<const uint2*>(e);
-      }
+      float* const p = part(c) + row;
+      if (c0 == 0) p[0] = p[kTcRows] = 0.f;
+#pragma unroll 16
+      for (int ch = c0; ch < c0 + D / 2; ++ch) p[(2 + ch) * kTcRows] = 0.f;
     }
   }
-  named_sync(1, kTcSoftmax);  // the references have been read
-  for (int c = first; c <= last; ++c)
-    if (tid < live) part(c)[tid] = part(c)[kTcRows + tid] = 0.f;
 }
 
 // ------------------------------------------------------------------- kernel
 
-// A softmax thread's row of a unit.
-struct TcRow {
-  long long out;  // row of out and lse
-  int t;          // round token
-  bool mine;      // the row exists
+// What a softmax thread knows of its unit.  Units of few rows are laid down
+// `copies` times; lane l holds row l mod (128 / copies), copy l / (128 / copies).
+struct TcUnit {
+  int t, hq;      // the row's round token and query head
+  int live;       // rows of the unit
+  int cs, copies, copy;  // copies = 1 << cs
+  bool mine;      // the lane holds a row
+  __device__ __forceinline__ bool warp_live(int quarter) const {
+    return ((quarter * 32) & ((kTcRows >> cs) - 1)) < live;
+  }
 };
+__device__ __forceinline__ TcUnit tc_unit(const KvAttnProblem& a,
+                                          const KaCursor<kTcRows, kTcBlock>& cur, int lane_row) {
+  TcUnit u;
+  u.live = min(kTcRows, cur.l.n * a.G - cur.tile * kTcRows);
+  u.cs = u.live <= 32 ? 2 : u.live <= 64 ? 1 : 0;
+  u.copies = 1 << u.cs;
+  const int step = kTcRows >> u.cs, r = lane_row & (step - 1);
+  u.copy = lane_row >> (7 - u.cs);
+  u.mine = r < u.live;
+  const int g = u.mine ? cur.tile * kTcRows + r : 0;
+  u.t = ka_div_g(a, g);
+  u.hq = cur.head * a.G + g - u.t * a.G;
+  return u;
+}
 
-// The unit's queries into tensor memory, as halves: thread = row, set s the
-// s-th half of the channels.  Returns scale * log2(e) * 2^(the row's
-// exponent): bf16 rows are scaled by a power of two into the halves' range.
+// Which of the 16 positions of a block's piece the row sees (an edge block).
+__device__ __forceinline__ uint32_t tc_seen(const KvAttnProblem& a, int b, const TcUnit& u,
+                                            const TcMeta& m, int piece) {
+  if (!u.mine || m.s[piece].x < 0.f) return 0u;
+  const int r0 = m.round + piece * 16;  // round index of the first (negative: prefix)
+  const int tokens = m.tokens - piece * 16;
+  if (tokens <= 0) return 0u;
+  uint32_t seen;
+  if (r0 <= -16) {
+    seen = 0xffffu;
+  } else if (a.mask == nullptr) {
+    const int cols = u.t - r0 + 1;
+    seen = cols >= 16 ? 0xffffu : cols <= 0 ? 0u : (1u << cols) - 1;
+  } else {
+    const unsigned* mw = a.mask + (static_cast<long long>(b) * a.T + u.t) * a.words;
+    const uint64_t mb = mw[0] | (a.T > 32 ? static_cast<uint64_t>(mw[1]) << 32 : 0ull);
+    seen = r0 >= 64 ? 0u
+           : r0 >= 0 ? static_cast<uint32_t>(mb >> r0) & 0xffffu
+                     : (static_cast<uint32_t>(mb << -r0) | ((1u << -r0) - 1)) & 0xffffu;
+  }
+  return tokens >= 16 ? seen : seen & ((1u << tokens) - 1);
+}
+
+// The unit's queries into shared memory, as halves, in the operands' layout:
+// thread = row, set s the s-th half of the channels.  Returns |scale| log2(e)
+// 2^(the row's exponent) (the sign goes to the queries): bf16 rows are scaled
+// by a power of two into the halves' range, found by the row's two threads
+// together.
 template <int D, class T>
 __device__ __forceinline__ float tc_load_q(const KvAttnProblem& a, const T* qp, bool mine, int set,
-                                           unsigned tq) {
+                                           unsigned char* qh, float (*exch)[kTcRows], int row,
+                                           int quarter) {
+  constexpr int N = D / 8;
+  uint2 w[N];
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    w[i] = make_uint2(0, 0);
+    if (mine) {
+      const T* p = qp + set * (D / 2) + 4 * i;
+      w[i] = a.q_vec ? *reinterpret_cast<const uint2*>(p)
+                     : ka_load4(reinterpret_cast<const unsigned short*>(p));
+    }
+  }
   int ex = 0;
   if (!__is_same(T, __half)) {
     float m = 0.f;
-    if (mine) {
-      if (a.q_vec) {
-#pragma unroll 8
-        for (int c = 0; c < D; c += 4) {
-          const uint2 w = *reinterpret_cast<const uint2*>(qp + c);
-          m = fmaxf(fmaxf(m, fmaxf(fabsf(bf16lo(w.x)), fabsf(bf16hi(w.x)))),
-                    fmaxf(fabsf(bf16lo(w.y)), fabsf(bf16hi(w.y))));
-        }
-      } else {
-        for (int c = 0; c < D; c += 2) {
-          const float2 f = ka_two(qp + c);
-          m = fmaxf(m, fmaxf(fabsf(f.x), fabsf(f.y)));
-        }
-      }
-    }
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+      m = fmaxf(fmaxf(m, fmaxf(fabsf(bf16lo(w[i].x)), fabsf(bf16hi(w[i].x)))),
+                fmaxf(fabsf(bf16lo(w[i].y)), fabsf(bf16hi(w[i].y))));
+    exch[set][row] = m;
+    named_sync(2 + quarter, 64);
+    m = fmaxf(m, exch[set ^ 1][row]);
     // the row's largest value lands in [2^14, 2^15)
     ex = min(max(static_cast<int>(__float_as_uint(m) >> 23) - 127 - 14, -100), 100);
   }
-  const float k = pow2f(-ex);
-#pragma unroll 1
-  for (int c0 = 0; c0 < D / 2; c0 += 32) {
-    unsigned w[16];
+  const float k = a.scale_log2 < 0.f ? -pow2f(-ex) : pow2f(-ex);
 #pragma unroll
-    for (int c = 0; c < 32; c += 4) {
-      alignas(8) T e[4];
-      const T* p = qp + set * (D / 2) + c0 + c;
-      if (a.q_vec) {
-        *reinterpret_cast<uint2*>(e) = mine ? *reinterpret_cast<const uint2*>(p)
-                                            : make_uint2(0, 0);
-      } else {
-#pragma unroll
-        for (int j = 0; j < 4; ++j) e[j] = mine ? p[j] : from_float<T>(0.f);
-      }
-      const float2 x = ka_two(e), y = ka_two(e + 2);
-      w[c / 2] = half2_of(x.x * k, x.y * k);
-      w[c / 2 + 1] = half2_of(y.x * k, y.y * k);
-    }
-    __syncwarp();
-    tc_st16(tq + set * (D / 4) + c0 / 2, w);
+  for (int i = 0; i < N; i += 2) {
+    uint4 h;
+    const T* e = reinterpret_cast<const T*>(&w[i]);
+    float2 x = ka_two(e), y = ka_two(e + 2);
+    h.x = half2_of(x.x * k, x.y * k);
+    h.y = half2_of(y.x * k, y.y * k);
+    e = reinterpret_cast<const T*>(&w[i + 1]);
+    x = ka_two(e);
+    y = ka_two(e + 2);
+    h.z = half2_of(x.x * k, x.y * k);
+    h.w = half2_of(y.x * k, y.y * k);
+    const int piece = (set * (D / 2) + 4 * i) / 8;  // 16-byte piece of the row
+    *reinterpret_cast<uint4*>(qh + (piece >> 3) * (kTcRows * 128) + row * 128 +
+                              (((piece & 7) ^ (row & 7)) << 4)) = h;
   }
-  tc_wait_st();
-  tc_fence_before();
-  return a.scale_log2 * pow2f(ex);
+  fence_proxy_async_shared();
+  // (not 0: masked scores are -inf and stay so)
+  return fmaxf(fabsf(a.scale_log2) * pow2f(ex), 1e-30f);
+}
+
+// The queries of a unit on their way into the cache, two batches before the
+// softmax warps ask for them.
+template <int D, class T, class Item>
+__device__ __forceinline__ void tc_prefetch_q(const KvAttnProblem& a, const Item& it, int lane,
+                                              int lanes) {
+  const int live = min(kTcRows, it.rows - it.tile * kTcRows);
+  for (int r = lane; r < live; r += lanes) {
+    const int g = it.tile * kTcRows + r;
+    const int t = ka_div_g(a, g);
+    const T* p = static_cast<const T*>(a.q) + it.b * a.q_batch + t * a.q_token +
+                 (it.head * a.G + g - t * a.G) * a.q_head;
+    prefetch_l2(p);
+    if (D == 128) prefetch_l2(p + 64);
+  }
 }
 
 template <int D, class T>
@@ -334,15 +405,14 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv_attn_tc_kernel(const KvAttnP
   // the operands want 1024-byte alignment; the launch asks for the slack
   unsigned char* base = tc_smem + ((1024u - (smem_u32(tc_smem) & 1023u)) & 1023u);
   TcShared<D>& sh = *reinterpret_cast<TcShared<D>*>(base);
-  constexpr unsigned kS = 0, kO = 2 * kTcBlock, kQ = kO + D;
-  static_assert(kQ + D / 2 <= 512, "tensor memory");
-  static_assert(offsetof(TcShared<D>, meta) % 16 == 0 && offsetof(TcMeta, ks) % 16 == 0 &&
-                    offsetof(TcMeta, ev) % 16 == 0 && offsetof(TcMeta, zin) % 16 == 0 &&
+  constexpr unsigned kS = 0, kO = 2 * kTcBlock;
+  static_assert(kO + 2 * D <= 512, "tensor memory");
+  static_assert(offsetof(TcShared<D>, meta) % 16 == 0 && offsetof(TcMeta, s) % 16 == 0 &&
                     offsetof(TcShared<D>, raw) % 1024 == 0 && offsetof(TcShared<D>, rawfull) % 8 == 0,
                 "alignment");
   constexpr unsigned kHalf = kTcBlock * 128;  // bytes of 64 channels of a block, as halves
   const int tid = static_cast<int>(threadIdx.x), warp = tid >> 5, lane = tid & 31;
-  const int grid = static_cast<int>(gridDim.x), cta = static_cast<int>(blockIdx.x);
+  const int cta = static_cast<int>(blockIdx.x);
   int* const dead = &sh.dead;
 
   if (warp == 17) {
@@ -354,12 +424,12 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv_attn_tc_kernel(const KvAttnP
         mbar_init(&sh.rawempty[s], kTcConvert / 32);
       }
       for (int s = 0; s < 2; ++s) {
-        mbar_init(&sh.kfull[s], kTcConvert / 32);
-        mbar_init(&sh.vfull[s], kTcConvert / 32);
         mbar_init(&sh.sfull[s], 1);
-        mbar_init(&sh.pfull[s], kTcSoftmax / 32);
+        mbar_init(&sh.pfull[s], 4);
         mbar_init(&sh.pvdone[s], 1);
       }
+      mbar_init(&sh.kfull, kTcConvert / 32);
+      mbar_init(&sh.vfull, kTcConvert / 32);
       mbar_init(&sh.qfull, kTcSoftmax / 32);
       sh.dead = 0;
       fence_mbar_init();
@@ -368,16 +438,25 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv_attn_tc_kernel(const KvAttnP
     tc_fence_before();
   }
   grid_dependency_wait();
-  const long long total =
+  const int total =
       ka_prefix<kTcRows, kTcBlock, kTcThreads>(a, sh.prefix, sh.scan, cta == 0);
   tc_fence_after();
   const unsigned tmem = sh.tmem;
-  ka_clear_rows<T, D, kTcThreads>(a);
+  if (tid == 0) {
+    sh.total = total;
+    sh.nanany = 0;
+  }
+  for (int j = tid; j < D / 64 * kTcRows; j += kTcThreads) (&sh.nanrow[0][0])[j] = 0;
+  __syncthreads();
 
-  const long long parts = max(1ll, min(static_cast<long long>(grid), total / kTcMinBlocks));
-  const long long w0 = cta < parts ? total * cta / parts : 0;
-  const long long w1 = cta < parts ? total * (cta + 1) / parts : 0;
-  const int n = static_cast<int>(w1 - w0);  // blocks of this CTA
+  int w0 = 0, n = 0;  // blocks of this CTA
+  {
+    const KaParts parts(total, static_cast<int>(gridDim.x), kTcMinBlocks);
+    if (cta < parts.count) {
+      w0 = parts.begin(cta);
+      n = parts.begin(cta + 1) - w0;
+    }
+  }
 
   if (n > 0 && warp == 18) {
     // ------------------------------------------------------------ producer
@@ -385,12 +464,15 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv_attn_tc_kernel(const KvAttnP
     using Feed = KaFeed<kTcRows, kTcBlock>;
     Feed feed;
     feed.start(a, sh.prefix, w0, n, lane);
-    auto item = feed.resolve(a);
-    feed.look(a, false);
+    typename Feed::Item item = {}, next = {};
     int i = 0;
-    for (int i0 = 0; i0 < n; i0 += Feed::NB) {
-      const auto next = feed.resolve(a);
-      feed.look(a, false);
+#pragma unroll 1
+    for (int i0 = -2 * Feed::NB; i0 < n; i0 += Feed::NB) {
+      item = next;
+      next = feed.resolve(a);
+      feed.look(a, i0 < -Feed::NB);
+      if (i0 < 0) continue;
+      const unsigned missing = __ballot_sync(0xffffffffu, item.scale < 0.f);
       for (int j = 0; j < Feed::NB && i < n; ++j, ++i) {
 #pragma unroll 1
         for (int side = 0; side < 2; ++side) {
@@ -400,8 +482,8 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv_attn_tc_kernel(const KvAttnP
           if (lane / Feed::kCopies == j) {
             const bool here = feed.is_v == (side == 1);
             if (here && item.src != nullptr && !*static_cast<volatile int*>(dead)) {
-              mbar_expect_tx(&sh.rawfull[slot], 16 * D);
-              bulk_copy_g2s_hint(&sh.raw[slot][feed.sub * 16 * D], item.src, 16 * D,
+              mbar_expect_tx(&sh.rawfull[slot], item.bytes);
+              bulk_copy_g2s_hint(&sh.raw[slot][feed.sub * 16 * D], item.src, item.bytes,
                                  &sh.rawfull[slot], pol);
             }
             if (side == 0) {
@@ -409,15 +491,18 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv_attn_tc_kernel(const KvAttnP
               // before the keys are announced
               TcMeta& m = sh.meta[i % kTcMeta];
               const int e = scale_exp(item.scale);
+              if (item.first) tc_prefetch_q<D, T>(a, item, lane % Feed::kCopies, Feed::kCopies);
               if (feed.is_v) {
-                m.ev[feed.sub] = static_cast<float>(e);
-                m.zin[feed.sub] = pow2f(-e);
+                m.s[feed.sub].y = static_cast<float>(e);
+                m.s[feed.sub].z = pow2f(-e);
               } else {
-                m.ks[feed.sub] = item.scale < 0.f ? -1.f : pow2f(e);
+                m.s[feed.sub].x = item.scale < 0.f ? -1.f : pow2f(e);
                 if (feed.sub == 0) {
                   m.first = item.first;
                   m.tokens = item.tokens;
                   m.round = item.round;
+                  m.edge = item.round + kTcBlock > 0 ||
+                           (missing >> (j * Feed::kCopies) & ((1u << Feed::kCopies) - 1)) != 0;
                   m.nan = 0;
                 }
               }
@@ -427,7 +512,6 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv_attn_tc_kernel(const KvAttnP
           if (lane / Feed::kCopies == j && feed.is_v == (side == 1)) mbar_arrive(&sh.rawfull[slot]);
         }
       }
-      item = next;
     }
     // copies of the last slots must land before the block ends
     for (int x = max(0, 2 * n - kTcSlots); x < 2 * n; ++x)
@@ -450,30 +534,25 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv_attn_tc_kernel(const KvAttnP
     const unsigned off0 = off + (((c0 + flip) ^ (tok0 & 7)) << 4);
     const unsigned off1 = off + (((c0 + 1 - flip) ^ (tok0 & 7)) << 4);
     static_assert(STEP % 8 == 0, "swizzle phase");
-    uint64_t* const full = side ? sh.vfull : sh.kfull;
+    uint64_t* const full = side ? &sh.vfull : &sh.kfull;
     uint64_t* const freed = side ? sh.pvdone : sh.sfull;
     for (int i = 0; i < n; ++i) {
-      const int x = 2 * i + side, slot = x % kTcSlots, buf = i & 1;
+      const int x = 2 * i + side, slot = x % kTcSlots;
       tc_wait(&sh.rawfull[slot], static_cast<uint32_t>(x / kTcSlots) & 1, dead, a.err);
-      uint4 code[ITEMS];
-#pragma unroll
-      for (int j = 0; j < ITEMS; ++j)
-        code[j] = *reinterpret_cast<const uint4*>(&sh.raw[slot][(ct + j * kTcConvert) * 16]);
       TcMeta& m = sh.meta[i % kTcMeta];
-      bool edge = m.round + kTcBlock > 0;
-#pragma unroll
-      for (int u = 0; u < 8; ++u) edge |= m.ks[u] < 0.f;
-      if (edge) {
+      if (__builtin_expect(m.edge, 0)) {
         // Codes nobody wrote become zeros.  NaN value codes leave the
         // product, where they would meet the zero weights of rows that do
         // not see them, and go to a mask the softmax warps look at.
-        if (side == 1 && i >= 2)  // the mask's last reader: block i - 2
-          tc_wait(&sh.pvdone[buf], static_cast<uint32_t>((i >> 1) - 1) & 1, dead, a.err);
-#pragma unroll
+        if (side == 1 && i >= 1)  // the mask's last reader: block i - 1
+          tc_wait(&sh.pvdone[(i - 1) & 1], static_cast<uint32_t>((i - 1) >> 1) & 1, dead, a.err);
+#pragma unroll 1
         for (int j = 0; j < ITEMS; ++j) {
           const int tok = tok0 + j * STEP;
-          const bool there = tok < m.tokens && m.ks[tok >> 4] >= 0.f;
-          unsigned* w = reinterpret_cast<unsigned*>(&code[j]);
+          const bool there = tok < m.tokens && m.s[tok >> 4].x >= 0.f;
+          uint4* const at = reinterpret_cast<uint4*>(&sh.raw[slot][(ct + j * kTcConvert) * 16]);
+          uint4 c = *at;
+          unsigned* w = reinterpret_cast<unsigned*>(&c);
           unsigned mask = 0;
 #pragma unroll
           for (int q = 0; q < 4; ++q) {
@@ -485,50 +564,68 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv_attn_tc_kernel(const KvAttnP
                       << (4 * q);
             }
           }
+          *at = c;
           if (side == 1) {
-            sh.nanmask[buf][tok][piece] = static_cast<unsigned short>(mask);
+            sh.nanmask[tok][piece] = static_cast<unsigned short>(mask);
             if (mask) m.nan = 1;
           }
         }
       }
-      // the buffer's last reader: the products of block i - 2
-      if (i >= 2) tc_wait(&freed[buf], static_cast<uint32_t>((i >> 1) - 1) & 1, dead, a.err);
-      unsigned char* dst = side ? sh.vh[buf] : sh.kh[buf];
+      uint4 code[ITEMS];
+#pragma unroll
+      for (int j = 0; j < ITEMS; ++j)
+        code[j] = *reinterpret_cast<const uint4*>(&sh.raw[slot][(ct + j * kTcConvert) * 16]);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sh.rawempty[slot]);  // in registers: the slot is free
+      // half of the codes are converted before the wait for the buffer (all
+      // of them would not fit the registers)
+      constexpr int AHEAD = ITEMS / 2;
+      uint4 lo[AHEAD], hi[AHEAD];
+      auto halves = [&](const uint4& c, uint4& l, uint4& h) {
+        l = make_uint4(half2_lo(c.x), half2_hi(c.x), half2_lo(c.y), half2_hi(c.y));
+        h = make_uint4(half2_lo(c.z), half2_hi(c.z), half2_lo(c.w), half2_hi(c.w));
+      };
+#pragma unroll
+      for (int j = 0; j < AHEAD; ++j) halves(code[j], lo[j], hi[j]);
+      // the buffer's last reader: the products of block i - 1
+      if (i >= 1)
+        tc_wait(&freed[(i - 1) & 1], static_cast<uint32_t>((i - 1) >> 1) & 1, dead, a.err);
+      unsigned char* dst = side ? sh.vh : sh.kh;
 #pragma unroll
       for (int j = 0; j < ITEMS; ++j) {
-        const uint4 lo = make_uint4(half2_lo(code[j].x), half2_hi(code[j].x),
-                                    half2_lo(code[j].y), half2_hi(code[j].y));
-        const uint4 hi = make_uint4(half2_lo(code[j].z), half2_hi(code[j].z),
-                                    half2_lo(code[j].w), half2_hi(code[j].w));
-        *reinterpret_cast<uint4*>(dst + off0 + j * (STEP * 128)) = flip ? hi : lo;
-        *reinterpret_cast<uint4*>(dst + off1 + j * (STEP * 128)) = flip ? lo : hi;
+        uint4 l, h;
+        if (j < AHEAD) {
+          l = lo[j];
+          h = hi[j];
+        } else {
+          halves(code[j], l, h);
+        }
+        *reinterpret_cast<uint4*>(dst + off0 + j * (STEP * 128)) = flip ? h : l;
+        *reinterpret_cast<uint4*>(dst + off1 + j * (STEP * 128)) = flip ? l : h;
       }
       fence_proxy_async_shared();
       __syncwarp();
-      if (lane == 0) {
-        mbar_arrive(&full[buf]);
-        mbar_arrive(&sh.rawempty[slot]);
-      }
+      if (lane == 0) mbar_arrive(full);
     }
   } else if (n > 0 && warp == 16) {
     // ---------------------------------------------------------- S = Q K^T
     if (lane == 0) {
       constexpr unsigned id = tc_idesc(kTcBlock, false);
-      const unsigned k0 = smem_u32(sh.kh[0]);
+      const uint64_t d = tc_desc(smem_u32(sh.kh), 16), q = tc_desc(smem_u32(sh.qh), 16);
       uint32_t segs = 0;
       for (int i = 0; i < n; ++i) {
         const int s = i & 1;
         const uint32_t ph = static_cast<uint32_t>(i >> 1) & 1;
-        ka_wait(&sh.kfull[s], ph, dead, a.err);
+        ka_wait(&sh.kfull, static_cast<uint32_t>(i) & 1, dead, a.err);
         if (sh.meta[i % kTcMeta].first) ka_wait(&sh.qfull, segs++ & 1, dead, a.err);
         // S_s and the weights in it: read by the products of block i - 2
         if (i >= 2) ka_wait(&sh.pvdone[s], ph ^ 1, dead, a.err);
         tc_fence_after();
-        const uint64_t d = tc_desc(k0 + s * (kTcBlock * D * 2), 16);
 #pragma unroll
-        for (int k = 0; k < D / 16; ++k)
-          tc_mma(tmem + kS + s * kTcBlock, tmem + kQ + k * 8,
-                 d + static_cast<uint64_t>(((k & 3) * 32 + (k >> 2) * kHalf) >> 4), id, k > 0);
+        for (int k = 0; k < D / 16; ++k) {
+          const uint64_t at = static_cast<uint64_t>(((k & 3) * 32 + (k >> 2) * kHalf) >> 4);
+          tc_mma_ss(tmem + kS + s * kTcBlock, q + at, d + at, id, k > 0);
+        }
         tc_commit(&sh.sfull[s]);
       }
     }
@@ -537,275 +634,342 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv_attn_tc_kernel(const KvAttnP
     // ------------------------------------------------------------ O += P V
     if (lane == 0) {
       constexpr unsigned id = tc_idesc(D, true);
-      const unsigned v0 = smem_u32(sh.vh[0]);
+      const uint64_t d = tc_desc(smem_u32(sh.vh), kHalf);
+      int seg = 0;  // first block of the segment
       for (int i = 0; i < n; ++i) {
         const int s = i & 1;
         const uint32_t ph = static_cast<uint32_t>(i >> 1) & 1;
-        ka_wait(&sh.vfull[s], ph, dead, a.err);
-        const bool first = sh.meta[i % kTcMeta].first != 0;
+        ka_wait(&sh.vfull, static_cast<uint32_t>(i) & 1, dead, a.err);
+        if (sh.meta[i % kTcMeta].first) seg = i;
         ka_wait(&sh.pfull[s], ph, dead, a.err);
         tc_fence_after();
-        const uint64_t d = tc_desc(v0 + s * (kTcBlock * D * 2), kHalf);
 #pragma unroll
         for (int k = 0; k < kTcBlock / 16; ++k)
-          tc_mma(tmem + kO, tmem + kS + s * kTcBlock + (k >> 2) * 64 + (k & 3) * 8,
-                 d + static_cast<uint64_t>(k * (16 * 128 >> 4)), id, !first || k > 0);
+          tc_mma(tmem + kO + s * D, tmem + kS + s * kTcBlock + k * 16,
+                 d + static_cast<uint64_t>(k * (16 * 128 >> 4)), id, i - seg >= 2 || k > 0);
         tc_commit(&sh.pvdone[s]);
       }
-      ka_wait(&sh.pvdone[(n - 1) & 1], static_cast<uint32_t>((n - 1) >> 1) & 1, dead, a.err);
+      for (int i = max(0, n - 2); i < n; ++i)
+        ka_wait(&sh.pvdone[i & 1], static_cast<uint32_t>(i >> 1) & 1, dead, a.err);
     }
     __syncwarp();
   } else if (n > 0 && warp < 8) {
     // ------------------------------------------------------------- softmax
+    // What is not needed block by block stays in shared memory and is read
+    // again: with all of shared memory in use there is no L1 to speak of, and
+    // a spilled register's way to L2 took 500 clocks and more of each block.
     const int set = warp >> 2, quarter = warp & 3, row = tid & (kTcRows - 1);
     // tensor-memory address of the warp's lanes (bits 31..16: lane)
     const unsigned tm = tmem + (static_cast<unsigned>(quarter) << 21);
-    KaCursor<kTcRows, kTcBlock> cur;
-    cur.seek(a, sh.prefix, w0);
-    auto row_of = [&]() {
-      TcRow r;
-      const int g = cur.tile * kTcRows + row;
-      r.mine = g < cur.l.n * a.G;
-      r.t = r.mine ? g / a.G : 0;
-      const int hq = cur.head * a.G + (r.mine ? g % a.G : 0);
-      r.out = (static_cast<long long>(cur.b) * a.T + r.t) * a.Hq + hq;
-      return r;
-    };
-    auto load_q = [&](const TcRow& r) {
-      float c = 0.f;
-      if (cur.tile * kTcRows + quarter * 32 < cur.l.n * a.G)
-        c = tc_load_q<D, T>(a,
-                            static_cast<const T*>(a.q) + cur.b * a.q_batch + r.t * a.q_token +
-                                (r.out % a.Hq) * a.q_head,
-                            r.mine, set, tm + kQ);
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&sh.qfull);
-      return c;
-    };
     constexpr int PF = kTcPartialFloats<D>;
-    TcRow me = row_of();
-    float c2 = load_q(me);
-    int seg = 0;
-    for (int i0 = 0; i0 < n; ++seg) {
-      const int blk0 = cur.blk, tile = cur.tile;
-      const int nb = min(cur.nblk - blk0, n - i0);
-      const int live = min(kTcRows, cur.l.n * a.G - tile * kTcRows);
-      const bool warp_live = quarter * 32 < live;
+    {
+      KaCursor<kTcRows, kTcBlock> cur;
+      cur.seek(a, sh.prefix, w0);
+      if (lane == 0) sh.cur[warp] = cur;
+      __syncwarp();
+    }
+    // One unit a turn; the first turn (i0 < 0) only loads the first queries.
+    float c2 = 0.f;
+    for (int i0 = -1; i0 < n;) {
+      int nb = 0, cs = 0, base = 0;
+      bool warp_live = false;
+      if (i0 >= 0) {
+        const KaCursor<kTcRows, kTcBlock> cur = sh.cur[warp];
+        const TcUnit me = tc_unit(a, cur, row);
+        nb = min(cur.nblk - cur.blk, n - i0);
+        cs = me.cs;
+        base = me.copy << (3 - cs);
+        warp_live = me.warp_live(quarter);
+      }
+      // of a block's eight 16-position pieces: `own` from `base` on
+      const int own = 8 >> cs;
       float ref = kNegInf, z = 0.f;
-      uint64_t nanc[D / 64];  // channels in which the row sees a NaN
-#pragma unroll
-      for (int j = 0; j < D / 64; ++j) nanc[j] = 0;
+      bool had = false;  // this stream has taken a block of the unit
 
 #pragma unroll 1
-      for (int i = i0; i < i0 + nb; ++i) {
-        const int buf = i & 1;
+      for (int i = i0 + ((i0 ^ set) & 1); i < i0 + nb; i += 2) {
         const uint32_t ph = static_cast<uint32_t>(i >> 1) & 1;
-        const unsigned ts = tm + kS + buf * kTcBlock + set * 64;
-        tc_wait(&sh.sfull[buf], ph, dead, a.err);
+        tc_wait(&sh.sfull[set], ph, dead, a.err);
         tc_fence_after();
         if (warp_live) {
           const TcMeta& m = sh.meta[i % kTcMeta];
-          float4 ks = *reinterpret_cast<const float4*>(&m.ks[set * 4]);
-          const float4 ev = *reinterpret_cast<const float4*>(&m.ev[set * 4]);
-          const float4 zi = *reinterpret_cast<const float4*>(&m.zin[set * 4]);
-          const bool edge =
-              m.round + kTcBlock > 0 || fminf(fminf(ks.x, ks.y), fminf(ks.z, ks.w)) < 0.f;
-          uint64_t seen = ~0ull;  // of the warp's 64 positions
-          if (edge) {
-            seen = 0;
-            const int r0 = m.round + set * 64;  // round index of column 0 (negative: prefix)
-            const int tokens = m.tokens - set * 64;
-            if (me.mine) {
-              if (a.mask == nullptr) {
-                const int cols = me.t - r0 + 1;
-                seen = cols >= 64 ? ~0ull : cols <= 0 ? 0ull : (1ull << cols) - 1;
-              } else {
-                const unsigned* mw = a.mask + (me.out / a.Hq) * a.words;
-                const uint64_t mb = mw[0] | (a.T > 32 ? static_cast<uint64_t>(mw[1]) << 32 : 0ull);
-                seen = r0 >= 64    ? 0ull
-                       : r0 >= 0   ? mb >> r0
-                       : r0 <= -64 ? ~0ull
-                                   : (mb << -r0) | ((1ull << -r0) - 1);
-              }
-              if (tokens < 64) seen &= tokens <= 0 ? 0ull : (1ull << tokens) - 1;
-              if (ks.x < 0.f) seen &= ~0xffffull;
-              if (ks.y < 0.f) seen &= ~(0xffffull << 16);
-              if (ks.z < 0.f) seen &= ~(0xffffull << 32);
-              if (ks.w < 0.f) seen &= ~(0xffffull << 48);
-            }
-            tc_wait(&sh.vfull[buf], ph, dead, a.err);  // the converters' NaN mask
-            if (*static_cast<const volatile int*>(&m.nan)) {
+          const unsigned ts = tm + kS + set * kTcBlock + base * 16;
+          if (__builtin_expect(m.edge, 0)) {
+            // scores of positions the row does not see become -inf
+            const TcUnit me = tc_unit(a, sh.cur[warp], row);
+            tc_wait(&sh.vfull, static_cast<uint32_t>(i) & 1, dead, a.err);  // the NaN mask
+            const bool nan = *static_cast<const volatile int*>(&m.nan) != 0;
 #pragma unroll 1
-              for (int tok = 0; tok < 64; ++tok)
-                if (seen >> tok & 1)
-#pragma unroll
-                  for (int j = 0; j < D / 16; ++j)
-                    nanc[j >> 2] |= static_cast<uint64_t>(sh.nanmask[buf][set * 64 + tok][j])
-                                    << (16 * (j & 3));
-            }
-            __syncwarp();
-          }
-          // x = S c2 2^ek + ev - bs, against the present reference; where the
-          // maximum, known to both threads of the row, turns out too high for
-          // it (rarely after a unit's first block) they are taken again.
-          unsigned p[32];
-          float zs, bs = ref == kNegInf ? 0.f : ref - kRefShift;
-          for (int attempt = 0;; ++attempt) {
-            float mx = kNegInf;
-            zs = 0.f;
-#pragma unroll
-            for (int u = 0; u < 4; ++u) {  // 16 positions: one page's scales
+            for (int u = 0; u < own; ++u) {
+              const uint32_t seen = tc_seen(a, sh.cur[warp].b, me, m, base + u);
               unsigned x[16];
+              __syncwarp();
               tc_ld16(x, ts + u * 16);
-              const float sc = c2 * (u == 0 ? ks.x : u == 1 ? ks.y : u == 2 ? ks.z : ks.w);
-              const float vb = (u == 0 ? ev.x : u == 1 ? ev.y : u == 2 ? ev.z : ev.w) - bs;
 #pragma unroll
               for (int j = 0; j < 16; ++j)
-                x[j] = __float_as_uint(fmaf(__uint_as_float(x[j]), sc, vb));
-              if (edge) {
-                const unsigned in = static_cast<unsigned>(seen >> (16 * u));
+                if (!(seen >> j & 1)) x[j] = 0xff800000u;
+              __syncwarp();
+              tc_st16(ts + u * 16, x);
+              if (nan) {
+                uint64_t c[D / 64];
 #pragma unroll
-                for (int j = 0; j < 16; ++j)
-                  if (!(in >> j & 1)) x[j] = 0xff800000u;  // -inf
-              }
-              float z0 = 0.f;
-#pragma unroll
-              for (int j = 0; j < 16; j += 2) {
-                const float x0 = __uint_as_float(x[j]), x1 = __uint_as_float(x[j + 1]);
-                mx = fmaxf(mx, fmaxf(x0, x1));
-                const float e0 = fast_exp2(x0), e1 = fast_exp2(x1);
-                z0 += e0 + e1;
-                p[u * 8 + j / 2] = half2_of(e0, e1);
-              }
-              zs = fmaf(z0, u == 0 ? zi.x : u == 1 ? zi.y : u == 2 ? zi.z : zi.w, zs);
-            }
-            if (attempt) break;
-            sh.exch[buf][set][row] = mx;
-            named_sync(2 + quarter, 64);
-            mx = fmaxf(mx, sh.exch[buf][set ^ 1][row]);
-            const bool rise = ref == kNegInf ? mx > kNegInf : mx > kRefShift + kRefSlack;
-            if (!__any_sync(0xffffffffu, rise)) break;
-            if (i > i0) {
-              // O whole: the products of block i - 1 are done.  Each set
-              // rescales its half of the channels.
-              tc_wait(&sh.pvdone[buf ^ 1], static_cast<uint32_t>((i - 1) >> 1) & 1, dead, a.err);
-              tc_fence_after();
-              const float f = !rise ? 1.f : ref == kNegInf ? 0.f : fast_exp2(ref - (mx + bs));
+                for (int j = 0; j < D / 64; ++j) c[j] = 0;
 #pragma unroll 1
-              for (int c = set * (D / 2); c < (set + 1) * (D / 2); c += 16) {
+                for (int tok = 0; tok < 16; ++tok)
+                  if (seen >> tok & 1)
+#pragma unroll
+                    for (int j = 0; j < D / 16; ++j)
+                      c[j >> 2] |= static_cast<uint64_t>(sh.nanmask[(base + u) * 16 + tok][j])
+                                   << (16 * (j & 3));
+#pragma unroll
+                for (int j = 0; j < D / 64; ++j)
+                  if (c[j]) {
+                    atomicOr(&sh.nanrow[j][row], static_cast<unsigned long long>(c[j]));
+                    sh.nanany = 1;
+                  }
+              }
+            }
+            tc_wait_st();
+          }
+          // x = S c2 2^ek + ev: the maximum first (the scales are positive),
+          // 32 positions at a time, the last of which stay in registers
+          float mx = kNegInf;
+          unsigned x[32];
+#pragma unroll 1
+          for (int u = 0; u < own; u += 2) {
+            __syncwarp();
+            tc_ld32(x, ts + u * 16);
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              const float4 ms = m.s[base + u + h];
+              float v[4];
+#pragma unroll
+              for (int j = 0; j < 4; ++j)
+                v[j] = fmaxf(
+                    fmaxf(__uint_as_float(x[16 * h + j]), __uint_as_float(x[16 * h + 4 + j])),
+                    fmaxf(__uint_as_float(x[16 * h + 8 + j]), __uint_as_float(x[16 * h + 12 + j])));
+              mx = fmaxf(mx, fmaf(fmaxf(fmaxf(v[0], v[1]), fmaxf(v[2], v[3])),
+                                  c2 * fabsf(ms.x), ms.y));
+            }
+          }
+          const bool rise = mx > ref + kRefSlack;
+          if (__builtin_expect(__any_sync(0xffffffffu, rise), 0)) {
+            const float f = !rise ? 1.f : ref == kNegInf ? 0.f : fast_exp2(ref - mx);
+            if (rise) ref = mx;
+            if (had) {
+              // O_s whole: the products of block i - 2 are done (their weights
+              // made way for these scores)
+              z *= f;
+#pragma unroll 1
+              for (int c = 0; c < D; c += 16) {
                 unsigned o[16];
-                tc_ld16(o, tm + kO + c);
+                __syncwarp();
+                tc_ld16(o, tm + kO + set * D + c);
 #pragma unroll
                 for (int j = 0; j < 16; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * f);
-                tc_st16(tm + kO + c, o);
+                tc_st16(tm + kO + set * D + c, o);
               }
-              z *= f;
             }
-            if (rise) ref = mx + bs;
-            bs = ref == kNegInf ? 0.f : ref - kRefShift;
           }
-          z += zs;
-          __syncwarp();
-          tc_st32(ts, p);
+          had = true;
+          // the weights, over the scores they come from
+          const float bs = ref == kNegInf ? 0.f : ref - kRefShift;
+#pragma unroll 1
+          for (int u = own - 2;; u -= 2) {
+            unsigned p[16];
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              const float4 ms = m.s[base + u + h];
+              const float sc = c2 * fabsf(ms.x), vb = ms.y - bs;
+              float z0 = 0.f, z1 = 0.f;
+#pragma unroll
+              for (int j = 0; j < 16; j += 2) {
+                const float e0 = fast_exp2(fmaf(__uint_as_float(x[16 * h + j]), sc, vb));
+                const float e1 = fast_exp2(fmaf(__uint_as_float(x[16 * h + j + 1]), sc, vb));
+                z0 += e0;
+                z1 += e1;
+                p[8 * h + j / 2] = half2_of(e0, e1);
+              }
+              z = fmaf(z0 + z1, ms.z, z);
+            }
+            __syncwarp();
+            tc_st8(ts + u * 16, p);
+            tc_st8(ts + u * 16 + 16, p + 8);
+            if (u == 0) break;
+            tc_ld32(x, ts + (u - 2) * 16);
+          }
+          if (cs > 0) {
+            // no weight in the other copies' positions
+            const unsigned p[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+#pragma unroll
+            for (int c = 0; c < 8; ++c)
+              if ((c ^ base) >> (3 - cs) != 0) tc_st8(tm + kS + set * kTcBlock + c * 16, p);
+          }
           tc_wait_st();
           tc_fence_before();
         }
         __syncwarp();
-        if (lane == 0) mbar_arrive(&sh.pfull[buf]);
+        if (lane == 0) mbar_arrive(&sh.pfull[set]);
       }
 
       // The next unit's queries first: its products run while this one's
       // result is written.
-      const TcRow my = me;
-      const bool whole = blk0 == 0 && nb == cur.nblk;
-      const int first = ka_cta_of(cur.unit0, parts, total);
-      const int last = ka_cta_of(cur.unit0 + cur.nblk - 1, parts, total);
-      const long long req = static_cast<long long>(cur.b) * a.T * a.Hq + cur.head * a.G;
-      cur.blk += nb;
-      if (cur.blk == cur.nblk) cur.next_unit(a);
-      if (i0 + nb < n) {
-        me = row_of();
-        c2 = load_q(me);
+      KaCursor<kTcRows, kTcBlock> cur = sh.cur[warp];
+      const TcUnit my = tc_unit(a, cur, row);
+      const bool whole = cur.blk == 0 && nb == cur.nblk;
+      const KaParts parts(sh.total, static_cast<int>(gridDim.x), kTcMinBlocks);
+      const int first = parts.of(cur.unit0), last = parts.of(cur.unit0 + cur.nblk - 1);
+      const long long req = static_cast<long long>(cur.b) * a.T * a.Hq;
+      const long long orow = req + static_cast<long long>(my.t) * a.Hq + my.hq;
+      const int tile = cur.tile, head0 = cur.head * a.G;
+      float* const part = a.partials + (2ll * cta + (cur.blk == 0 ? 1 : 0)) * PF;
+      // blocks each stream had; the unit's last products of each
+      const int cnt[2] = {(nb + 1 - (i0 & 1)) / 2, (nb + (i0 & 1)) / 2};
+      if (i0 >= 0) {
+        cur.blk += nb;
+        if (cur.blk == cur.nblk) cur.next_unit(a);
+        __syncwarp();
+        if (lane == 0) sh.cur[warp] = cur;
+        __syncwarp();
+        // The other stream's last scores too must be through with the queries.
+        // (They also mean that its products are at most one block behind,
+        // which the wait for them below, on a parity, relies on.)
+        const int io = i0 + nb - 1 - ((i0 + nb - 1 + set + 1) & 1);
+        if (cnt[set ^ 1] > 0)
+          tc_wait(&sh.sfull[set ^ 1], static_cast<uint32_t>(io >> 1) & 1, dead, a.err);
       }
-      // the two sets' sums, and whether any row saw a NaN
-      sh.zsum[seg & 1][set][row] = z;
-      bool nan = false;
+      if (max(i0, 0) + nb < n) {
+        const TcUnit me = tc_unit(a, cur, row);
+        if (me.warp_live(quarter))
+          c2 = tc_load_q<D, T>(a,
+                               static_cast<const T*>(a.q) + cur.b * a.q_batch +
+                                   me.t * a.q_token + me.hq * a.q_head,
+                               me.mine, set, sh.qh, sh.scratch, row, quarter);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh.qfull);
+      }
+      if (i0 < 0) {
+        i0 = 0;
+        continue;
+      }
+      // the streams' references and sums, and whether any row saw a NaN
+      sh.ends[set][0][row] = ref;
+      sh.ends[set][1][row] = z;
 #pragma unroll
-      for (int j = 0; j < D / 64; ++j) nan |= nanc[j] != 0;
-      const int iz = i0 + nb - 1;
-      tc_wait(&sh.pvdone[iz & 1], static_cast<uint32_t>(iz >> 1) & 1, dead, a.err);
+      for (int q = 0; q < 2; ++q) {
+        const int iz = i0 + nb - 1 - ((i0 + nb - 1 + q) & 1);
+        if (cnt[q] > 0)
+          tc_wait(&sh.pvdone[q], static_cast<uint32_t>(iz >> 1) & 1, dead, a.err);
+      }
       tc_fence_after();
-      if (named_sync_or(1, kTcSoftmax, nan)) {
+      const int step = kTcRows >> my.cs;  // lanes between a row's copies
+      named_sync(1, kTcSoftmax);
+      uint64_t nanw = 0;  // the row's NaN channels, whichever of its lanes saw them
+      if (sh.nanany)
+        for (int l = row & (step - 1); l < kTcRows; l += step)
+          nanw |= sh.nanrow[D == 128 ? set : 0][l];
+      float f0, f1;  // this copy's factors, of both streams
+      {
+        const int l0 = row & (step - 1);
+        ref = kNegInf;
+        for (int l = l0; l < kTcRows; l += step)
+          ref = fmaxf(ref, fmaxf(sh.ends[0][0][l], sh.ends[1][0][l]));
+        // what saw nothing has z = 0 and O = 0 (or NaN, which stays), or no O
+        // at all (no block)
+        auto factor = [&](float r) { return r == kNegInf ? 1.f : fast_exp2(r - ref); };
+        z = 0.f;
+        for (int l = l0; l < kTcRows; l += step)
+          z += sh.ends[0][1][l] * factor(sh.ends[0][0][l]) +
+               sh.ends[1][1][l] * factor(sh.ends[1][0][l]);
+        f0 = factor(sh.ends[0][0][row]);
+        f1 = factor(sh.ends[1][0][row]);
+      }
+      const int r = row & (step - 1);  // row of the unit
+      const bool any = !(z == 0.f);    // true for NaN
+      const float inv = !whole ? 1.f : any ? 1.f / z : 0.f;
+      const bool writes = my.mine && my.copy == 0;
 #pragma unroll 1
-        for (int j = 0; j < D / 32; ++j) {
-          unsigned w = 0;
+      for (int c = set * (D / 2); c < (set + 1) * (D / 2); c += 8) {
+        float x[8];
+        if (warp_live) {
+          unsigned o0[8], o1[8];
+          __syncwarp();
+          tc_ld8(o0, tm + kO + c);
+          tc_ld8(o1, tm + kO + D + c);
 #pragma unroll
-          for (int q = 0; q < D / 32; ++q)
-            if (q == j) w = static_cast<unsigned>(nanc[q >> 1] >> (32 * (q & 1)));
-          sh.exch[0][set][row] = __uint_as_float(w);
-          named_sync(1, kTcSoftmax);
-          w |= __float_as_uint(sh.exch[0][set ^ 1][row]);
+          for (int j = 0; j < 8; ++j)
+            x[j] = (cnt[0] > 0 ? __uint_as_float(o0[j]) * f0 : 0.f) +
+                   (cnt[1] > 0 ? __uint_as_float(o1[j]) * f1 : 0.f);
+        }
+        if (my.copies > 1) {
+          // the other copies' lanes hand theirs to copy 0
+          float4* const jb = reinterpret_cast<float4*>(sh.join[set][row]);
+          if (my.copy > 0 && my.mine) {
+            jb[0] = make_float4(x[0], x[1], x[2], x[3]);
+            jb[1] = make_float4(x[4], x[5], x[6], x[7]);
+          }
+          named_sync(6 + set, kTcRows);
+          if (writes)
+#pragma unroll 1
+            for (int l = row + step; l < kTcRows; l += step) {
+              const float4* const q = reinterpret_cast<const float4*>(sh.join[set][l]);
+              const float4 u = q[0], v = q[1];
+              x[0] += u.x;
+              x[1] += u.y;
+              x[2] += u.z;
+              x[3] += u.w;
+              x[4] += v.x;
+              x[5] += v.y;
+              x[6] += v.z;
+              x[7] += v.w;
+            }
+          named_sync(6 + set, kTcRows);
+        }
+        if (writes) {
 #pragma unroll
-          for (int q = 0; q < D / 32; ++q)
-            if (q == j) nanc[q >> 1] |= static_cast<uint64_t>(w) << (32 * (q & 1));
-          named_sync(1, kTcSoftmax);
+          for (int j = 0; j < 8; ++j) {
+            x[j] = any || !whole ? x[j] * inv : 0.f;
+            if (nanw >> ((c + j) & 63) & 1) x[j] = __int_as_float(0x7fc00000);
+          }
+          if (whole) {
+            alignas(16) T e[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) e[j] = from_float<T>(x[j]);
+            *reinterpret_cast<uint4*>(static_cast<T*>(a.out) + orow * D + c) =
+                *reinterpret_cast<const uint4*>(e);
+          } else {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) part[(2 + c + j) * kTcRows + r] = x[j];
+          }
         }
       }
-      z = sh.zsum[seg & 1][0][row] + sh.zsum[seg & 1][1][row];
-      float* const part = a.partials + (2ll * cta + (blk0 == 0 ? 1 : 0)) * PF;
-      const bool any = !(z == 0.f);  // true for NaN
-      const float inv = any ? 1.f / z : 0.f;
-      if (warp_live) {
-        const uint64_t nanw = nanc[D == 128 ? set : 0];
-#pragma unroll 1
-        for (int c = set * (D / 2); c < (set + 1) * (D / 2); c += 16) {
-          unsigned x[16];
-          __syncwarp();
-          tc_ld16(x, tm + kO + c);
-          if (nanw != 0) {
-#pragma unroll
-            for (int j = 0; j < 16; ++j)
-              if (nanw >> ((c + j) & 63) & 1) x[j] = 0x7fc00000u;
-          }
-          if (my.mine) {
-            if (whole) {
-              T* op = static_cast<T*>(a.out) + my.out * D + c;
-#pragma unroll
-              for (int j = 0; j < 16; j += 8) {
-                alignas(16) T e[8];
-#pragma unroll
-                for (int q = 0; q < 8; ++q)
-                  e[q] = from_float<T>(any ? __uint_as_float(x[j + q]) * inv : 0.f);
-                *reinterpret_cast<uint4*>(op + j) = *reinterpret_cast<const uint4*>(e);
-              }
-            } else {
-              uint4* pp = reinterpret_cast<uint4*>(part + 2 * kTcRows + row * D + c);
-#pragma unroll
-              for (int j = 0; j < 4; ++j)
-                pp[j] = make_uint4(x[4 * j], x[4 * j + 1], x[4 * j + 2], x[4 * j + 3]);
-            }
-          }
-        }
-        if (my.mine && set == 0) {
-          if (whole) {
-            if (a.lse)
-              a.lse[my.out] = any ? (log2f(z) + ref - kRefShift) * 0.69314718055994531f : kNegInf;
-          } else {
-            part[row] = ref;
-            part[kTcRows + row] = z;
-          }
+      if (writes && set == 0) {
+        if (whole) {
+          if (a.lse)
+            a.lse[orow] = any ? (log2f(z) + ref - kRefShift) * 0.69314718055994531f : kNegInf;
+        } else {
+          part[r] = ref;
+          part[kTcRows + r] = z;
         }
       }
       tc_fence_before();
-      if (!whole) {
-        __threadfence();
+      if (!whole) __threadfence();
+      named_sync(1, kTcSoftmax);  // O, the references and sums have been read
+      if (sh.nanany) {
         named_sync(1, kTcSoftmax);
+        if (set == 0)
+#pragma unroll
+          for (int j = 0; j < D / 64; ++j) sh.nanrow[j][row] = 0;
+        if (tid == 0) sh.nanany = 0;
+        named_sync(1, kTcSoftmax);
+      }
+      if (!whole) {
         if (tid == 0)
           sh.last = atomic_add_acq_rel(&a.tickets[first], 1u) == static_cast<unsigned>(last - first);
         named_sync(1, kTcSoftmax);
         if (sh.last) {
           __threadfence();
-          tc_join<D, T>(a, sh.exch[0][0], first, last, live, tile, req);
+          tc_join<D, T>(a, first, last, my.live, tile, req + head0);
           if (tid == 0) a.tickets[first] = 0u;
         }
         named_sync(1, kTcSoftmax);
@@ -813,6 +977,8 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv_attn_tc_kernel(const KvAttnP
       i0 += nb;
     }
   }
+
+  if (warp == 18) ka_clear_rows<T, D, 32>(a, lane);
 
   tc_fence_before();
   __syncthreads();

@@ -115,7 +115,7 @@ __device__ __forceinline__ float elem16(const Raw16<__half>& r, int i) {
 
 struct KvWriteProblem {
   KvCache c;
-  int B, T, pages;  // pages a request can touch: ceil(T / page_size) + 1
+  int B, T, pages;  // pages a request can touch
   int group;        // threads of one (page, head, side): 32 .. 256
   bool vec;         // 16-byte loads of the new values
   const void *k_new, *v_new;
@@ -137,16 +137,14 @@ __global__ void __launch_bounds__(kKvThreads) kv_write_kernel(const KvWriteProbl
   grid_dependency_wait();
   const int tid = static_cast<int>(threadIdx.x);
   const int GT = a.group, gl = tid & (GT - 1);
-  const long long task = static_cast<long long>(blockIdx.x) * (kKvThreads / GT) + tid / GT;
+  const int task = static_cast<int>(blockIdx.x) * (kKvThreads / GT) + tid / GT;
   const int Hkv = a.c.Hkv, D = a.c.D, P = a.c.page_size;
-  const int h = static_cast<int>(task % Hkv);
-  const int side = static_cast<int>(task / Hkv & 1);
-  const long long bi = task / Hkv / 2;
-  const int i = static_cast<int>(bi % a.pages);
-  const long long b = bi / a.pages;
+  const int b = static_cast<int>(blockIdx.y);
+  const int is = task / Hkv, h = task - is * Hkv;
+  const int side = is & 1, i = is >> 1;
 
   int kept = 0, first = 0, count = 0, page = 0, row0 = 0;
-  bool active = b < a.B;
+  bool active = i < a.pages;
   if (active) {
     const int len = a.kv_len[b];
     const int n = a.num_new ? a.num_new[b] : a.T;
@@ -161,7 +159,7 @@ __global__ void __launch_bounds__(kKvThreads) kv_write_kernel(const KvWriteProbl
       const long long to =
           min(static_cast<long long>(len) + n, (static_cast<long long>(slot) + 1) << a.c.page_shift);
       if (from < to) {
-        page = a.c.page_table[b * a.c.slots + slot];
+        page = a.c.page_table[static_cast<long long>(b) * a.c.slots + slot];
         if (page < 0 || page >= a.c.num_pages) {
           if (h == 0 && side == 0 && gl == 0) record_error(a.err, SV_DERR_PAGE);
         } else {
@@ -252,6 +250,8 @@ __global__ void __launch_bounds__(kKvThreads) kv_write_kernel(const KvWriteProbl
 struct KvReadProblem {
   KvCache c;
   int B, T;
+  int tokens;      // tokens a block takes
+  unsigned magic;  // floor(2^32 / (Hkv D / 16)) + 1
   bool vec;
   void *k_out, *v_out;
   long long batch, token, head;
@@ -282,77 +282,76 @@ template <class T>
 __global__ void __launch_bounds__(kKvThreads) kv_read_kernel(const KvReadProblem a) {
   grid_dependency_wait();
   const int Hkv = a.c.Hkv, D = a.c.D, P = a.c.page_size;
-  const int parts = D / 16;
-  const long long total = static_cast<long long>(a.B) * a.T * Hkv * parts;
-  const long long at0 =
-      static_cast<long long>(blockIdx.x) * (kKvThreads * kKvReadChunks) + threadIdx.x;
-  const int side = static_cast<int>(blockIdx.y);
-  const unsigned char* base = side ? a.c.v : a.c.k;
-  const float* scales = side ? a.c.v_scale : a.c.k_scale;
-  T* out = static_cast<T*>(side ? a.v_out : a.k_out);
-  uint4 code[kKvReadChunks];
-  float s[kKvReadChunks];
+  const int pshift = D == 64 ? 2 : 3, parts = 1 << pshift;  // chunks of a token and head
+  const int per = Hkv << pshift;                            // of a token
+  const int b = static_cast<int>(blockIdx.y);
+  const int t0 = static_cast<int>(blockIdx.x) * a.tokens;
+  const int chunks = min(a.tokens, a.T - t0) * per;
+  const int side = static_cast<int>(blockIdx.z);
+  const unsigned char* const base = side ? a.c.v : a.c.k;
+  const float* const scales = side ? a.c.v_scale : a.c.k_scale;
+  T* const out = static_cast<T*>(side ? a.v_out : a.k_out) + b * a.batch;
+  const int n = a.num ? a.num[b] : a.T;
+  const bool ok = n >= 0 && n <= a.T;
+  if (!ok && blockIdx.x == 0 && side == 0 && threadIdx.x == 0) record_error(a.err, SV_DERR_ARG);
+  const long long start = a.start ? a.start[b] : 0;
+#pragma unroll 1
+  for (int at0 = static_cast<int>(threadIdx.x); at0 < chunks; at0 += kKvThreads * kKvReadChunks) {
+    uint4 code[kKvReadChunks];
+    float s[kKvReadChunks];
+    int th[kKvReadChunks];  // token of the block, and head
 #pragma unroll
-  for (int j = 0; j < kKvReadChunks; ++j) {
-    const long long at = at0 + j * kKvThreads;
-    code[j] = make_uint4(0, 0, 0, 0);
-    s[j] = 0.f;
-    if (at >= total) continue;
-    const int part = static_cast<int>(at) & (parts - 1);
-    const long long th = at / parts;
-    const int h = static_cast<int>(th % Hkv);
-    const long long bt = th / Hkv;
-    const int t = static_cast<int>(bt % a.T);
-    const long long b = bt / a.T;
-    const int n = a.num ? a.num[b] : a.T;
-    const bool report = side == 0 && h == 0 && part == 0;
-    if (n < 0 || n > a.T) {
-      if (report && t == 0) record_error(a.err, SV_DERR_ARG);
-      continue;
+    for (int j = 0; j < kKvReadChunks; ++j) {
+      const int at = at0 + j * kKvThreads;
+      code[j] = make_uint4(0, 0, 0, 0);
+      s[j] = 0.f;
+      // at < 2^32 / per, which makes the product's high word the quotient
+      const int tl = per == 1 ? at : static_cast<int>(__umulhi(static_cast<unsigned>(at), a.magic));
+      const int h = (at - tl * per) >> pshift, part = at & (parts - 1);
+      th[j] = tl << 8 | h;
+      const int t = t0 + tl;
+      if (at >= chunks || !ok || t >= n) continue;
+      const bool report = side == 0 && h == 0 && part == 0;
+      const long long pos =
+          start + (a.rows ? a.rows[static_cast<long long>(b) * a.T + t] : t);
+      if (pos < 0 || pos >= static_cast<long long>(a.c.slots) * P) {
+        if (report) record_error(a.err, SV_DERR_ARG);
+        continue;
+      }
+      const int page =
+          a.c.page_table[static_cast<long long>(b) * a.c.slots + (pos >> a.c.page_shift)];
+      if (page < 0 || page >= a.c.num_pages) {
+        if (report) record_error(a.err, SV_DERR_PAGE);
+        continue;
+      }
+      code[j] = __ldg(reinterpret_cast<const uint4*>(
+          base + page * a.c.page_stride + h * a.c.head_stride + (pos & (P - 1)) * D + part * 16));
+      s[j] = scales[static_cast<long long>(page) * Hkv + h];
     }
-    if (t >= n) continue;
-    const long long pos = static_cast<long long>(a.start ? a.start[b] : 0) +
-                          (a.rows ? a.rows[b * a.T + t] : t);
-    if (pos < 0 || pos >= static_cast<long long>(a.c.slots) * P) {
-      if (report) record_error(a.err, SV_DERR_ARG);
-      continue;
-    }
-    const int page = a.c.page_table[b * a.c.slots + (pos >> a.c.page_shift)];
-    if (page < 0 || page >= a.c.num_pages) {
-      if (report) record_error(a.err, SV_DERR_PAGE);
-      continue;
-    }
-    code[j] = *reinterpret_cast<const uint4*>(base + page * a.c.page_stride +
-                                              h * a.c.head_stride +
-                                              (pos & (P - 1)) * D + part * 16);
-    s[j] = scales[static_cast<long long>(page) * Hkv + h];
-  }
 #pragma unroll
-  for (int j = 0; j < kKvReadChunks; ++j) {
-    const long long at = at0 + j * kKvThreads;
-    if (at >= total) continue;
-    const int part = static_cast<int>(at) & (parts - 1);
-    const long long th = at / parts;
-    const int h = static_cast<int>(th % Hkv);
-    const long long bt = th / Hkv;
-    T* p = out + bt / a.T * a.batch + bt % a.T * a.token + h * a.head + part * 16;
-    Raw16<T> y;
-    T* e = reinterpret_cast<T*>(y.w);
-    const unsigned* w = reinterpret_cast<const unsigned*>(&code[j]);
+    for (int j = 0; j < kKvReadChunks; ++j) {
+      const int at = at0 + j * kKvThreads;
+      if (at >= chunks) break;
+      T* p = out + (t0 + (th[j] >> 8)) * a.token + (th[j] & 255) * a.head + (at & (parts - 1)) * 16;
+      Raw16<T> y;
+      T* e = reinterpret_cast<T*>(y.w);
+      const unsigned* w = reinterpret_cast<const unsigned*>(&code[j]);
 #pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      const float2 lo = float2_of_half2(half2_lo(w[q])), hi = float2_of_half2(half2_hi(w[q]));
-      e[4 * q] = from_float<T>(lo.x * s[j]);
-      e[4 * q + 1] = from_float<T>(lo.y * s[j]);
-      e[4 * q + 2] = from_float<T>(hi.x * s[j]);
-      e[4 * q + 3] = from_float<T>(hi.y * s[j]);
-    }
-    if (a.vec) {
+      for (int q = 0; q < 4; ++q) {
+        const float2 lo = float2_of_half2(half2_lo(w[q])), hi = float2_of_half2(half2_hi(w[q]));
+        e[4 * q] = from_float<T>(lo.x * s[j]);
+        e[4 * q + 1] = from_float<T>(lo.y * s[j]);
+        e[4 * q + 2] = from_float<T>(hi.x * s[j]);
+        e[4 * q + 3] = from_float<T>(hi.y * s[j]);
+      }
+      if (a.vec) {
 #pragma unroll
-      for (int q = 0; q < static_cast<int>(sizeof(T)); ++q) reinterpret_cast<uint4*>(p)[q] = y.w[q];
-    } else {
+        for (int q = 0; q < static_cast<int>(sizeof(T)); ++q)
+          __stcs(reinterpret_cast<uint4*>(p) + q, y.w[q]);
+      } else {
 #pragma unroll
-      for (int q = 0; q < 16; ++q) p[q] = e[q];
+        for (int q = 0; q < 16; ++q) p[q] = e[q];
+      }
     }
   }
 }

@@ -202,15 +202,21 @@ def test_division_of_work(seed):
     first CTA's alone.  The integer expressions are the kernel's."""
     rng = np.random.default_rng(seed)
     units = rng.integers(1, rng.choice([2, 5, 80, 700]), rng.integers(1, 300))
-    total, grid, least = int(units.sum()), int(rng.integers(1, 305)), 4
+    total, grid, least = int(units.sum()), int(rng.integers(1, 305)), int(rng.choice([2, 4]))
     parts = max(1, min(grid, total // least))
-    bound = [total * c // parts for c in range(parts + 1)]
+    per = total // parts
+    more = total - per * parts
+    bound = [c * per + min(c, more) for c in range(parts + 1)]
+
+    def part_of(x):
+        cut = more * (per + 1)
+        return x // (per + 1) if x < cut else more + (x - cut) // per
+
     held, tickets, slots = np.zeros(total, int), {}, set()
     starts = np.concatenate([[0], np.cumsum(units)])
     for u, n in enumerate(units):
         u0 = int(starts[u])
-        first = ((u0 + 1) * parts - 1) // total
-        last = ((u0 + int(n)) * parts - 1) // total
+        first, last = part_of(u0), part_of(u0 + int(n) - 1)
         assert bound[first] <= u0 < bound[first + 1]
         assert bound[last] <= u0 + n - 1 < bound[last + 1]
         if first == last:
@@ -225,4 +231,28 @@ def test_division_of_work(seed):
     for c in range(parts):
         assert bound[c] < bound[c + 1]
         held[bound[c]:bound[c + 1]] += 1
-    assert (held == 1).all()
+    assert bound[-1] == total and (held == 1).all()
+
+
+def test_rows_divide_by_the_group():
+    """A row's round token is the high word of row * (floor(2^32 / G) + 1),
+    for every group and every row a call can have."""
+    for G in range(2, 257):
+        magic = 2 ** 32 // G + 1
+        rows = np.unique(np.concatenate([np.arange(0, 3000), 65536 * G - 1 - np.arange(0, 3000),
+                                         G * np.random.default_rng(G).integers(0, 65536, 3000)
+                                         - 1 + np.array([[0], [1]])], axis=None))
+        rows = rows[(rows >= 0) & (rows < 65536 * G)].astype(np.uint64)
+        assert (rows < 2 ** 24).all() and ((rows * np.uint64(magic)) >> np.uint64(32)
+                                           == rows // np.uint64(G)).all(), G
+
+
+def test_chunks_divide_by_a_tokens_chunks():
+    """The read kernel's division of a block's chunk index (below 1024 + one
+    token's chunks) by the chunks of a token."""
+    for heads in range(1, 257):
+        for d in (4, 8):
+            per = heads * d
+            at = np.arange(0, max(1, 1024 // per) * per + 1024, dtype=np.uint64)
+            magic = 2 ** 32 // per + 1
+            assert ((at * np.uint64(magic)) >> np.uint64(32) == at // np.uint64(per)).all()
