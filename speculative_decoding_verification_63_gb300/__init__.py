@@ -34,9 +34,10 @@ def workspace(nbytes: int, device=None, key=None) -> torch.Tensor:
     """A zeroed, 256-byte aligned device workspace of at least nbytes,
     cached per (device, key).  Calls sharing one workspace must not overlap
     on the GPU."""
-    device = torch.device(device if device is not None else "cuda")
-    if device.index is None:
-        device = torch.device("cuda", torch.cuda.current_device())
+    if not isinstance(device, torch.device) or device.index is None:
+        device = torch.device(device if device is not None else "cuda")
+        if device.index is None:
+            device = torch.device("cuda", torch.cuda.current_device())
     k = (device, key)
     with _ws_lock:
         buf = _ws_cache.get(k)
@@ -182,10 +183,10 @@ def kv_read(cache: dict, page_table, start, num, T: int, rows=None, dtype=torch.
     """Read tokens back as values: row t < num[b] is position start[b] + t, or
     start[b] + rows[b][t]; later rows are zero.  Returns k and v
     [B][T][heads][D] (device tensors)."""
-    pages, H, P, D = cache["k"].shape
-    B, dev = page_table.shape[0], page_table.device
-    out = dict(k=torch.empty((B, T, H, D), dtype=dtype, device=dev),
-               v=torch.empty((B, T, H, D), dtype=dtype, device=dev))
+    _, H, _, D = cache["k"].shape
+    dev = page_table.device
+    k, v = torch.empty((2, page_table.shape[0], T, H, D), dtype=dtype, device=dev).unbind()
+    out = dict(k=k, v=v)
     if ws is None:
         ws = workspace(SV_MIN_WORKSPACE_BYTES, dev, "kv")
     sv_kv_read(cache, page_table, start, num, out["k"], out["v"], ws, rows=rows)
@@ -201,7 +202,7 @@ def kv_attention(q, cache: dict, page_table, kv_len, num_new=None, mask=None,
     [B][T][words] (tree_mask).  scale defaults to 1 / sqrt(D).  Returns out
     [B][T][heads][D] and, when with_lse, lse [B][T][heads] (device tensors)."""
     B, T, Hq, D = q.shape
-    out = dict(out=torch.empty((B, T, Hq, D), dtype=q.dtype, device=q.device))
+    out = dict(out=torch.empty_like(q, memory_format=torch.contiguous_format))
     if with_lse:
         out["lse"] = torch.empty((B, T, Hq), dtype=torch.float32, device=q.device)
     if ws is None:

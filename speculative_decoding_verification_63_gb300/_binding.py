@@ -9,6 +9,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 
 import torch
 
@@ -141,9 +142,8 @@ def lib(path: str | None = None):
     h.sv_tree_mask.restype = ctypes.c_int
     h.sv_row_stats.argtypes = [ctypes.POINTER(SvChainArgs), _P, _P, _P, ctypes.c_size_t, _P]
     h.sv_row_stats.restype = ctypes.c_int
-    for f, args in [("sv_kv_write", SvKvWriteArgs), ("sv_kv_read", SvKvReadArgs),
-                    ("sv_kv_attention", SvKvAttentionArgs)]:
-        getattr(h, f).argtypes = [ctypes.POINTER(args), _P, ctypes.c_size_t, _P]
+    for f in ("sv_kv_write", "sv_kv_read", "sv_kv_attention"):
+        getattr(h, f).argtypes = [_P, _P, ctypes.c_size_t, _P]  # the arguments come packed
         getattr(h, f).restype = ctypes.c_int
     h.sv_kv_attention_workspace_bytes.argtypes = [_i32, _i32, _i32, _i32, _i32]
     h.sv_kv_attention_workspace_bytes.restype = ctypes.c_size_t
@@ -438,91 +438,129 @@ def sv_row_stats(target_logits, draft_logits, temperature, alpha, expected, work
 
 
 # ------------------------------------------------- 8-bit key/value cache
+#
+# These calls are made once a layer and round, so their marshalling counts:
+# the arguments are packed in one go (struct.pack in the C layout of the
+# ctypes structures above), and each tensor's facts are read once.
 
 _KV_DTYPES = {torch.bfloat16: SV_BF16, torch.float32: SV_FP32, torch.float16: SV_FP16}
+_PACK_CODES = {_i32: "i", _i64: "q", _P: "P", ctypes.c_float: "f"}
 
 
-def _kv_cache(c: SvKvCache, cache: dict, page_table, B: int) -> None:
-    """Fill an sv_kv_cache from the cache's tensors (k, v [pages][Hkv][P][D]
-    e4m3, k_scale, v_scale [pages][Hkv] fp32) and the page table [B][slots]."""
-    k, v, ks, vs = cache["k"], cache["v"], cache["k_scale"], cache["v_scale"]
-    if k.dtype != torch.float8_e4m3fn or k.dim() != 4:
+def _packer(cls) -> struct.Struct:
+    """struct.Struct of a ctypes structure (an embedded one ends on its own
+    alignment)."""
+    def fmt(c):
+        return "".join(fmt(t) + "0q" if issubclass(t, ctypes.Structure) else _PACK_CODES[t]
+                       for _, t in c._fields_)
+    packer = struct.Struct("@" + fmt(cls) + "0q")
+    assert packer.size == ctypes.sizeof(cls)
+    return packer
+
+
+_pack_write, _pack_read = _packer(SvKvWriteArgs).pack, _packer(SvKvReadArgs).pack
+_pack_attention = _packer(SvKvAttentionArgs).pack
+
+
+def _addr(t, dtype, shape, what: str) -> int:
+    """Address of a contiguous device tensor of the given type and shape (0
+    for None)."""
+    if t is None:
+        return 0
+    if t.dtype != dtype or t.shape != shape or not t.is_contiguous():
+        raise ValueError(f"{what}: expected contiguous {dtype} {tuple(shape)}, "
+                         f"got {t.dtype} {tuple(t.shape)}")
+    if not t.is_cuda:
+        raise ValueError("libspecverify takes device tensors")
+    return t.data_ptr()
+
+
+def _kv_cache(cache: dict, page_table, B: int) -> tuple:
+    """The fields of an sv_kv_cache, from the cache's tensors (k, v
+    [pages][Hkv][P][D] e4m3, k_scale, v_scale [pages][Hkv] fp32) and the page
+    table [B][slots]."""
+    k, v = cache["k"], cache["v"]
+    shape, st = k.shape, k.stride()
+    if k.dtype != torch.float8_e4m3fn or len(shape) != 4:
         raise ValueError(f"cache k: expected float8_e4m3fn [pages][heads][page][D], got {k.dtype} "
-                         f"{tuple(k.shape)}")
-    pages, H, P, D = k.shape
-    st = k.stride()
-    if v.dtype != k.dtype or v.shape != k.shape or v.stride() != st:
+                         f"{tuple(shape)}")
+    pages, H, P, D = shape
+    if v.dtype != k.dtype or v.shape != shape or v.stride() != st:
         raise ValueError("cache v: expected k's dtype, shape and strides")
     if st[3] != 1 or st[2] != D:
         raise ValueError("cache: the tokens of a page and head must be contiguous")
-    _check(ks, torch.float32, (pages, H), "k_scale")
-    _check(vs, torch.float32, (pages, H), "v_scale")
-    if page_table.dtype != torch.int32 or page_table.dim() != 2 or page_table.shape[0] != B \
-            or not page_table.is_contiguous():
+    ks = _addr(cache["k_scale"], torch.float32, (pages, H), "k_scale")
+    vs = _addr(cache["v_scale"], torch.float32, (pages, H), "v_scale")
+    if page_table.dim() != 2:
         raise ValueError(f"page_table: expected contiguous int32 [{B}][slots]")
-    c.num_pages, c.page_size, c.Hkv, c.D = pages, P, H, D
-    c.k, c.v = _ptr(k), _ptr(v)
-    c.page_stride = st[0] if pages > 1 else 0
-    c.head_stride = st[1] if H > 1 else P * D
-    c.k_scale, c.v_scale, c.page_table = _ptr(ks), _ptr(vs), _ptr(page_table)
-    c.slots = page_table.shape[1]
+    slots = page_table.shape[1]
+    table = _addr(page_table, torch.int32, (B, slots), "page_table")
+    if not (k.is_cuda and v.is_cuda):
+        raise ValueError("libspecverify takes device tensors")
+    return (pages, P, H, D, k.data_ptr(), v.data_ptr(), st[0] if pages > 1 else 0,
+            st[1] if H > 1 else P * D, ks, vs, table, slots)
 
 
-def _rows4(t, shape, what: str):
-    """The (batch, token, head) strides of a [B][T][heads][D] tensor with
-    contiguous D."""
-    if tuple(t.shape) != shape or t.stride(3) != 1:
-        raise ValueError(f"{what}: expected {shape} with contiguous rows, got {tuple(t.shape)}")
+def _rows4(t, shape, what: str) -> tuple:
+    """(address, batch, token and head stride) of a [B][T][heads][D] tensor
+    with contiguous D."""
+    st = t.stride()
+    if t.shape != shape or st[3] != 1:
+        raise ValueError(f"{what}: expected {tuple(shape)} with contiguous rows, got "
+                         f"{tuple(t.shape)}")
     if t.dtype not in _KV_DTYPES:
         raise ValueError(f"{what}: expected bfloat16, float16 or float32, got {t.dtype}")
-    return t.stride()[:3]
+    if not t.is_cuda:
+        raise ValueError("libspecverify takes device tensors")
+    return t.data_ptr(), st[0], st[1], st[2]
+
+
+def _kv_call(name: str, packed: bytes, workspace, stream) -> None:
+    if not workspace.is_cuda:
+        raise ValueError("libspecverify takes device tensors")
+    if stream is None:
+        # the current stream's handle, without a Stream object around it
+        stream = torch._C._cuda_getCurrentRawStream(workspace.get_device())
+    elif hasattr(stream, "cuda_stream"):
+        stream = stream.cuda_stream
+    st = getattr(_lib_handle or lib(), name)(packed, workspace.data_ptr(), workspace.nbytes, stream)
+    if st != SV_OK:
+        raise SpecVerifyError(st, name)
 
 
 def sv_kv_write(cache: dict, page_table, kv_len, k_new, v_new, workspace, num_new=None,
                 stream=None) -> None:
     """Enqueue sv_kv_write: quantise k_new, v_new [B][T][Hkv][D] into the
     cache at positions kv_len[b] .. of each request."""
-    B, T, H, D = k_new.shape
-    a = SvKvWriteArgs()
-    _kv_cache(a.cache, cache, page_table, B)
-    shape = (B, T, a.cache.Hkv, a.cache.D)
-    a.k_batch_stride, a.k_token_stride, a.k_head_stride = _rows4(k_new, shape, "k_new")
-    a.v_batch_stride, a.v_token_stride, a.v_head_stride = _rows4(v_new, shape, "v_new")
+    B, T = k_new.shape[:2]
+    c = _kv_cache(cache, page_table, B)
+    shape = (B, T, c[2], c[3])
+    k, *k_strides = _rows4(k_new, shape, "k_new")
+    v, *v_strides = _rows4(v_new, shape, "v_new")
     if v_new.dtype != k_new.dtype:
         raise ValueError("v_new: expected k_new's dtype")
-    _check(kv_len, torch.int32, (B,), "kv_len")
-    _check(num_new, torch.int32, (B,), "num_new")
-    a.B, a.T, a.dtype = B, T, _KV_DTYPES[k_new.dtype]
-    a.k_new, a.v_new = _ptr(k_new), _ptr(v_new)
-    a.kv_len, a.num_new = _ptr(kv_len), _ptr(num_new)
-    st = lib().sv_kv_write(ctypes.byref(a), _ptr(workspace),
-                           workspace.numel() * workspace.element_size(), _stream(stream))
-    if st != SV_OK:
-        raise SpecVerifyError(st, "sv_kv_write")
+    length = _addr(kv_len, torch.int32, (B,), "kv_len")
+    num = _addr(num_new, torch.int32, (B,), "num_new")
+    _kv_call("sv_kv_write", _pack_write(*c, B, T, _KV_DTYPES[k_new.dtype], k, v, *k_strides,
+                                        *v_strides, length, num), workspace, stream)
 
 
 def sv_kv_read(cache: dict, page_table, start, num, k_out, v_out, workspace, rows=None,
                stream=None) -> None:
     """Enqueue sv_kv_read: the values at positions start[b] + t, or start[b]
     + rows[b][t], into k_out, v_out [B][T][Hkv][D] (rows t >= num[b] zero)."""
-    B, T, H, D = k_out.shape
-    a = SvKvReadArgs()
-    _kv_cache(a.cache, cache, page_table, B)
-    shape = (B, T, a.cache.Hkv, a.cache.D)
-    strides = _rows4(k_out, shape, "k_out")
-    if _rows4(v_out, shape, "v_out") != strides or v_out.dtype != k_out.dtype:
+    B, T = k_out.shape[:2]
+    c = _kv_cache(cache, page_table, B)
+    shape = (B, T, c[2], c[3])
+    k, *strides = _rows4(k_out, shape, "k_out")
+    v, *v_strides = _rows4(v_out, shape, "v_out")
+    if v_strides != strides or v_out.dtype != k_out.dtype:
         raise ValueError("v_out: expected k_out's dtype and strides")
-    a.out_batch_stride, a.out_token_stride, a.out_head_stride = strides
-    _check(start, torch.int32, (B,), "start")
-    _check(num, torch.int32, (B,), "num")
-    _check(rows, torch.int32, (B, T), "rows")
-    a.B, a.T, a.dtype = B, T, _KV_DTYPES[k_out.dtype]
-    a.k_out, a.v_out = _ptr(k_out), _ptr(v_out)
-    a.start, a.num, a.rows = _ptr(start), _ptr(num), _ptr(rows)
-    st = lib().sv_kv_read(ctypes.byref(a), _ptr(workspace),
-                          workspace.numel() * workspace.element_size(), _stream(stream))
-    if st != SV_OK:
-        raise SpecVerifyError(st, "sv_kv_read")
+    first = _addr(start, torch.int32, (B,), "start")
+    count = _addr(num, torch.int32, (B,), "num")
+    which = _addr(rows, torch.int32, (B, T), "rows")
+    _kv_call("sv_kv_read", _pack_read(*c, B, T, _KV_DTYPES[k_out.dtype], k, v, *strides, first,
+                                      count, which), workspace, stream)
 
 
 def sv_kv_attention_workspace_bytes(B: int, T: int, Hq: int, Hkv: int, D: int) -> int:
@@ -533,26 +571,23 @@ def sv_kv_attention(q, cache: dict, page_table, kv_len, out, workspace, scale: f
                     num_new=None, mask=None, lse=None, stream=None) -> None:
     """Enqueue sv_kv_attention: q [B][T][Hq][D] over the cache into out (the
     same shape, contiguous) and, optionally, lse [B][T][Hq] fp32."""
-    B, T, Hq, D = q.shape
-    a = SvKvAttentionArgs()
-    _kv_cache(a.cache, cache, page_table, B)
-    if D != a.cache.D or q.dtype == torch.float32:
-        raise ValueError(f"q: expected bfloat16 or float16 [B][T][Hq][{a.cache.D}], got {q.dtype} "
-                         f"{tuple(q.shape)}")
-    a.q_batch_stride, a.q_token_stride, a.q_head_stride = _rows4(q, (B, T, Hq, D), "q")
-    _check(out, q.dtype, (B, T, Hq, D), "out")
-    _check(lse, torch.float32, (B, T, Hq), "lse")
-    _check(kv_len, torch.int32, (B,), "kv_len")
-    _check(num_new, torch.int32, (B,), "num_new")
+    shape = q.shape
+    B, T, Hq, D = shape
+    c = _kv_cache(cache, page_table, B)
+    if D != c[3] or q.dtype == torch.float32:
+        raise ValueError(f"q: expected bfloat16 or float16 [B][T][Hq][{c[3]}], got {q.dtype} "
+                         f"{tuple(shape)}")
+    qp, *strides = _rows4(q, shape, "q")
+    o = _addr(out, q.dtype, shape, "out")
+    ls = _addr(lse, torch.float32, (B, T, Hq), "lse")
+    length = _addr(kv_len, torch.int32, (B,), "kv_len")
+    num = _addr(num_new, torch.int32, (B,), "num_new")
+    words = 0
     if mask is not None:
         if mask.dim() != 3:
             raise ValueError("mask: expected [B][T][words]")
-        _check(mask, torch.int32, (B, T, mask.shape[2]), "mask")
-        a.mask, a.words = _ptr(mask), mask.shape[2]
-    a.B, a.T, a.Hq, a.dtype = B, T, Hq, _KV_DTYPES[q.dtype]
-    a.q, a.out, a.lse = _ptr(q), _ptr(out), _ptr(lse)
-    a.kv_len, a.num_new, a.scale = _ptr(kv_len), _ptr(num_new), scale
-    st = lib().sv_kv_attention(ctypes.byref(a), _ptr(workspace),
-                               workspace.numel() * workspace.element_size(), _stream(stream))
-    if st != SV_OK:
-        raise SpecVerifyError(st, "sv_kv_attention")
+        words = mask.shape[2]
+    m = _addr(mask, torch.int32, (B, T, words), "mask")
+    _kv_call("sv_kv_attention", _pack_attention(*c, B, T, Hq, _KV_DTYPES[q.dtype], qp, *strides,
+                                                o, ls, length, num, m, words, scale),
+             workspace, stream)

@@ -70,7 +70,7 @@ def _args(b, op, cache=None, **kw):
 
 
 def _call(b, op, a, ws=WS, n=BIG):
-    return getattr(b.lib(), "sv_kv_" + op)(ctypes.byref(a), ws, n, None)
+    return getattr(b.lib(), "sv_kv_" + op)(bytes(a), ws, n, None)
 
 
 BAD_CACHES = [dict(num_pages=0), dict(slots=0), dict(Hkv=0), dict(Hkv=257), dict(page_size=8),
@@ -161,6 +161,22 @@ def test_binding_refuses_wrong_tensors(b):
     refused(lambda a: a.update(q=q.float()), "attention")
     refused(lambda a: a.update(q=q[..., :32]), "attention")
     refused(lambda a: a.update(mask=torch.zeros(2, 3, dtype=torch.int32)), "attention")
+
+
+def test_packed_arguments_are_the_structs(b):
+    """The binding's packed arguments have the layout of the C structs."""
+    import struct
+    for cls in (b.SvKvWriteArgs, b.SvKvReadArgs, b.SvKvAttentionArgs):
+        packer = b._packer(cls)
+        flat = []
+        for name, t in cls._fields_:
+            flat += [(name, f, u) for f, u in t._fields_] if issubclass(t, ctypes.Structure) \
+                else [(None, name, t)]
+        values = [0.25 * i if t is ctypes.c_float else 1000 + i for i, (_, _, t) in enumerate(flat)]
+        a = cls.from_buffer_copy(packer.pack(*values))
+        for (outer, name, _), want in zip(flat, values):
+            assert getattr(getattr(a, outer) if outer else a, name) == want, name
+        assert isinstance(packer, struct.Struct)
 
 
 # ------------------------------------------------ the plain implementation
