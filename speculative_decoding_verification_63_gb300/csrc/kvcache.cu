@@ -114,16 +114,13 @@ sv_status launch(void (*kernel)(P), const P& p, dim3 grid, int threads, size_t s
   return e == cudaSuccess ? SV_OK : SV_ECUDA;
 }
 
-template <int D, class T>
-sv_status launch_attention(const KvAttnProblem& p, int sms, cudaStream_t stream) {
-  constexpr size_t smem = sizeof(KaShared<D>);
-  static_assert(kKaCtasPerSm * (smem + 1024) <= 228 * 1024, "kKaCtasPerSm CTAs fit an SM");
-  if (cudaFuncSetAttribute(kv_attn_kernel<D, T>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+sv_status launch_warps(void (*kernel)(KvAttnProblem), size_t smem, const KvAttnProblem& p, int sms,
+                       cudaStream_t stream) {
+  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                            static_cast<int>(smem)) != cudaSuccess)
     return SV_ECUDA;
   const int grid = std::min(kKaCtasPerSm * sms, kKaMaxCtas);
-  return launch(kv_attn_kernel<D, T>, p, dim3(static_cast<unsigned>(grid)), kKaThreads, smem,
-                stream);
+  return launch(kernel, p, dim3(static_cast<unsigned>(grid)), kKaThreads, smem, stream);
 }
 
 template <int D, class T>
@@ -139,15 +136,19 @@ sv_status launch_attention_tc(const KvAttnProblem& p, int sms, cudaStream_t stre
 }
 
 // Rounds of up to kKaFewRows query rows a key/value head take the warp-level
-// products, larger ones the tensor-memory ones.  A chain round of 28 rows (64
-// requests, 4096 tokens): 117 us against 194 us; a tree of 128 rows: 372 us
-// against 174 us.
+// products (each tile of 16 rows reads the cache: the second time from L2),
+// larger ones the tensor-memory ones.  A chain round of 28 rows (64 requests,
+// up to 4096 tokens): 92 us against 153 us; a tree of 128 rows: 372 us against
+// 104 us.
 constexpr int kKaFewRows = 32;
 
 template <int D, class T>
 sv_status run_attention(const KvAttnProblem& p, int sms, cudaStream_t stream) {
-  return p.T * p.G <= kKaFewRows ? launch_attention<D, T>(p, sms, stream)
-                              : launch_attention_tc<D, T>(p, sms, stream);
+  static_assert(kKaCtasPerSm * (sizeof(KaShared<D>) + 1024) <= 228 * 1024,
+                "kKaCtasPerSm CTAs fit an SM");
+  return p.T * p.G <= kKaFewRows
+             ? launch_warps(kv_attn_kernel<D, T>, sizeof(KaShared<D>), p, sms, stream)
+             : launch_attention_tc<D, T>(p, sms, stream);
 }
 
 // Strides of 16-byte accesses to rows of elements of `es` bytes.
@@ -276,9 +277,10 @@ size_t sv_kv_attention_workspace_bytes(int32_t B, int32_t T, int32_t Hq, int32_t
   if (B < 0 || B > SV_MAX_B || T < 1 || T > SV_MAX_KV_T || Hkv < 1 || Hq < Hkv ||
       Hq > SV_MAX_KV_HEADS || Hq % Hkv != 0 || (D != 64 && D != 128))
     return 0;
-  const size_t few = 2 * kKaMaxCtas * (D == 64 ? kKaPartialFloats<64> : kKaPartialFloats<128>);
-  const size_t many = 2 * kTcMaxCtas * (D == 64 ? kTcPartialFloats<64> : kTcPartialFloats<128>);
-  return kPartialsAt + sizeof(float) * (T * (Hq / Hkv) <= kKaFewRows ? few : many);
+  const size_t few = kKaMaxCtas * (D == 64 ? kKaPartialFloats<64> : kKaPartialFloats<128>);
+  const size_t many = kTcMaxCtas * (D == 64 ? kTcPartialFloats<64> : kTcPartialFloats<128>);
+  const bool is_few = static_cast<int64_t>(T) * (Hq / Hkv) <= kKaFewRows;
+  return kPartialsAt + sizeof(float) * 2 * (is_few ? few : many);  // two parts a CTA
 }
 
 sv_status sv_kv_attention(const sv_kv_attention_args* a, void* workspace, size_t ws_bytes,

@@ -15,8 +15,10 @@
 // The reference follows the running maximum only when that has risen more
 // than kRefSlack above it, so the rescaling of O is rare; the weights are
 // shifted up by kRefShift, which keeps them within the halves' range
-// (2^(kRefShift + kRefSlack) = 2^15) and moves the halves' underflow to
-// 2^-32 of the reference.
+// (2^(kRefShift + kRefSlack) = 2^15): below 2^-18 of the reference they are
+// off by up to 2^-29 of it instead, which 2^17 positions together turn into
+// 2^-12.  (With scores of deviation 2.8 a warp of 32 rows rescales in one of
+// 25 blocks; with a slack of 7, in one of 6.)
 //
 // Work.  A unit is 16 query rows (round tokens x heads of one group) of one
 // request and key/value head; its blocks are 64 positions each.  The blocks
@@ -33,13 +35,13 @@ namespace sv {
 
 constexpr int kKaRows = 16;           // query rows of a unit: one m16 tile
 constexpr int kKaBlock = 64;          // positions of a block
-constexpr int kKaStages = 5;
+constexpr int kKaStages = 4;
 constexpr int kKaWarps = 4;           // consumer warps
 constexpr int kKaThreads = kKaWarps * 32 + 32;
 constexpr int kKaCtasPerSm = 2;
 constexpr int kKaMaxCtas = 2 * 160;   // tickets and partials are sized for this many
 constexpr int kKaMinBlocks = 4;       // blocks below which a CTA is not worth starting
-constexpr float kRefShift = 8.f, kRefSlack = 7.f;
+constexpr float kRefShift = 4.f, kRefSlack = 11.f;
 
 struct KvAttnProblem {
   KvCache c;
@@ -234,12 +236,13 @@ struct KaParts {
 
 // What the producer warp knows of the blocks ahead.  A block's page ids hang
 // on the page table, its scales on the page ids: two round trips to memory.
-// Each lane owns 16 positions, keys or values, of one block of a batch of
-// NB = 32 / (BLOCK / 8) blocks, and the two lookups run two and one
-// batches ahead of the copies, so neither is waited for.
-template <int ROWS, int BLOCK>
+// Each lane owns 16 positions, keys or values, of one block of a batch of NB
+// blocks, and the two lookups run two and one batches ahead of the copies, so
+// neither is waited for.  SIDES: 2 if the warp copies keys and values, 1 if
+// only one of them.
+template <int ROWS, int BLOCK, int SIDES>
 struct KaFeed {
-  static constexpr int kCopies = BLOCK / 8, NB = 32 / kCopies;
+  static constexpr int kCopies = BLOCK / 16 * SIDES, NB = 32 / kCopies;
   KaCursor<ROWS, BLOCK> cur;  // the lane's block, two batches ahead
   int left;                   // blocks from there to the end of the CTA's part
   int sub, page;              // 16-position piece; its page (-2: none)
@@ -247,7 +250,7 @@ struct KaFeed {
   struct Item {
     const unsigned char* src;  // null: nothing to copy
     int bytes;
-    float scale;               // < 0: no such page
+    float scale, v_scale;      // of the lane's side, of the values; < 0: no such page
     int first, tokens, round;  // the block begins a segment; its place
     int b, head, tile, rows;   // its unit; rows of the request
   };
@@ -283,7 +286,7 @@ struct KaFeed {
     Item it;
     it.src = nullptr;
     it.bytes = 0;
-    it.scale = -1.f;
+    it.scale = it.v_scale = -1.f;
     it.first = a_first;
     it.tokens = a_tokens;
     it.round = a_round;
@@ -299,8 +302,9 @@ struct KaFeed {
       if ((a_pos & (run - 1)) == 0)
         it.src = (is_v ? a.c.v : a.c.k) + page * a.c.page_stride + a_head * a.c.head_stride +
                (a_pos & (a.c.page_size - 1)) * a.c.D;
-      it.scale =
-          (is_v ? a.c.v_scale : a.c.k_scale)[static_cast<long long>(page) * a.c.Hkv + a_head];
+      const long long at = static_cast<long long>(page) * a.c.Hkv + a_head;
+      it.scale = (is_v ? a.c.v_scale : a.c.k_scale)[at];
+      if (SIDES == 1) it.v_scale = a.c.v_scale[at];
     } else if (page != -2) {
       record_error(a.err, SV_DERR_PAGE);
     }
@@ -308,11 +312,11 @@ struct KaFeed {
   }
   // positions the lane at its block of the first batch; look() comes next
   __device__ __forceinline__ void start(const KvAttnProblem& a, const int* prefix, int w0, int n,
-                                        int lane) {
+                                        int lane, bool v = false) {
     cur.seek(a, prefix, w0);
     left = n;
-    sub = lane % (kCopies / 2);
-    is_v = lane % kCopies >= kCopies / 2;
+    sub = lane % (BLOCK / 16);
+    is_v = SIDES == 1 ? v : lane % kCopies >= BLOCK / 16;
     page = -2;
     advance(a, lane / kCopies);
   }
@@ -435,6 +439,45 @@ __device__ __forceinline__ float2 ka_two(const __nv_bfloat16* p) {
   return make_float2(__bfloat162float(p[0]), __bfloat162float(p[1]));
 }
 
+// The producer warp: n blocks from w0 on, through the ring of stages.
+template <int D, class Feed, class Shared>
+__device__ __forceinline__ void ka_produce(const KvAttnProblem& a, Shared& sh, int w0, int n,
+                                           int lane) {
+  const uint64_t pol = policy_evict_first();
+  Feed feed;
+  feed.start(a, sh.prefix, w0, n, lane);
+  typename Feed::Item item = {}, next = {};
+  int i = 0;
+#pragma unroll 1
+  for (int i0 = -2 * Feed::NB; i0 < n; i0 += Feed::NB) {
+    item = next;
+    next = feed.resolve(a);
+    feed.look(a, i0 < -Feed::NB);
+    if (i0 < 0) continue;
+    for (int j = 0; j < Feed::NB && i < n; ++j, ++i) {
+      const int s = i % kKaStages;
+      if (i >= kKaStages)
+        ka_wait(&sh.empty[s], static_cast<uint32_t>(i / kKaStages - 1) & 1, &sh.dead, a.err);
+      __syncwarp();
+      if (lane / Feed::kCopies == j) {
+        if (item.src != nullptr && !*static_cast<volatile int*>(&sh.dead)) {
+          mbar_expect_tx(&sh.full[s], item.bytes);
+          bulk_copy_g2s_hint((feed.is_v ? sh.v[s] : sh.k[s]) + feed.sub * 16 * D, item.src,
+                             item.bytes, &sh.full[s], pol);
+        }
+        (feed.is_v ? sh.v_scale[s] : sh.k_scale[s])[feed.sub] = item.scale;
+        mbar_arrive(&sh.full[s]);
+      }
+      __syncwarp();
+    }
+  }
+  // copies of the last stages must land before the block ends
+  for (int j = max(0, n - kKaStages); j < n; ++j)
+    if (!mbar_wait_bounded(&sh.full[j % kKaStages], static_cast<uint32_t>(j / kKaStages) & 1,
+                           1000000000ull))
+      record_error(a.err, SV_DERR_TIMEOUT);
+}
+
 template <int D, class T>
 __global__ void __launch_bounds__(kKaThreads, kKaCtasPerSm) kv_attn_kernel(const KvAttnProblem a) {
   extern __shared__ __align__(128) unsigned char ka_smem[];
@@ -443,7 +486,7 @@ __global__ void __launch_bounds__(kKaThreads, kKaCtasPerSm) kv_attn_kernel(const
   const int grid = static_cast<int>(gridDim.x), cta = static_cast<int>(blockIdx.x);
   if (tid == 0) {
     for (int s = 0; s < kKaStages; ++s) {
-      mbar_init(&sh.full[s], KaFeed<kKaRows, kKaBlock>::kCopies);
+      mbar_init(&sh.full[s], KaFeed<kKaRows, kKaBlock, 2>::kCopies);
       mbar_init(&sh.empty[s], kKaWarps / 2);
     }
     sh.dead = 0;
@@ -462,39 +505,7 @@ __global__ void __launch_bounds__(kKaThreads, kKaCtasPerSm) kv_attn_kernel(const
 
   if (warp == kKaWarps) {
     // ------------------------------------------------------------ producer
-    const uint64_t pol = policy_evict_first();
-    KaFeed<kKaRows, kKaBlock> feed;
-    feed.start(a, sh.prefix, w0, n, lane);
-    typename KaFeed<kKaRows, kKaBlock>::Item item = {}, next = {};
-    int i = 0;
-#pragma unroll 1
-    for (int i0 = -2 * feed.NB; i0 < n; i0 += feed.NB) {
-      item = next;
-      next = feed.resolve(a);
-      feed.look(a, i0 < -feed.NB);
-      if (i0 < 0) continue;
-      for (int j = 0; j < feed.NB && i < n; ++j, ++i) {
-        const int s = i % kKaStages;
-        if (i >= kKaStages)
-          ka_wait(&sh.empty[s], static_cast<uint32_t>(i / kKaStages - 1) & 1, &sh.dead, a.err);
-        __syncwarp();
-        if (lane / feed.kCopies == j) {
-          if (item.src != nullptr && !*static_cast<volatile int*>(&sh.dead)) {
-            mbar_expect_tx(&sh.full[s], item.bytes);
-            bulk_copy_g2s_hint((feed.is_v ? sh.v[s] : sh.k[s]) + feed.sub * 16 * D, item.src,
-                               item.bytes, &sh.full[s], pol);
-          }
-          (feed.is_v ? sh.v_scale[s] : sh.k_scale[s])[feed.sub] = item.scale;
-          mbar_arrive(&sh.full[s]);
-        }
-        __syncwarp();
-      }
-    }
-    // copies of the last stages must land before the block ends
-    for (int j = max(0, n - kKaStages); j < n; ++j)
-      if (!mbar_wait_bounded(&sh.full[j % kKaStages],
-                             static_cast<uint32_t>(j / kKaStages) & 1, 1000000000ull))
-        record_error(a.err, SV_DERR_TIMEOUT);
+    ka_produce<D, KaFeed<kKaRows, kKaBlock, 2>>(a, sh, w0, n, lane);
     return;
   }
 

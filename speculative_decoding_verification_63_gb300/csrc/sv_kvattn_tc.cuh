@@ -17,7 +17,10 @@
 //   16     issues S_s = Q K^T.
 //   17     allocates tensor memory, issues O_s += P_s V (P_s: the weights as
 //          halves, in the columns of S_s they came from).
-//   18     bulk copies of raw codes, scales, the blocks' descriptions.
+//   18, 19 bulk copies of raw key and value codes; 18 also the scales and the
+//          blocks' descriptions.  (One warp for both needed 1100 clocks for
+//          each side of a block, all of it latency of its own instructions:
+//          it, not the memory, set the pace.)
 // Shared memory is the busiest unit: a block of 128 channels carries 64 KB of
 // raw codes (written, read), 64 KB of halves written and 96 KB read by the
 // products, 1750 clocks at 128 bytes a clock, against 1024 clocks of products
@@ -41,11 +44,14 @@ namespace sv {
 
 constexpr int kTcRows = 128;
 constexpr int kTcBlock = 128;
-// Raw ring: keys and values of a block in turn, 16 KB each at D = 128.
-constexpr int kTcSlots = 7;
-constexpr int kTcMeta = 8;     // block descriptions (at most seven blocks in flight)
+// Raw rings of key and of value codes, 16 KB a slot at D = 128; values wait
+// longer, for the block's weights.
+constexpr int kTcKeySlots = 3, kTcValueSlots = 4, kTcSlots = kTcKeySlots + kTcValueSlots;
+// Block descriptions.  The keys of block i come once those of i - 3 are taken,
+// so after the scores of i - 5, so after the products of i - 7.
+constexpr int kTcMeta = 8;
 constexpr int kTcSoftmax = 256, kTcConvert = 128;
-constexpr int kTcThreads = kTcSoftmax + 2 * kTcConvert + 96;
+constexpr int kTcThreads = kTcSoftmax + 2 * kTcConvert + 128;
 constexpr int kTcMaxCtas = 160;
 constexpr int kTcMinBlocks = 2;
 
@@ -60,7 +66,19 @@ struct alignas(16) TcMeta {
   int round;     // the block's first position, from the round's first token
   int edge;      // rows may see different positions, or a page is missing
   float4 s[8];   // of its 16-position pieces: 2^ek (< 0: no such page), ev, 2^-ev
-  int nan;       // a value code of an edge block is NaN (set by the converters)
+  // the same from the values' producer, for the values' converters
+  int v_tokens, v_edge, v_missing;  // bit per piece: no such page
+  int nan;  // a value code of an edge block is NaN (set by the converters)
+};
+
+// Where block i of a side lies in the ring, and its use of the slot (parity).
+struct TcSlot {
+  int slots, slot;
+  uint32_t phase;
+  __device__ __forceinline__ TcSlot(int side, int i)
+      : slots(side ? kTcValueSlots : kTcKeySlots),
+        slot(side ? kTcKeySlots + i % kTcValueSlots : i % kTcKeySlots),
+        phase((side ? i / kTcValueSlots : i / kTcKeySlots) & 1) {}
 };
 
 template <int D>
@@ -77,16 +95,43 @@ struct TcShared {
   unsigned short nanmask[kTcBlock][D / 16];
   TcMeta meta[kTcMeta];
   float scratch[2][kTcRows];  // the queries' largest values
+  float c2[2][kTcRows];       // the score factors of the unit's rows (tc_load_q)
   float ends[2][2][kTcRows];  // references and sums of the streams
   unsigned long long nanrow[D / 64][kTcRows];  // channels in which a lane's row saw a NaN
   KaCursor<kTcRows, kTcBlock> cur[8];          // the softmax warps' places
   int total, nanany;
   uint64_t rawfull[kTcSlots], rawempty[kTcSlots];
-  uint64_t kfull, vfull, sfull[2], pfull[2], pvdone[2], qfull;
+  uint64_t kfull, vfull[2], sfull[2], pfull[2], pvdone[2], qfull;
   unsigned tmem;
   int dead;
   unsigned last;
 };
+
+// Two 32-bit operations in one instruction.
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 d;
+  asm("{\n\t.reg .b64 a, b, c, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
+      "mov.b64 c, {%6, %7};\n\tfma.rn.f32x2 d, a, b, c;\n\tmov.b64 {%0, %1}, d;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return d;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  float2 d;
+  asm("{\n\t.reg .b64 a, b, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
+      "add.rn.f32x2 d, a, b;\n\tmov.b64 {%0, %1}, d;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+__device__ __forceinline__ float max3(const unsigned* x) {
+  return max3(__uint_as_float(x[0]), __uint_as_float(x[1]), __uint_as_float(x[2]));
+}
 
 // ------------------------------------------------------- tcgen05 primitives
 
@@ -162,14 +207,6 @@ __device__ __forceinline__ void tc_ld16(unsigned (&x)[16], unsigned addr) {
       : "r"(addr)
       : "memory");
 }
-__device__ __forceinline__ void tc_ld8(unsigned (&x)[8], unsigned addr) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];\n\t"
-      "tcgen05.wait::ld.sync.aligned;"
-      : SV_R4(x, 0), SV_R4(x, 4)
-      : "r"(addr)
-      : "memory");
-}
 __device__ __forceinline__ void tc_st8(unsigned addr, const unsigned* x) {
   asm volatile(
       "tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(addr),
@@ -205,76 +242,21 @@ __device__ __forceinline__ void tc_wait(uint64_t* bar, uint32_t parity, int* dea
   __syncwarp();
 }
 
-// The last CTA to arrive joins a cut unit's parts (CTAs first .. last, in
-// order, two at a time with their loads in flight together) and leaves zeros
-// behind.  All softmax threads: thread = row, set s the s-th half of the
-// channels, sixteen at a time.
-template <int D, class T>
-__device__ __noinline__ void tc_join(const KvAttnProblem& a, int first, int last, int live,
-                                     int tile, long long req) {
-  constexpr int PF = kTcPartialFloats<D>, N = 16;
-  const int row = static_cast<int>(threadIdx.x) & (kTcRows - 1);
-  const int c0 = (static_cast<int>(threadIdx.x) / kTcRows) * (D / 2);
-  auto part = [&](int c) { return a.partials + (2ll * c + (c == first ? 1 : 0)) * PF; };
-  const int g = tile * kTcRows + row, t = ka_div_g(a, g);
-  const long long orow = req + static_cast<long long>(t) * a.Hq + g - t * a.G;
-  if (row < live) {
-#pragma unroll 1
-    for (int ch = c0; ch < c0 + D / 2; ch += N) {
-      float m = kNegInf, z = 0.f, acc[N];
-#pragma unroll
-      for (int j = 0; j < N; ++j) acc[j] = 0.f;
-#pragma unroll 1
-      for (int c = first; c <= last; c += 2) {
-        float* const p = part(c) + row;
-        float* const q = part(min(c + 1, last)) + row;
-        float v[N], w[N];
-        const float r0 = __ldcg(p), z0 = __ldcg(p + kTcRows);
-        float r1 = __ldcg(q), z1 = __ldcg(q + kTcRows);
-#pragma unroll
-        for (int j = 0; j < N; ++j) v[j] = __ldcg(p + (2 + ch + j) * kTcRows);
-#pragma unroll
-        for (int j = 0; j < N; ++j) w[j] = __ldcg(q + (2 + ch + j) * kTcRows);
-        if (c == last) {  // no second one
-          r1 = kNegInf;
-          z1 = 0.f;
-#pragma unroll
-          for (int j = 0; j < N; ++j) w[j] = 0.f;
-        }
-        const float n = fmaxf(m, fmaxf(r0, r1));
-        // a part that saw nothing has z = 0 and O = 0 (or NaN, which stays)
-        const float fm = m == kNegInf ? 1.f : fast_exp2(m - n);
-        const float f0 = r0 == kNegInf ? 1.f : fast_exp2(r0 - n);
-        const float f1 = r1 == kNegInf ? 1.f : fast_exp2(r1 - n);
-        m = n;
-        z = z * fm + z0 * f0 + z1 * f1;
-#pragma unroll
-        for (int j = 0; j < N; ++j) acc[j] = acc[j] * fm + v[j] * f0 + w[j] * f1;
-      }
-      const bool any = !(z == 0.f);
-      const float inv = any ? 1.f / z : 0.f;
-      T* const o = static_cast<T*>(a.out) + orow * D + ch;
-#pragma unroll
-      for (int j = 0; j < N; j += 8) {
-        alignas(16) T e[8];
-#pragma unroll
-        for (int k = 0; k < 8; ++k) e[k] = from_float<T>(any ? acc[j + k] * inv : 0.f);
-        *reinterpret_cast<uint4*>(o + j) = *reinterpret_cast<const uint4*>(e);
-      }
-      if (a.lse && ch == 0)
-        a.lse[orow] = any ? (log2f(z) + m - kRefShift) * 0.69314718055994531f : kNegInf;
-    }
-  }
-  named_sync(1, kTcSoftmax);  // everything has been read
-  if (row < live) {
-#pragma unroll 1
-    for (int c = first; c <= last; ++c) {
-      float* const p = part(c) + row;
-      if (c0 == 0) p[0] = p[kTcRows] = 0.f;
-#pragma unroll 16
-      for (int ch = c0; ch < c0 + D / 2; ++ch) p[(2 + ch) * kTcRows] = 0.f;
-    }
-  }
+// The part of a cut unit that CTA c holds: its last one where the unit begins
+// with it, else its first.
+template <int D>
+__device__ __forceinline__ float* tc_part(const KvAttnProblem& a, int c, int first) {
+  return a.partials + (2ll * c + (c == first ? 1 : 0)) * kTcPartialFloats<D>;
+}
+// What a part with reference r counts against a reference m.  One that saw
+// nothing has z = 0 and O = 0 (or NaN, which stays).
+__device__ __forceinline__ float tc_factor(float r, float m) {
+  return r == kNegInf ? 1.f : fast_exp2(r - m);
+}
+__device__ __forceinline__ unsigned tc_acquire(const unsigned* p) {
+  unsigned v;
+  asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
+  return v;
 }
 
 // ------------------------------------------------------------------- kernel
@@ -424,12 +406,12 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv_attn_tc_kernel(const KvAttnP
         mbar_init(&sh.rawempty[s], kTcConvert / 32);
       }
       for (int s = 0; s < 2; ++s) {
+        mbar_init(&sh.vfull[s], kTcConvert / 32);
         mbar_init(&sh.sfull[s], 1);
         mbar_init(&sh.pfull[s], 4);
         mbar_init(&sh.pvdone[s], 1);
       }
       mbar_init(&sh.kfull, kTcConvert / 32);
-      mbar_init(&sh.vfull, kTcConvert / 32);
       mbar_init(&sh.qfull, kTcSoftmax / 32);
       sh.dead = 0;
       fence_mbar_init();
@@ -458,12 +440,13 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv_attn_tc_kernel(const KvAttnP
     }
   }
 
-  if (n > 0 && warp == 18) {
-    // ------------------------------------------------------------ producer
+  if (n > 0 && warp >= 18) {
+    // ----------------------------------------------------------- producers
+    const int side = warp - 18;  // keys, values
     const uint64_t pol = policy_evict_first();
-    using Feed = KaFeed<kTcRows, kTcBlock>;
+    using Feed = KaFeed<kTcRows, kTcBlock, 1>;
     Feed feed;
-    feed.start(a, sh.prefix, w0, n, lane);
+    feed.start(a, sh.prefix, w0, n, lane, side == 1);
     typename Feed::Item item = {}, next = {};
     int i = 0;
 #pragma unroll 1
@@ -473,51 +456,54 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv_attn_tc_kernel(const KvAttnP
       feed.look(a, i0 < -Feed::NB);
       if (i0 < 0) continue;
       const unsigned missing = __ballot_sync(0xffffffffu, item.scale < 0.f);
-      for (int j = 0; j < Feed::NB && i < n; ++j, ++i) {
 #pragma unroll 1
-        for (int side = 0; side < 2; ++side) {
-          const int x = 2 * i + side, slot = x % kTcSlots;
-          if (x >= kTcSlots)
-            tc_wait(&sh.rawempty[slot], static_cast<uint32_t>(x / kTcSlots - 1) & 1, dead, a.err);
-          if (lane / Feed::kCopies == j) {
-            const bool here = feed.is_v == (side == 1);
-            if (here && item.src != nullptr && !*static_cast<volatile int*>(dead)) {
-              mbar_expect_tx(&sh.rawfull[slot], item.bytes);
-              bulk_copy_g2s_hint(&sh.raw[slot][feed.sub * 16 * D], item.src, item.bytes,
-                                 &sh.rawfull[slot], pol);
-            }
-            if (side == 0) {
-              // the block's description, values' scales included: complete
-              // before the keys are announced
-              TcMeta& m = sh.meta[i % kTcMeta];
-              const int e = scale_exp(item.scale);
-              if (item.first) tc_prefetch_q<D, T>(a, item, lane % Feed::kCopies, Feed::kCopies);
-              if (feed.is_v) {
-                m.s[feed.sub].y = static_cast<float>(e);
-                m.s[feed.sub].z = pow2f(-e);
-              } else {
-                m.s[feed.sub].x = item.scale < 0.f ? -1.f : pow2f(e);
-                if (feed.sub == 0) {
-                  m.first = item.first;
-                  m.tokens = item.tokens;
-                  m.round = item.round;
-                  m.edge = item.round + kTcBlock > 0 ||
-                           (missing >> (j * Feed::kCopies) & ((1u << Feed::kCopies) - 1)) != 0;
-                  m.nan = 0;
-                }
-              }
-            }
+      for (int j = 0; j < Feed::NB && i < n; ++j, ++i) {
+        const TcSlot at(side, i);
+        const int slot = at.slot;
+        if (i >= at.slots) tc_wait(&sh.rawempty[slot], at.phase ^ 1, dead, a.err);
+        if (lane / Feed::kCopies == j) {
+          if (item.src != nullptr && !*static_cast<volatile int*>(dead)) {
+            mbar_expect_tx(&sh.rawfull[slot], item.bytes);
+            bulk_copy_g2s_hint(&sh.raw[slot][feed.sub * 16 * D], item.src, item.bytes,
+                               &sh.rawfull[slot], pol);
           }
-          __syncwarp();
-          if (lane / Feed::kCopies == j && feed.is_v == (side == 1)) mbar_arrive(&sh.rawfull[slot]);
+          const unsigned gone = missing >> (j * Feed::kCopies) & ((1u << Feed::kCopies) - 1);
+          // the last position that every row of the unit sees, in the round
+          const int all = a.mask ? -1 : ka_div_g(a, item.tile * kTcRows);
+          const bool edge = item.round + kTcBlock - 1 > all || gone != 0;
+          if (side == 0) {
+            // the block's description, values' scales included: complete
+            // before the keys are announced
+            TcMeta& m = sh.meta[i % kTcMeta];
+            if (item.first) tc_prefetch_q<D, T>(a, item, lane % Feed::kCopies, Feed::kCopies);
+            const int e = scale_exp(item.v_scale);
+            m.s[feed.sub].x = item.scale < 0.f ? -1.f : pow2f(scale_exp(item.scale));
+            m.s[feed.sub].y = static_cast<float>(e);
+            m.s[feed.sub].z = pow2f(-e);
+            if (feed.sub == 0) {
+              m.first = item.first;
+              m.tokens = item.tokens;
+              m.round = item.round;
+              m.edge = edge;
+            }
+          } else if (feed.sub == 0) {
+            TcMeta& m = sh.meta[i % kTcMeta];
+            m.v_tokens = item.tokens;
+            m.v_edge = edge;
+            m.v_missing = gone;
+            m.nan = 0;
+          }
         }
+        __syncwarp();
+        if (lane / Feed::kCopies == j) mbar_arrive(&sh.rawfull[slot]);
       }
     }
     // copies of the last slots must land before the block ends
-    for (int x = max(0, 2 * n - kTcSlots); x < 2 * n; ++x)
-      if (!mbar_wait_bounded(&sh.rawfull[x % kTcSlots],
-                             static_cast<uint32_t>(x / kTcSlots) & 1, 1000000000ull))
+    for (int k = max(0, n - TcSlot(side, 0).slots); k < n; ++k) {
+      const TcSlot at(side, k);
+      if (!mbar_wait_bounded(&sh.rawfull[at.slot], at.phase, 1000000000ull))
         record_error(a.err, SV_DERR_TIMEOUT);
+    }
   } else if (n > 0 && warp >= 8 && warp < 16) {
     // ---------------------------------------------------------- converters
     const int side = warp >= 12 ? 1 : 0;  // keys, values
@@ -534,13 +520,13 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv_attn_tc_kernel(const KvAttnP
     const unsigned off0 = off + (((c0 + flip) ^ (tok0 & 7)) << 4);
     const unsigned off1 = off + (((c0 + 1 - flip) ^ (tok0 & 7)) << 4);
     static_assert(STEP % 8 == 0, "swizzle phase");
-    uint64_t* const full = side ? &sh.vfull : &sh.kfull;
     uint64_t* const freed = side ? sh.pvdone : sh.sfull;
     for (int i = 0; i < n; ++i) {
-      const int x = 2 * i + side, slot = x % kTcSlots;
-      tc_wait(&sh.rawfull[slot], static_cast<uint32_t>(x / kTcSlots) & 1, dead, a.err);
+      const TcSlot at(side, i);
+      const int slot = at.slot;
+      tc_wait(&sh.rawfull[slot], at.phase, dead, a.err);
       TcMeta& m = sh.meta[i % kTcMeta];
-      if (__builtin_expect(m.edge, 0)) {
+      if (__builtin_expect(side ? m.v_edge : m.edge, 0)) {
         // Codes nobody wrote become zeros.  NaN value codes leave the
         // product, where they would meet the zero weights of rows that do
         // not see them, and go to a mask the softmax warps look at.
@@ -549,9 +535,11 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv_attn_tc_kernel(const KvAttnP
 #pragma unroll 1
         for (int j = 0; j < ITEMS; ++j) {
           const int tok = tok0 + j * STEP;
-          const bool there = tok < m.tokens && m.s[tok >> 4].x >= 0.f;
-          uint4* const at = reinterpret_cast<uint4*>(&sh.raw[slot][(ct + j * kTcConvert) * 16]);
-          uint4 c = *at;
+          const bool there = side ? tok < m.v_tokens && !(m.v_missing >> (tok >> 4) & 1)
+                                  : tok < m.tokens && m.s[tok >> 4].x >= 0.f;
+          uint4* const where =
+              reinterpret_cast<uint4*>(&sh.raw[slot][(ct + j * kTcConvert) * 16]);
+          uint4 c = *where;
           unsigned* w = reinterpret_cast<unsigned*>(&c);
           unsigned mask = 0;
 #pragma unroll
@@ -564,12 +552,13 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv_attn_tc_kernel(const KvAttnP
                       << (4 * q);
             }
           }
-          *at = c;
+          *where = c;
           if (side == 1) {
             sh.nanmask[tok][piece] = static_cast<unsigned short>(mask);
             if (mask) m.nan = 1;
           }
         }
+        fence_proxy_async_shared();  // before the slot's next copy
       }
       uint4 code[ITEMS];
 #pragma unroll
@@ -605,7 +594,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv_attn_tc_kernel(const KvAttnP
       }
       fence_proxy_async_shared();
       __syncwarp();
-      if (lane == 0) mbar_arrive(full);
+      if (lane == 0) mbar_arrive(side ? &sh.vfull[i & 1] : &sh.kfull);
     }
   } else if (n > 0 && warp == 16) {
     // ---------------------------------------------------------- S = Q K^T
@@ -639,9 +628,9 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv_attn_tc_kernel(const KvAttnP
       for (int i = 0; i < n; ++i) {
         const int s = i & 1;
         const uint32_t ph = static_cast<uint32_t>(i >> 1) & 1;
-        ka_wait(&sh.vfull, static_cast<uint32_t>(i) & 1, dead, a.err);
-        if (sh.meta[i % kTcMeta].first) seg = i;
+        ka_wait(&sh.vfull[s], ph, dead, a.err);
         ka_wait(&sh.pfull[s], ph, dead, a.err);
+        if (sh.meta[i % kTcMeta].first) seg = i;
         tc_fence_after();
 #pragma unroll
         for (int k = 0; k < kTcBlock / 16; ++k)
@@ -661,7 +650,6 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv_attn_tc_kernel(const KvAttnP
     const int set = warp >> 2, quarter = warp & 3, row = tid & (kTcRows - 1);
     // tensor-memory address of the warp's lanes (bits 31..16: lane)
     const unsigned tm = tmem + (static_cast<unsigned>(quarter) << 21);
-    constexpr int PF = kTcPartialFloats<D>;
     {
       KaCursor<kTcRows, kTcBlock> cur;
       cur.seek(a, sh.prefix, w0);
@@ -669,7 +657,6 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv_attn_tc_kernel(const KvAttnP
       __syncwarp();
     }
     // One unit a turn; the first turn (i0 < 0) only loads the first queries.
-    float c2 = 0.f;
     for (int i0 = -1; i0 < n;) {
       int nb = 0, cs = 0, base = 0;
       bool warp_live = false;
@@ -683,6 +670,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv_attn_tc_kernel(const KvAttnP
       }
       // of a block's eight 16-position pieces: `own` from `base` on
       const int own = 8 >> cs;
+      const float c2 = sh.c2[set][row];
       float ref = kNegInf, z = 0.f;
       bool had = false;  // this stream has taken a block of the unit
 
@@ -697,7 +685,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv_attn_tc_kernel(const KvAttnP
           if (__builtin_expect(m.edge, 0)) {
             // scores of positions the row does not see become -inf
             const TcUnit me = tc_unit(a, sh.cur[warp], row);
-            tc_wait(&sh.vfull, static_cast<uint32_t>(i) & 1, dead, a.err);  // the NaN mask
+            tc_wait(&sh.vfull[set], ph, dead, a.err);  // the NaN mask
             const bool nan = *static_cast<const volatile int*>(&m.nan) != 0;
 #pragma unroll 1
             for (int u = 0; u < own; ++u) {
@@ -742,14 +730,12 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv_attn_tc_kernel(const KvAttnP
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
               const float4 ms = m.s[base + u + h];
-              float v[4];
+              float v[5];
 #pragma unroll
-              for (int j = 0; j < 4; ++j)
-                v[j] = fmaxf(
-                    fmaxf(__uint_as_float(x[16 * h + j]), __uint_as_float(x[16 * h + 4 + j])),
-                    fmaxf(__uint_as_float(x[16 * h + 8 + j]), __uint_as_float(x[16 * h + 12 + j])));
-              mx = fmaxf(mx, fmaf(fmaxf(fmaxf(v[0], v[1]), fmaxf(v[2], v[3])),
-                                  c2 * fabsf(ms.x), ms.y));
+              for (int j = 0; j < 5; ++j) v[j] = max3(&x[16 * h + 3 * j]);
+              v[0] = max3(v[0], v[1], v[2]);
+              v[0] = max3(v[0], v[3], max3(v[4], __uint_as_float(x[16 * h + 15]), v[0]));
+              mx = fmaxf(mx, fmaf(v[0], c2 * fabsf(ms.x), ms.y));
             }
           }
           const bool rise = mx > ref + kRefSlack;
@@ -781,16 +767,19 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv_attn_tc_kernel(const KvAttnP
             for (int h = 0; h < 2; ++h) {
               const float4 ms = m.s[base + u + h];
               const float sc = c2 * fabsf(ms.x), vb = ms.y - bs;
-              float z0 = 0.f, z1 = 0.f;
+              const float2 sc2 = make_float2(sc, sc), vb2 = make_float2(vb, vb);
+              float2 zz = make_float2(0.f, 0.f);
 #pragma unroll
               for (int j = 0; j < 16; j += 2) {
-                const float e0 = fast_exp2(fmaf(__uint_as_float(x[16 * h + j]), sc, vb));
-                const float e1 = fast_exp2(fmaf(__uint_as_float(x[16 * h + j + 1]), sc, vb));
-                z0 += e0;
-                z1 += e1;
-                p[8 * h + j / 2] = half2_of(e0, e1);
+                float2 e = fma2(make_float2(__uint_as_float(x[16 * h + j]),
+                                            __uint_as_float(x[16 * h + j + 1])),
+                                sc2, vb2);
+                e.x = fast_exp2(e.x);
+                e.y = fast_exp2(e.y);
+                zz = add2(zz, e);
+                p[8 * h + j / 2] = half2_of(e.x, e.y);
               }
-              z = fmaf(z0 + z1, ms.z, z);
+              z = fmaf(zz.x + zz.y, ms.z, z);
             }
             __syncwarp();
             tc_st8(ts + u * 16, p);
@@ -819,10 +808,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv_attn_tc_kernel(const KvAttnP
       const bool whole = cur.blk == 0 && nb == cur.nblk;
       const KaParts parts(sh.total, static_cast<int>(gridDim.x), kTcMinBlocks);
       const int first = parts.of(cur.unit0), last = parts.of(cur.unit0 + cur.nblk - 1);
-      const long long req = static_cast<long long>(cur.b) * a.T * a.Hq;
-      const long long orow = req + static_cast<long long>(my.t) * a.Hq + my.hq;
-      const int tile = cur.tile, head0 = cur.head * a.G;
-      float* const part = a.partials + (2ll * cta + (cur.blk == 0 ? 1 : 0)) * PF;
+      const long long orow = (static_cast<long long>(cur.b) * a.T + my.t) * a.Hq + my.hq;
       // blocks each stream had; the unit's last products of each
       const int cnt[2] = {(nb + 1 - (i0 & 1)) / 2, (nb + (i0 & 1)) / 2};
       if (i0 >= 0) {
@@ -841,7 +827,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv_attn_tc_kernel(const KvAttnP
       if (max(i0, 0) + nb < n) {
         const TcUnit me = tc_unit(a, cur, row);
         if (me.warp_live(quarter))
-          c2 = tc_load_q<D, T>(a,
+          sh.c2[set][row] = tc_load_q<D, T>(a,
                                static_cast<const T*>(a.q) + cur.b * a.q_batch +
                                    me.t * a.q_token + me.hq * a.q_head,
                                me.mine, set, sh.qh, sh.scratch, row, quarter);
@@ -885,75 +871,172 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv_attn_tc_kernel(const KvAttnP
         f1 = factor(sh.ends[1][0][row]);
       }
       const int r = row & (step - 1);  // row of the unit
-      const bool any = !(z == 0.f);    // true for NaN
-      const float inv = !whole ? 1.f : any ? 1.f / z : 0.f;
       const bool writes = my.mine && my.copy == 0;
+      // A unit that is cut: the CTA that finds the others' parts already there
+      // joins them with its own (in the CTAs' order, so it does not matter
+      // which CTA that is) and writes the result; any other leaves its part.
+      // Parts begin at a CTA's first unit and end at its last, so the one that
+      // joins is as a rule the CTA that holds the unit's beginning, at its
+      // end, with the others' parts long written.  Two CTAs that look at the
+      // same time both leave theirs: then the last one to arrive joins from
+      // memory alone.
+      bool joins = whole;
+      if (!whole) {
+        if (tid == 0) sh.last = tc_acquire(&a.tickets[first]) == static_cast<unsigned>(last - first);
+        named_sync(1, kTcSoftmax);
+        joins = sh.last != 0;
+        if (joins) __threadfence();
+        named_sync(1, kTcSoftmax);
+      }
 #pragma unroll 1
-      for (int c = set * (D / 2); c < (set + 1) * (D / 2); c += 8) {
-        float x[8];
-        if (warp_live) {
-          unsigned o0[8], o1[8];
-          __syncwarp();
-          tc_ld8(o0, tm + kO + c);
-          tc_ld8(o1, tm + kO + D + c);
-#pragma unroll
-          for (int j = 0; j < 8; ++j)
-            x[j] = (cnt[0] > 0 ? __uint_as_float(o0[j]) * f0 : 0.f) +
-                   (cnt[1] > 0 ? __uint_as_float(o1[j]) * f1 : 0.f);
-        }
-        if (my.copies > 1) {
-          // the other copies' lanes hand theirs to copy 0
-          float4* const jb = reinterpret_cast<float4*>(sh.join[set][row]);
-          if (my.copy > 0 && my.mine) {
-            jb[0] = make_float4(x[0], x[1], x[2], x[3]);
-            jb[1] = make_float4(x[4], x[5], x[6], x[7]);
+      for (bool memory = false;; memory = true) {
+        // (memory: the second turn of a CTA that left its part and arrived last)
+        float m = ref, zt = z;  // of the whole row
+        if (joins && !whole && writes) {
+#pragma unroll 1
+          for (int c = first; c <= last; ++c)
+            if (c != cta) m = fmaxf(m, __ldcg(tc_part<D>(a, c, first) + r));
+          zt = 0.f;
+#pragma unroll 1
+          for (int c = first; c <= last; ++c) {
+            const float* const p = tc_part<D>(a, c, first);
+            const float rc = c == cta ? ref : __ldcg(p + r);
+            const float zc = c == cta ? z : __ldcg(p + kTcRows + r);
+            zt = fmaf(zc, tc_factor(rc, m), zt);
           }
-          named_sync(6 + set, kTcRows);
-          if (writes)
+        }
+        const bool any = !(zt == 0.f);  // true for NaN
+        const float inv = any ? 1.f / zt : 0.f;
 #pragma unroll 1
-            for (int l = row + step; l < kTcRows; l += step) {
-              const float4* const q = reinterpret_cast<const float4*>(sh.join[set][l]);
-              const float4 u = q[0], v = q[1];
-              x[0] += u.x;
-              x[1] += u.y;
-              x[2] += u.z;
-              x[3] += u.w;
-              x[4] += v.x;
-              x[5] += v.y;
-              x[6] += v.z;
-              x[7] += v.w;
+        for (int c = set * (D / 2); c < (set + 1) * (D / 2); c += 16) {
+          float x[16];
+          if (memory) {
+            if (writes) {
+#pragma unroll
+              for (int j = 0; j < 16; ++j)
+                x[j] = __ldcg(tc_part<D>(a, cta, first) + (2 + c + j) * kTcRows + r);
             }
-          named_sync(6 + set, kTcRows);
-        }
-        if (writes) {
+          } else {
+            if (warp_live) {
+              unsigned o[16];
+              __syncwarp();
+              tc_ld16(o, tm + kO + c);
 #pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            x[j] = any || !whole ? x[j] * inv : 0.f;
-            if (nanw >> ((c + j) & 63) & 1) x[j] = __int_as_float(0x7fc00000);
+              for (int j = 0; j < 16; ++j) x[j] = cnt[0] > 0 ? __uint_as_float(o[j]) * f0 : 0.f;
+              tc_ld16(o, tm + kO + D + c);
+#pragma unroll
+              for (int j = 0; j < 16; ++j)
+                x[j] = cnt[1] > 0 ? fmaf(__uint_as_float(o[j]), f1, x[j]) : x[j];
+            }
+            if (my.copies > 1) {
+              // the other copies' lanes hand theirs to copy 0, eight at a time
+#pragma unroll
+              for (int q = 0; q < 16; q += 8) {
+                float4* const jb = reinterpret_cast<float4*>(sh.join[set][row]);
+                if (my.copy > 0 && my.mine) {
+                  jb[0] = make_float4(x[q], x[q + 1], x[q + 2], x[q + 3]);
+                  jb[1] = make_float4(x[q + 4], x[q + 5], x[q + 6], x[q + 7]);
+                }
+                named_sync(6 + set, kTcRows);
+                if (writes)
+#pragma unroll 1
+                  for (int l = row + step; l < kTcRows; l += step) {
+                    const float4* const y = reinterpret_cast<const float4*>(sh.join[set][l]);
+                    const float4 u = y[0], v = y[1];
+                    x[q] += u.x;
+                    x[q + 1] += u.y;
+                    x[q + 2] += u.z;
+                    x[q + 3] += u.w;
+                    x[q + 4] += v.x;
+                    x[q + 5] += v.y;
+                    x[q + 6] += v.z;
+                    x[q + 7] += v.w;
+                  }
+                named_sync(6 + set, kTcRows);
+              }
+            }
+            if (nanw != 0) {
+#pragma unroll
+              for (int j = 0; j < 16; ++j)
+                if (nanw >> ((c + j) & 63) & 1) x[j] = __int_as_float(0x7fc00000);
+            }
           }
-          if (whole) {
+          if (!writes) continue;
+          if (!joins) {
+            float* const p = tc_part<D>(a, cta, first) + (2 + c) * kTcRows + r;
+#pragma unroll
+            for (int j = 0; j < 16; ++j) p[j * kTcRows] = x[j];
+            continue;
+          }
+          if (!whole) {
+            float y[16];
+#pragma unroll
+            for (int j = 0; j < 16; ++j) y[j] = 0.f;
+#pragma unroll 1
+            for (int k = first; k <= last; ++k) {
+              float* const p = tc_part<D>(a, k, first) + (2 + c) * kTcRows + r;
+              float v[16];
+              float rk = ref;
+              if (k != cta) {
+                rk = __ldcg(tc_part<D>(a, k, first) + r);
+#pragma unroll
+                for (int j = 0; j < 16; ++j) v[j] = __ldcg(p + j * kTcRows);
+              } else {
+#pragma unroll
+                for (int j = 0; j < 16; ++j) v[j] = x[j];
+              }
+              const float f = tc_factor(rk, m);
+#pragma unroll
+              for (int j = 0; j < 16; ++j) y[j] = fmaf(v[j], f, y[j]);
+              if (k != cta || memory) {
+#pragma unroll
+                for (int j = 0; j < 16; ++j) p[j * kTcRows] = 0.f;
+              }
+            }
+#pragma unroll
+            for (int j = 0; j < 16; ++j) x[j] = y[j];
+          }
+#pragma unroll
+          for (int j = 0; j < 16; j += 8) {
             alignas(16) T e[8];
 #pragma unroll
-            for (int j = 0; j < 8; ++j) e[j] = from_float<T>(x[j]);
-            *reinterpret_cast<uint4*>(static_cast<T*>(a.out) + orow * D + c) =
+            for (int q = 0; q < 8; ++q) e[q] = from_float<T>(any ? x[j + q] * inv : 0.f);
+            *reinterpret_cast<uint4*>(static_cast<T*>(a.out) + orow * D + c + j) =
                 *reinterpret_cast<const uint4*>(e);
-          } else {
-#pragma unroll
-            for (int j = 0; j < 8; ++j) part[(2 + c + j) * kTcRows + r] = x[j];
           }
         }
-      }
-      if (writes && set == 0) {
-        if (whole) {
-          if (a.lse)
-            a.lse[orow] = any ? (log2f(z) + ref - kRefShift) * 0.69314718055994531f : kNegInf;
-        } else {
-          part[r] = ref;
-          part[kTcRows + r] = z;
+        if (writes && set == 0) {
+          if (!joins) {
+            float* const p = tc_part<D>(a, cta, first) + r;
+            p[0] = ref;
+            p[kTcRows] = z;
+          } else if (a.lse) {
+            a.lse[orow] = any ? (log2f(zt) + m - kRefShift) * 0.69314718055994531f : kNegInf;
+          }
         }
+        if (whole) break;
+        if (joins) {
+          named_sync(1, kTcSoftmax);  // the parts' statistics have been read
+          if (writes && set == 0)
+#pragma unroll 1
+            for (int c = first; c <= last; ++c)
+              if (c != cta || memory) {
+                float* const p = tc_part<D>(a, c, first) + r;
+                p[0] = p[kTcRows] = 0.f;
+              }
+          if (tid == 0) a.tickets[first] = 0u;
+          break;
+        }
+        __threadfence();
+        named_sync(1, kTcSoftmax);
+        if (tid == 0)
+          sh.last = atomic_add_acq_rel(&a.tickets[first], 1u) == static_cast<unsigned>(last - first);
+        named_sync(1, kTcSoftmax);
+        if (!sh.last) break;
+        __threadfence();
+        joins = true;
       }
       tc_fence_before();
-      if (!whole) __threadfence();
       named_sync(1, kTcSoftmax);  // O, the references and sums have been read
       if (sh.nanany) {
         named_sync(1, kTcSoftmax);
@@ -961,17 +1044,6 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv_attn_tc_kernel(const KvAttnP
 #pragma unroll
           for (int j = 0; j < D / 64; ++j) sh.nanrow[j][row] = 0;
         if (tid == 0) sh.nanany = 0;
-        named_sync(1, kTcSoftmax);
-      }
-      if (!whole) {
-        if (tid == 0)
-          sh.last = atomic_add_acq_rel(&a.tickets[first], 1u) == static_cast<unsigned>(last - first);
-        named_sync(1, kTcSoftmax);
-        if (sh.last) {
-          __threadfence();
-          tc_join<D, T>(a, first, last, my.live, tile, req + head0);
-          if (tid == 0) a.tickets[first] = 0u;
-        }
         named_sync(1, kTcSoftmax);
       }
       i0 += nb;

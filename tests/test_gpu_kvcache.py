@@ -287,6 +287,9 @@ ATTENTION = [  # lens, new, T, Hq, H, P, D, dtype
     ([2000], [3], 3, 12, 12, 16, 64, "fp16"),
     ([6001], [5], 5, 16, 1, 128, 128, "bf16"),
     ([37, 0, 300], [200, 150, 77], 200, 4, 2, 64, 128, "bf16"),
+    ([77, 0, 64, 129], [25, 24, 1, 0], 25, 4, 2, 16, 64, "bf16"),
+    ([150, 65], [20, 17], 20, 5, 5, 64, 64, "fp16"),
+    ([3001, 4], [8, 5], 8, 8, 2, 128, 128, "bf16"),
 ]
 
 
@@ -300,6 +303,8 @@ def test_attention_causal(lens, new, T, Hq, H, P, D, dtype):
     ([200, 5], [64, 63], 64, 8, 4, 64, 64, "fp16"),
     ([1000, 31], [33, 32], 33, 10, 2, 128, 128, "bf16"),
     ([3], [1], 1, 2, 2, 32, 64, "bf16"),
+    ([60, 0, 31], [16, 9, 1], 16, 4, 2, 16, 128, "fp16"),
+    ([10, 500], [31, 30], 31, 1, 1, 32, 64, "bf16"),
 ])
 def test_attention_tree(lens, new, T, Hq, H, P, D, dtype):
     rng = np.random.default_rng(T)
@@ -325,7 +330,7 @@ def test_attention_layouts(split):
         return wide[..., 1:]
 
     for q_of in (fused, odd):
-        for T, Hq in ((4, 6), (30, 8)):
+        for T, Hq in ((4, 6), (7, 8), (30, 8)):
             check_attention(rng, [100, 30], [T, T - 1], T, Hq, 2, 32, 128, "bf16", split=split,
                             q_of=q_of)
 
@@ -337,7 +342,7 @@ def test_attention_of_wide_scores():
     H, P, D = 2, 16, 64
     lens, new = [900, 20], [4, 4]
     pages = 60
-    for T in (4, 40):
+    for T in (4, 10, 40):
         new = [T, T]
         c = ku.random_cache(rng, 64, H, P, D)
         c.ks = 2.0 ** rng.integers(-12, -2, c.ks.shape)
@@ -356,14 +361,15 @@ def test_attention_of_wide_scores():
                 <= dx + 2.0 ** -22 * np.abs(lse) + 2.0 ** -20).all()
 
 
-@pytest.mark.parametrize("T", [4, 40])
+@pytest.mark.parametrize("T", [4, 10, 40])
 @pytest.mark.parametrize("scale", [0.0, -0.25, 40.0])
 def test_attention_scales(T, scale):
     check_attention(np.random.default_rng(13), [70, 3], [T, T], T, 4, 2, 16, 64, "fp16",
                     scale=scale, spread=0.02)
 
 
-@pytest.mark.parametrize("T,Hq,H,D", [(6, 2, 1, 64), (40, 6, 2, 128)])
+@pytest.mark.parametrize("T,Hq,H,D", [(6, 2, 1, 64), (40, 6, 2, 128), (7, 8, 2, 128), (10, 2, 1, 64),
+                                       (12, 8, 2, 64)])
 def test_what_a_row_does_not_see_does_not_reach_it(T, Hq, H, D):
     """NaN codes in places a row does not see, in stale tokens behind the
     round and in unused page slots leave its result as it is; rows that see
@@ -416,7 +422,7 @@ def test_what_a_row_does_not_see_does_not_reach_it(T, Hq, H, D):
     assert (np.abs(o - out) <= tol)[~want_nan].all()
 
 
-@pytest.mark.parametrize("T", [3, 40])
+@pytest.mark.parametrize("T", [3, 12, 40])
 def test_attention_bad_requests(T):
     """Requests out of range give zero rows, pages that do not exist are seen
     by no row; the others keep their results."""
@@ -488,7 +494,7 @@ def test_offsets_beyond_32_bits():
     for s in "kv":
         assert np.array_equal(got[s][0].double().cpu().numpy(),
                               small.values(s, st[0], np.arange(140)))
-    for T in (2, 40):
+    for T in (2, 4, 40):
         q, q64 = as_type(rng.normal(size=(1, T, 16, D)), "bf16")
         o = sv.kv_attention(q, dev, table, i32([140 - T]))["out"].double().cpu().numpy()
         out, _, spr, xerr = ku.attention(q64, small, st, [140 - T], [T], None, D ** -0.5)
@@ -496,7 +502,7 @@ def test_offsets_beyond_32_bits():
         assert (np.abs(o - out) <= tol).all()
 
 
-@pytest.mark.parametrize("T", [1, 7, 32])
+@pytest.mark.parametrize("T", [1, 4, 7, 32])
 def test_a_round_on_a_side_stream_and_in_a_graph(T):
     """write, attention and read on a stream of their own, then captured in a
     CUDA graph and replayed on new inputs: the eager results."""
