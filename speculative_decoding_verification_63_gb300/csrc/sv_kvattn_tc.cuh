@@ -89,10 +89,10 @@ struct TcShared {
   unsigned char raw[kTcSlots][kTcBlock * D];
   union {
     int prefix[SV_MAX_B + 1];        // until every warp has found its place
-    float join[2][kTcRows][8];       // copies of rows at a unit's end
+    float join[2][kTcRows][4];       // copies of rows at a unit's end
   };
   int scan[kTcThreads / 32 + 1];
-  unsigned short nanmask[kTcBlock][D / 16];
+  unsigned short nanmask[2][kTcBlock][D / 16];  // NaN value codes of the streams' edge blocks
   TcMeta meta[kTcMeta];
   float scratch[2][kTcRows];  // the queries' largest values
   float c2[2][kTcRows];       // the score factors of the unit's rows (tc_load_q)
@@ -101,7 +101,7 @@ struct TcShared {
   KaCursor<kTcRows, kTcBlock> cur[8];          // the softmax warps' places
   int total, nanany;
   uint64_t rawfull[kTcSlots], rawempty[kTcSlots];
-  uint64_t kfull, vfull[2], sfull[2], pfull[2], pvdone[2], qfull;
+  uint64_t kfull, vfull[2], nanfull[2], sfull[2], pfull[2], pvdone[2], qfull;
   unsigned tmem;
   int dead;
   unsigned last;
@@ -213,7 +213,7 @@ __device__ __forceinline__ void tc_st8(unsigned addr, const unsigned* x) {
       SV_I4(x, 0), SV_I4(x, 4)
       : "memory");
 }
-__device__ __forceinline__ void tc_st16(unsigned addr, const unsigned (&x)[16]) {
+__device__ __forceinline__ void tc_st16(unsigned addr, const unsigned* x) {
   asm volatile(
       "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,"
       "%14,%15,%16};" ::"r"(addr),
@@ -287,25 +287,25 @@ __device__ __forceinline__ TcUnit tc_unit(const KvAttnProblem& a,
   return u;
 }
 
-// Which of the 16 positions of a block's piece the row sees (an edge block).
-__device__ __forceinline__ uint32_t tc_seen(const KvAttnProblem& a, int b, const TcUnit& u,
-                                            const TcMeta& m, int piece) {
-  if (!u.mine || m.s[piece].x < 0.f) return 0u;
+// Which of the 16 positions of a block's piece round token t sees (an edge
+// block); row: t, whether there are masks, its mask.
+__device__ __forceinline__ uint32_t tc_seen(int4 row, const TcMeta& m, int piece) {
+  if (m.s[piece].x < 0.f) return 0u;
   const int r0 = m.round + piece * 16;  // round index of the first (negative: prefix)
   const int tokens = m.tokens - piece * 16;
   if (tokens <= 0) return 0u;
   uint32_t seen;
   if (r0 <= -16) {
     seen = 0xffffu;
-  } else if (a.mask == nullptr) {
-    const int cols = u.t - r0 + 1;
+  } else if (!row.y) {
+    const int cols = row.x - r0 + 1;
     seen = cols >= 16 ? 0xffffu : cols <= 0 ? 0u : (1u << cols) - 1;
   } else {
-    const unsigned* mw = a.mask + (static_cast<long long>(b) * a.T + u.t) * a.words;
-    const uint64_t mb = mw[0] | (a.T > 32 ? static_cast<uint64_t>(mw[1]) << 32 : 0ull);
+    const uint64_t tree =
+        static_cast<unsigned>(row.z) | static_cast<uint64_t>(static_cast<unsigned>(row.w)) << 32;
     seen = r0 >= 64 ? 0u
-           : r0 >= 0 ? static_cast<uint32_t>(mb >> r0) & 0xffffu
-                     : (static_cast<uint32_t>(mb << -r0) | ((1u << -r0) - 1)) & 0xffffu;
+           : r0 >= 0 ? static_cast<uint32_t>(tree >> r0) & 0xffffu
+                     : (static_cast<uint32_t>(tree << -r0) | ((1u << -r0) - 1)) & 0xffffu;
   }
   return tokens >= 16 ? seen : seen & ((1u << tokens) - 1);
 }
@@ -381,6 +381,27 @@ __device__ __forceinline__ void tc_prefetch_q(const KvAttnProblem& a, const Item
   }
 }
 
+// The channels in which the row meets a NaN, of 16 positions it sees.
+template <int D>
+__device__ __noinline__ void tc_nan_seen(TcShared<D>& sh, int set, int row, int pos,
+                                         uint32_t seen) {
+  uint64_t c[D / 64];
+#pragma unroll
+  for (int j = 0; j < D / 64; ++j) c[j] = 0;
+#pragma unroll 1
+  for (int tok = 0; tok < 16; ++tok)
+    if (seen >> tok & 1)
+#pragma unroll
+      for (int j = 0; j < D / 16; ++j)
+        c[j >> 2] |= static_cast<uint64_t>(sh.nanmask[set][pos + tok][j]) << (16 * (j & 3));
+#pragma unroll
+  for (int j = 0; j < D / 64; ++j)
+    if (c[j]) {
+      atomicOr(&sh.nanrow[j][row], static_cast<unsigned long long>(c[j]));
+      sh.nanany = 1;
+    }
+}
+
 template <int D, class T>
 __global__ void __launch_bounds__(kTcThreads, 1) kv_attn_tc_kernel(const KvAttnProblem a) {
   extern __shared__ __align__(1024) unsigned char tc_smem[];
@@ -407,6 +428,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv_attn_tc_kernel(const KvAttnP
       }
       for (int s = 0; s < 2; ++s) {
         mbar_init(&sh.vfull[s], kTcConvert / 32);
+        mbar_init(&sh.nanfull[s], kTcConvert / 32);
         mbar_init(&sh.sfull[s], 1);
         mbar_init(&sh.pfull[s], 4);
         mbar_init(&sh.pvdone[s], 1);
@@ -526,17 +548,17 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv_attn_tc_kernel(const KvAttnP
       const int slot = at.slot;
       tc_wait(&sh.rawfull[slot], at.phase, dead, a.err);
       TcMeta& m = sh.meta[i % kTcMeta];
-      if (__builtin_expect(side ? m.v_edge : m.edge, 0)) {
-        // Codes nobody wrote become zeros.  NaN value codes leave the
-        // product, where they would meet the zero weights of rows that do
-        // not see them, and go to a mask the softmax warps look at.
-        if (side == 1 && i >= 1)  // the mask's last reader: block i - 1
-          tc_wait(&sh.pvdone[(i - 1) & 1], static_cast<uint32_t>((i - 1) >> 1) & 1, dead, a.err);
+      if (__builtin_expect(side == 1 && m.v_edge, 0)) {
+        // Value codes nobody wrote become zeros.  NaN codes leave the product,
+        // where they would meet the zero weights of rows that do not see them,
+        // and go to a mask the softmax warps look at.  (The mask's last
+        // reader, block i - 2, is through: this warp has seen its products
+        // done.)  Scores of keys that a row does not see are replaced, so the
+        // keys may be anything.
 #pragma unroll 1
         for (int j = 0; j < ITEMS; ++j) {
           const int tok = tok0 + j * STEP;
-          const bool there = side ? tok < m.v_tokens && !(m.v_missing >> (tok >> 4) & 1)
-                                  : tok < m.tokens && m.s[tok >> 4].x >= 0.f;
+          const bool there = tok < m.v_tokens && !(m.v_missing >> (tok >> 4) & 1);
           uint4* const where =
               reinterpret_cast<uint4*>(&sh.raw[slot][(ct + j * kTcConvert) * 16]);
           uint4 c = *where;
@@ -545,18 +567,13 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv_attn_tc_kernel(const KvAttnP
 #pragma unroll
           for (int q = 0; q < 4; ++q) {
             if (!there) w[q] = 0u;
-            if (side == 1) {
-              const unsigned is = ((w[q] & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;
-              w[q] &= ~((is >> 7) * 0xffu);
-              mask |= ((is >> 7 & 1) | (is >> 14 & 2) | (is >> 21 & 4) | (is >> 28 & 8))
-                      << (4 * q);
-            }
+            const unsigned is = ((w[q] & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;
+            w[q] &= ~((is >> 7) * 0xffu);
+            mask |= ((is >> 7 & 1) | (is >> 14 & 2) | (is >> 21 & 4) | (is >> 28 & 8)) << (4 * q);
           }
           *where = c;
-          if (side == 1) {
-            sh.nanmask[tok][piece] = static_cast<unsigned short>(mask);
-            if (mask) m.nan = 1;
-          }
+          sh.nanmask[i & 1][tok][piece] = static_cast<unsigned short>(mask);
+          if (mask) m.nan = 1;
         }
         fence_proxy_async_shared();  // before the slot's next copy
       }
@@ -565,7 +582,10 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv_attn_tc_kernel(const KvAttnP
       for (int j = 0; j < ITEMS; ++j)
         code[j] = *reinterpret_cast<const uint4*>(&sh.raw[slot][(ct + j * kTcConvert) * 16]);
       __syncwarp();
-      if (lane == 0) mbar_arrive(&sh.rawempty[slot]);  // in registers: the slot is free
+      if (lane == 0) {
+        mbar_arrive(&sh.rawempty[slot]);  // in registers: the slot is free
+        if (side == 1) mbar_arrive(&sh.nanfull[i & 1]);
+      }
       // half of the codes are converted before the wait for the buffer (all
       // of them would not fit the registers)
       constexpr int AHEAD = ITEMS / 2;
@@ -683,13 +703,20 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv_attn_tc_kernel(const KvAttnP
           const TcMeta& m = sh.meta[i % kTcMeta];
           const unsigned ts = tm + kS + set * kTcBlock + base * 16;
           if (__builtin_expect(m.edge, 0)) {
-            // scores of positions the row does not see become -inf
-            const TcUnit me = tc_unit(a, sh.cur[warp], row);
-            tc_wait(&sh.vfull[set], ph, dead, a.err);  // the NaN mask
+            const int t = tc_unit(a, sh.cur[warp], row).t;
+            uint2 tree = make_uint2(0, 0);
+            if (a.mask) {
+              const unsigned* mw =
+                  a.mask + (static_cast<long long>(sh.cur[warp].b) * a.T + t) * a.words;
+              tree = make_uint2(mw[0], a.T > 32 ? mw[1] : 0u);
+            }
+            const int4 e = make_int4(t, a.mask != nullptr, tree.x, tree.y);
+            tc_wait(&sh.nanfull[set], ph, dead, a.err);
             const bool nan = *static_cast<const volatile int*>(&m.nan) != 0;
+            // scores of positions the row does not see become -inf
 #pragma unroll 1
             for (int u = 0; u < own; ++u) {
-              const uint32_t seen = tc_seen(a, sh.cur[warp].b, me, m, base + u);
+              const uint32_t seen = tc_seen(e, m, base + u);
               unsigned x[16];
               __syncwarp();
               tc_ld16(x, ts + u * 16);
@@ -698,24 +725,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv_attn_tc_kernel(const KvAttnP
                 if (!(seen >> j & 1)) x[j] = 0xff800000u;
               __syncwarp();
               tc_st16(ts + u * 16, x);
-              if (nan) {
-                uint64_t c[D / 64];
-#pragma unroll
-                for (int j = 0; j < D / 64; ++j) c[j] = 0;
-#pragma unroll 1
-                for (int tok = 0; tok < 16; ++tok)
-                  if (seen >> tok & 1)
-#pragma unroll
-                    for (int j = 0; j < D / 16; ++j)
-                      c[j >> 2] |= static_cast<uint64_t>(sh.nanmask[(base + u) * 16 + tok][j])
-                                   << (16 * (j & 3));
-#pragma unroll
-                for (int j = 0; j < D / 64; ++j)
-                  if (c[j]) {
-                    atomicOr(&sh.nanrow[j][row], static_cast<unsigned long long>(c[j]));
-                    sh.nanany = 1;
-                  }
-              }
+              if (nan) tc_nan_seen<D>(sh, set, row, (base + u) * 16, seen);
             }
             tc_wait_st();
           }
@@ -929,28 +939,20 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv_attn_tc_kernel(const KvAttnP
                 x[j] = cnt[1] > 0 ? fmaf(__uint_as_float(o[j]), f1, x[j]) : x[j];
             }
             if (my.copies > 1) {
-              // the other copies' lanes hand theirs to copy 0, eight at a time
+              // the other copies' lanes hand theirs to copy 0, four at a time
 #pragma unroll
-              for (int q = 0; q < 16; q += 8) {
-                float4* const jb = reinterpret_cast<float4*>(sh.join[set][row]);
-                if (my.copy > 0 && my.mine) {
-                  jb[0] = make_float4(x[q], x[q + 1], x[q + 2], x[q + 3]);
-                  jb[1] = make_float4(x[q + 4], x[q + 5], x[q + 6], x[q + 7]);
-                }
+              for (int q = 0; q < 16; q += 4) {
+                float4* const jb = reinterpret_cast<float4*>(sh.join[set]);
+                if (my.copy > 0 && my.mine) jb[row] = make_float4(x[q], x[q + 1], x[q + 2], x[q + 3]);
                 named_sync(6 + set, kTcRows);
                 if (writes)
 #pragma unroll 1
                   for (int l = row + step; l < kTcRows; l += step) {
-                    const float4* const y = reinterpret_cast<const float4*>(sh.join[set][l]);
-                    const float4 u = y[0], v = y[1];
-                    x[q] += u.x;
-                    x[q + 1] += u.y;
-                    x[q + 2] += u.z;
-                    x[q + 3] += u.w;
-                    x[q + 4] += v.x;
-                    x[q + 5] += v.y;
-                    x[q + 6] += v.z;
-                    x[q + 7] += v.w;
+                    const float4 y = jb[l];
+                    x[q] += y.x;
+                    x[q + 1] += y.y;
+                    x[q + 2] += y.z;
+                    x[q + 3] += y.w;
                   }
                 named_sync(6 + set, kTcRows);
               }
