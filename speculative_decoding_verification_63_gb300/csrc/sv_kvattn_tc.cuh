@@ -590,9 +590,11 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv_attn_tc_kernel(const KvAttnP
       // of them would not fit the registers)
       constexpr int AHEAD = ITEMS / 2;
       uint4 lo[AHEAD], hi[AHEAD];
-      auto halves = [&](const uint4& c, uint4& l, uint4& h) {
-        l = make_uint4(half2_lo(c.x), half2_hi(c.x), half2_lo(c.y), half2_hi(c.y));
-        h = make_uint4(half2_lo(c.z), half2_hi(c.z), half2_lo(c.w), half2_hi(c.w));
+      auto halves = [&](const uint4& c, uint4& l, uint4& h) {  // in the order of the stores
+        const uint2 p = flip ? make_uint2(c.z, c.w) : make_uint2(c.x, c.y);
+        const uint2 q = flip ? make_uint2(c.x, c.y) : make_uint2(c.z, c.w);
+        l = make_uint4(half2_lo(p.x), half2_hi(p.x), half2_lo(p.y), half2_hi(p.y));
+        h = make_uint4(half2_lo(q.x), half2_hi(q.x), half2_lo(q.y), half2_hi(q.y));
       };
 #pragma unroll
       for (int j = 0; j < AHEAD; ++j) halves(code[j], lo[j], hi[j]);
@@ -609,8 +611,8 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv_attn_tc_kernel(const KvAttnP
         } else {
           halves(code[j], l, h);
         }
-        *reinterpret_cast<uint4*>(dst + off0 + j * (STEP * 128)) = flip ? h : l;
-        *reinterpret_cast<uint4*>(dst + off1 + j * (STEP * 128)) = flip ? l : h;
+        *reinterpret_cast<uint4*>(dst + off0 + j * (STEP * 128)) = l;
+        *reinterpret_cast<uint4*>(dst + off1 + j * (STEP * 128)) = h;
       }
       fence_proxy_async_shared();
       __syncwarp();
