@@ -23,6 +23,7 @@ constexpr size_t kAlign = 256;
 // its own (left zeroed), and the attention's partials after them.
 constexpr size_t kTicketsAt = 256;
 constexpr size_t kPartialsAt = kTicketsAt + sizeof(unsigned) * 2 * SV_MAX_B;
+static_assert(kPartialsAt % 16 == 0, "partials are read as float4");
 static_assert(sizeof(WsHeader) <= kTicketsAt && kKaMaxCtas <= 2 * SV_MAX_B, "workspace layout");
 
 struct Device {

@@ -41,6 +41,7 @@ constexpr int kKaThreads = kKaWarps * 32 + 32;
 constexpr int kKaCtasPerSm = 2;
 constexpr int kKaMaxCtas = 2 * 160;   // tickets and partials are sized for this many
 constexpr int kKaMinBlocks = 4;       // blocks below which a CTA is not worth starting
+constexpr int kKaUneven = 8;          // blocks a part may grow by to keep within its unit
 constexpr float kRefShift = 4.f, kRefSlack = 11.f;
 
 struct KvAttnProblem {
@@ -69,7 +70,7 @@ template <int D>
 struct KaShared {
   unsigned char k[kKaStages][kKaBlock * D];
   unsigned char v[kKaStages][kKaBlock * D];
-  float merge[2][kKaPartialFloats<D>];
+  alignas(16) float merge[2][kKaPartialFloats<D>];
   // cumulated block counts of the requests
   int prefix[SV_MAX_B + 1];
   int scan[8];
@@ -111,6 +112,11 @@ __device__ __forceinline__ int ka_tile_blocks(const KvAttnProblem& a, const KaLe
   return (l.len + last + 1 + BLOCK - 1) / BLOCK;
 }
 
+// A unit's place in the list when every unit begins at a multiple of pad.
+__device__ __forceinline__ int ka_padded(int nblk, int pad) {
+  return pad == 1 ? nblk : (nblk + pad - 1) / pad * pad;
+}
+
 // A position in the list of all blocks: request, unit of the request
 // (key/value head major, row tile minor) and block of the unit.
 template <int ROWS, int BLOCK>
@@ -123,7 +129,8 @@ struct KaCursor {
     l = ka_len(a, b, &bad);
     tiles = (l.n * a.G + ROWS - 1) / ROWS;
   }
-  __device__ __forceinline__ void seek(const KvAttnProblem& a, const int* prefix, int at) {
+  __device__ __forceinline__ void seek(const KvAttnProblem& a, const int* prefix, int at,
+                                       int pad = 1) {
     int lo = 0, hi = a.B;  // the last b with prefix[b] <= at
     while (hi - lo > 1) {
       const int mid = (lo + hi) / 2;
@@ -137,8 +144,9 @@ struct KaCursor {
 #pragma unroll 1
     for (tile = 0;; ++tile) {
       nblk = ka_tile_blocks<ROWS, BLOCK>(a, l, tile);
-      if (at < unit0 + nblk || tile + 1 >= tiles) break;
-      unit0 += nblk;
+      const int all = ka_padded(nblk, pad);
+      if (at < unit0 + all || tile + 1 >= tiles) break;
+      unit0 += all;
     }
     blk = at - unit0;
   }
@@ -164,7 +172,7 @@ struct KaCursor {
 // thread of the block calls this); returns their total.
 template <int ROWS, int BLOCK, int THREADS>
 __device__ __forceinline__ int ka_prefix(const KvAttnProblem& a, int* prefix, int* scan,
-                                         bool report) {
+                                         bool report, int pad = 1) {
   const int tid = static_cast<int>(threadIdx.x), warp = tid >> 5, lane = tid & 31;
   int total = 0;
 #pragma unroll 1
@@ -177,7 +185,8 @@ __device__ __forceinline__ int ka_prefix(const KvAttnProblem& a, int* prefix, in
       if (bad && report) record_error(a.err, SV_DERR_ARG);
       const int tiles = (l.n * a.G + ROWS - 1) / ROWS;
 #pragma unroll 1
-      for (int tile = 0; tile < tiles; ++tile) mine += ka_tile_blocks<ROWS, BLOCK>(a, l, tile);
+      for (int tile = 0; tile < tiles; ++tile)
+        mine += ka_padded(ka_tile_blocks<ROWS, BLOCK>(a, l, tile), pad);
       mine *= a.c.Hkv;
     }
     int x = mine;
@@ -221,6 +230,7 @@ __device__ __forceinline__ void ka_clear_rows(const KvAttnProblem& a, int thread
 // the others `per`.  (The calls' sizes keep the number of blocks below 2^31.)
 struct KaParts {
   int count, per, more;
+  __device__ __forceinline__ KaParts(int count_, int per_) : count(count_), per(per_), more(0) {}
   __device__ __forceinline__ KaParts(int total, int most, int least) {
     count = max(1, min(most, total / least));
     per = total / count;
@@ -311,14 +321,17 @@ struct KaFeed {
     return it;
   }
   // positions the lane at its block of the first batch; look() comes next
-  __device__ __forceinline__ void start(const KvAttnProblem& a, const int* prefix, int w0, int n,
-                                        int lane, bool v = false) {
-    cur.seek(a, prefix, w0);
+  __device__ __forceinline__ int start(const KvAttnProblem& a, const int* prefix, int w0, int n,
+                                        int lane, bool v = false, int pad = 1) {
+    cur = {};
+    cur.seek(a, prefix, w0, pad);
+    if (pad > 1) n = min(n, cur.nblk - cur.blk);  // the part ends with its unit
     left = n;
     sub = lane % (BLOCK / 16);
     is_v = SIDES == 1 ? v : lane % kCopies >= BLOCK / 16;
     page = -2;
     advance(a, lane / kCopies);
+    return n;
   }
 };
 
@@ -390,36 +403,34 @@ struct KaAcc {
 #pragma unroll
     for (int j = 0; j < D / 8; ++j) o[j][0] = o[j][1] = o[j][2] = o[j][3] = 0.f;
   }
-  // join with another partial (its statistics given, its O read through get)
-  template <class Get>
-  __device__ __forceinline__ void join(float r0, float r1, float z0, float z1, Get get) {
-    const float n0 = fmaxf(ref[0], r0), n1 = fmaxf(ref[1], r1);
+  // join with another partial
+  __device__ __forceinline__ void join(const float* p, int lane) {
+    const float4* const q = reinterpret_cast<const float4*>(p) + lane;
+    const float4 s = q[0];
+    const float n0 = fmaxf(ref[0], s.x), n1 = fmaxf(ref[1], s.y);
     const float a0 = ref[0] == kNegInf ? 0.f : fast_exp2(ref[0] - n0);
     const float a1 = ref[1] == kNegInf ? 0.f : fast_exp2(ref[1] - n1);
-    const float b0 = r0 == kNegInf ? 0.f : fast_exp2(r0 - n0);
-    const float b1 = r1 == kNegInf ? 0.f : fast_exp2(r1 - n1);
+    const float b0 = s.x == kNegInf ? 0.f : fast_exp2(s.x - n0);
+    const float b1 = s.y == kNegInf ? 0.f : fast_exp2(s.y - n1);
     ref[0] = n0;
     ref[1] = n1;
-    z[0] = z[0] * a0 + z0 * b0;
-    z[1] = z[1] * a1 + z1 * b1;
+    z[0] = z[0] * a0 + s.z * b0;
+    z[1] = z[1] * a1 + s.w * b1;
 #pragma unroll
     for (int j = 0; j < D / 8; ++j) {
-      o[j][0] = o[j][0] * a0 + get(4 * j) * b0;
-      o[j][1] = o[j][1] * a0 + get(4 * j + 1) * b0;
-      o[j][2] = o[j][2] * a1 + get(4 * j + 2) * b1;
-      o[j][3] = o[j][3] * a1 + get(4 * j + 3) * b1;
+      const float4 v = q[(1 + j) * 32];
+      o[j][0] = o[j][0] * a0 + v.x * b0;
+      o[j][1] = o[j][1] * a0 + v.y * b0;
+      o[j][2] = o[j][2] * a1 + v.z * b1;
+      o[j][3] = o[j][3] * a1 + v.w * b1;
     }
   }
-  // p[i * 32 + lane]: every access of a warp is one line
   __device__ __forceinline__ void store(float* p, int lane) const {
-    p[lane] = ref[0];
-    p[32 + lane] = ref[1];
-    p[64 + lane] = z[0];
-    p[96 + lane] = z[1];
+    float4* const q = reinterpret_cast<float4*>(p) + lane;
+    q[0] = make_float4(ref[0], ref[1], z[0], z[1]);
 #pragma unroll
     for (int j = 0; j < D / 8; ++j)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) p[(4 + 4 * j + i) * 32 + lane] = o[j][i];
+      q[(1 + j) * 32] = make_float4(o[j][0], o[j][1], o[j][2], o[j][3]);
   }
 };
 
@@ -442,10 +453,10 @@ __device__ __forceinline__ float2 ka_two(const __nv_bfloat16* p) {
 // The producer warp: n blocks from w0 on, through the ring of stages.
 template <int D, class Feed, class Shared>
 __device__ __forceinline__ void ka_produce(const KvAttnProblem& a, Shared& sh, int w0, int n,
-                                           int lane) {
+                                           int lane, int pad) {
   const uint64_t pol = policy_evict_first();
   Feed feed;
-  feed.start(a, sh.prefix, w0, n, lane);
+  n = feed.start(a, sh.prefix, w0, n, lane, false, pad);
   typename Feed::Item item = {}, next = {};
   int i = 0;
 #pragma unroll 1
@@ -494,18 +505,33 @@ __global__ void __launch_bounds__(kKaThreads, kKaCtasPerSm) kv_attn_kernel(const
   }
   grid_dependency_wait();
 
-  const int total = ka_prefix<kKaRows, kKaBlock, kKaThreads>(a, sh.prefix, sh.scan, cta == 0);
+  // Few units: parts that do not cross from one unit to the next, as long as
+  // they get at most kKaUneven blocks longer by that (a block takes a CTA 0.6
+  // us, a second unit 6 us: B = 7, 12 heads, 1500 tokens 18.8 -> 14 us).  Their
+  // number stays below the grid's: sum ceil(n_u / q) <= total / q + units.
+  int total, pad = 1;
+#pragma unroll 1
+  for (;;) {
+    total = ka_prefix<kKaRows, kKaBlock, kKaThreads>(a, sh.prefix, sh.scan, cta == 0, pad);
+    const int units = a.B * a.c.Hkv * ((a.T * a.G + kKaRows - 1) / kKaRows);
+    if (pad > 1 || 2 * units > grid || total >= 1 << 30) break;
+    const int room = grid - units;
+    const int q = max(kKaMinBlocks, (total + room - 1) / room);
+    if (q > total / grid + kKaUneven) break;
+    pad = q;
+  }
   ka_clear_rows<T, D, kKaThreads>(a, tid);
 
   // this CTA's part of the blocks
-  const KaParts parts(total, grid, kKaMinBlocks);
+  const KaParts parts = pad > 1 ? KaParts(total / pad, pad) : KaParts(total, grid, kKaMinBlocks);
   if (cta >= parts.count) return;
-  const int w0 = parts.begin(cta), n = parts.begin(cta + 1) - w0;
+  const int w0 = parts.begin(cta);
+  int n = parts.begin(cta + 1) - w0;
   if (n <= 0) return;
 
   if (warp == kKaWarps) {
     // ------------------------------------------------------------ producer
-    ka_produce<D, KaFeed<kKaRows, kKaBlock, 2>>(a, sh, w0, n, lane);
+    ka_produce<D, KaFeed<kKaRows, kKaBlock, 2>>(a, sh, w0, n, lane, pad);
     return;
   }
 
@@ -513,8 +539,9 @@ __global__ void __launch_bounds__(kKaThreads, kKaCtasPerSm) kv_attn_kernel(const
   const int g = lane >> 2, t = lane & 3;
   const int pair = warp >> 1, half = warp & 1;  // pairs take alternate blocks, warps a half each
   constexpr int KS = D / 16;
-  KaCursor<kKaRows, kKaBlock> cur;
-  cur.seek(a, sh.prefix, w0);
+  KaCursor<kKaRows, kKaBlock> cur{};
+  cur.seek(a, sh.prefix, w0, pad);
+  if (pad > 1) n = min(n, cur.nblk - cur.blk);
   for (int w = 0; w < n;) {
     const int h = cur.head, tile = cur.tile;
     const int blk0 = cur.blk;
@@ -765,18 +792,14 @@ __global__ void __launch_bounds__(kKaThreads, kKaCtasPerSm) kv_attn_kernel(const
     // join the four warps: 1 -> 0 and 3 -> 2, then 2 -> 0
     acc.z[0] = quad_sum(acc.z[0]);
     acc.z[1] = quad_sum(acc.z[1]);
-    auto join_smem = [&](const float* p) {
-      acc.join(p[lane], p[32 + lane], p[64 + lane], p[96 + lane],
-               [&](int i) { return p[(4 + i) * 32 + lane]; });
-    };
     named_sync(1, kKaWarps * 32);  // the buffers are free
     if (warp & 1) acc.store(sh.merge[warp >> 1], lane);
     named_sync(1, kKaWarps * 32);
-    if (!(warp & 1)) join_smem(sh.merge[warp >> 1]);
+    if (!(warp & 1)) acc.join(sh.merge[warp >> 1], lane);
     named_sync(1, kKaWarps * 32);
     if (warp == 2) acc.store(sh.merge[0], lane);
     named_sync(1, kKaWarps * 32);
-    if (warp == 0) join_smem(sh.merge[0]);
+    if (warp == 0) acc.join(sh.merge[0], lane);
 
     const bool starts = blk0 == 0, ends = blk1 == cur.nblk;
     // the rows' results, channels of tiles j0 .. j0 + NJ - 1
@@ -837,40 +860,44 @@ __global__ void __launch_bounds__(kKaThreads, kKaCtasPerSm) kv_attn_kernel(const
         // the channels, and leaves zeros behind.
         __threadfence();
         constexpr int NJ = D / 32;
-        auto part = [&](int c) { return a.partials + (2ll * c + (c == first ? 1 : 0)) * PF; };
-        float m0 = kNegInf, m1 = kNegInf;
-#pragma unroll 8
-        for (int c = first; c <= last; ++c) {
-          m0 = fmaxf(m0, __ldcg(part(c) + lane));
-          m1 = fmaxf(m1, __ldcg(part(c) + 32 + lane));
-        }
-        float z0 = 0.f, z1 = 0.f, o[4 * NJ];
+        auto part = [&](int c) {
+          return reinterpret_cast<float4*>(a.partials + (2ll * c + (c == first ? 1 : 0)) * PF) + lane;
+        };
+        float m0 = kNegInf, m1 = kNegInf, z0 = 0.f, z1 = 0.f, o[4 * NJ];
 #pragma unroll
         for (int i = 0; i < 4 * NJ; ++i) o[i] = 0.f;
-#pragma unroll 2
+#pragma unroll 4
         for (int c = first; c <= last; ++c) {
-          float* p = part(c);
-          const float r0 = __ldcg(p + lane), r1 = __ldcg(p + 32 + lane);
-          // a part that saw nothing has Z = 0 and O = 0 (or NaN, which stays)
-          const float f0 = r0 == kNegInf ? 1.f : fast_exp2(r0 - m0);
-          const float f1 = r1 == kNegInf ? 1.f : fast_exp2(r1 - m1);
-          z0 = fmaf(__ldcg(p + 64 + lane), f0, z0);
-          z1 = fmaf(__ldcg(p + 96 + lane), f1, z1);
-          float* po = p + (4 + 4 * NJ * warp) * 32 + lane;
+          const float4* const q = part(c);
+          const float4 st = __ldcg(q);
+          const float n0 = fmaxf(m0, st.x), n1 = fmaxf(m1, st.y);
+          // what saw nothing has Z = 0 and O = 0 (or NaN, which stays)
+          auto factor = [](float r, float n) { return r == kNegInf ? 1.f : fast_exp2(r - n); };
+          const float a0 = factor(m0, n0), a1 = factor(m1, n1);
+          const float f0 = factor(st.x, n0), f1 = factor(st.y, n1);
+          m0 = n0;
+          m1 = n1;
+          z0 = fmaf(st.z, f0, z0 * a0);
+          z1 = fmaf(st.w, f1, z1 * a1);
 #pragma unroll
-          for (int i = 0; i < 4 * NJ; ++i)
-            o[i] = fmaf(__ldcg(po + i * 32), (i & 2) ? f1 : f0, o[i]);
+          for (int j = 0; j < NJ; ++j) {
+            const float4 v = __ldcg(q + (1 + NJ * warp + j) * 32);
+            o[4 * j] = fmaf(v.x, f0, o[4 * j] * a0);
+            o[4 * j + 1] = fmaf(v.y, f0, o[4 * j + 1] * a0);
+            o[4 * j + 2] = fmaf(v.z, f1, o[4 * j + 2] * a1);
+            o[4 * j + 3] = fmaf(v.w, f1, o[4 * j + 3] * a1);
+          }
         }
+        finish(z0, z1, m0, m1, NJ * warp, KaInt<NJ>(), [&](int i) { return o[i]; });
         named_sync(1, kKaWarps * 32);  // the statistics have been read
         for (int c = first; c <= last; ++c) {
-          float* p = part(c);
-          p[warp * 32 + lane] = 0.f;
-          float* po = p + (4 + 4 * NJ * warp) * 32 + lane;
+          float4* const q = part(c);
+          const float4 none = make_float4(0.f, 0.f, 0.f, 0.f);
+          if (warp == 0) q[0] = none;
 #pragma unroll
-          for (int i = 0; i < 4 * NJ; ++i) po[i * 32] = 0.f;
+          for (int j = 0; j < NJ; ++j) q[(1 + NJ * warp + j) * 32] = none;
         }
         if (tid == 0) a.tickets[first] = 0u;
-        finish(z0, z1, m0, m1, NJ * warp, KaInt<NJ>(), [&](int i) { return o[i]; });
       }
     }
     w += blk1 - blk0;
