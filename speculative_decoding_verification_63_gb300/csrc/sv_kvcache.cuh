@@ -296,7 +296,8 @@ __global__ void __launch_bounds__(kKvThreads) kv_read_kernel(const KvReadProblem
   if (!ok && blockIdx.x == 0 && side == 0 && threadIdx.x == 0) record_error(a.err, SV_DERR_ARG);
   const long long start = a.start ? a.start[b] : 0;
 #pragma unroll 1
-  for (int at0 = static_cast<int>(threadIdx.x); at0 < chunks; at0 += kKvThreads * kKvReadChunks) {
+  for (int at0 = static_cast<int>(threadIdx.x); (at0 & ~31) < chunks;  // whole warps
+       at0 += kKvThreads * kKvReadChunks) {
     uint4 code[kKvReadChunks];
     float s[kKvReadChunks];
     int th[kKvReadChunks];  // token of the block, and head
@@ -331,7 +332,6 @@ __global__ void __launch_bounds__(kKvThreads) kv_read_kernel(const KvReadProblem
 #pragma unroll
     for (int j = 0; j < kKvReadChunks; ++j) {
       const int at = at0 + j * kKvThreads;
-      if (at >= chunks) break;
       T* p = out + (t0 + (th[j] >> 8)) * a.token + (th[j] & 255) * a.head + (at & (parts - 1)) * 16;
       Raw16<T> y;
       T* e = reinterpret_cast<T*>(y.w);
@@ -345,10 +345,23 @@ __global__ void __launch_bounds__(kKvThreads) kv_read_kernel(const KvReadProblem
         e[4 * q + 3] = from_float<T>(hi.y * s[j]);
       }
       if (a.vec) {
+        // Two lanes hold neighbouring chunks (a token and head has an even
+        // number): they swap halves, so that each store fills whole sectors.
+        const bool odd = threadIdx.x & 1;
+        uint4* const pair = reinterpret_cast<uint4*>(p - (odd ? 16 : 0)) + odd;
 #pragma unroll
-        for (int q = 0; q < static_cast<int>(sizeof(T)); ++q)
-          __stcs(reinterpret_cast<uint4*>(p) + q, y.w[q]);
-      } else {
+        for (int q = 0; q < static_cast<int>(sizeof(T)); q += 2) {
+          const uint4 mine = odd ? y.w[q + 1] : y.w[q], give = odd ? y.w[q] : y.w[q + 1];
+          uint4 got;
+          got.x = __shfl_xor_sync(0xffffffffu, give.x, 1);
+          got.y = __shfl_xor_sync(0xffffffffu, give.y, 1);
+          got.z = __shfl_xor_sync(0xffffffffu, give.z, 1);
+          got.w = __shfl_xor_sync(0xffffffffu, give.w, 1);
+          if (at >= chunks) continue;
+          __stcs(pair + q, odd ? got : mine);
+          __stcs(pair + sizeof(T) + q, odd ? mine : got);
+        }
+      } else if (at < chunks) {
 #pragma unroll
         for (int q = 0; q < 16; ++q) p[q] = e[q];
       }
