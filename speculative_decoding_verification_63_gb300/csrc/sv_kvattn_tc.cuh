@@ -94,8 +94,7 @@ struct TcShared {
   int scan[kTcThreads / 32 + 1];
   unsigned short nanmask[2][kTcBlock][D / 16];  // NaN value codes of the streams' edge blocks
   TcMeta meta[kTcMeta];
-  float scratch[2][kTcRows];  // the queries' largest values
-  float c2[2][kTcRows];       // the score factors of the unit's rows (tc_load_q)
+  float c2[2][kTcRows];       // the score factors of two units' rows (tc_load_q)
   float ends[2][2][kTcRows];  // references and sums of the streams
   unsigned long long nanrow[D / 64][kTcRows];  // channels in which a lane's row saw a NaN
   KaCursor<kTcRows, kTcBlock> cur[8];          // the softmax warps' places
@@ -310,59 +309,64 @@ __device__ __forceinline__ uint32_t tc_seen(int4 row, const TcMeta& m, int piece
   return tokens >= 16 ? seen : seen & ((1u << tokens) - 1);
 }
 
-// The unit's queries into shared memory, as halves, in the operands' layout:
-// thread = row, set s the s-th half of the channels.  Returns |scale| log2(e)
-// 2^(the row's exponent) (the sign goes to the queries): bf16 rows are scaled
-// by a power of two into the halves' range, found by the row's two threads
-// together.
+// Sixteen rows of the unit's queries into shared memory, as halves, in the
+// operands' layout, by one warp: a lane takes eight channels.  c2[row] becomes
+// |scale| log2(e) 2^(the row's exponent) (the sign goes to the queries): bf16
+// rows are scaled by a power of two into the halves' range.  (Whole warps on a
+// row keep this code short: it runs once a unit, mostly from a cold
+// instruction cache.)
 template <int D, class T>
-__device__ __forceinline__ float tc_load_q(const KvAttnProblem& a, const T* qp, bool mine, int set,
-                                           unsigned char* qh, float (*exch)[kTcRows], int row,
-                                           int quarter) {
-  constexpr int N = D / 8;
-  uint2 w[N];
+__device__ __forceinline__ void tc_load_q(const KvAttnProblem& a,
+                                          const KaCursor<kTcRows, kTcBlock>& cur,
+                                          unsigned char* qh, float* c2, int row0, int lane) {
+  constexpr int LANES = D / 8, ROWS = 32 / LANES, BATCH = 4;
+  const int piece = lane % LANES;  // 16 bytes of the row
+#pragma unroll 1
+  for (int k0 = 0; k0 < 16; k0 += ROWS * BATCH) {
+    uint2 w[BATCH][2];
 #pragma unroll
-  for (int i = 0; i < N; ++i) {
-    w[i] = make_uint2(0, 0);
-    if (mine) {
-      const T* p = qp + set * (D / 2) + 4 * i;
-      w[i] = a.q_vec ? *reinterpret_cast<const uint2*>(p)
-                     : ka_load4(reinterpret_cast<const unsigned short*>(p));
+    for (int k = 0; k < BATCH; ++k) {
+      const TcUnit u = tc_unit(a, cur, row0 + k0 + k * ROWS + lane / LANES);
+      w[k][0] = w[k][1] = make_uint2(0, 0);
+      if (u.mine) {
+        const T* const p = static_cast<const T*>(a.q) + cur.b * a.q_batch + u.t * a.q_token +
+                           u.hq * a.q_head + piece * 8;
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+          w[k][h] = a.q_vec ? *reinterpret_cast<const uint2*>(p + 4 * h)
+                            : ka_load4(reinterpret_cast<const unsigned short*>(p + 4 * h));
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < BATCH; ++k) {
+      const int row = row0 + k0 + k * ROWS + lane / LANES;
+      int ex = 0;
+      if (!__is_same(T, __half)) {
+        float m = 0.f;
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+          m = fmaxf(fmaxf(m, fmaxf(fabsf(bf16lo(w[k][h].x)), fabsf(bf16hi(w[k][h].x)))),
+                    fmaxf(fabsf(bf16lo(w[k][h].y)), fabsf(bf16hi(w[k][h].y))));
+#pragma unroll
+        for (int o = 1; o < LANES; o <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+        // the row's largest value lands in [2^14, 2^15)
+        ex = min(max(static_cast<int>(__float_as_uint(m) >> 23) - 127 - 14, -100), 100);
+      }
+      const float f = a.scale_log2 < 0.f ? -pow2f(-ex) : pow2f(-ex);
+      unsigned h[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const float2 x = ka_two(reinterpret_cast<const T*>(&w[k][0]) + 2 * j);
+        h[j] = half2_of(x.x * f, x.y * f);
+      }
+      *reinterpret_cast<uint4*>(qh + (piece >> 3) * (kTcRows * 128) + row * 128 +
+                                (((piece & 7) ^ (row & 7)) << 4)) =
+          make_uint4(h[0], h[1], h[2], h[3]);
+      // (not 0: masked scores are -inf and stay so)
+      if (piece == 0) c2[row] = fmaxf(fabsf(a.scale_log2) * pow2f(ex), 1e-30f);
     }
   }
-  int ex = 0;
-  if (!__is_same(T, __half)) {
-    float m = 0.f;
-#pragma unroll
-    for (int i = 0; i < N; ++i)
-      m = fmaxf(fmaxf(m, fmaxf(fabsf(bf16lo(w[i].x)), fabsf(bf16hi(w[i].x)))),
-                fmaxf(fabsf(bf16lo(w[i].y)), fabsf(bf16hi(w[i].y))));
-    exch[set][row] = m;
-    named_sync(2 + quarter, 64);
-    m = fmaxf(m, exch[set ^ 1][row]);
-    // the row's largest value lands in [2^14, 2^15)
-    ex = min(max(static_cast<int>(__float_as_uint(m) >> 23) - 127 - 14, -100), 100);
-  }
-  const float k = a.scale_log2 < 0.f ? -pow2f(-ex) : pow2f(-ex);
-#pragma unroll
-  for (int i = 0; i < N; i += 2) {
-    uint4 h;
-    const T* e = reinterpret_cast<const T*>(&w[i]);
-    float2 x = ka_two(e), y = ka_two(e + 2);
-    h.x = half2_of(x.x * k, x.y * k);
-    h.y = half2_of(y.x * k, y.y * k);
-    e = reinterpret_cast<const T*>(&w[i + 1]);
-    x = ka_two(e);
-    y = ka_two(e + 2);
-    h.z = half2_of(x.x * k, x.y * k);
-    h.w = half2_of(y.x * k, y.y * k);
-    const int piece = (set * (D / 2) + 4 * i) / 8;  // 16-byte piece of the row
-    *reinterpret_cast<uint4*>(qh + (piece >> 3) * (kTcRows * 128) + row * 128 +
-                              (((piece & 7) ^ (row & 7)) << 4)) = h;
-  }
   fence_proxy_async_shared();
-  // (not 0: masked scores are -inf and stay so)
-  return fmaxf(fabsf(a.scale_log2) * pow2f(ex), 1e-30f);
 }
 
 // The queries of a unit on their way into the cache, two batches before the
@@ -679,6 +683,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv_attn_tc_kernel(const KvAttnP
       __syncwarp();
     }
     // One unit a turn; the first turn (i0 < 0) only loads the first queries.
+    int odd = 0;  // of the unit, by turns
     for (int i0 = -1; i0 < n;) {
       int nb = 0, cs = 0, base = 0;
       bool warp_live = false;
@@ -692,7 +697,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv_attn_tc_kernel(const KvAttnP
       }
       // of a block's eight 16-position pieces: `own` from `base` on
       const int own = 8 >> cs;
-      const float c2 = sh.c2[set][row];
+      const float c2 = sh.c2[odd][row];
       float ref = kNegInf, z = 0.f;
       bool had = false;  // this stream has taken a block of the unit
 
@@ -837,15 +842,14 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv_attn_tc_kernel(const KvAttnP
           tc_wait(&sh.sfull[set ^ 1], static_cast<uint32_t>(io >> 1) & 1, dead, a.err);
       }
       if (max(i0, 0) + nb < n) {
-        const TcUnit me = tc_unit(a, cur, row);
-        if (me.warp_live(quarter))
-          sh.c2[set][row] = tc_load_q<D, T>(a,
-                               static_cast<const T*>(a.q) + cur.b * a.q_batch +
-                                   me.t * a.q_token + me.hq * a.q_head,
-                               me.mine, set, sh.qh, sh.scratch, row, quarter);
+        if (tc_unit(a, cur, row).warp_live(quarter)) {
+          tc_load_q<D, T>(a, cur, sh.qh, sh.c2[odd ^ 1], quarter * 32 + set * 16, lane);
+          named_sync(2 + quarter, 64);  // the other warp's factors
+        }
         __syncwarp();
         if (lane == 0) mbar_arrive(&sh.qfull);
       }
+      odd ^= 1;
       if (i0 < 0) {
         i0 = 0;
         continue;
