@@ -137,11 +137,12 @@ sv_status launch_attention_tc(const KvAttnProblem& p, int sms, cudaStream_t stre
 }
 
 // Rounds of up to kKaFewRows query rows a key/value head take the warp-level
-// products (each tile of 16 rows reads the cache: the second time from L2),
-// larger ones the tensor-memory ones.  A chain round of 28 rows (64 requests,
-// up to 4096 tokens): 92 us against 153 us; a tree of 128 rows: 372 us against
-// 104 us.
-constexpr int kKaFewRows = 32;
+// products (each tile of 16 rows reads the cache, all but the first from L2),
+// larger ones the tensor-memory ones.  64 requests of up to 4096 tokens: 28
+// rows 91 us against 132, 36 rows 111 against 144, 48 rows 149 against 152, 64
+// rows 176 against 149; 8 requests of 16000: 32 rows 53 against 75, 48 rows 80
+// against 76.
+constexpr int kKaFewRows = 48;
 
 template <int D, class T>
 sv_status run_attention(const KvAttnProblem& p, int sms, cudaStream_t stream) {

@@ -909,11 +909,11 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv_attn_tc_kernel(const KvAttnP
         // (memory: the second turn of a CTA that left its part and arrived last)
         float m = ref, zt = z;  // of the whole row
         if (joins && !whole && writes) {
-#pragma unroll 1
+#pragma unroll 4
           for (int c = first; c <= last; ++c)
-            if (c != cta) m = fmaxf(m, __ldcg(tc_part<D>(a, c, first) + r));
+            m = fmaxf(m, c == cta ? ref : __ldcg(tc_part<D>(a, c, first) + r));
           zt = 0.f;
-#pragma unroll 1
+#pragma unroll 4
           for (int c = first; c <= last; ++c) {
             const float* const p = tc_part<D>(a, c, first);
             const float rc = c == cta ? ref : __ldcg(p + r);
@@ -980,25 +980,34 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv_attn_tc_kernel(const KvAttnP
             float y[16];
 #pragma unroll
             for (int j = 0; j < 16; ++j) y[j] = 0.f;
+            // two parts at a time: their loads are under way together
 #pragma unroll 1
-            for (int k = first; k <= last; ++k) {
-              float* const p = tc_part<D>(a, k, first) + (2 + c) * kTcRows + r;
-              float v[16];
-              float rk = ref;
-              if (k != cta) {
-                rk = __ldcg(tc_part<D>(a, k, first) + r);
+            for (int k = first; k <= last; k += 2) {
+              float v[2][16], rk[2];
 #pragma unroll
-                for (int j = 0; j < 16; ++j) v[j] = __ldcg(p + j * kTcRows);
-              } else {
+              for (int q = 0; q < 2; ++q) {
+                // (a place past the last part reads the first one, for nothing)
+                const bool own = k + q == cta && !memory;
+                const float* const p = tc_part<D>(a, k + q <= last ? k + q : first, first) + r;
+                rk[q] = __ldcg(p);
 #pragma unroll
-                for (int j = 0; j < 16; ++j) v[j] = x[j];
+                for (int j = 0; j < 16; ++j) v[q][j] = __ldcg(p + (2 + c + j) * kTcRows);
+                if (own) {
+                  rk[q] = ref;
+#pragma unroll
+                  for (int j = 0; j < 16; ++j) v[q][j] = x[j];
+                }
               }
-              const float f = tc_factor(rk, m);
 #pragma unroll
-              for (int j = 0; j < 16; ++j) y[j] = fmaf(v[j], f, y[j]);
-              if (k != cta || memory) {
+              for (int q = 0; q < 2; ++q) {
+                if (k + q > last) break;
+                const float f = tc_factor(rk[q], m);
+                float* const p = tc_part<D>(a, k + q, first) + (2 + c) * kTcRows + r;
 #pragma unroll
-                for (int j = 0; j < 16; ++j) p[j * kTcRows] = 0.f;
+                for (int j = 0; j < 16; ++j) y[j] = fmaf(v[q][j], f, y[j]);
+                if (k + q != cta || memory)
+#pragma unroll
+                  for (int j = 0; j < 16; ++j) p[j * kTcRows] = 0.f;
               }
             }
 #pragma unroll

@@ -290,6 +290,8 @@ ATTENTION = [  # lens, new, T, Hq, H, P, D, dtype
     ([77, 0, 64, 129], [25, 24, 1, 0], 25, 4, 2, 16, 64, "bf16"),
     ([150, 65], [20, 17], 20, 5, 5, 64, 64, "fp16"),
     ([3001, 4], [8, 5], 8, 8, 2, 128, 128, "bf16"),
+    ([5000, 0, 700], [60, 60, 1], 60, 1, 1, 64, 128, "bf16"),
+    ([9000], [12], 12, 16, 4, 32, 64, "fp16"),
 ]
 
 
