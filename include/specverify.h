@@ -415,6 +415,8 @@ sv_status sv_kv_read(const sv_kv_read_args* args, void* workspace, size_t ws_byt
  * kv_len < 0, num_new outside [0, T] or a length past slots * page_size
  * records SV_DERR_ARG (all rows of the request as if n were 0); a page id
  * outside [0, num_pages) records SV_DERR_PAGE and no row sees that page.
+ * SV_EINVAL also for slots * page_size > 2^30 and for
+ * B * Hkv * ceil(T * Hq / Hkv / 16) * ceil(slots * page_size / 64) >= 2^31.
  */
 typedef struct {
   sv_kv_cache cache;

@@ -185,8 +185,8 @@ def kv_read(cache: dict, page_table, start, num, T: int, rows=None, dtype=torch.
     [B][T][heads][D] (device tensors)."""
     _, H, _, D = cache["k"].shape
     dev = page_table.device
-    k, v = torch.empty((2, page_table.shape[0], T, H, D), dtype=dtype, device=dev).unbind()
-    out = dict(k=k, v=v)
+    k = torch.empty((page_table.shape[0], T, H, D), dtype=dtype, device=dev)
+    out = dict(k=k, v=torch.empty_like(k))
     if ws is None:
         ws = workspace(SV_MIN_WORKSPACE_BYTES, dev, "kv")
     sv_kv_read(cache, page_table, start, num, out["k"], out["v"], ws, rows=rows)

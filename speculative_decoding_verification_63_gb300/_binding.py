@@ -8,6 +8,7 @@ the library is missing or returns an error status.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 import struct
 
@@ -563,6 +564,7 @@ def sv_kv_read(cache: dict, page_table, start, num, k_out, v_out, workspace, row
                                       count, which), workspace, stream)
 
 
+@functools.lru_cache(maxsize=1024)
 def sv_kv_attention_workspace_bytes(B: int, T: int, Hq: int, Hkv: int, D: int) -> int:
     return lib().sv_kv_attention_workspace_bytes(B, T, Hq, Hkv, D)
 

@@ -115,25 +115,12 @@ sv_status launch(void (*kernel)(P), const P& p, dim3 grid, int threads, size_t s
   return e == cudaSuccess ? SV_OK : SV_ECUDA;
 }
 
-sv_status launch_warps(void (*kernel)(KvAttnProblem), size_t smem, const KvAttnProblem& p, int sms,
-                       cudaStream_t stream) {
+sv_status launch_large(void (*kernel)(KvAttnProblem), const KvAttnProblem& p, int grid,
+                       int threads, size_t smem, cudaStream_t stream) {
   if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                            static_cast<int>(smem)) != cudaSuccess)
     return SV_ECUDA;
-  const int grid = std::min(kKaCtasPerSm * sms, kKaMaxCtas);
-  return launch(kernel, p, dim3(static_cast<unsigned>(grid)), kKaThreads, smem, stream);
-}
-
-template <int D, class T>
-sv_status launch_attention_tc(const KvAttnProblem& p, int sms, cudaStream_t stream) {
-  constexpr size_t smem = sizeof(TcShared<D>) + 1024;
-  static_assert(smem <= 227 * 1024, "a CTA fits an SM");
-  if (cudaFuncSetAttribute(kv_attn_tc_kernel<D, T>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                           static_cast<int>(smem)) != cudaSuccess)
-    return SV_ECUDA;
-  const int grid = std::min(sms, kTcMaxCtas);
-  return launch(kv_attn_tc_kernel<D, T>, p, dim3(static_cast<unsigned>(grid)), kTcThreads, smem,
-                stream);
+  return launch(kernel, p, dim3(static_cast<unsigned>(grid)), threads, smem, stream);
 }
 
 // Rounds of up to kKaFewRows query rows a key/value head take the warp-level
@@ -148,9 +135,12 @@ template <int D, class T>
 sv_status run_attention(const KvAttnProblem& p, int sms, cudaStream_t stream) {
   static_assert(kKaCtasPerSm * (sizeof(KaShared<D>) + 1024) <= 228 * 1024,
                 "kKaCtasPerSm CTAs fit an SM");
-  return p.T * p.G <= kKaFewRows
-             ? launch_warps(kv_attn_kernel<D, T>, sizeof(KaShared<D>), p, sms, stream)
-             : launch_attention_tc<D, T>(p, sms, stream);
+  static_assert(sizeof(TcShared<D>) + 1024 <= 227 * 1024, "a CTA fits an SM");
+  if (p.T * p.G <= kKaFewRows)
+    return launch_large(kv_attn_kernel<D, T>, p, std::min(kKaCtasPerSm * sms, kKaMaxCtas),
+                        kKaThreads, sizeof(KaShared<D>), stream);
+  return launch_large(kv_attn_tc_kernel<D, T>, p, std::min(sms, kTcMaxCtas), kTcThreads,
+                      sizeof(TcShared<D>) + 1024, stream);
 }
 
 // Strides of 16-byte accesses to rows of elements of `es` bytes.

@@ -1,5 +1,5 @@
 // sv_kvattn_tc.cuh -- attention over the 8-bit cache for rounds of more than
-// 16 query rows a key/value head (drafts x heads of a group: chains, trees,
+// kKaFewRows query rows a key/value head (drafts x heads of a group: trees,
 // prompt chunks), on the 5th-generation tensor cores.  The mathematics is
 // that of sv_kvattn.cuh.
 //
@@ -18,15 +18,26 @@
 //   17     allocates tensor memory, issues O_s += P_s V (P_s: the weights as
 //          halves, in the columns of S_s they came from).
 //   18, 19 bulk copies of raw key and value codes; 18 also the scales and the
-//          blocks' descriptions.  (One warp for both needed 1100 clocks for
-//          each side of a block, all of it latency of its own instructions:
-//          it, not the memory, set the pace.)
+//          blocks' descriptions.  (One warp for both takes 2700 clocks a
+//          block, all of it latency of its own instructions.)
 // Shared memory is the busiest unit: a block of 128 channels carries 64 KB of
 // raw codes (written, read), 64 KB of halves written and 96 KB read by the
 // products, 1750 clocks at 128 bytes a clock, against 1024 clocks of products
 // and the 1390 clocks in which HBM delivers those codes to one SM.  Blocks of
 // 64 positions would double the clocks of S: a product of 64 columns takes as
 // long as one of 128 (64 clocks, measured).
+//
+// What sets the pace is none of these but the way of a block through its
+// stream: scores 900 clocks, maximum 900, weights 1600, their way to the
+// products 400, products 800, with two streams 2350 clocks a block (one warp's
+// instructions share their scheduler with four others').  To that come, a unit,
+// some 5 us for the queries, masks and the result, and the join of cut units
+// (16 requests of up to 8192 tokens, 32 nodes, 128 rows: 86 us; 2 requests with
+// chunks of 1024 tokens: 167 us).  Tried: three score buffers and one
+// accumulator (streams hand their reference on): 107 and 324 us, a rise of the
+// maximum stalls both streams; weights in one pass over the scores: 116 and 231
+// us; all conversions of a block before the wait for its buffer: 92 and 177 us
+// (spills).
 //
 // Few rows.  The products take 128 rows at a time whatever they hold, but a
 // warp sees only 32 of them, so units of up to 64 (32) rows are laid down two
