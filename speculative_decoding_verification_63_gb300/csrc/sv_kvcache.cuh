@@ -111,6 +111,25 @@ __device__ __forceinline__ float elem16(const Raw16<__half>& r, int i) {
   return __half2float(reinterpret_cast<const __half*>(r.w)[i]);
 }
 
+// The largest magnitude, as bits, of sixteen values and m: bit patterns order
+// as magnitudes do, so two 16-bit values take one instruction.
+template <class T>
+__device__ __forceinline__ unsigned max_bits(const Raw16<T>& r, unsigned m) {
+  const unsigned* w = reinterpret_cast<const unsigned*>(r.w);
+#pragma unroll
+  for (int i = 0; i < 4 * static_cast<int>(sizeof(T)); ++i)
+    m = sizeof(T) == 2 ? __vmaxu2(m, w[i] & 0x7fff7fffu) : max(m, w[i] & 0x7fffffffu);
+  return m;
+}
+// Its value (both halves of m joined), infinite or NaN if one of them was.
+template <class T>
+__device__ __forceinline__ float value_of_bits(unsigned m) {
+  if (sizeof(T) == 4) return __uint_as_float(m);
+  const unsigned v = max(m & 0xffffu, m >> 16);
+  return __is_same(T, __half) ? __half2float(__ushort_as_half(static_cast<unsigned short>(v)))
+                              : __uint_as_float(v << 16);
+}
+
 // ------------------------------------------------------------------- write
 
 struct KvWriteProblem {
@@ -182,27 +201,30 @@ __global__ void __launch_bounds__(kKvThreads) kv_write_kernel(const KvWriteProbl
                  (side ? b * a.v_batch + h * a.v_head : b * a.k_batch + h * a.k_head);
   const long long tstride = side ? a.v_token : a.k_token;
   Raw16<T> x[CH];
-  float amax = 0.f;
-  bool bad = false;
 #pragma unroll
   for (int j = 0; j < CH; ++j) {
     const int c = gl + j * GT;
     if (c < chunks)
       load16(x[j], src + (first + (c >> pshift)) * tstride + (c & (parts - 1)) * 16, a.vec);
   }
+  unsigned bits = 0;
 #pragma unroll
-  for (int j = 0; j < CH; ++j) {
-    if (gl + j * GT < chunks) {
+  for (int j = 0; j < CH; ++j)
+    if (gl + j * GT < chunks) bits = max_bits(x[j], bits);
+  float amax = value_of_bits<T>(bits);
+  if (__builtin_expect(!(amax < kPosInf), 0)) {
+    // the finite ones only
+    record_error(a.err, SV_DERR_NONFINITE);
+    amax = 0.f;
 #pragma unroll
-      for (int k = 0; k < 16; ++k) {
-        const float m = fabsf(elem16(x[j], k));
-        const bool fin = m < kPosInf;  // false for NaN
-        bad |= !fin;
-        amax = fmaxf(amax, fin ? m : 0.f);
-      }
-    }
+    for (int j = 0; j < CH; ++j)
+      if (gl + j * GT < chunks)
+#pragma unroll
+        for (int k = 0; k < 16; ++k) {
+          const float m = fabsf(elem16(x[j], k));
+          amax = fmaxf(amax, m < kPosInf ? m : 0.f);
+        }
   }
-  if (bad) record_error(a.err, SV_DERR_NONFINITE);
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
   float* scale = (side ? a.c.v_scale : a.c.k_scale) + static_cast<long long>(page) * Hkv + h;
