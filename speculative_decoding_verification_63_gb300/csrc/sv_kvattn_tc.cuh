@@ -877,8 +877,12 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv_attn_tc_kernel(const KvAttnP
       tc_fence_after();
       const int step = kTcRows >> my.cs;  // lanes between a row's copies
       named_sync(1, kTcSoftmax);
+      // (Read here, where no warp can be in the next unit yet: behind the
+      // unit's last barrier a warp that is ahead may already set it again, and
+      // the warps would part at the barriers below.)
+      const bool nans = sh.nanany != 0;
       uint64_t nanw = 0;  // the row's NaN channels, whichever of its lanes saw them
-      if (sh.nanany)
+      if (nans)
         for (int l = row & (step - 1); l < kTcRows; l += step)
           nanw |= sh.nanrow[D == 128 ? set : 0][l];
       float f0, f1;  // this copy's factors, of both streams
@@ -1066,8 +1070,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv_attn_tc_kernel(const KvAttnP
       }
       tc_fence_before();
       named_sync(1, kTcSoftmax);  // O, the references and sums have been read
-      if (sh.nanany) {
-        named_sync(1, kTcSoftmax);
+      if (nans) {
         if (set == 0)
 #pragma unroll
           for (int j = 0; j < D / 64; ++j) sh.nanrow[j][row] = 0;
