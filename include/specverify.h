@@ -227,6 +227,12 @@ size_t sv_tree_workspace_bytes(int32_t B, int32_t N, int32_t M, int32_t V,
 /* Zero a workspace (cudaMemsetAsync on `stream`). */
 sv_status sv_workspace_init(void* workspace, size_t ws_bytes, sv_stream_t stream);
 
+/* The id of the capture that `stream` is part of, 0 outside captures: for
+   callers that keep a workspace for each graph (a workspace that a graph
+   uses must live as long as the graph, and be no other call's while the
+   graph may run). */
+sv_status sv_stream_capture_id(sv_stream_t stream, uint64_t* id);
+
 /* Enqueue one chain / tree verification on `stream`.  The workspace must be
    256-byte aligned and at least the size the matching *_workspace_bytes
    call returns. */

@@ -23,31 +23,76 @@ from ._binding import (  # noqa: F401
     SV_NOALLOC_SCRATCH_BYTES, sv_noalloc_get_error, sv_verify_chain_noalloc,
     SV_TREE_MSS, SV_TREE_MSS_NOREPLACE, SV_TREE_NAIVE, TREE_MODES, SV_MIN_WORKSPACE_BYTES,
     sv_tree_mask, sv_row_stats, SV_FP16, SV_DERR_PAGE, SV_MAX_KV_HEADS, SV_MAX_KV_T,
-    sv_kv_attention, sv_kv_attention_workspace_bytes, sv_kv_read, sv_kv_write)
+    sv_kv_attention, sv_kv_attention_workspace_bytes, sv_kv_read, sv_kv_write,
+    sv_stream_capture_id, current_raw_stream)
 from ._build import build_library  # noqa: F401
 
 _ws_lock = threading.Lock()
 _ws_cache: dict = {}
+_ws_kept: list = []   # buffers that a larger one replaced: captured graphs may name them
+_ws_graph: dict = {}  # those of the capture under way: its id and its buffers
+# Calls that hold more than the error word in their workspace and are at home
+# on several streams at once (a prompt on one, decoding on another).
+_WS_PER_STREAM = ("kv_attention",)
 
 
 def workspace(nbytes: int, device=None, key=None) -> torch.Tensor:
     """A zeroed, 256-byte aligned device workspace of at least nbytes,
-    cached per (device, key).  Calls sharing one workspace must not overlap
-    on the GPU."""
+    cached per (device, key), and for key "kv_attention" per current stream
+    too.  Calls sharing one workspace must not overlap on the GPU.  A cached
+    buffer stays allocated when a larger one takes its place, so a graph
+    captured with it stays valid.
+
+    While the current stream is being captured, a buffer that does not exist
+    yet, and always one of "kv_attention", belongs to the graph: it comes from
+    the graph's memory and is zeroed by the graph, once, ahead of the first
+    call that uses it.  (To read the error word of such a call, get the
+    workspace inside the capture and keep it.)"""
     if not isinstance(device, torch.device) or device.index is None:
         device = torch.device(device if device is not None else "cuda")
         if device.index is None:
             device = torch.device("cuda", torch.cuda.current_device())
-    k = (device, key)
+    stream = current_raw_stream(device.index)
+    per_stream = key in _WS_PER_STREAM
+    k = (device, key, stream) if per_stream else (device, key)
+    capturing = torch.cuda.is_current_stream_capturing()
     with _ws_lock:
-        buf = _ws_cache.get(k)
-        if buf is None or buf.numel() < nbytes:
-            buf = torch.empty(max(nbytes, 256), dtype=torch.uint8, device=device)
-            if buf.data_ptr() % 256:
-                raise RuntimeError("torch returned a workspace that is not 256-byte aligned")
-            sv_workspace_init(buf)
-            _ws_cache[k] = buf
+        if not (capturing and per_stream):
+            buf = _ws_cache.get(k)
+            if buf is not None and buf.numel() >= nbytes:
+                return buf
+        if capturing:
+            return _graph_workspace(nbytes, device, (device, key, stream), stream)
+        # (sizes are rounded up to a power of two: all that a growing one
+        # leaves behind is smaller than the last)
+        if buf is not None:
+            _ws_kept.append(buf)
+        buf = _ws_cache[k] = _new_workspace(1 << (max(nbytes, 256) - 1).bit_length(), device,
+                                            stream)
+        if not per_stream:
+            torch.cuda.current_stream(device).synchronize()  # zeroed, for every stream
         return buf
+
+
+def _new_workspace(nbytes: int, device, stream: int) -> torch.Tensor:
+    buf = torch.empty(nbytes, dtype=torch.uint8, device=device)
+    if buf.data_ptr() % 256:
+        raise RuntimeError("torch returned a workspace that is not 256-byte aligned")
+    sv_workspace_init(buf, stream)
+    return buf
+
+
+def _graph_workspace(nbytes: int, device, k, stream: int) -> torch.Tensor:
+    """The buffer k of the capture that the current stream is part of.  Kept
+    here until the next capture begins; the memory is the graph's."""
+    capture = sv_stream_capture_id(stream)
+    if _ws_graph.get("capture") != capture:
+        _ws_graph.clear()
+        _ws_graph["capture"] = capture
+    buf = _ws_graph.get(k)
+    if buf is None or buf.numel() < nbytes:
+        buf = _ws_graph[k] = _new_workspace(max(nbytes, 256), device, stream)
+    return buf
 
 
 def dtype_code(t: torch.Tensor) -> int:
@@ -200,7 +245,10 @@ def kv_attention(q, cache: dict, page_table, kv_len, num_new=None, mask=None,
     the cache, which holds kv_len[b] earlier tokens and the round's own (see
     kv_write): causal among the round's tokens, or by the rows of a tree mask
     [B][T][words] (tree_mask).  scale defaults to 1 / sqrt(D).  Returns out
-    [B][T][heads][D] and, when with_lse, lse [B][T][heads] (device tensors)."""
+    [B][T][heads][D] and, when with_lse, lse [B][T][heads] (device tensors).
+    Without ws the current stream's own workspace serves (a captured call's,
+    the graph's: workspace()), so calls on several streams may overlap; calls
+    that are given one ws must not."""
     B, T, Hq, D = q.shape
     out = dict(out=torch.empty_like(q, memory_format=torch.contiguous_format))
     if with_lse:

@@ -33,6 +33,7 @@ EXPORTS = ("sv_chain_workspace_bytes", "sv_tree_workspace_bytes", "sv_workspace_
            "sv_verify_chain", "sv_verify_tree", "sv_get_error", "sv_selftest_wait_timeout",
            "sv_verify_chain_noalloc", "sv_noalloc_get_error", "sv_tree_mask", "sv_row_stats",
            "sv_kv_write", "sv_kv_read", "sv_kv_attention_workspace_bytes", "sv_kv_attention",
+           "sv_stream_capture_id",
            "sv_status_string", "sv_version")
 SV_MIN_WORKSPACE_BYTES = 8192
 SV_NOALLOC_SCRATCH_BYTES = 8 << 20
@@ -148,6 +149,8 @@ def lib(path: str | None = None):
         getattr(h, f).restype = ctypes.c_int
     h.sv_kv_attention_workspace_bytes.argtypes = [_i32, _i32, _i32, _i32, _i32]
     h.sv_kv_attention_workspace_bytes.restype = ctypes.c_size_t
+    h.sv_stream_capture_id.argtypes = [_P, ctypes.POINTER(ctypes.c_uint64)]
+    h.sv_stream_capture_id.restype = ctypes.c_int
     h.sv_status_string.argtypes = [ctypes.c_int]
     h.sv_status_string.restype = ctypes.c_char_p
     h.sv_version.argtypes = []
@@ -221,6 +224,20 @@ def sv_workspace_init(workspace: torch.Tensor, stream=None) -> None:
                                  _stream(stream))
     if st != SV_OK:
         raise SpecVerifyError(st, "sv_workspace_init")
+
+
+def current_raw_stream(device_index: int) -> int:
+    """Handle of a device's current stream, without a Stream object around it."""
+    return torch._C._cuda_getCurrentRawStream(device_index)
+
+
+def sv_stream_capture_id(stream) -> int:
+    """The id of the capture that a stream is part of, 0 outside captures."""
+    out = ctypes.c_uint64(0)
+    st = lib().sv_stream_capture_id(_stream(stream), ctypes.byref(out))
+    if st != SV_OK:
+        raise SpecVerifyError(st, "sv_stream_capture_id")
+    return out.value
 
 
 def sv_verify_chain(target_logits, draft_logits, draft_tokens, temperature, uniforms,
@@ -520,8 +537,7 @@ def _kv_call(name: str, packed: bytes, workspace, stream) -> None:
     if not workspace.is_cuda:
         raise ValueError("libspecverify takes device tensors")
     if stream is None:
-        # the current stream's handle, without a Stream object around it
-        stream = torch._C._cuda_getCurrentRawStream(workspace.get_device())
+        stream = current_raw_stream(workspace.get_device())
     elif hasattr(stream, "cuda_stream"):
         stream = stream.cuda_stream
     st = getattr(_lib_handle or lib(), name)(packed, workspace.data_ptr(), workspace.nbytes, stream)

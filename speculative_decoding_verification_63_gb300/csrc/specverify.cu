@@ -462,6 +462,18 @@ sv_status sv_workspace_init(void* workspace, size_t ws_bytes, sv_stream_t stream
              : SV_ECUDA;
 }
 
+sv_status sv_stream_capture_id(sv_stream_t stream, uint64_t* id) {
+  if (id == nullptr) return SV_EINVAL;
+  *id = 0;
+  cudaStreamCaptureStatus status = cudaStreamCaptureStatusNone;
+  unsigned long long capture = 0;
+  if (cudaStreamGetCaptureInfo(reinterpret_cast<cudaStream_t>(stream), &status, &capture) !=
+      cudaSuccess)
+    return SV_ECUDA;
+  if (status == cudaStreamCaptureStatusActive) *id = capture;
+  return SV_OK;
+}
+
 sv_status sv_verify_chain(const sv_chain_args* a, void* workspace, size_t ws_bytes,
                           sv_stream_t stream) {
   SV_RANGE("sv_verify_chain");

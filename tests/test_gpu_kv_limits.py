@@ -45,3 +45,115 @@ def test_nan_codes_in_some_of_many_units(T, Hq, H, D):
     for _ in range(20):
         assert torch.equal(run().view(torch.int16), got.view(torch.int16))
     assert flags(ws) == (sv.SV_OK, 0)
+
+
+# ------------------------------------------- workspaces the caller does not give
+
+def attention_call(seed, lens, T, Hq, H, P, D):
+    """A call without a workspace, and its result with one of its own."""
+    rng = np.random.default_rng(seed)
+    total = [a + T for a in lens]
+    c = ku.random_cache(rng, sum(-(-x // P) for x in total), H, P, D)
+    table, length, dev = i32(ku.tables(rng, c.k.shape[0], total, P)), i32(lens), ku.to_device(c)
+    q, _ = as_type(rng.normal(size=(len(lens), T, Hq, D)), "bf16")
+    run = lambda ws=None: sv.kv_attention(q, dev, table, length, ws=ws)["out"]
+    want = run(new_ws(sv.sv_kv_attention_workspace_bytes(len(lens), T, Hq, H, D)))
+    return run, want.clone()
+
+
+DECODE = (31, [3000, 17, 900], 1, 16, 2, 32, 128)   # cut units, few rows
+PROMPT = (32, [2000, 64], 120, 4, 2, 64, 128)       # cut units, tensor memory
+
+
+def capture(run):
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = run()
+    return graph, out
+
+
+@pytest.mark.parametrize("first", ["eager", "capture"])
+def test_a_graph_keeps_its_workspace(first, monkeypatch):
+    """A decode captured on the default workspace, larger calls and other
+    tensors in between, replayed; also when the capture is the first use."""
+    monkeypatch.setattr(sv, "_ws_cache", {})
+    decode, want = attention_call(*DECODE)
+    prompt, want_prompt = attention_call(*PROMPT)
+    if first == "eager":
+        assert torch.equal(decode(), want)
+    graph, out = capture(lambda: (decode(), decode())[1])
+    assert torch.equal(decode(), want)              # eager, before the first replay
+    for _ in range(3):
+        assert torch.equal(prompt(), want_prompt)
+        junk = [torch.full((n << 20,), 0xff, dtype=torch.uint8, device="cuda")
+                for n in (1, 2, 3, 5, 6, 8, 16, 21, 32)]
+        out.zero_()
+        graph.replay()
+        assert torch.equal(out, want)
+        assert all((x == 0xff).all() for x in junk)
+        del junk
+        assert torch.equal(decode(), want)
+    prompt_graph, prompt_out = capture(prompt)
+    for _ in range(3):
+        out.zero_(), prompt_out.zero_()
+        graph.replay()
+        prompt_graph.replay()
+        assert torch.equal(out, want) and torch.equal(prompt_out, want_prompt)
+
+
+def test_other_calls_captured_first(monkeypatch):
+    """Writes, reads and masks whose first use of their workspace is inside a
+    capture: neither the graph nor later calls find garbage."""
+    monkeypatch.setattr(sv, "_ws_cache", {})
+    parent = i32([[-1, 0, 0, 1]])
+    cache = sv.kv_cache(4, 16, 2, 64)
+    table, length = i32([[0, 1, 2, 3]]), i32([5])
+    x = torch.randn((1, 4, 2, 64), device="cuda", dtype=torch.bfloat16)
+
+    def run():
+        sv.kv_write(cache, table, length, x, x)
+        return sv.kv_read(cache, table, length, None, 4)["k"], sv.tree_mask(parent)["mask"]
+
+    graph, (k, mask) = capture(run)
+    junk = torch.full((64 << 20,), 0xff, dtype=torch.uint8, device="cuda")
+    del junk
+    graph.replay()
+    want_k, want_mask = run()
+    assert torch.equal(k, want_k) and torch.equal(mask, want_mask)
+    for key in ("kv", "mask"):
+        sv.check_device_errors(sv.workspace(1, "cuda", key))
+
+
+def test_streams_have_workspaces_of_their_own():
+    """Prompts on one stream, decoding on two others, at the same time."""
+    calls = [attention_call(*PROMPT), attention_call(*DECODE), attention_call(34, *DECODE[1:])]
+    streams = [torch.cuda.Stream() for _ in calls]
+    torch.cuda.synchronize()
+    got = [[] for _ in calls]
+    for _ in range(30):
+        for (run, _), stream, outs in zip(calls, streams, got):
+            with torch.cuda.stream(stream):
+                outs.append(run())
+    torch.cuda.synchronize()
+    for (_, want), outs in zip(calls, got):
+        assert all(torch.equal(o, want) for o in outs)
+
+
+def test_errors_of_a_captured_call():
+    """The graph's own workspace, asked for inside the capture."""
+    rng = np.random.default_rng(35)
+    dev = ku.to_device(ku.random_cache(rng, 4, 2, 16, 64))
+    q, _ = as_type(rng.normal(size=(2, 1, 4, 64)), "bf16")
+    table, length = i32([[0], [1]]), i32([5, 5])
+    need, held = sv.sv_kv_attention_workspace_bytes(2, 1, 4, 2, 64), {}
+
+    def run():
+        held["ws"] = sv.workspace(need, "cuda", "kv_attention")
+        return sv.kv_attention(q, dev, table, length)["out"]
+
+    graph, _ = capture(run)
+    graph.replay()
+    assert flags(held["ws"]) == (sv.SV_OK, 0)
+    length.copy_(i32([5, 99]))
+    graph.replay()
+    assert flags(held["ws"]) == (sv.SV_EDATA, sv.SV_DERR_ARG)
