@@ -91,6 +91,7 @@ struct KaShared {
   float v_scale[kKaStages][kKaBlock / 16];
   uint64_t full[kKaStages], empty[kKaStages];
   int dead;       // a wait ran out
+  int gaps;       // some request has rows without a token
   unsigned last;  // this CTA joins the unit
 };
 
@@ -105,16 +106,20 @@ __device__ __forceinline__ int ka_div_g(const KvAttnProblem& a, int n) {
 struct KaLen {
   int len, n;  // tokens before the round, round tokens (0 when invalid)
 };
-__device__ __forceinline__ KaLen ka_len(const KvAttnProblem& a, int b, bool* bad) {
+__device__ __forceinline__ KaLen ka_len(const int* kv_len, const int* num_new, int T,
+                                        long long room, int b, bool* bad) {
   KaLen r;
-  r.len = a.kv_len[b];
-  r.n = a.num_new ? a.num_new[b] : a.T;
-  if (r.len < 0 || r.n < 0 || r.n > a.T ||
-      static_cast<long long>(r.len) + r.n > static_cast<long long>(a.c.slots) * a.c.page_size) {
+  r.len = kv_len[b];
+  r.n = num_new ? num_new[b] : T;
+  if (r.len < 0 || r.n < 0 || r.n > T || static_cast<long long>(r.len) + r.n > room) {
     *bad = true;
     r.len = r.n = 0;
   }
   return r;
+}
+__device__ __forceinline__ KaLen ka_len(const KvAttnProblem& a, int b, bool* bad) {
+  return ka_len(a.kv_len, a.num_new, a.T, static_cast<long long>(a.c.slots) * a.c.page_size, b,
+                bad);
 }
 
 // Blocks of the row tile `tile` (ROWS rows each) of a request: up to the
@@ -182,20 +187,23 @@ struct KaCursor {
 };
 
 // The cumulated block counts of the requests into prefix[0 .. B] (every
-// thread of the block calls this); returns their total.
+// thread of the block calls this); returns their total.  *gaps (zero before)
+// becomes 1 if some request has rows without a token.
 template <int ROWS, int BLOCK, int THREADS>
 __device__ __forceinline__ int ka_prefix(const KvAttnProblem& a, int* prefix, int* scan,
-                                         bool report, int pad = 1) {
+                                         bool report, int* gaps, int pad = 1) {
   const int tid = static_cast<int>(threadIdx.x), warp = tid >> 5, lane = tid & 31;
   int total = 0;
 #pragma unroll 1
   for (int base = 0; base < a.B; base += THREADS) {
     const int b = base + tid;
     int mine = 0;
+    bool gap = false;
     if (b < a.B) {
       bool bad = false;
       const KaLen l = ka_len(a, b, &bad);
       if (bad && report) record_error(a.err, SV_DERR_ARG);
+      gap = l.n < a.T;
       const int tiles = (l.n * a.G + ROWS - 1) / ROWS;
 #pragma unroll 1
       for (int tile = 0; tile < tiles; ++tile)
@@ -209,6 +217,7 @@ __device__ __forceinline__ int ka_prefix(const KvAttnProblem& a, int* prefix, in
       if (lane >= o) x += y;
     }
     __syncthreads();
+    if (gap) *gaps = 1;
     if (lane == 31) scan[warp] = x;
     __syncthreads();
     int before = total;
@@ -224,19 +233,64 @@ __device__ __forceinline__ int ka_prefix(const KvAttnProblem& a, int* prefix, in
   return total;
 }
 
-// Rows of the round that hold no token: 0, lse -inf.
-template <class T, int D, int THREADS>
-__device__ __forceinline__ void ka_clear_rows(const KvAttnProblem& a, int thread) {
-  for (int b = static_cast<int>(blockIdx.x); b < a.B; b += static_cast<int>(gridDim.x)) {
+// Fills the rows of all requests that hold no token, `words` words of type V
+// each.  They make one list of words, which `threads` threads of the grid take
+// in turns.  A warp looks at 32 requests at once; a word's request is found by
+// bisection among them, so a batch of many short gaps costs no more than one
+// long one.
+template <class V>
+__device__ __forceinline__ void ka_fill_gaps(V* out, V value, int words, const int* kv_len,
+                                             const int* num_new, int B, int T, int Hq,
+                                             long long room, int thread, int threads) {
+  const int lane = static_cast<int>(threadIdx.x) & 31;
+  const long long request = static_cast<long long>(T) * Hq * words;
+  long long next = thread;  // the thread's next word, counted from the 32 requests' first
+#pragma unroll 1
+  for (int b0 = 0; b0 < B; b0 += 32) {
+    int n = T;  // tokens of request b0 + lane
     bool bad = false;
-    const KaLen l = ka_len(a, b, &bad);
-    const long long row0 = (static_cast<long long>(b) * a.T + l.n) * a.Hq;
-    const long long rows = static_cast<long long>(a.T - l.n) * a.Hq;
-    uint4* o = reinterpret_cast<uint4*>(static_cast<T*>(a.out) + row0 * D);
-    for (long long i = thread; i < rows * (D / 8); i += THREADS) o[i] = make_uint4(0, 0, 0, 0);
-    if (a.lse)
-      for (long long i = thread; i < rows; i += THREADS) a.lse[row0 + i] = kNegInf;
+    if (b0 + lane < B) n = ka_len(kv_len, num_new, T, room, b0 + lane, &bad).n;
+    // words up to the end of the lane's request
+    long long upto = static_cast<long long>(T - n) * Hq * words;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long y = __shfl_up_sync(0xffffffffu, upto, o);
+      if (lane >= o) upto += y;
+    }
+    const long long total = __shfl_sync(0xffffffffu, upto, 31);
+#pragma unroll 1
+    while (__any_sync(0xffffffffu, next < total)) {
+      int k = 0;  // the first request that ends behind `next` (31 when there is none)
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1)
+        if (__shfl_sync(0xffffffffu, upto, k + o - 1) <= next) k += o;
+      const long long end = __shfl_sync(0xffffffffu, upto, k);
+      // a request's gap is its end
+      V* const at = out + (b0 + k + 1) * request - end;
+#pragma unroll 1
+      for (; next < end; next += threads) at[next] = value;
+    }
+    next -= total;
   }
+}
+
+// Rows of the round that hold no token: 0, lse -inf.  A call with one prompt
+// chunk and requests of a single token has nearly all of its rows here (one
+// token in a call of T = 8192, 32 heads of 128, 67 MB: 26 us, a plain fill of
+// them 20; by one warp a request 1023).  (A function of its own, with few
+// arguments: inlined, it cost the kernels' loops registers, 97 us against 91
+// for chains of 28 rows.)
+__device__ __noinline__ void ka_clear_rows(uint4* out, float* lse, const int* kv_len,
+                                           const int* num_new, int B, int T, int Hq, int words,
+                                           long long room, int thread, int threads) {
+  ka_fill_gaps(out, make_uint4(0, 0, 0, 0), words, kv_len, num_new, B, T, Hq, room, thread,
+               threads);
+  if (lse) ka_fill_gaps(lse, kNegInf, 1, kv_len, num_new, B, T, Hq, room, thread, threads);
+}
+template <int D>
+__device__ __forceinline__ void ka_clear_rows(const KvAttnProblem& a, int thread, int threads) {
+  ka_clear_rows(static_cast<uint4*>(a.out), a.lse, a.kv_len, a.num_new, a.B, a.T, a.Hq, D / 8,
+                static_cast<long long>(a.c.slots) * a.c.page_size, thread, threads);
 }
 
 // The blocks in equal parts: the first `more` of them hold `per` + 1 blocks,
@@ -513,7 +567,7 @@ __global__ void __launch_bounds__(kKaThreads, kKaCtasPerSm) kv_attn_kernel(const
       mbar_init(&sh.full[s], KaFeed<kKaRows, kKaBlock, 2>::kCopies);
       mbar_init(&sh.empty[s], kKaWarps / 2);
     }
-    sh.dead = 0;
+    sh.dead = sh.gaps = 0;
     fence_mbar_init();
   }
   grid_dependency_wait();
@@ -525,7 +579,7 @@ __global__ void __launch_bounds__(kKaThreads, kKaCtasPerSm) kv_attn_kernel(const
   int total, pad = 1;
 #pragma unroll 1
   for (;;) {
-    total = ka_prefix<kKaRows, kKaBlock, kKaThreads>(a, sh.prefix, sh.scan, cta == 0, pad);
+    total = ka_prefix<kKaRows, kKaBlock, kKaThreads>(a, sh.prefix, sh.scan, cta == 0, &sh.gaps, pad);
     const int units = a.B * a.c.Hkv * ((a.T * a.G + kKaRows - 1) / kKaRows);
     if (pad > 1 || 2 * units > grid || total >= 1 << 30) break;
     const int room = grid - units;
@@ -533,7 +587,9 @@ __global__ void __launch_bounds__(kKaThreads, kKaCtasPerSm) kv_attn_kernel(const
     if (q > total / grid + kKaUneven) break;
     pad = q;
   }
-  ka_clear_rows<T, D, kKaThreads>(a, tid);
+  // By the consumers, while the first block is on its way.
+  if (sh.gaps && warp < kKaWarps)
+    ka_clear_rows<D>(a, cta * (kKaWarps * 32) + tid, grid * (kKaWarps * 32));
 
   // this CTA's part of the blocks
   const KaParts parts = pad > 1 ? KaParts(total / pad, pad) : KaParts(total, grid, kKaMinBlocks);

@@ -109,7 +109,7 @@ struct TcShared {
   float ends[2][2][kTcRows];  // references and sums of the streams
   unsigned long long nanrow[D / 64][kTcRows];  // channels in which a lane's row saw a NaN
   KaCursor<kTcRows, kTcBlock> cur[8];          // the softmax warps' places
-  int total, nanany;
+  int total, nanany, gaps;
   uint64_t rawfull[kTcSlots], rawempty[kTcSlots];
   uint64_t kfull, vfull[2], nanfull[2], sfull[2], pfull[2], pvdone[2], qfull;
   unsigned tmem;
@@ -450,7 +450,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv_attn_tc_kernel(const KvAttnP
       }
       mbar_init(&sh.kfull, kTcConvert / 32);
       mbar_init(&sh.qfull, kTcSoftmax / 32);
-      sh.dead = 0;
+      sh.dead = sh.gaps = 0;
       fence_mbar_init();
     }
     __syncwarp();
@@ -458,7 +458,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv_attn_tc_kernel(const KvAttnP
   }
   grid_dependency_wait();
   const int total =
-      ka_prefix<kTcRows, kTcBlock, kTcThreads>(a, sh.prefix, sh.scan, cta == 0);
+      ka_prefix<kTcRows, kTcBlock, kTcThreads>(a, sh.prefix, sh.scan, cta == 0, &sh.gaps);
   tc_fence_after();
   const unsigned tmem = sh.tmem;
   if (tid == 0) {
@@ -1081,7 +1081,10 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv_attn_tc_kernel(const KvAttnP
     }
   }
 
-  if (warp == 18) ka_clear_rows<T, D, 32>(a, lane);
+  // The converters are through some microseconds before the softmax warps.
+  if (sh.gaps && warp >= 8 && warp < 16)
+    ka_clear_rows<D>(a, cta * 2 * kTcConvert + tid - kTcSoftmax,
+                     static_cast<int>(gridDim.x) * 2 * kTcConvert);
 
   tc_fence_before();
   __syncthreads();

@@ -157,3 +157,58 @@ def test_errors_of_a_captured_call():
     length.copy_(i32([5, 99]))
     graph.replay()
     assert flags(held["ws"]) == (sv.SV_EDATA, sv.SV_DERR_ARG)
+
+
+# ------------------------------------------------- rows without a token
+
+@pytest.mark.parametrize("B,T,Hq,H,D", [(1, 5, 2, 1, 64), (33, 3, 8, 2, 128), (200, 2, 5, 5, 64),
+                                        (70, 40, 4, 2, 64), (33, 64, 1, 1, 128), (2, 700, 2, 2, 64)])
+def test_rows_without_a_token_are_cleared(B, T, Hq, H, D):
+    """Every row t >= num_new of every request, whatever the outputs held."""
+    rng = np.random.default_rng(41)
+    new = rng.integers(0, T + 1, B)
+    new[rng.random(B) < 0.3] = T
+    if B > 2:
+        new[B // 2] = T + 1  # out of range: no row holds a token
+    lens, P = rng.integers(0, 20, B), 32
+    slots = -(-(20 + T) // P)
+    c = ku.random_cache(rng, 40, H, P, D)
+    table = i32(rng.integers(0, 40, (B, slots)))
+    q, _ = as_type(rng.normal(size=(B, T, Hq, D)), "bf16")
+    out = torch.full((B, T, Hq, D), 7.0, dtype=torch.bfloat16, device="cuda")
+    lse = torch.full((B, T, Hq), 7.0, device="cuda")
+    ws = new_ws(sv.sv_kv_attention_workspace_bytes(B, T, Hq, H, D))
+    sv.sv_kv_attention(q, ku.to_device(c), table, i32(lens), out, ws, 0.1, num_new=i32(new), lse=lse)
+    assert flags(ws) == ((sv.SV_EDATA, sv.SV_DERR_ARG) if B > 2 else (sv.SV_OK, 0))
+    empty = torch.arange(T)[None] >= torch.from_numpy(np.where(new > T, 0, new))[:, None]
+    out, lse = out.cpu().float(), lse.cpu()
+    assert (out[empty] == 0).all() and torch.isneginf(lse[empty]).all()
+    assert torch.isfinite(lse[~empty]).all() and (out[~empty] != 7).any(-1).all()
+
+
+def test_a_ragged_prompt_costs_what_it_writes():
+    """One token in a call of 8192: 67 MB of zeros are the GPU's work, not one
+    warp's (a fill of the same buffer is the measure)."""
+    T, Hq, D = 8192, 32, 128
+    dev = sv.kv_cache(70, 128, 8, D)
+    table, length, new = i32([list(range(70))]), i32([100]), i32([1])
+    q = torch.zeros((1, T, Hq, D), dtype=torch.bfloat16, device="cuda")
+    out = torch.empty_like(q)
+    ws = new_ws(sv.sv_kv_attention_workspace_bytes(1, T, Hq, 8, D))
+
+    def best(call):
+        times = []
+        for _ in range(8):
+            a, b = (torch.cuda.Event(enable_timing=True) for _ in "ab")
+            a.record()
+            for _ in range(10):
+                call()
+            b.record()
+            b.synchronize()
+            times.append(a.elapsed_time(b) * 100)  # us a call
+        return min(times)
+
+    fill = best(out.zero_)
+    call = best(lambda: sv.sv_kv_attention(q, dev, table, length, out, ws, 0.1, num_new=new))
+    print(f"fill {fill:.1f} us, call {call:.1f} us")
+    assert call <= 3 * fill + 30, (call, fill)
