@@ -328,7 +328,7 @@ sv_status sv_kv_attention(const sv_kv_attention_args* a, void* workspace, size_t
   p.num_new = a->num_new;
   p.mask = a->mask;
   p.words = a->words;
-  p.scale_log2 = a->scale * 1.4426950408889634f;
+  p.scale_log2 = static_cast<float>(std::clamp(a->scale * 1.4426950408889634, -3.4e38, 3.4e38));
   char* ws = static_cast<char*>(workspace);
   p.tickets = reinterpret_cast<unsigned*>(ws + kTicketsAt);
   p.partials = reinterpret_cast<float*>(ws + kPartialsAt);

@@ -103,6 +103,17 @@ __device__ __forceinline__ int ka_div_g(const KvAttnProblem& a, int n) {
   return a.G == 1 ? n : static_cast<int>(__umulhi(static_cast<unsigned>(n), a.g_magic));
 }
 
+// The exponent that brings a bf16 row whose largest magnitude is m into the
+// halves' range, [2^14, 2^15).  (127 - 14 = 113 is the largest there is; below
+// -100 the row is far too small for its scores to matter.)
+__device__ __forceinline__ int ka_row_exp(float m) {
+  return min(max(static_cast<int>(__float_as_uint(m) >> 23) - 127 - 14, -100), 113);
+}
+// A score's factor (the row's |scale| log2(e) 2^ex, times 2^ek of the page),
+// kept finite: it may pass the range of fp32 where the score does not, 0 above
+// all.
+__device__ __forceinline__ float ka_finite(float c) { return fminf(c, 3.40282347e38f); }
+
 struct KaLen {
   int len, n;  // tokens before the round, round tokens (0 when invalid)
 };
@@ -620,7 +631,7 @@ __global__ void __launch_bounds__(kKaThreads, kKaCtasPerSm) kv_attn_kernel(const
     // the unit's queries as fragments: bf16 rows are scaled by a power of two
     // into the halves' range
     unsigned qf[KS][4];
-    float c2[2];  // log2(e) * scale * 2^(the row's exponent)
+    float c2[2];  // log2(e) |scale| 2^(the row's exponent); the sign goes to the queries
     int rt[2];    // round token of the row (T: none)
     {
 #pragma unroll
@@ -652,12 +663,12 @@ __global__ void __launch_bounds__(kKaThreads, kKaCtasPerSm) kv_attn_kernel(const
           for (int i = 0; i < D / 4; ++i) m = fmaxf(m, fabsf(f[i]));
           m = quad_max(m);
           // the row's largest value lands in [2^14, 2^15)
-          ex = min(max(static_cast<int>(__float_as_uint(m) >> 23) - 127 - 14, -100), 100);
-          const float k = pow2f(-ex);
-#pragma unroll
-          for (int i = 0; i < D / 4; ++i) f[i] *= k;
+          ex = ka_row_exp(m);
         }
-        c2[r] = a.scale_log2 * pow2f(ex);
+        const float k = a.scale_log2 < 0.f ? -pow2f(-ex) : pow2f(-ex);
+#pragma unroll
+        for (int i = 0; i < D / 4; ++i) f[i] *= k;
+        c2[r] = ka_finite(fabsf(a.scale_log2) * pow2f(ex));
 #pragma unroll
         for (int i = 0; i < KS; ++i) {
           qf[i][r] = half2_of(f[4 * i], f[4 * i + 1]);
@@ -702,10 +713,16 @@ __global__ void __launch_bounds__(kKaThreads, kKaCtasPerSm) kv_attn_kernel(const
         zin[u] = pow2f(-ev);
       }
 #pragma unroll
-      for (int nt = 0; nt < 4; ++nt)
+      for (int u = 0; u < 2; ++u)
 #pragma unroll
-        for (int i4 = 0; i4 < 4; ++i4)
-          x[nt][i4] = fmaf(x[nt][i4], c2[i4 >> 1] * kse[nt >> 1], vse[nt >> 1]);
+        for (int r = 0; r < 2; ++r) {
+          const float f = ka_finite(c2[r] * kse[u]);
+#pragma unroll
+          for (int nt = 2 * u; nt < 2 * u + 2; ++nt) {
+            x[nt][2 * r] = fmaf(x[nt][2 * r], f, vse[u]);
+            x[nt][2 * r + 1] = fmaf(x[nt][2 * r + 1], f, vse[u]);
+          }
+        }
 
       uint32_t seen[2] = {0xffffffffu, 0xffffffffu};  // bit nt * 2 + column of the thread's 8
       if (edge) {

@@ -361,7 +361,7 @@ __device__ __forceinline__ void tc_load_q(const KvAttnProblem& a,
 #pragma unroll
         for (int o = 1; o < LANES; o <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
         // the row's largest value lands in [2^14, 2^15)
-        ex = min(max(static_cast<int>(__float_as_uint(m) >> 23) - 127 - 14, -100), 100);
+        ex = ka_row_exp(m);
       }
       const float f = a.scale_log2 < 0.f ? -pow2f(-ex) : pow2f(-ex);
       unsigned h[4];
@@ -374,7 +374,7 @@ __device__ __forceinline__ void tc_load_q(const KvAttnProblem& a,
                                 (((piece & 7) ^ (row & 7)) << 4)) =
           make_uint4(h[0], h[1], h[2], h[3]);
       // (not 0: masked scores are -inf and stay so)
-      if (piece == 0) c2[row] = fmaxf(fabsf(a.scale_log2) * pow2f(ex), 1e-30f);
+      if (piece == 0) c2[row] = fmaxf(ka_finite(fabsf(a.scale_log2) * pow2f(ex)), 1e-30f);
     }
   }
   fence_proxy_async_shared();
@@ -763,7 +763,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv_attn_tc_kernel(const KvAttnP
               for (int j = 0; j < 5; ++j) v[j] = max3(&x[16 * h + 3 * j]);
               v[0] = max3(v[0], v[1], v[2]);
               v[0] = max3(v[0], v[3], max3(v[4], __uint_as_float(x[16 * h + 15]), v[0]));
-              mx = fmaxf(mx, fmaf(v[0], c2 * fabsf(ms.x), ms.y));
+              mx = fmaxf(mx, fmaf(v[0], ka_finite(c2 * fabsf(ms.x)), ms.y));
             }
           }
           const bool rise = mx > ref + kRefSlack;
@@ -794,7 +794,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv_attn_tc_kernel(const KvAttnP
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
               const float4 ms = m.s[base + u + h];
-              const float sc = c2 * fabsf(ms.x), vb = ms.y - bs;
+              const float sc = ka_finite(c2 * fabsf(ms.x)), vb = ms.y - bs;
               const float2 sc2 = make_float2(sc, sc), vb2 = make_float2(vb, vb);
               float2 zz = make_float2(0.f, 0.f);
 #pragma unroll

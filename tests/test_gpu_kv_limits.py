@@ -212,3 +212,38 @@ def test_a_ragged_prompt_costs_what_it_writes():
     call = best(lambda: sv.sv_kv_attention(q, dev, table, length, out, ws, 0.1, num_new=new))
     print(f"fill {fill:.1f} us, call {call:.1f} us")
     assert call <= 3 * fill + 30, (call, fill)
+
+
+# --------------------------------------------------- far ends of the ranges
+
+@pytest.mark.parametrize("T", [4, 12, 40])
+@pytest.mark.parametrize("qexp,kexp,scale,coded", [
+    (116, -48, 2.0 ** -60, True), (126, -48, 2.0 ** -70, True), (126, 0, 2.0 ** -120, True),
+    (126, 48, 0.125, False), (20, 0, 2.0 ** 127, False), (-110, -48, 0.125, True)])
+def test_attention_at_the_ends_of_the_ranges(T, qexp, kexp, scale, coded):
+    """Queries up to bf16's largest, scales and pages at the ends of theirs:
+    scores are moderate (channel 0 of every second key) or exactly zero, while
+    a factor of theirs, or the factors' product, passes the range of fp32."""
+    rng = np.random.default_rng(51)
+    H, P, D, Hq, B = 2, 16, 64, 4, 2
+    lens = [60, 150]
+    total = [a + T for a in lens]
+    c = ku.random_cache(rng, sum(-(-x // P) for x in total), H, P, D)
+    c.ks[:] = 2.0 ** kexp
+    c.k[:] = 0                       # zero codes ..
+    c.k[..., 1:] = np.where(rng.random(c.k[..., 1:].shape) < 0.5, 0, 0x80)
+    if coded:
+        c.k[:, :, ::2, 0] = 0x01     # .. and one smallest code in every second key
+    table = ku.tables(rng, c.k.shape[0], total, P)
+    q, q64 = as_type(1.5 * 2.0 ** qexp * rng.choice([-1.0, 1.0], (B, T, Hq, D)), "bf16")
+    assert np.isfinite(q64).all()
+    ws = new_ws(sv.sv_kv_attention_workspace_bytes(B, T, Hq, H, D))
+    got = sv.kv_attention(q, ku.to_device(c), i32(table), i32(lens), scale=scale, with_lse=True,
+                          ws=ws)
+    assert flags(ws) == (sv.SV_OK, 0)
+    out, lse, spr, xerr = ku.attention(q64, c, table, lens, [T] * B, None, scale)
+    tol, dx = ku.out_bounds(out, spr, xerr, D, torch.bfloat16)
+    o, l = got["out"].double().cpu().numpy(), got["lse"].double().cpu().numpy()
+    assert np.isfinite(o).all() and np.isfinite(l).all()
+    assert (np.abs(o - out) <= tol).all()
+    assert (np.abs(l - lse) <= dx + 2.0 ** -22 * np.abs(lse) + 2.0 ** -20).all()
