@@ -415,8 +415,15 @@ sv_status sv_kv_read(const sv_kv_read_args* args, void* workspace, size_t ws_byt
  * set (sv_tree_mask's rows: a node's ancestors and itself; T <= 64).  A row
  * that sees nothing, and every row t >= n, is 0 with lse = -inf.  What a
  * row does not see does not reach it, NaN and stale codes included.
- * Products and sums are taken in 32 bits; the queries enter the products
- * as they are, the weights exp(x_i - max) rounded to 11 bits (fp16).
+ * Products and sums are taken in 32 bits.  What enters the products in 16:
+ *   - fp16 queries as they are; bf16 queries exactly too, but for channels
+ *     below 2^-31 of the row's largest, which are off by up to 2^-39 of it;
+ *   - the weights exp(x_i - max) as halves: rounded to 11 bits or, where that
+ *     is coarser, off by up to 2^-19 of the largest weight among the 128
+ *     positions (a multiple of 128 on) around position i, and by no more than
+ *     2^-28 of the row's largest (in blocks more than 2^30 below it the second
+ *     may be the only bound).  Weights count with their page's v_scale here.
+ *     The sum in the denominator has them unrounded.
  *
  * kv_len < 0, num_new outside [0, T] or a length past slots * page_size
  * records SV_DERR_ARG (all rows of the request as if n were 0); a page id

@@ -12,13 +12,19 @@
 // Folding ev into the exponent costs nothing and keeps the weights of pages
 // with different scales comparable in 16 bits.  The weights are rounded to
 // halves (relative 2^-11) for the second product; Z sums them unrounded.
-// The reference follows the running maximum only when that has risen more
-// than kRefSlack above it, so the rescaling of O is rare; the weights are
-// shifted up by kRefShift, which keeps them within the halves' range
-// (2^(kRefShift + kRefSlack) = 2^15): below 2^-18 of the reference they are
-// off by up to 2^-29 of it instead, which 2^17 positions together turn into
-// 2^-12.  (With scores of deviation 2.8 a warp of 32 rows rescales in one of
-// 25 blocks; with a slack of 7, in one of 6.)
+// The reference follows the blocks' maxima only when one is more than kRefReach
+// above or below it, so the rescaling of O is rare; the weights are shifted up
+// by kRefShift, which keeps them within the halves' range (2^(kRefShift +
+// kRefReach) = 2^15.5).  Below 2^-19 of the reference they are off by up to 2^-30
+// of it instead.  Because the reference comes down to a block far below it, that
+// is less than 2^-19 of the block's own largest weight (and 2^-28 of the row's):
+// 2^-12 for all of a block's positions together, also in the long tail behind
+// one dominant key, which with a reference that only rises lost whole percents.
+// O and Z grow by as much as the reference falls; Z stays below 2^64 by that
+// (kRefRoom), O, with the largest page scale, below 2^121.
+// (With scores of deviation 2.8 and pages of different sizes a warp of 32 rows
+// rescales in one of ten blocks, one of forty if the reference only rose: trees
+// 88.4 us against 86.7, prompts 174 against 170.)
 //
 // Work.  A unit is 16 query rows (round tokens x heads of one group) of one
 // request and key/value head; its blocks are 64 positions each.  The blocks
@@ -55,7 +61,7 @@ constexpr int kKaCtasPerSm = 2;
 constexpr int kKaMaxCtas = 2 * 160;   // tickets and partials are sized for this many
 constexpr int kKaMinBlocks = 4;       // blocks below which a CTA is not worth starting
 constexpr int kKaUneven = 8;          // blocks a part may grow by to keep within its unit
-constexpr float kRefShift = 4.f, kRefSlack = 11.f;
+constexpr float kRefShift = 5.f, kRefReach = 10.5f, kRefRoom = 0x1p64f;
 
 struct KvAttnProblem {
   KvCache c;
@@ -113,6 +119,21 @@ __device__ __forceinline__ int ka_row_exp(float m) {
 // kept finite: it may pass the range of fp32 where the score does not, 0 above
 // all.
 __device__ __forceinline__ float ka_finite(float c) { return fminf(c, 3.40282347e38f); }
+
+// Whether the reference has to follow a block whose largest score is mx.
+// (Not if both are -inf: then neither block nor row has anything to weigh.)
+__device__ __forceinline__ bool ka_far(float mx, float ref) { return fabsf(mx - ref) > kRefReach; }
+// Moves the reference to a block's mx where that is far from it; returns what
+// the sums so far (z: the row's) are to be multiplied by.  References are whole
+// numbers, so that factor is a power of two.
+__device__ __forceinline__ float ka_move(float mx, float& ref, float z) {
+  if (!ka_far(mx, ref)) return 1.f;
+  const float to = ceilf(mx);
+  const float f = ref == kNegInf ? 0.f : fast_exp2(ref - to);
+  if (mx < ref && !(z * f < kRefRoom)) return 1.f;
+  ref = to;
+  return f;
+}
 
 struct KaLen {
   int len, n;  // tokens before the round, round tokens (0 when invalid)
@@ -760,13 +781,12 @@ __global__ void __launch_bounds__(kKaThreads, kKaCtasPerSm) kv_attn_kernel(const
         for (int nt = 0; nt < 4; ++nt) m = fmaxf(m, fmaxf(x[nt][2 * r], x[nt][2 * r + 1]));
         mx[r] = quad_max(m);
       }
-      const bool rise = mx[0] > acc.ref[0] + kRefSlack || mx[1] > acc.ref[1] + kRefSlack;
-      if (__any_sync(0xffffffffu, rise)) {
+      const bool far = ka_far(mx[0], acc.ref[0]) || ka_far(mx[1], acc.ref[1]);
+      if (__builtin_expect(__any_sync(0xffffffffu, far), 0)) {
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
-          if (mx[r] > acc.ref[r] + kRefSlack) {
-            const float f = acc.ref[r] == kNegInf ? 0.f : fast_exp2(acc.ref[r] - mx[r]);
-            acc.ref[r] = mx[r];
+          const float f = ka_move(mx[r], acc.ref[r], quad_sum(acc.z[r]));
+          if (f != 1.f) {
             acc.z[r] *= f;
 #pragma unroll
             for (int j = 0; j < D / 8; ++j) {

@@ -766,23 +766,24 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv_attn_tc_kernel(const KvAttnP
               mx = fmaxf(mx, fmaf(v[0], ka_finite(c2 * fabsf(ms.x)), ms.y));
             }
           }
-          const bool rise = mx > ref + kRefSlack;
-          if (__builtin_expect(__any_sync(0xffffffffu, rise), 0)) {
-            const float f = !rise ? 1.f : ref == kNegInf ? 0.f : fast_exp2(ref - mx);
-            if (rise) ref = mx;
-            if (had) {
+          if (__builtin_expect(__any_sync(0xffffffffu, ka_far(mx, ref)), 0)) {
+            const float f = ka_move(mx, ref, z);
+            if (had && __any_sync(0xffffffffu, f != 1.f)) {
               // O_s whole: the products of block i - 2 are done (their weights
-              // made way for these scores)
+              // made way for these scores).  It goes through the registers of
+              // the scores, which are loaded again: half as many waits as
+              // 16 columns at a time beside them.
               z *= f;
 #pragma unroll 1
-              for (int c = 0; c < D; c += 16) {
-                unsigned o[16];
+              for (int c = 0; c < D; c += 32) {
                 __syncwarp();
-                tc_ld16(o, tm + kO + set * D + c);
+                tc_ld32(x, tm + kO + set * D + c);
 #pragma unroll
-                for (int j = 0; j < 16; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * f);
-                tc_st16(tm + kO + set * D + c, o);
+                for (int j = 0; j < 32; ++j) x[j] = __float_as_uint(__uint_as_float(x[j]) * f);
+                tc_st16(tm + kO + set * D + c, x);
+                tc_st16(tm + kO + set * D + c + 16, x + 16);
               }
+              tc_ld32(x, ts + (own - 2) * 16);
             }
           }
           had = true;

@@ -6,7 +6,7 @@ import torch
 
 import kv_util as ku
 import speculative_decoding_verification_63_gb300 as sv
-from test_gpu_kvcache import as_type, flags, i32, new_ws
+from test_gpu_kvcache import TYPES, as_type, flags, i32, new_ws
 
 pytestmark = pytest.mark.gpu
 
@@ -247,3 +247,86 @@ def test_attention_at_the_ends_of_the_ranges(T, qexp, kexp, scale, coded):
     assert np.isfinite(o).all() and np.isfinite(l).all()
     assert (np.abs(o - out) <= tol).all()
     assert (np.abs(l - lse) <= dx + 2.0 ** -22 * np.abs(lse) + 2.0 ** -20).all()
+
+
+# ------------------------------------- a dominant key and a long tail behind it
+
+@pytest.mark.parametrize("where", [0, 100, 7000])
+@pytest.mark.parametrize("nats", [12, 15, 18])
+@pytest.mark.parametrize("T,G,D,dtype", [(1, 1, 64, "fp16"), (1, 4, 128, "bf16"), (5, 4, 64, "fp16"),
+                                         (13, 4, 128, "fp16"), (40, 2, 64, "bf16"),
+                                         (32, 4, 128, "fp16")])
+def test_a_dominant_key_leaves_the_tail_its_bits(T, G, D, dtype, nats, where):
+    """One key with a value of zero, `nats` above a nearly uniform context:
+    the output is the context's, weighted 2^-17 to 2^-26 of the key's.  Bound:
+    a weight is off by 2^-11 of itself, or by 2^-19 of the largest in its
+    aligned 128 positions and at most 2^-28 of the row's largest; sums in 32
+    bits as in kv_util.out_bounds.  (Every request holds the same pages: long
+    contexts for each CTA.)"""
+    rng = np.random.default_rng(61)
+    B, P, L = 320, 128, 8000 - T
+    slots = -(-(L + T) // P)
+    c = ku.random_cache(rng, slots, 1, P, D)
+    c.ks[:], c.vs[:] = 1.0, 2.0 ** -6
+    c.k[:] = ku.encode(rng.normal(size=c.k.shape) * 0.002)  # few bits, far below channel 0
+    c.k[..., 0] = ku.encode(rng.uniform(-0.3, 0.3, c.k.shape[:-1]))
+    c.v[:] = ku.encode((1 + 0.3 * rng.normal(size=c.v.shape)) * 64)
+    c.k[where // P, 0, where % P, 0] = ku.encode(np.array(float(nats)))
+    c.v[where // P, 0, where % P] = 0
+    order = rng.permutation(slots).astype(np.int32)
+    dev = ku.to_device(ku.Cache(c.k[np.argsort(order)], c.v[np.argsort(order)], c.ks, c.vs))
+    q = rng.normal(size=(B, T, G, D)) * 0.1
+    q[..., 0] = rng.choice([3.75, 4.0], (B, T, G))
+    q, q64 = as_type(q, dtype)
+    half = torch.finfo(TYPES[dtype]).eps / 2
+    got = sv.kv_attention(q, dev, i32(np.tile(order, (B, 1))), i32([L] * B), scale=0.25,
+                          with_lse=True)
+    o, l = got["out"].double().cpu().numpy(), got["lse"].double().cpu().numpy()
+    assert np.isfinite(o).all()
+    row = np.arange(slots, dtype=np.int64)
+    k, v = (c.values(s, row, np.arange(L + T))[:, 0] for s in "kv")
+    for b in (0, 7, 151, 152, 319):
+        for t in {0, T // 2, T - 1}:
+            n = L + t + 1
+            for g in {0, G - 1}:
+                x = k[:n] @ q64[b, t, g] * 0.25
+                dx = D * 2.0 ** -24 * (np.abs(k[:n]) @ np.abs(q64[b, t, g])).max() * 0.25 + 2.0 ** -21
+                w = np.exp(x - x.max())
+                blocks = np.pad(w, (0, -n % 128)).reshape(-1, 128).max(1)
+                dw = np.maximum(2.0 ** -11 * w, np.minimum(2.0 ** -19 * np.repeat(blocks, 128)[:n],
+                                                           2.0 ** -28 * w.max()))
+                z = w.sum()
+                want, spread = w @ v[:n] / z, w @ np.abs(v[:n]) / z
+                d = dw @ np.abs(v[:n]) / z + spread * (2.0 ** -12 + 2 * dx)
+                tol = d + half * (np.abs(want) + d) + 2.0 ** -24
+                assert (np.abs(o[b, t, g] - want) <= tol).all(), (np.abs(o[b, t, g] - want) / tol).max()
+                lse = x.max() + np.log(z)
+                assert abs(l[b, t, g] - lse) <= dx + 2.0 ** -22 * abs(lse) + 2.0 ** -20
+
+
+@pytest.mark.parametrize("shape", ["falling", "rising", "alternating"])
+@pytest.mark.parametrize("T,G,D", [(1, 4, 64), (13, 4, 128), (40, 2, 64)])
+def test_scores_that_fall_or_alternate_far(T, G, D, shape):
+    """Scores over hundreds of powers of two, block by block: the reference
+    moves at every block, up to where the sums' range ends."""
+    rng = np.random.default_rng(62)
+    B, P, L = 320, 64, 2900 - T
+    slots = -(-(L + T) // P)
+    c = ku.random_cache(rng, slots, 1, P, D)
+    c.ks[:], c.vs[:] = 1.0, 2.0 ** -6
+    at = np.arange(slots * P).reshape(slots, P)
+    size = {"falling": 400 - 800 * at / (L + T), "rising": 800 * at / (L + T) - 400,
+            "alternating": np.where(at // 128 % 2, 200.0, 160.0)}[shape]
+    c.k[:, 0] = ku.encode(rng.normal(size=c.k[:, 0].shape) * 0.01)
+    c.k[:, 0, :, 0] = ku.encode(size)
+    table = np.tile(np.arange(slots, dtype=np.int32), (B, 1))
+    q = rng.normal(size=(B, T, G, D))
+    q[..., 0] = 1.0
+    q, q64 = as_type(q, "bf16")
+    got = sv.kv_attention(q, ku.to_device(c), i32(table), i32([L] * B), scale=1.0, with_lse=True)
+    o, l = got["out"].double().cpu().numpy(), got["lse"].double().cpu().numpy()
+    pick = [0, 151, 319]
+    out, lse, spr, xerr = ku.attention(q64[pick], c, table[pick], [L] * 3, [T] * 3, None, 1.0)
+    tol, dx = ku.out_bounds(out, spr, xerr, D, torch.bfloat16)
+    assert (np.abs(o[pick] - out) <= tol).all()
+    assert (np.abs(l[pick] - lse) <= dx + 2.0 ** -22 * np.abs(lse) + 2.0 ** -20).all()
