@@ -226,6 +226,10 @@ def sv_workspace_init(workspace: torch.Tensor, stream=None) -> None:
         raise SpecVerifyError(st, "sv_workspace_init")
 
 
+def _current_device() -> int:
+    return torch._C._cuda_getDevice()
+
+
 def current_raw_stream(device_index: int) -> int:
     """Handle of a device's current stream, without a Stream object around it."""
     return torch._C._cuda_getCurrentRawStream(device_index)
@@ -481,15 +485,13 @@ _pack_attention = _packer(SvKvAttentionArgs).pack
 
 
 def _addr(t, dtype, shape, what: str) -> int:
-    """Address of a contiguous device tensor of the given type and shape (0
-    for None)."""
+    """Address of a contiguous tensor of the given type and shape (0 for None;
+    its device is _kv_call's to check)."""
     if t is None:
         return 0
     if t.dtype != dtype or t.shape != shape or not t.is_contiguous():
         raise ValueError(f"{what}: expected contiguous {dtype} {tuple(shape)}, "
                          f"got {t.dtype} {tuple(t.shape)}")
-    if not t.is_cuda:
-        raise ValueError("libspecverify takes device tensors")
     return t.data_ptr()
 
 
@@ -513,8 +515,6 @@ def _kv_cache(cache: dict, page_table, B: int) -> tuple:
         raise ValueError(f"page_table: expected contiguous int32 [{B}][slots]")
     slots = page_table.shape[1]
     table = _addr(page_table, torch.int32, (B, slots), "page_table")
-    if not (k.is_cuda and v.is_cuda):
-        raise ValueError("libspecverify takes device tensors")
     return (pages, P, H, D, k.data_ptr(), v.data_ptr(), st[0] if pages > 1 else 0,
             st[1] if H > 1 else P * D, ks, vs, table, slots)
 
@@ -528,16 +528,24 @@ def _rows4(t, shape, what: str) -> tuple:
                          f"{tuple(t.shape)}")
     if t.dtype not in _KV_DTYPES:
         raise ValueError(f"{what}: expected bfloat16, float16 or float32, got {t.dtype}")
-    if not t.is_cuda:
-        raise ValueError("libspecverify takes device tensors")
     return t.data_ptr(), st[0], st[1], st[2]
 
 
-def _kv_call(name: str, packed: bytes, workspace, stream) -> None:
-    if not workspace.is_cuda:
+def _kv_call(name: str, packed: bytes, workspace, stream, cache: dict, *tensors) -> None:
+    # The library launches on the current device: every pointer has to be
+    # that device's.
+    dev = workspace.get_device()
+    for t in (cache["k"], cache["v"], cache["k_scale"], cache["v_scale"], *tensors):
+        if t is not None and t.get_device() != dev:
+            raise ValueError(f"{name}: expected tensors of one device, got {t.device} beside a "
+                             f"workspace on {workspace.device}")
+    if dev < 0:
         raise ValueError("libspecverify takes device tensors")
+    if dev != _current_device():
+        raise ValueError(f"{name}: the tensors are on {workspace.device}, the current device is "
+                         f"cuda:{_current_device()}")
     if stream is None:
-        stream = current_raw_stream(workspace.get_device())
+        stream = current_raw_stream(dev)
     elif hasattr(stream, "cuda_stream"):
         stream = stream.cuda_stream
     st = getattr(_lib_handle or lib(), name)(packed, workspace.data_ptr(), workspace.nbytes, stream)
@@ -559,7 +567,8 @@ def sv_kv_write(cache: dict, page_table, kv_len, k_new, v_new, workspace, num_ne
     length = _addr(kv_len, torch.int32, (B,), "kv_len")
     num = _addr(num_new, torch.int32, (B,), "num_new")
     _kv_call("sv_kv_write", _pack_write(*c, B, T, _KV_DTYPES[k_new.dtype], k, v, *k_strides,
-                                        *v_strides, length, num), workspace, stream)
+                                        *v_strides, length, num), workspace, stream,
+             cache, page_table, kv_len, k_new, v_new, num_new)
 
 
 def sv_kv_read(cache: dict, page_table, start, num, k_out, v_out, workspace, rows=None,
@@ -577,7 +586,8 @@ def sv_kv_read(cache: dict, page_table, start, num, k_out, v_out, workspace, row
     count = _addr(num, torch.int32, (B,), "num")
     which = _addr(rows, torch.int32, (B, T), "rows")
     _kv_call("sv_kv_read", _pack_read(*c, B, T, _KV_DTYPES[k_out.dtype], k, v, *strides, first,
-                                      count, which), workspace, stream)
+                                      count, which), workspace, stream,
+             cache, page_table, start, num, k_out, v_out, rows)
 
 
 @functools.lru_cache(maxsize=1024)
@@ -608,4 +618,4 @@ def sv_kv_attention(q, cache: dict, page_table, kv_len, out, workspace, scale: f
     m = _addr(mask, torch.int32, (B, T, words), "mask")
     _kv_call("sv_kv_attention", _pack_attention(*c, B, T, Hq, _KV_DTYPES[q.dtype], qp, *strides,
                                                 o, ls, length, num, m, words, scale),
-             workspace, stream)
+             workspace, stream, cache, page_table, kv_len, q, out, num_new, mask, lse)

@@ -79,3 +79,90 @@ def test_a_capture_has_workspaces_of_its_own(gpu):
     gpu.capture = 0
     assert sv.workspace(100, DEV, "kv_attention") is eager
     assert sv.workspace(100, DEV, "tree") is not new  # the graph's stays the graph's
+
+
+# ------------------------------------------------------------------ devices
+
+class OnDevice:
+    """A CPU tensor that says it lives on a GPU."""
+
+    def __init__(self, t, index):
+        self.t, self.index = t, index
+
+    def __getattr__(self, name):
+        return getattr(self.t, name)
+
+    def get_device(self):
+        return self.index
+
+    @property
+    def device(self):
+        return torch.device("cuda", self.index)
+
+    @property
+    def is_cuda(self):
+        return True
+
+
+class Launches(list):
+    def __getattr__(self, name):
+        return lambda *args: (self.append(name), 0)[1]
+
+
+OPERANDS = {"write": ["page_table", "kv_len", "k_new", "v_new", "num_new", "workspace"],
+            "read": ["page_table", "start", "num", "k_out", "v_out", "rows", "workspace"],
+            "attention": ["page_table", "kv_len", "q", "out", "num_new", "mask", "lse",
+                          "workspace"]}
+
+
+def kv_arguments(op):
+    i32 = lambda *shape: torch.zeros(shape, dtype=torch.int32)
+    z = lambda: torch.zeros((4, 2, 16, 64), dtype=torch.uint8).view(torch.float8_e4m3fn)
+    x = lambda h: torch.zeros((2, 3, h, 64), dtype=torch.bfloat16)
+    a = dict(k=z(), v=z(), k_scale=torch.ones(4, 2), v_scale=torch.ones(4, 2), page_table=i32(2, 2),
+             workspace=torch.zeros(8192, dtype=torch.uint8))
+    a.update({"write": dict(kv_len=i32(2), k_new=x(2), v_new=x(2), num_new=i32(2)),
+              "read": dict(start=i32(2), num=i32(2), k_out=x(2), v_out=x(2), rows=i32(2, 3)),
+              "attention": dict(kv_len=i32(2), q=x(4), out=x(4), num_new=i32(2), mask=i32(2, 3, 1),
+                                lse=torch.zeros(2, 3, 4))}[op])
+    return a
+
+
+def kv_call(op, a):
+    a = dict(a)
+    cache = {n: a.pop(n) for n in ("k", "v", "k_scale", "v_scale")}
+    if op == "attention":
+        a["scale"] = 0.125
+    getattr(sv, "sv_kv_" + op)(cache, **a) if op != "attention" else \
+        sv.sv_kv_attention(a.pop("q"), cache, **a)
+
+
+@pytest.mark.parametrize("op", ["write", "read", "attention"])
+def test_tensors_of_another_device_are_refused(op, monkeypatch):
+    """Every tensor has to be on the workspace's device and that one be current;
+    nothing is launched otherwise."""
+    b = sv._binding
+    launches = Launches()
+    monkeypatch.setattr(b, "_lib_handle", launches)
+    current = [0]
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: current[0], raising=False)
+    monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda d: 0, raising=False)
+    args = kv_arguments(op)
+    names = ["k", "v", "k_scale", "v_scale"] + OPERANDS[op]
+    assert sorted(names) == sorted(args)
+    everywhere = lambda index: {n: OnDevice(t, index) for n, t in args.items()}
+    kv_call(op, everywhere(0))
+    assert launches == ["sv_kv_" + op]
+    for n in names:
+        with pytest.raises(ValueError, match="device"):
+            kv_call(op, dict(everywhere(0), **{n: OnDevice(args[n], 1)}))
+        with pytest.raises(ValueError, match="device"):
+            kv_call(op, dict(everywhere(0), **{n: args[n]}))
+    with pytest.raises(ValueError, match="current device"):
+        kv_call(op, everywhere(1))
+    with pytest.raises(ValueError, match="device tensors"):
+        kv_call(op, args)
+    assert len(launches) == 1
+    current[0] = 1
+    kv_call(op, everywhere(1))
+    assert len(launches) == 2
