@@ -52,25 +52,36 @@ def workspace(nbytes: int, device=None, key=None) -> torch.Tensor:
         device = torch.device(device if device is not None else "cuda")
         if device.index is None:
             device = torch.device("cuda", torch.cuda.current_device())
-    stream = current_raw_stream(device.index)
-    per_stream = key in _WS_PER_STREAM
-    k = (device, key, stream) if per_stream else (device, key)
-    capturing = torch.cuda.is_current_stream_capturing()
+    if key in _WS_PER_STREAM:
+        stream = current_raw_stream(device.index)
+        capturing = torch.cuda.is_current_stream_capturing()
+        buf = None if capturing else _ws_cache.get((device, key, stream))
+        if buf is None or buf.numel() < nbytes:
+            buf = _make_workspace(nbytes, device, (device, key, stream), stream, capturing)
+    else:
+        buf = _ws_cache.get((device, key))
+        if buf is None or buf.numel() < nbytes:
+            stream = current_raw_stream(device.index)
+            capturing = torch.cuda.is_current_stream_capturing()
+            buf = _make_workspace(nbytes, device, (device, key), stream, capturing)
+    return buf
+
+
+def _make_workspace(nbytes: int, device, k, stream: int, capturing: bool) -> torch.Tensor:
     with _ws_lock:
-        if not (capturing and per_stream):
-            buf = _ws_cache.get(k)
-            if buf is not None and buf.numel() >= nbytes:
-                return buf
         if capturing:
-            return _graph_workspace(nbytes, device, (device, key, stream), stream)
+            return _graph_workspace(nbytes, device, (k, stream), stream)
+        old = _ws_cache.get(k)
+        if old is not None and old.numel() >= nbytes:
+            return old  # another thread's, meanwhile
+        if old is not None:
+            _ws_kept.append(old)
         # (sizes are rounded up to a power of two: all that a growing one
         # leaves behind is smaller than the last)
-        if buf is not None:
-            _ws_kept.append(buf)
-        buf = _ws_cache[k] = _new_workspace(1 << (max(nbytes, 256) - 1).bit_length(), device,
-                                            stream)
-        if not per_stream:
-            torch.cuda.current_stream(device).synchronize()  # zeroed, for every stream
+        buf = _new_workspace(1 << (max(nbytes, 256) - 1).bit_length(), device, stream)
+        if len(k) == 2:  # any stream may be the next to use it: zeroed by then
+            torch.cuda.current_stream(device).synchronize()
+        _ws_cache[k] = buf
         return buf
 
 
