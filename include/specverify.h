@@ -321,7 +321,9 @@ sv_status sv_row_stats(const sv_chain_args* args, float* alpha, float* expected,
  *     value = code * k_scale[p * Hkv + h].
  * A scale is a power of two, 2^e with -48 <= e <= 48: the largest value of
  * a page and head decides e (below), so codes lose no more than e4m3's own
- * rounding, and changing a page's scale moves codes by whole exponents.
+ * rounding, and changing a page's scale moves codes by whole exponents.  A
+ * stored scale that is none of these records SV_DERR_ARG in a call that uses
+ * it; it counts as the power of two of its exponent bits, clamped.
  * Token position i of request b lives in page page_table[b * slots + i /
  * page_size]; entries a call does not need are not read and may hold
  * anything.  Several requests may name one page as long as no call writes

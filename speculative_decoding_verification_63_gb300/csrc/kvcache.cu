@@ -252,7 +252,7 @@ sv_status sv_kv_read(const sv_kv_read_args* a, void* workspace, size_t ws_bytes,
   p.rows = a->rows;
   p.err = error_word(workspace);
   // Chunks of sixteen values, eight per thread once that fills the GPU (four
-  // blocks an SM), else one: 8 requests of 16000 tokens take 119 us against 164
+  // blocks an SM), else one: 8 requests of 16000 tokens take 118 us against 164
   // with one, 2048 tokens 19.3 against 22.0, 1024 (below the rule) 11.8 against
   // 11.9, 16 tokens 4.0 against 2.1.
   const int per = p.c.Hkv * (p.c.D / 16);

@@ -358,8 +358,8 @@ struct KaFeed {
   bool is_v;
   struct Item {
     const unsigned char* src;  // null: nothing to copy
-    int bytes;
-    float scale, v_scale;      // of the lane's side, of the values; < 0: no such page
+    int bytes;                 // 0: no such page
+    float scale, v_scale;      // as stored: of the lane's side, of the values
     int first, tokens, round;  // the block begins a segment; its place
     int b, head, tile, rows;   // its unit; rows of the request
   };
@@ -391,11 +391,19 @@ struct KaFeed {
       advance(a, NB);
     }
   }
+  // The scale of an item, < 0 if there is no such page.  (A batch later than the
+  // load: its value must not be waited for there.)
+  static __device__ __forceinline__ float scale_of(const KvAttnProblem& a, const Item& it) {
+    if (it.bytes == 0) return -1.f;
+    const float s = scale_value(it.scale);
+    if (s != it.scale) record_error(a.err, SV_DERR_ARG);
+    return s;
+  }
   __device__ __forceinline__ Item resolve(const KvAttnProblem& a) {
     Item it;
     it.src = nullptr;
     it.bytes = 0;
-    it.scale = it.v_scale = -1.f;
+    it.scale = it.v_scale = 1.f;
     it.first = a_first;
     it.tokens = a_tokens;
     it.round = a_round;
@@ -575,7 +583,7 @@ __device__ __forceinline__ void ka_produce(const KvAttnProblem& a, Shared& sh, i
           bulk_copy_g2s_hint((feed.is_v ? sh.v[s] : sh.k[s]) + feed.sub * 16 * D, item.src,
                              item.bytes, &sh.full[s], pol);
         }
-        (feed.is_v ? sh.v_scale[s] : sh.k_scale[s])[feed.sub] = item.scale;
+        (feed.is_v ? sh.v_scale[s] : sh.k_scale[s])[feed.sub] = Feed::scale_of(a, item);
         mbar_arrive(&sh.full[s]);
       }
       __syncwarp();

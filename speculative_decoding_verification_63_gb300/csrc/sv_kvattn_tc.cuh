@@ -492,7 +492,8 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv_attn_tc_kernel(const KvAttnP
       next = feed.resolve(a);
       feed.look(a, i0 < -Feed::NB);
       if (i0 < 0) continue;
-      const unsigned missing = __ballot_sync(0xffffffffu, item.scale < 0.f);
+      const float scale = Feed::scale_of(a, item);
+      const unsigned missing = __ballot_sync(0xffffffffu, scale < 0.f);
 #pragma unroll 1
       for (int j = 0; j < Feed::NB && i < n; ++j, ++i) {
         const TcSlot at(side, i);
@@ -514,7 +515,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv_attn_tc_kernel(const KvAttnP
             TcMeta& m = sh.meta[i % kTcMeta];
             if (item.first) tc_prefetch_q<D, T>(a, item, lane % Feed::kCopies, Feed::kCopies);
             const int e = scale_exp(item.v_scale);
-            m.s[feed.sub].x = item.scale < 0.f ? -1.f : pow2f(scale_exp(item.scale));
+            m.s[feed.sub].x = scale;
             m.s[feed.sub].y = static_cast<float>(e);
             m.s[feed.sub].z = pow2f(-e);
             if (feed.sub == 0) {

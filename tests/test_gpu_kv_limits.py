@@ -330,3 +330,39 @@ def test_scores_that_fall_or_alternate_far(T, G, D, shape):
     tol, dx = ku.out_bounds(out, spr, xerr, D, torch.bfloat16)
     assert (np.abs(o[pick] - out) <= tol).all()
     assert (np.abs(l[pick] - lse) <= dx + 2.0 ** -22 * np.abs(lse) + 2.0 ** -20).all()
+
+
+# ------------------------------------------------- scales that no write made
+
+@pytest.mark.parametrize("T,Hq", [(2, 4), (9, 8), (40, 6)])
+@pytest.mark.parametrize("bad,counts", [(3.0, 2.0), (0.75, 0.5), (-2.0, 2.0), (0.0, 2.0 ** -48),
+                                        (2.0 ** -60, 2.0 ** -48), (2.0 ** 90, 2.0 ** 48),
+                                        (float("inf"), 2.0 ** 48), (float("nan"), 2.0 ** 48)])
+def test_scales_that_are_no_powers_of_two(bad, counts, T, Hq):
+    """Reads, attention and writes take such a scale as the same power of two
+    and say so."""
+    rng = np.random.default_rng(71)
+    H, P, D, lens = 2, 16, 64, [50, 20]
+    table = i32([[0, 1, 2, 3, 4, 5], [6, 7, 8, 9, 10, 11]])
+    c = ku.random_cache(rng, 12, H, P, D)
+    q, _ = as_type(rng.normal(size=(2, T, Hq, D)) * 0.1, "bf16")
+    x, _ = as_type(rng.normal(size=(2, 2, H, D)), "bf16")
+    side = rng.choice(["k", "v"])
+    results = []
+    for value in (bad, counts):
+        dev = ku.to_device(c)
+        dev[side + "_scale"][1, 0] = value
+        ws = new_ws(sv.sv_kv_attention_workspace_bytes(2, T, Hq, H, D))
+        want = (sv.SV_OK, 0) if value == counts else (sv.SV_EDATA, sv.SV_DERR_ARG)
+        read = sv.kv_read(dev, table, i32([0, 0]), i32([40, 20]), 40, dtype=torch.float32, ws=ws)
+        assert flags(ws) == want
+        att = sv.kv_attention(q, dev, table, i32(lens), num_new=i32([T, 1]), with_lse=True, ws=ws)
+        assert flags(ws) == want
+        # a write behind tokens of that page that stay
+        sv.kv_write(dev, table, i32([25, 3]), x, x, ws=ws)
+        assert flags(ws) == want
+        again = sv.kv_read(dev, table, i32([0, 0]), i32([27, 5]), 27, dtype=torch.float32, ws=ws)
+        results.append([read["k"], read["v"], att["out"], att["lse"], again["k"], again["v"]])
+    for a, b in zip(*results):
+        assert torch.equal(torch.nan_to_num(a), torch.nan_to_num(b))
+        assert torch.equal(torch.isnan(a), torch.isnan(b))
