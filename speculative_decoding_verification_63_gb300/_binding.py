@@ -500,13 +500,18 @@ def _kv_cache(cache: dict, page_table, B: int) -> tuple:
     [pages][Hkv][P][D] e4m3, k_scale, v_scale [pages][Hkv] fp32) and the page
     table [B][slots]."""
     k, v = cache["k"], cache["v"]
-    shape, st = k.shape, k.stride()
+    shape = k.shape
     if k.dtype != torch.float8_e4m3fn or len(shape) != 4:
         raise ValueError(f"cache k: expected float8_e4m3fn [pages][heads][page][D], got {k.dtype} "
                          f"{tuple(shape)}")
     pages, H, P, D = shape
-    if v.dtype != k.dtype or v.shape != shape or v.stride() != st:
+    if v.dtype != k.dtype or v.shape != shape:
         raise ValueError("cache v: expected k's dtype, shape and strides")
+    st, v_st = k.stride(), v.stride()
+    if v_st != st:
+        # the stride of a dimension of size 1 says nothing
+        if any(a != b for a, b, n in zip(st, v_st, shape) if n > 1):
+            raise ValueError("cache v: expected k's dtype, shape and strides")
     if st[3] != 1 or st[2] != D:
         raise ValueError("cache: the tokens of a page and head must be contiguous")
     ks = _addr(cache["k_scale"], torch.float32, (pages, H), "k_scale")
@@ -521,13 +526,16 @@ def _kv_cache(cache: dict, page_table, B: int) -> tuple:
 
 def _rows4(t, shape, what: str) -> tuple:
     """(address, batch, token and head stride) of a [B][T][heads][D] tensor
-    with contiguous D."""
-    st = t.stride()
-    if t.shape != shape or st[3] != 1:
+    with contiguous D; the stride of a dimension of size 1, which says nothing,
+    is 0."""
+    if t.shape != shape or t.stride(3) != 1:
         raise ValueError(f"{what}: expected {tuple(shape)} with contiguous rows, got "
                          f"{tuple(t.shape)}")
     if t.dtype not in _KV_DTYPES:
         raise ValueError(f"{what}: expected bfloat16, float16 or float32, got {t.dtype}")
+    st = t.stride()
+    if 1 in shape[:3]:
+        st = [x if n > 1 else 0 for x, n in zip(st, shape)]
     return t.data_ptr(), st[0], st[1], st[2]
 
 

@@ -166,3 +166,57 @@ def test_tensors_of_another_device_are_refused(op, monkeypatch):
     current[0] = 1
     kv_call(op, everywhere(1))
     assert len(launches) == 2
+
+
+# ------------------------------------------------------------------ strides
+
+def packed_arguments(op, args, monkeypatch):
+    """The C arguments of a call, without launching it."""
+    b, out = sv._binding, []
+    cls = {"write": b.SvKvWriteArgs, "read": b.SvKvReadArgs, "attention": b.SvKvAttentionArgs}[op]
+    monkeypatch.setattr(b, "_kv_call", lambda name, packed, *rest: out.append(packed))
+    kv_call(op, args)
+    return cls.from_buffer_copy(out[0])
+
+
+def test_strides_of_dimensions_of_one(monkeypatch):
+    """They say nothing, and differ between tensors that are laid out alike."""
+    odd = lambda t, dim, stride: t.as_strided(
+        t.shape, [stride if i == dim else s for i, s in enumerate(t.stride())])
+    raw = torch.zeros((1, 1, 16, 64), dtype=torch.uint8)
+    code = lambda t: t.view(torch.float8_e4m3fn)
+    cache = dict(k=code(raw), v=code(odd(odd(raw, 0, 8), 1, 8)), k_scale=torch.ones(1, 1),
+                 v_scale=torch.ones(1, 1))
+    i32 = lambda *shape: torch.zeros(shape, dtype=torch.int32)
+    ws = torch.zeros(8192, dtype=torch.uint8)
+    x = torch.zeros((1, 1, 1, 64), dtype=torch.bfloat16)
+    y = odd(odd(odd(x, 0, 3), 1, 5), 2, 7)
+    a = packed_arguments("read", dict(cache, page_table=i32(1, 1), start=i32(1), num=i32(1), k_out=x,
+                                      v_out=y, workspace=ws), monkeypatch)
+    assert (a.cache.page_stride, a.cache.head_stride) == (0, 16 * 64)
+    assert (a.out_batch_stride, a.out_token_stride, a.out_head_stride) == (0, 0, 0)
+    a = packed_arguments("write", dict(cache, page_table=i32(1, 1), kv_len=i32(1), k_new=y, v_new=x,
+                                       workspace=ws), monkeypatch)
+    assert (a.k_batch_stride, a.k_token_stride, a.k_head_stride) == (0, 0, 0)
+    a = packed_arguments("attention", dict(cache, page_table=i32(1, 1), kv_len=i32(1), q=y,
+                                           out=torch.zeros_like(x), workspace=ws), monkeypatch)
+    assert (a.q_batch_stride, a.q_token_stride, a.q_head_stride) == (0, 0, 0)
+    # strides of other dimensions count as before
+    args = kv_arguments("read")
+    a = packed_arguments("read", args, monkeypatch)
+    assert (a.out_batch_stride, a.out_token_stride, a.out_head_stride) == (384, 128, 64)
+    wide = torch.zeros((2, 3, 2, 80), dtype=torch.bfloat16)[..., :64]
+    with pytest.raises(ValueError):
+        packed_arguments("read", dict(args, v_out=wide), monkeypatch)
+    with pytest.raises(ValueError):
+        packed_arguments("read", dict(args, v=torch.zeros((4, 2, 17, 64), dtype=torch.uint8).view(
+            torch.float8_e4m3fn)[:, :, :16]), monkeypatch)
+
+
+@pytest.mark.parametrize("op,name", [("write", "k_new"), ("write", "v_new"), ("read", "v_out"),
+                                     ("attention", "q"), ("write", "k"), ("read", "page_table")])
+def test_other_numbers_of_dimensions_are_refused(op, name):
+    args = kv_arguments(op)
+    for t in (args[name][0], args[name][None], args[name].flatten()):
+        with pytest.raises(ValueError):
+            kv_call(op, dict(args, **{name: t}))
