@@ -385,7 +385,8 @@ struct KaFeed {
       a_first = cur.blk == 0 || (first && threadIdx.x % 32 < kCopies);
       a_tokens = cur.l.len + cur.l.n - cur.blk * BLOCK;
       a_round = cur.blk * BLOCK - cur.l.len;
-      if (a_pos < cur.l.len + cur.l.n)
+      if (a_pos < cur.l.len + cur.l.n &&
+          SV_CHECK(cur.b < a.B && a_pos >= 0 && (a_pos >> a.c.page_shift) < a.c.slots, a.err))
         page = a.c.page_table[static_cast<long long>(cur.b) * a.c.slots +
                               (a_pos >> a.c.page_shift)];
       advance(a, NB);
@@ -578,10 +579,13 @@ __device__ __forceinline__ void ka_produce(const KvAttnProblem& a, Shared& sh, i
         ka_wait(&sh.empty[s], static_cast<uint32_t>(i / kKaStages - 1) & 1, &sh.dead, a.err);
       __syncwarp();
       if (lane / Feed::kCopies == j) {
-        if (item.src != nullptr && !*static_cast<volatile int*>(&sh.dead)) {
+        unsigned char* const dst = (feed.is_v ? sh.v[s] : sh.k[s]) + feed.sub * 16 * D;
+        if (item.src != nullptr && !*static_cast<volatile int*>(&sh.dead) &&
+            SV_CHECK(bulk_args_ok(dst, item.src, item.bytes) &&
+                         feed.sub * 16 * D + item.bytes <= kKaBlock * D,
+                     a.err)) {
           mbar_expect_tx(&sh.full[s], item.bytes);
-          bulk_copy_g2s_hint((feed.is_v ? sh.v[s] : sh.k[s]) + feed.sub * 16 * D, item.src,
-                             item.bytes, &sh.full[s], pol);
+          bulk_copy_g2s_hint(dst, item.src, item.bytes, &sh.full[s], pol);
         }
         (feed.is_v ? sh.v_scale[s] : sh.k_scale[s])[feed.sub] = Feed::scale_of(a, item);
         mbar_arrive(&sh.full[s]);
@@ -959,6 +963,9 @@ __global__ void __launch_bounds__(kKaThreads, kKaCtasPerSm) kv_attn_kernel(const
       // the unit is cut: CTAs first .. last hold a part of it
       const int first = parts.of(cur.unit0), last = parts.of(cur.unit0 + cur.nblk - 1);
       constexpr int PF = kKaPartialFloats<D>;
+      if (!SV_CHECK(first >= 0 && first <= cta && cta <= last && last < min(grid, kKaMaxCtas),
+                    a.err))
+        return;  // (all consumers: the sizes are the CTA's)
       if (warp == 0) {
         // a part that begins inside the unit is its CTA's first
         acc.store(a.partials + (2ll * cta + (starts ? 1 : 0)) * PF, lane);

@@ -256,6 +256,7 @@ __device__ __forceinline__ void tc_wait(uint64_t* bar, uint32_t parity, int* dea
 // with it, else its first.
 template <int D>
 __device__ __forceinline__ float* tc_part(const KvAttnProblem& a, int c, int first) {
+  if (!SV_CHECK(c >= 0 && c < min(static_cast<int>(gridDim.x), kTcMaxCtas), a.err)) c = 0;
   return a.partials + (2ll * c + (c == first ? 1 : 0)) * kTcPartialFloats<D>;
 }
 // What a part with reference r counts against a reference m.  One that saw
@@ -500,10 +501,13 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv_attn_tc_kernel(const KvAttnP
         const int slot = at.slot;
         if (i >= at.slots) tc_wait(&sh.rawempty[slot], at.phase ^ 1, dead, a.err);
         if (lane / Feed::kCopies == j) {
-          if (item.src != nullptr && !*static_cast<volatile int*>(dead)) {
+          unsigned char* const dst = &sh.raw[slot][feed.sub * 16 * D];
+          if (item.src != nullptr && !*static_cast<volatile int*>(dead) &&
+              SV_CHECK(bulk_args_ok(dst, item.src, item.bytes) &&
+                           feed.sub * 16 * D + item.bytes <= kTcBlock * D,
+                       a.err)) {
             mbar_expect_tx(&sh.rawfull[slot], item.bytes);
-            bulk_copy_g2s_hint(&sh.raw[slot][feed.sub * 16 * D], item.src, item.bytes,
-                               &sh.rawfull[slot], pol);
+            bulk_copy_g2s_hint(dst, item.src, item.bytes, &sh.rawfull[slot], pol);
           }
           const unsigned gone = missing >> (j * Feed::kCopies) & ((1u << Feed::kCopies) - 1);
           // the last position that every row of the unit sees, in the round

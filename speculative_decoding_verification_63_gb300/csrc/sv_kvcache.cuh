@@ -185,16 +185,18 @@ __global__ void __launch_bounds__(kKvThreads) kv_write_kernel(const KvWriteProbl
       const int from = max(len, slot << a.c.page_shift);
       const long long to =
           min(static_cast<long long>(len) + n, (static_cast<long long>(slot) + 1) << a.c.page_shift);
-      if (from < to) {
+      if (from < to && SV_CHECK(slot >= 0 && slot < a.c.slots, a.err)) {
         page = a.c.page_table[static_cast<long long>(b) * a.c.slots + slot];
         if (page < 0 || page >= a.c.num_pages) {
           if (h == 0 && side == 0 && gl == 0) record_error(a.err, SV_DERR_PAGE);
         } else {
-          active = true;
           kept = i == 0 ? len & (P - 1) : 0;
           first = from - len;
           count = static_cast<int>(to - from);
           row0 = from & (P - 1);
+          active = SV_CHECK(row0 + count <= P && first + count <= a.T && first >= 0 &&
+                                count * (D / 16) <= GT * CH,
+                            a.err);
         }
       }
     }
@@ -372,6 +374,7 @@ __global__ void __launch_bounds__(kKvThreads, 4) kv_read_kernel(const KvReadProb
         if (report) record_error(a.err, SV_DERR_ARG);
         continue;
       }
+      if (!SV_CHECK(h < Hkv && (pos >> a.c.page_shift) < a.c.slots, a.err)) continue;
       const int page =
           a.c.page_table[static_cast<long long>(b) * a.c.slots + (pos >> a.c.page_shift)];
       if (page < 0 || page >= a.c.num_pages) {
