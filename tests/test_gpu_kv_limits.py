@@ -6,7 +6,7 @@ import torch
 
 import kv_util as ku
 import speculative_decoding_verification_63_gb300 as sv
-from test_gpu_kvcache import TYPES, as_type, flags, i32, new_ws
+from test_gpu_kvcache import TYPES, as_type, check_attention, flags, i32, new_ws
 
 pytestmark = pytest.mark.gpu
 
@@ -366,3 +366,25 @@ def test_scales_that_are_no_powers_of_two(bad, counts, T, Hq):
     for a, b in zip(*results):
         assert torch.equal(torch.nan_to_num(a), torch.nan_to_num(b))
         assert torch.equal(torch.isnan(a), torch.isnan(b))
+
+
+# ------------------------------------------------------- many requests, wide groups
+
+@pytest.mark.parametrize("B,T,Hq,H,D", [(500, 2, 2, 1, 64), (1024, 1, 3, 3, 64), (700, 50, 1, 1, 64),
+                                        (1000, 13, 4, 1, 128)])
+def test_attention_of_more_requests_than_a_pass_scans(B, T, Hq, H, D):
+    rng = np.random.default_rng(91)
+    lens, new = rng.integers(0, 50, B).tolist(), rng.integers(0, T + 1, B).tolist()
+    check_attention(rng, lens, new, T, Hq, H, 16, D, "bf16")
+
+
+@pytest.mark.parametrize("lens,new,T,Hq,H,P,D,dtype", [
+    ([300, 5], [1, 1], 1, 17, 1, 64, 64, "bf16"),
+    ([300, 70, 0], [1, 1, 1], 1, 64, 2, 16, 128, "fp16"),
+    ([1000], [1], 1, 48, 1, 64, 128, "bf16"),
+    ([130, 7], [1, 1], 1, 256, 1, 32, 64, "bf16"),
+    ([200, 0], [5, 3], 5, 100, 4, 64, 128, "bf16"),
+    ([90], [3], 3, 256, 256, 16, 64, "fp16"),
+])
+def test_attention_of_wide_groups(lens, new, T, Hq, H, P, D, dtype):
+    check_attention(np.random.default_rng(92), lens, new, T, Hq, H, P, D, dtype)
