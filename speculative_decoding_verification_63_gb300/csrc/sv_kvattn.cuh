@@ -121,7 +121,8 @@ __device__ __forceinline__ int ka_row_exp(float m) {
 __device__ __forceinline__ float ka_finite(float c) { return fminf(c, 3.40282347e38f); }
 
 // Whether the reference has to follow a block whose largest score is mx.
-// (Not if both are -inf: then neither block nor row has anything to weigh.)
+// (A row's first block becomes its reference before: there is nothing to
+// multiply yet.  Both are -inf while the row has seen nothing.)
 __device__ __forceinline__ bool ka_far(float mx, float ref) { return fabsf(mx - ref) > kRefReach; }
 // Moves the reference to a block's mx where that is far from it; returns what
 // the sums so far (z: the row's) are to be multiplied by.  (To mx itself, not to
@@ -131,7 +132,7 @@ __device__ __forceinline__ bool ka_far(float mx, float ref) { return fabsf(mx - 
 // with whole numbers 2.95e-4.)
 __device__ __forceinline__ float ka_move(float mx, float& ref, float z) {
   if (!ka_far(mx, ref)) return 1.f;
-  const float f = ref == kNegInf ? 0.f : fast_exp2(ref - mx);
+  const float f = fast_exp2(ref - mx);
   if (mx < ref && !(z * f < kRefRoom)) return 1.f;
   ref = mx;
   return f;
@@ -795,6 +796,9 @@ __global__ void __launch_bounds__(kKaThreads, kKaCtasPerSm) kv_attn_kernel(const
         for (int nt = 0; nt < 4; ++nt) m = fmaxf(m, fmaxf(x[nt][2 * r], x[nt][2 * r + 1]));
         mx[r] = quad_max(m);
       }
+#pragma unroll
+      for (int r = 0; r < 2; ++r)
+        if (acc.ref[r] == kNegInf) acc.ref[r] = mx[r];
       const bool far = ka_far(mx[0], acc.ref[0]) || ka_far(mx[1], acc.ref[1]);
       if (__builtin_expect(__any_sync(0xffffffffu, far), 0)) {
 #pragma unroll

@@ -715,7 +715,6 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv_attn_tc_kernel(const KvAttnP
       const int own = 8 >> cs;
       const float c2 = sh.c2[odd][row];
       float ref = kNegInf, z = 0.f;
-      bool had = false;  // this stream has taken a block of the unit
 
 #pragma unroll 1
       for (int i = i0 + ((i0 ^ set) & 1); i < i0 + nb; i += 2) {
@@ -771,9 +770,10 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv_attn_tc_kernel(const KvAttnP
               mx = fmaxf(mx, fmaf(v[0], ka_finite(c2 * fabsf(ms.x)), ms.y));
             }
           }
+          if (ref == kNegInf) ref = mx;
           if (__builtin_expect(__any_sync(0xffffffffu, ka_far(mx, ref)), 0)) {
             const float f = ka_move(mx, ref, z);
-            if (had && __any_sync(0xffffffffu, f != 1.f)) {
+            if (__any_sync(0xffffffffu, f != 1.f)) {
               // O_s whole: the products of block i - 2 are done (their weights
               // made way for these scores).  It goes through the registers of
               // the scores, which are loaded again: half as many waits as
@@ -791,7 +791,6 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv_attn_tc_kernel(const KvAttnP
               tc_ld32(x, ts + (own - 2) * 16);
             }
           }
-          had = true;
           // the weights, over the scores they come from
           const float bs = ref == kNegInf ? 0.f : ref - kRefShift;
 #pragma unroll 1
