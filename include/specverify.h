@@ -358,7 +358,7 @@ typedef struct {
  * token written are not touched.
  *
  * NaN or inf in the new values records SV_DERR_NONFINITE; kv_len < 0,
- * num_new outside [0, T] or a length past slots * page_size records
+ * num_new outside [0, T] or tokens past slots * page_size record
  * SV_DERR_ARG and the request is not written; a page id outside
  * [0, num_pages) records SV_DERR_PAGE and that page is not written.  Only
  * the workspace's error word is used (SV_MIN_WORKSPACE_BYTES).

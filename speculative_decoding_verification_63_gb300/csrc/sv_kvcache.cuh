@@ -176,7 +176,8 @@ __global__ void __launch_bounds__(kKvThreads) kv_write_kernel(const KvWriteProbl
     const int len = a.kv_len[b];
     const int n = a.num_new ? a.num_new[b] : a.T;
     const bool ok = len >= 0 && n >= 0 && n <= a.T &&
-                    static_cast<long long>(len) + n <= static_cast<long long>(a.c.slots) * P;
+                    (n == 0 ||
+                     static_cast<long long>(len) + n <= static_cast<long long>(a.c.slots) * P);
     active = false;
     if (!ok) {
       if (i == 0 && h == 0 && side == 0 && gl == 0) record_error(a.err, SV_DERR_ARG);

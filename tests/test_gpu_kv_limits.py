@@ -6,7 +6,7 @@ import torch
 
 import kv_util as ku
 import speculative_decoding_verification_63_gb300 as sv
-from test_gpu_kvcache import TYPES, as_type, check_attention, flags, i32, new_ws
+from test_gpu_kvcache import TYPES, as_type, check_attention, flags, i32, new_ws, same_cache
 
 pytestmark = pytest.mark.gpu
 
@@ -388,3 +388,30 @@ def test_attention_of_more_requests_than_a_pass_scans(B, T, Hq, H, D):
 ])
 def test_attention_of_wide_groups(lens, new, T, Hq, H, P, D, dtype):
     check_attention(np.random.default_rng(92), lens, new, T, Hq, H, P, D, dtype)
+
+
+def test_commit_beside_a_full_request():
+    """A request that holds as many tokens as its pages do, and takes no part in
+    the round, is no error of the batch's."""
+    rng = np.random.default_rng(95)
+    H, P, D = 2, 16, 64
+    c = ku.random_cache(rng, 6, H, P, D)
+    table = np.array([[0, 1], [2, 3], [4, 5]], np.int32)
+    lens, accept = [2 * P, 10, 2 * P - 1], [0, 2, 0]
+    nodes = np.array([[-1, -1], [2, 5], [-1, -1]], np.int32)
+    dev, ws = ku.to_device(c), new_ws()
+    x, x64 = as_type(rng.normal(size=(3, 6, H, D)), "bf16")
+    new = [0, 6, 1]
+    sv.kv_write(dev, i32(table), i32(lens), x, x, num_new=i32(new), ws=ws)
+    c.write(table, lens, new, x64, x64)
+    moved = {s: np.zeros((3, 2, H, D)) for s in "kv"}
+    for s in "kv":
+        moved[s][1] = c.values(s, table[1], 10 + nodes[1])
+    c.write(table, [n + 1 for n in lens], accept, moved["k"], moved["v"])
+    sv.kv_commit(dev, i32(table), i32(lens), i32(accept), i32(nodes), ws=ws)
+    assert flags(ws) == (sv.SV_OK, 0)
+    same_cache(dev, c)
+    # tokens that do not fit stay one
+    sv.kv_write(dev, i32(table), i32(lens), x, x, num_new=i32([1, 0, 0]), ws=ws)
+    assert flags(ws) == (sv.SV_EDATA, sv.SV_DERR_ARG)
+    same_cache(dev, c)
