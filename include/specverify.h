@@ -439,7 +439,7 @@ typedef struct {
   sv_dtype dtype;            /* of q and out: SV_BF16 or SV_FP16 */
   const void* q;             /* [B][T][Hq][D], D contiguous */
   int64_t q_batch_stride, q_token_stride, q_head_stride; /* elements */
-  void* out;                 /* [B][T][Hq][D] contiguous */
+  void* out;                 /* [B][T][Hq][D] contiguous; apart from q and the cache */
   float* lse;                /* optional [B][T][Hq] */
   const int32_t* kv_len;     /* [B] tokens before the round */
   const int32_t* num_new;    /* [B] in [0, T], or NULL (= T) */

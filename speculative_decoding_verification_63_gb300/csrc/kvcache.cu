@@ -126,9 +126,9 @@ sv_status launch_large(void (*kernel)(KvAttnProblem), const KvAttnProblem& p, in
 // Rounds of up to kKaFewRows query rows a key/value head take the warp-level
 // products (each tile of 16 rows reads the cache, all but the first from L2),
 // larger ones the tensor-memory ones.  64 requests of up to 4096 tokens: 28
-// rows 91 us against 132, 36 rows 111 against 144, 48 rows 149 against 152, 64
-// rows 176 against 149; 8 requests of 16000: 32 rows 53 against 75, 48 rows 80
-// against 76.
+// rows 92 us against 137, 36 rows 114 against 148, 48 rows 152 against 158, 64
+// rows 182 against 157; 8 requests of 16000: 32 rows 54 against 75, 48 rows 82
+// against 78.
 constexpr int kKaFewRows = 48;
 
 template <int D, class T>

@@ -40,10 +40,10 @@
 // fragments take straight from shared memory into registers.  One producer
 // warp of bulk copies, four consumer warps (pairs on alternate blocks, a half
 // of the positions each), two CTAs an SM.  Bound: HBM for one tile (64
-// requests of up to 8192 tokens, 16 rows or fewer: 137 us, 88 % of the copy
+// requests of up to 8192 tokens, 16 rows or fewer: 138 us, 87 % of the copy
 // bandwidth); for more, the products and conversions, 512 of the 697 clocks in
 // which HBM delivers a block of 64 (28 rows, 64 requests of up to 4096 tokens:
-// 91 us against 52); for a single short request (2047 tokens: 13.9 us) the
+// 91 us against 52); for a single short request (2047 tokens: 14.4 us) the
 // chain launch, lengths, page ids, scales, copies, two blocks, join, of one to
 // three microseconds each.
 #pragma once

@@ -32,8 +32,9 @@
 // products 400, products 800, with two streams 2350 clocks a block (one warp's
 // instructions share their scheduler with four others').  To that come, a unit,
 // some 5 us for the queries, masks and the result, and the join of cut units
-// (16 requests of up to 8192 tokens, 32 nodes, 128 rows: 86 us; 2 requests with
-// chunks of 1024 tokens: 167 us).  Tried: three score buffers and one
+// (16 requests of up to 8192 tokens, 32 nodes, 128 rows: 88 us; 2 requests with
+// chunks of 1024 tokens: 174 us; 86 and 167 before the reference followed low
+// blocks too, which is what the figures below compare with).  Tried: three score buffers and one
 // accumulator (streams hand their reference on): 107 and 324 us, a rise of the
 // maximum stalls both streams; weights in one pass over the scores: 116 and 231
 // us; all conversions of a block before the wait for its buffer: 92 and 177 us
