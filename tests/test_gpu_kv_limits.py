@@ -1,5 +1,7 @@
-"""The cache's attention where rounds, requests and codes are unusual: many
-units to a CTA with NaN codes among them."""
+"""The cache's calls at their limits: NaN codes among many short units, default
+workspaces in graphs and on several streams, rows without a token, the ends of
+the number ranges, dominant keys, scales no write made, many requests, wide
+groups, full requests."""
 import numpy as np
 import pytest
 import torch
