@@ -226,13 +226,10 @@ def sv_workspace_init(workspace: torch.Tensor, stream=None) -> None:
         raise SpecVerifyError(st, "sv_workspace_init")
 
 
-def _current_device() -> int:
-    return torch._C._cuda_getDevice()
-
-
-def current_raw_stream(device_index: int) -> int:
-    """Handle of a device's current stream, without a Stream object around it."""
-    return torch._C._cuda_getCurrentRawStream(device_index)
+# The current device, and the handle of a device's current stream (without a
+# Stream object around it).
+_current_device = torch._C._cuda_getDevice
+current_raw_stream = torch._C._cuda_getCurrentRawStream
 
 
 def sv_stream_capture_id(stream) -> int:
@@ -484,18 +481,25 @@ _pack_write, _pack_read = _packer(SvKvWriteArgs).pack, _packer(SvKvReadArgs).pac
 _pack_attention = _packer(SvKvAttentionArgs).pack
 
 
-def _addr(t, dtype, shape, what: str) -> int:
-    """Address of a contiguous tensor of the given type and shape (0 for None;
-    its device is _kv_call's to check)."""
+def _wrong_device(t, dev: int) -> None:
+    raise ValueError(f"expected tensors of one device, got one on {t.device} beside a workspace "
+                     f"on {'cpu' if dev < 0 else f'cuda:{dev}'}")
+
+
+def _addr(t, dtype, shape, what: str, dev: int) -> int:
+    """Address of a contiguous tensor of the given type, shape and device (0
+    for None)."""
     if t is None:
         return 0
     if t.dtype != dtype or t.shape != shape or not t.is_contiguous():
         raise ValueError(f"{what}: expected contiguous {dtype} {tuple(shape)}, "
                          f"got {t.dtype} {tuple(t.shape)}")
+    if t.get_device() != dev:
+        _wrong_device(t, dev)
     return t.data_ptr()
 
 
-def _kv_cache(cache: dict, page_table, B: int) -> tuple:
+def _kv_cache(cache: dict, page_table, B: int, dev: int) -> tuple:
     """The fields of an sv_kv_cache, from the cache's tensors (k, v
     [pages][Hkv][P][D] e4m3, k_scale, v_scale [pages][Hkv] fp32) and the page
     table [B][slots]."""
@@ -514,17 +518,19 @@ def _kv_cache(cache: dict, page_table, B: int) -> tuple:
             raise ValueError("cache v: expected k's dtype, shape and strides")
     if st[3] != 1 or st[2] != D:
         raise ValueError("cache: the tokens of a page and head must be contiguous")
-    ks = _addr(cache["k_scale"], torch.float32, (pages, H), "k_scale")
-    vs = _addr(cache["v_scale"], torch.float32, (pages, H), "v_scale")
+    if k.get_device() != dev or v.get_device() != dev:
+        _wrong_device(v if k.get_device() == dev else k, dev)
+    ks = _addr(cache["k_scale"], torch.float32, (pages, H), "k_scale", dev)
+    vs = _addr(cache["v_scale"], torch.float32, (pages, H), "v_scale", dev)
     if page_table.dim() != 2:
         raise ValueError(f"page_table: expected contiguous int32 [{B}][slots]")
     slots = page_table.shape[1]
-    table = _addr(page_table, torch.int32, (B, slots), "page_table")
+    table = _addr(page_table, torch.int32, (B, slots), "page_table", dev)
     return (pages, P, H, D, k.data_ptr(), v.data_ptr(), st[0] if pages > 1 else 0,
             st[1] if H > 1 else P * D, ks, vs, table, slots)
 
 
-def _rows4(t, shape, what: str) -> tuple:
+def _rows4(t, shape, what: str, dev: int) -> tuple:
     """(address, batch, token and head stride) of a [B][T][heads][D] tensor
     with contiguous D; the stride of a dimension of size 1, which says nothing,
     is 0."""
@@ -533,24 +539,19 @@ def _rows4(t, shape, what: str) -> tuple:
                          f"{tuple(t.shape)}")
     if t.dtype not in _KV_DTYPES:
         raise ValueError(f"{what}: expected bfloat16, float16 or float32, got {t.dtype}")
-    st = t.stride()
-    if 1 in shape[:3]:
-        st = [x if n > 1 else 0 for x, n in zip(st, shape)]
-    return t.data_ptr(), st[0], st[1], st[2]
+    if t.get_device() != dev:
+        _wrong_device(t, dev)
+    B, T, H, _ = shape
+    batch, token, head, _ = t.stride()
+    return t.data_ptr(), batch if B > 1 else 0, token if T > 1 else 0, head if H > 1 else 0
 
 
-def _kv_call(name: str, packed: bytes, workspace, stream, cache: dict, *tensors) -> None:
-    # The library launches on the current device: every pointer has to be
-    # that device's.
-    dev = workspace.get_device()
-    for t in (cache["k"], cache["v"], cache["k_scale"], cache["v_scale"], *tensors):
-        if t is not None and t.get_device() != dev:
-            raise ValueError(f"{name}: expected tensors of one device, got {t.device} beside a "
-                             f"workspace on {workspace.device}")
+def _kv_call(name: str, packed: bytes, workspace, dev: int, stream) -> None:
+    # The library launches on the current device.
     if dev < 0:
         raise ValueError("libspecverify takes device tensors")
     if dev != _current_device():
-        raise ValueError(f"{name}: the tensors are on {workspace.device}, the current device is "
+        raise ValueError(f"{name}: the tensors are on cuda:{dev}, the current device is "
                          f"cuda:{_current_device()}")
     if stream is None:
         stream = current_raw_stream(dev)
@@ -566,17 +567,17 @@ def sv_kv_write(cache: dict, page_table, kv_len, k_new, v_new, workspace, num_ne
     """Enqueue sv_kv_write: quantise k_new, v_new [B][T][Hkv][D] into the
     cache at positions kv_len[b] .. of each request."""
     B, T = k_new.shape[:2]
-    c = _kv_cache(cache, page_table, B)
+    dev = workspace.get_device()
+    c = _kv_cache(cache, page_table, B, dev)
     shape = (B, T, c[2], c[3])
-    k, *k_strides = _rows4(k_new, shape, "k_new")
-    v, *v_strides = _rows4(v_new, shape, "v_new")
+    k, *k_strides = _rows4(k_new, shape, "k_new", dev)
+    v, *v_strides = _rows4(v_new, shape, "v_new", dev)
     if v_new.dtype != k_new.dtype:
         raise ValueError("v_new: expected k_new's dtype")
-    length = _addr(kv_len, torch.int32, (B,), "kv_len")
-    num = _addr(num_new, torch.int32, (B,), "num_new")
+    length = _addr(kv_len, torch.int32, (B,), "kv_len", dev)
+    num = _addr(num_new, torch.int32, (B,), "num_new", dev)
     _kv_call("sv_kv_write", _pack_write(*c, B, T, _KV_DTYPES[k_new.dtype], k, v, *k_strides,
-                                        *v_strides, length, num), workspace, stream,
-             cache, page_table, kv_len, k_new, v_new, num_new)
+                                        *v_strides, length, num), workspace, dev, stream)
 
 
 def sv_kv_read(cache: dict, page_table, start, num, k_out, v_out, workspace, rows=None,
@@ -584,18 +585,18 @@ def sv_kv_read(cache: dict, page_table, start, num, k_out, v_out, workspace, row
     """Enqueue sv_kv_read: the values at positions start[b] + t, or start[b]
     + rows[b][t], into k_out, v_out [B][T][Hkv][D] (rows t >= num[b] zero)."""
     B, T = k_out.shape[:2]
-    c = _kv_cache(cache, page_table, B)
+    dev = workspace.get_device()
+    c = _kv_cache(cache, page_table, B, dev)
     shape = (B, T, c[2], c[3])
-    k, *strides = _rows4(k_out, shape, "k_out")
-    v, *v_strides = _rows4(v_out, shape, "v_out")
+    k, *strides = _rows4(k_out, shape, "k_out", dev)
+    v, *v_strides = _rows4(v_out, shape, "v_out", dev)
     if v_strides != strides or v_out.dtype != k_out.dtype:
         raise ValueError("v_out: expected k_out's dtype and strides")
-    first = _addr(start, torch.int32, (B,), "start")
-    count = _addr(num, torch.int32, (B,), "num")
-    which = _addr(rows, torch.int32, (B, T), "rows")
+    first = _addr(start, torch.int32, (B,), "start", dev)
+    count = _addr(num, torch.int32, (B,), "num", dev)
+    which = _addr(rows, torch.int32, (B, T), "rows", dev)
     _kv_call("sv_kv_read", _pack_read(*c, B, T, _KV_DTYPES[k_out.dtype], k, v, *strides, first,
-                                      count, which), workspace, stream,
-             cache, page_table, start, num, k_out, v_out, rows)
+                                      count, which), workspace, dev, stream)
 
 
 @functools.lru_cache(maxsize=1024)
@@ -609,21 +610,22 @@ def sv_kv_attention(q, cache: dict, page_table, kv_len, out, workspace, scale: f
     same shape, contiguous) and, optionally, lse [B][T][Hq] fp32."""
     shape = q.shape
     B, T, Hq, D = shape
-    c = _kv_cache(cache, page_table, B)
+    dev = workspace.get_device()
+    c = _kv_cache(cache, page_table, B, dev)
     if D != c[3] or q.dtype == torch.float32:
         raise ValueError(f"q: expected bfloat16 or float16 [B][T][Hq][{c[3]}], got {q.dtype} "
                          f"{tuple(shape)}")
-    qp, *strides = _rows4(q, shape, "q")
-    o = _addr(out, q.dtype, shape, "out")
-    ls = _addr(lse, torch.float32, (B, T, Hq), "lse")
-    length = _addr(kv_len, torch.int32, (B,), "kv_len")
-    num = _addr(num_new, torch.int32, (B,), "num_new")
+    qp, *strides = _rows4(q, shape, "q", dev)
+    o = _addr(out, q.dtype, shape, "out", dev)
+    ls = _addr(lse, torch.float32, (B, T, Hq), "lse", dev)
+    length = _addr(kv_len, torch.int32, (B,), "kv_len", dev)
+    num = _addr(num_new, torch.int32, (B,), "num_new", dev)
     words = 0
     if mask is not None:
         if mask.dim() != 3:
             raise ValueError("mask: expected [B][T][words]")
         words = mask.shape[2]
-    m = _addr(mask, torch.int32, (B, T, words), "mask")
+    m = _addr(mask, torch.int32, (B, T, words), "mask", dev)
     _kv_call("sv_kv_attention", _pack_attention(*c, B, T, Hq, _KV_DTYPES[q.dtype], qp, *strides,
                                                 o, ls, length, num, m, words, scale),
-             workspace, stream, cache, page_table, kv_len, q, out, num_new, mask, lse)
+             workspace, dev, stream)

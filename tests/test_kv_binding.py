@@ -28,8 +28,7 @@ class FakeGpu:
         mp.setattr(torch, "empty", lambda n, **kw: FakeBuffer(n))
         mp.setattr(sv, "sv_workspace_init", lambda buf, stream=None: None)
         mp.setattr(sv, "sv_stream_capture_id", lambda stream: self.capture, raising=False)
-        mp.setattr(torch._C, "_cuda_getCurrentRawStream", lambda device: self.stream,
-                   raising=False)
+        mp.setattr(sv, "current_raw_stream", lambda device: self.stream)
         mp.setattr(torch.cuda, "is_current_stream_capturing", lambda: self.capture != 0)
         mp.setattr(torch.cuda, "current_stream", lambda device=None: self)
 
@@ -145,8 +144,8 @@ def test_tensors_of_another_device_are_refused(op, monkeypatch):
     launches = Launches()
     monkeypatch.setattr(b, "_lib_handle", launches)
     current = [0]
-    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: current[0], raising=False)
-    monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda d: 0, raising=False)
+    monkeypatch.setattr(b, "_current_device", lambda: current[0])
+    monkeypatch.setattr(b, "current_raw_stream", lambda d: 0)
     args = kv_arguments(op)
     names = ["k", "v", "k_scale", "v_scale"] + OPERANDS[op]
     assert sorted(names) == sorted(args)
