@@ -115,6 +115,8 @@ typedef enum {
 #define SV_MAX_TREE_B 1024  /* requests per tree call */
 #define SV_MAX_KV_T 65536   /* tokens a request adds to the cache in one call */
 #define SV_MAX_KV_HEADS 256 /* key/value heads, and query heads */
+#define SV_MAX_ROTATE_D 256 /* channels of a head that sv_rotate takes */
+#define SV_MAX_GIVEN 1024   /* tokens asked of one row of logits */
 
 /*
  * Chain verification, one request per b ([L17] sec. 2.4 Algorithm 1).
@@ -453,6 +455,141 @@ size_t sv_kv_attention_workspace_bytes(int32_t B, int32_t T, int32_t Hq, int32_t
 
 sv_status sv_kv_attention(const sv_kv_attention_args* args, void* workspace, size_t ws_bytes,
                           sv_stream_t stream);
+
+/* ---- Norms and positions of queries and keys (no counterpart on the pages:
+ * what a target model does between its projections and its attention) ----
+ *
+ * A head's vector x of D channels becomes
+ *   y_i = x_i / sqrt(mean_j x_j^2 + eps) * w_i            (if it has a norm),
+ * and pair c (0 <= c < dim / 2) of its first dim channels turns by the
+ * angle of the token's position p:
+ *   a = 2 pi * frac(p * freq[c] / 2^64),
+ *   (u, v) -> scale * (u cos a - v sin a, v cos a + u sin a),
+ * where (u, v) are channels (c, c + dim / 2) of y or, interleaved,
+ * (2c, 2c + 1).  Channels dim .. D are y's.  Everything is computed in 32 bits
+ * (the fraction of the turn exactly, as whole numbers) and rounded once.
+ *
+ * freq holds turns a position as 64-bit fractions: a frequency of f radians a
+ * position is round(f / (2 pi) * 2^64).  However frequencies were stretched for
+ * long contexts, they and scale carry it.
+ */
+typedef struct {
+  int32_t dim;             /* channels that turn: a multiple of 16, 0 .. D (0: none) */
+  int32_t interleaved;     /* pairs (2c, 2c + 1) instead of (c, c + dim / 2) */
+  float scale;             /* factor of the channels that turn, finite (1: none) */
+  const uint64_t* freq;    /* [dim / 2], 16-byte aligned; may be NULL when dim is 0 */
+} sv_rope;
+
+typedef struct {
+  const void* weight;      /* [D], or NULL (ones) */
+  sv_dtype weight_dtype;   /* SV_BF16, SV_FP16 or SV_FP32 */
+  float eps;               /* 1e-30 or more; 0: no norm (weight must be NULL) */
+} sv_head_norm;
+
+/* Heads of one kind, in and out: element (b, t, h, i) at b * batch_stride + t *
+   token_stride + h * head_stride + i. */
+typedef struct {
+  const void* x;
+  void* out;               /* x itself (the same strides and type) or apart from it */
+  int32_t heads;           /* 0: none (the other fields are not read) */
+  sv_dtype out_dtype;      /* SV_BF16, SV_FP16 or SV_FP32 */
+  int64_t batch_stride, token_stride, head_stride; /* of x, in elements */
+  int64_t out_batch_stride, out_token_stride, out_head_stride;
+  sv_head_norm norm;
+} sv_heads;
+
+/*
+ * Norm and rotate queries and keys.  Token t < n = num[b] of request b has
+ * position start[b] + (offset ? offset[b][t] : t); offsets are, for a token
+ * tree, sv_tree_mask's depths.  Rows t >= n of out become zero.
+ *
+ * num outside [0, T] records SV_DERR_ARG (all rows of the request become
+ * zero).  Positions may be any sum of two 32-bit integers.  Only the
+ * workspace's error word is used.
+ */
+typedef struct {
+  int32_t B, T, D;           /* 0 <= B <= SV_MAX_B, 1 <= T <= SV_MAX_KV_T; D: a
+                                multiple of 16, 16 .. SV_MAX_ROTATE_D */
+  sv_dtype dtype;            /* of x: SV_BF16, SV_FP16 or SV_FP32 */
+  sv_heads q, k;
+  const int32_t* start;      /* [B], or NULL (= 0) */
+  const int32_t* num;        /* [B] in [0, T], or NULL (= T) */
+  const int32_t* offset;     /* [B][T], or NULL (= t) */
+  sv_rope rope;
+} sv_rotate_args;
+
+sv_status sv_rotate(const sv_rotate_args* args, void* workspace, size_t ws_bytes,
+                    sv_stream_t stream);
+
+/*
+ * A round's tokens on their way to sv_kv_attention, in one launch: keys are
+ * normed, rotated and, with the values, written into the cache as sv_kv_write
+ * would write them (positions, scales, codes, errors: see there; the scales
+ * are those of the rotated keys, which are not rounded in between); queries
+ * are normed and rotated as by sv_rotate.  A token's position is kv_len[b] +
+ * (offset ? offset[b][t] : t); its place in the cache is kv_len[b] + t.
+ */
+typedef struct {
+  sv_kv_cache cache;
+  int32_t B, T;              /* 0 <= B <= SV_MAX_B, 1 <= T <= SV_MAX_KV_T */
+  sv_dtype dtype;            /* of q, k_new, v_new: SV_BF16, SV_FP16 or SV_FP32 */
+  sv_heads q;                /* heads 0: no queries */
+  const void* k_new;         /* [B][T][Hkv][D], D contiguous */
+  const void* v_new;
+  int64_t k_batch_stride, k_token_stride, k_head_stride; /* elements */
+  int64_t v_batch_stride, v_token_stride, v_head_stride;
+  sv_head_norm k_norm;
+  const int32_t* kv_len;     /* [B] tokens the request holds before the call */
+  const int32_t* num_new;    /* [B] in [0, T], or NULL (= T) */
+  const int32_t* offset;     /* [B][T], or NULL (= t) */
+  sv_rope rope;
+} sv_kv_append_args;
+
+sv_status sv_kv_append(const sv_kv_append_args* args, void* workspace, size_t ws_bytes,
+                       sv_stream_t stream);
+
+/*
+ * Log probabilities of given tokens, entropies and likeliest tokens of rows of
+ * logits ([N02] sec. 5: temperature softmax), without the probabilities
+ * themselves: what a server reports beside the tokens that sv_verify_chain or
+ * sv_verify_tree emitted, and what scores a prompt.
+ *
+ * Output row r < n = num_rows[b] of request b is row i = rows ? rows[b][r] : r
+ * of its logits (for a tree: 0, then the accepted nodes).  With x the row, t =
+ * temperature[b] (0 and NULL: 1) and ln p_j = x_j / t - ln sum_k exp(x_k / t):
+ *   logprob[b][r][m] = ln p of tokens[b][r][m]; NaN where that is -1;
+ *   entropy[b][r]    = - sum_j p_j ln p_j (logits of -inf add nothing);
+ *   top_token[b][r][], top_logprob[b][r][]: the `top` largest logits, the lower
+ *     token first among equal ones; -1 and -inf where fewer than `top` tokens
+ *     have a logit above -inf.
+ * Rows r >= n: NaN, and -1 for top_token.  Sums are taken in 32 bits.
+ *
+ * A row with NaN or +inf records SV_DERR_NONFINITE, one with only -inf
+ * SV_DERR_MASS, a row index outside [0, N), num_rows outside [0, R] or a
+ * temperature that is negative, infinite or NaN SV_DERR_ARG: these rows (for
+ * num_rows and temperature, all of the request) are as rows r >= n.  A token
+ * outside [-1, V) records SV_DERR_TOKEN and its logprob is NaN.  Only the
+ * workspace's error word is used.
+ */
+typedef struct {
+  int32_t B, N, R, M, V;      /* 0 <= B <= SV_MAX_B; N rows of logits and R of output a
+                                 request, 1 .. 65536; 0 <= M <= SV_MAX_GIVEN */
+  sv_dtype dtype;             /* SV_BF16 or SV_FP32 */
+  const void* logits;         /* [B][N][V], V contiguous */
+  int64_t batch_stride, row_stride; /* elements, >= 0 */
+  const int32_t* tokens;      /* [B][R][M]; may be NULL when M is 0 */
+  const int32_t* num_rows;    /* [B] in [0, R], or NULL (= R) */
+  const int32_t* rows;        /* [B][R], or NULL (row r; then R <= N) */
+  const float* temperature;   /* [B], or NULL */
+  int32_t top;                /* 0 .. SV_MAX_TOPK */
+  float* logprob;             /* [B][R][M]; may be NULL when M is 0 */
+  float* entropy;             /* [B][R], or NULL */
+  int32_t* top_token;         /* [B][R][top]; may be NULL when top is 0 */
+  float* top_logprob;         /* [B][R][top]; may be NULL when top is 0 */
+} sv_token_logprobs_args;
+
+sv_status sv_token_logprobs(const sv_token_logprobs_args* args, void* workspace, size_t ws_bytes,
+                            sv_stream_t stream);
 
 /* Synchronise `stream`, read and clear the workspace error word.
    *device_flags receives the SV_DERR_* bits (may be NULL).  Returns SV_OK,

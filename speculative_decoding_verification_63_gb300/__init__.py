@@ -9,6 +9,7 @@ library every call raises.
 """
 from __future__ import annotations
 
+import math
 import threading
 
 import torch
@@ -24,7 +25,8 @@ from ._binding import (  # noqa: F401
     SV_TREE_MSS, SV_TREE_MSS_NOREPLACE, SV_TREE_NAIVE, TREE_MODES, SV_MIN_WORKSPACE_BYTES,
     sv_tree_mask, sv_row_stats, SV_FP16, SV_DERR_PAGE, SV_MAX_KV_HEADS, SV_MAX_KV_T,
     sv_kv_attention, sv_kv_attention_workspace_bytes, sv_kv_read, sv_kv_write,
-    sv_stream_capture_id, current_raw_stream)
+    sv_stream_capture_id, current_raw_stream, SV_MAX_GIVEN, SV_MAX_ROTATE_D, sv_kv_append,
+    sv_rotate, sv_token_logprobs)
 from ._build import build_library  # noqa: F401
 
 _ws_lock = threading.Lock()
@@ -287,6 +289,149 @@ def kv_commit(cache: dict, page_table, kv_len, accept_len, accepted_nodes,
         return
     path = kv_read(cache, page_table, kv_len, accept_len, T, rows=accepted_nodes, ws=ws)
     kv_write(cache, page_table, kv_len + 1, path["k"], path["v"], num_new=accept_len, ws=ws)
+
+
+def rope(dim: int, base: float = 10000.0, interleaved: bool = False, scaling: dict | None = None,
+         device=None) -> dict:
+    """The positions' rotation that rotate and kv_append take: the first dim
+    channels of a head turn in pairs, (c, c + dim/2) or, interleaved, (2c, 2c +
+    1), by position * f_c with f_c = base^(-2c/dim) radians.  scaling stretches
+    the frequencies for contexts longer than the trained one:
+
+      {"type": "linear", "factor": s}      f_c / s
+      {"type": "ntk", "factor": s}         base * s^(dim / (dim - 2)) for base
+      {"type": "yarn", "factor": s, "context": trained length, "fast": 32, "slow": 1,
+       "attention": 0.1 ln s + 1}          pairs that turn more than `fast` times over the
+                                           trained context keep f_c, those that turn less than
+                                           `slow` times get f_c / s, a ramp over the pairs
+                                           between; the turned channels are scaled by `attention`
+      {"type": "wavelength", "factor": s, "context": trained length, "low": 1, "high": 4}
+                                           f_c / s for wavelengths above context / low, f_c for
+                                           those below context / high, between by context /
+                                           wavelength
+      {"type": "factors", "factors": [dim/2 numbers], "attention": 1}
+                                           f_c / factors[c]
+
+    Returns freq [dim/2] (int64: turns a position in units of 2^-64), dim,
+    interleaved and scale; a table of one's own will do as well."""
+    if dim < 16 or dim % 16 or dim > SV_MAX_ROTATE_D:
+        raise ValueError(f"rope: dim must be a multiple of 16 up to {SV_MAX_ROTATE_D}, got {dim}")
+    if not (base > 0 and math.isfinite(base)):
+        raise ValueError(f"rope: base must be a positive number, got {base}")
+    how = dict(scaling or {"type": "none"})
+    kind = how.pop("type", None)
+    pairs = dim // 2
+    if kind == "ntk":
+        if dim <= 2:
+            raise ValueError("rope: ntk scaling needs more than one pair")
+        base *= how["factor"] ** (dim / (dim - 2))
+    f = [base ** (-2.0 * c / dim) for c in range(pairs)]
+    scale = 1.0
+    if kind == "linear":
+        f = [x / how["factor"] for x in f]
+    elif kind == "yarn":
+        s, context = how["factor"], how["context"]
+
+        def pair(turns):  # the pair that turns so often over the trained context
+            return dim * math.log(context / (turns * 2 * math.pi)) / (2 * math.log(base))
+        lo = max(math.floor(pair(how.get("fast", 32.0))), 0)
+        hi = min(math.ceil(pair(how.get("slow", 1.0))), dim - 1)
+        ramp = [min(1.0, max(0.0, (c - lo) / max(hi - lo, 1e-3))) for c in range(pairs)]
+        f = [x * (1 - r) + x / s * r for x, r in zip(f, ramp)]
+        scale = how.get("attention", 0.1 * math.log(s) + 1.0 if s > 1 else 1.0)
+    elif kind == "wavelength":
+        s, context = how["factor"], how["context"]
+        low, high = how.get("low", 1.0), how.get("high", 4.0)
+        keep = [min(1.0, max(0.0, (context * x / (2 * math.pi) - low) / (high - low))) for x in f]
+        f = [x * k + x / s * (1 - k) for x, k in zip(f, keep)]
+    elif kind == "factors":
+        if len(how["factors"]) != pairs:
+            raise ValueError(f"rope: expected {pairs} factors, got {len(how['factors'])}")
+        f = [x / y for x, y in zip(f, how["factors"])]
+        scale = how.get("attention", 1.0)
+    elif kind not in ("none", "ntk"):
+        raise ValueError(f"rope: no scaling of type {kind!r}")
+    return dict(freq=rope_turns(f, device), dim=dim, interleaved=bool(interleaved),
+                scale=float(scale))
+
+
+def rope_turns(radians, device=None) -> torch.Tensor:
+    """Frequencies in radians a position as the 64-bit fractions of a turn that
+    sv_rope's freq holds (int64 storage)."""
+    turns = [round(x / (2 * math.pi) * 2.0 ** 64) % (1 << 64) for x in radians]
+    turns = [x - (1 << 64) if x >> 63 else x for x in turns]
+    return torch.tensor(turns, dtype=torch.int64,
+                        device=torch.device(device if device is not None else "cuda"))
+
+
+def rotate(q, k=None, start=None, num=None, offset=None, rope=None, q_weight=None, k_weight=None,
+           eps: float | None = None, inplace: bool = False,
+           ws: torch.Tensor | None = None) -> dict:
+    """Norm (eps, q_weight, k_weight [D]) the heads of q and k [B][T][heads][D]
+    (bf16, fp16 or fp32) and turn them by their positions: token t < num[b] of
+    request b is at start[b] + t, or start[b] + offset[b][t] (tree_mask's
+    depths); later rows become zero.  rope: rope()'s dict, None for norms
+    alone; eps None: no norm.  Returns q and k (device tensors), which are the
+    arguments themselves when inplace."""
+    out = dict(q=q if inplace else torch.empty_like(q, memory_format=torch.contiguous_format))
+    if k is not None:
+        out["k"] = k if inplace else torch.empty_like(k, memory_format=torch.contiguous_format)
+    if ws is None:
+        ws = workspace(SV_MIN_WORKSPACE_BYTES, q.device, "kv")
+    sv_rotate(q, out["q"], ws, k=k, k_out=out.get("k"), start=start, num=num, offset=offset,
+              rope=rope, q_weight=q_weight, k_weight=k_weight, eps=eps)
+    return out
+
+
+def kv_append(cache: dict, page_table, kv_len, q, k_new, v_new, num_new=None, offset=None,
+              rope=None, q_weight=None, k_weight=None, eps: float | None = None, q_dtype=None,
+              ws: torch.Tensor | None = None) -> dict:
+    """A round's projections on their way to kv_attention: keys k_new are
+    normed and turned as by rotate and, with the values v_new, quantised into
+    the cache as by kv_write; queries q (or None) are normed and turned.  All
+    [B][T][heads][D], bf16, fp16 or fp32.  Token t < num_new[b] goes to place
+    kv_len[b] + t of request b and has position kv_len[b] + t, or kv_len[b] +
+    offset[b][t] (tree_mask's depths).  Returns q (q_dtype, its own by
+    default; rows behind the last token zero)."""
+    out = {}
+    if q is not None:
+        out["q"] = torch.empty_like(q, dtype=q_dtype, memory_format=torch.contiguous_format)
+    if ws is None:
+        ws = workspace(SV_MIN_WORKSPACE_BYTES, k_new.device, "kv")
+    sv_kv_append(cache, page_table, kv_len, k_new, v_new, ws, q=q, q_out=out.get("q"),
+                 num_new=num_new, offset=offset, rope=rope, q_weight=q_weight, k_weight=k_weight,
+                 eps=eps)
+    return out
+
+
+def token_logprobs(logits, tokens=None, num_rows=None, rows=None, R: int | None = None,
+                   temperature=None, top: int = 0, ws: torch.Tensor | None = None) -> dict:
+    """Log probabilities of given tokens under logits [B][N][V] (bf16 or
+    fp32), the entropy of each row and its `top` likeliest tokens.
+
+    Row r < num_rows[b] of request b is row r of its logits, or rows[b][r];
+    tokens [B][R] or [B][R][M] int32 are the tokens asked of it (-1: none).
+    For what verify_chain emitted: tokens=out_tokens, num_rows=out_len; for a
+    tree round also rows = 0, then accepted_nodes.  temperature [B]: as the
+    verification's, but 0 (greedy) counts as 1.  Returns entropy [B][R],
+    logprobs (tokens' shape), top_tokens and top_logprobs [B][R][top] (device
+    tensors): equal logits list the lower token first, tokens of logit -inf are
+    not listed (-1, -inf), and rows from num_rows on are NaN and -1."""
+    B, N = logits.shape[:2]
+    dev = logits.device
+    if R is None:
+        R = tokens.shape[1] if tokens is not None else rows.shape[1] if rows is not None else N
+    out = dict(entropy=torch.empty((B, R), dtype=torch.float32, device=dev))
+    if tokens is not None:
+        out["logprobs"] = torch.empty(tokens.shape, dtype=torch.float32, device=dev)
+    if top > 0:
+        out["top_tokens"] = torch.empty((B, R, top), dtype=torch.int32, device=dev)
+        out["top_logprobs"] = torch.empty((B, R, top), dtype=torch.float32, device=dev)
+    if ws is None:
+        ws = workspace(SV_MIN_WORKSPACE_BYTES, dev, "kv")
+    sv_token_logprobs(logits, ws, R, tokens=tokens, num_rows=num_rows, rows=rows,
+                      temperature=temperature, top=top, **out)
+    return out
 
 
 def check_device_errors(ws: torch.Tensor) -> None:

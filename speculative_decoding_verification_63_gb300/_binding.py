@@ -27,13 +27,14 @@ SV_DERR_PAGE = 0x80
 SV_MAX_K, SV_MAX_B, SV_MAX_V, SV_MAX_TOPK = 32, 1024, 1 << 20, 64
 SV_MAX_TREE_NODES, SV_MAX_TREE_B = 64, 1024
 SV_MAX_KV_T, SV_MAX_KV_HEADS = 65536, 256
+SV_MAX_ROTATE_D, SV_MAX_GIVEN = 256, 1024
 
 # every symbol include/specverify.h declares
 EXPORTS = ("sv_chain_workspace_bytes", "sv_tree_workspace_bytes", "sv_workspace_init",
            "sv_verify_chain", "sv_verify_tree", "sv_get_error", "sv_selftest_wait_timeout",
            "sv_verify_chain_noalloc", "sv_noalloc_get_error", "sv_tree_mask", "sv_row_stats",
            "sv_kv_write", "sv_kv_read", "sv_kv_attention_workspace_bytes", "sv_kv_attention",
-           "sv_stream_capture_id",
+           "sv_stream_capture_id", "sv_rotate", "sv_kv_append", "sv_token_logprobs",
            "sv_status_string", "sv_version")
 SV_MIN_WORKSPACE_BYTES = 8192
 SV_NOALLOC_SCRATCH_BYTES = 8 << 20
@@ -97,6 +98,42 @@ class SvKvAttentionArgs(ctypes.Structure):
                 ("num_new", _P), ("mask", _P), ("words", _i32), ("scale", ctypes.c_float)]
 
 
+class SvRope(ctypes.Structure):
+    _fields_ = [("dim", _i32), ("interleaved", _i32), ("scale", ctypes.c_float), ("freq", _P)]
+
+
+class SvHeadNorm(ctypes.Structure):
+    _fields_ = [("weight", _P), ("weight_dtype", _i32), ("eps", ctypes.c_float)]
+
+
+class SvHeads(ctypes.Structure):
+    _fields_ = [("x", _P), ("out", _P), ("heads", _i32), ("out_dtype", _i32),
+                ("batch_stride", _i64), ("token_stride", _i64), ("head_stride", _i64),
+                ("out_batch_stride", _i64), ("out_token_stride", _i64), ("out_head_stride", _i64),
+                ("norm", SvHeadNorm)]
+
+
+class SvRotateArgs(ctypes.Structure):
+    _fields_ = [("B", _i32), ("T", _i32), ("D", _i32), ("dtype", _i32), ("q", SvHeads),
+                ("k", SvHeads), ("start", _P), ("num", _P), ("offset", _P), ("rope", SvRope)]
+
+
+class SvKvAppendArgs(ctypes.Structure):
+    _fields_ = [("cache", SvKvCache), ("B", _i32), ("T", _i32), ("dtype", _i32), ("q", SvHeads),
+                ("k_new", _P), ("v_new", _P),
+                ("k_batch_stride", _i64), ("k_token_stride", _i64), ("k_head_stride", _i64),
+                ("v_batch_stride", _i64), ("v_token_stride", _i64), ("v_head_stride", _i64),
+                ("k_norm", SvHeadNorm), ("kv_len", _P), ("num_new", _P), ("offset", _P),
+                ("rope", SvRope)]
+
+
+class SvTokenLogprobsArgs(ctypes.Structure):
+    _fields_ = [("B", _i32), ("N", _i32), ("R", _i32), ("M", _i32), ("V", _i32), ("dtype", _i32),
+                ("logits", _P), ("batch_stride", _i64), ("row_stride", _i64), ("tokens", _P),
+                ("num_rows", _P), ("rows", _P), ("temperature", _P), ("top", _i32),
+                ("logprob", _P), ("entropy", _P), ("top_token", _P), ("top_logprob", _P)]
+
+
 class SpecVerifyError(RuntimeError):
     def __init__(self, status: int, what: str = "", flags: int = 0):
         self.status = status
@@ -144,7 +181,8 @@ def lib(path: str | None = None):
     h.sv_tree_mask.restype = ctypes.c_int
     h.sv_row_stats.argtypes = [ctypes.POINTER(SvChainArgs), _P, _P, _P, ctypes.c_size_t, _P]
     h.sv_row_stats.restype = ctypes.c_int
-    for f in ("sv_kv_write", "sv_kv_read", "sv_kv_attention"):
+    for f in ("sv_kv_write", "sv_kv_read", "sv_kv_attention", "sv_rotate", "sv_kv_append",
+              "sv_token_logprobs"):
         getattr(h, f).argtypes = [_P, _P, ctypes.c_size_t, _P]  # the arguments come packed
         getattr(h, f).restype = ctypes.c_int
     h.sv_kv_attention_workspace_bytes.argtypes = [_i32, _i32, _i32, _i32, _i32]
@@ -629,3 +667,128 @@ def sv_kv_attention(q, cache: dict, page_table, kv_len, out, workspace, scale: f
     _kv_call("sv_kv_attention", _pack_attention(*c, B, T, Hq, _KV_DTYPES[q.dtype], qp, *strides,
                                                 o, ls, length, num, m, words, scale),
              workspace, dev, stream)
+
+
+# --------------------- norms and positions of queries and keys, log probabilities
+
+_pack_rotate, _pack_append = _packer(SvRotateArgs).pack, _packer(SvKvAppendArgs).pack
+_pack_logprobs = _packer(SvTokenLogprobsArgs).pack
+_NO_NORM = (0, 0, 0.0)
+_NO_HEADS = (0, 0, 0, 0, 0, 0, 0, 0, 0, 0) + _NO_NORM
+_NO_ROPE = (0, 0, 1.0, 0)
+
+
+def _rope_fields(rope, dev: int) -> tuple:
+    """The fields of an sv_rope, from the dict that rope() makes."""
+    if rope is None:
+        return _NO_ROPE
+    dim = rope["dim"]
+    return (dim, 1 if rope["interleaved"] else 0, rope["scale"],
+            _addr(rope["freq"], torch.int64, (dim // 2,), "rope freq", dev))
+
+
+def _norm_fields(weight, eps, D: int, what: str, dev: int) -> tuple:
+    """The fields of an sv_head_norm: none without eps."""
+    if eps is None:
+        if weight is not None:
+            raise ValueError(f"{what}: a norm's weight, but no eps")
+        return _NO_NORM
+    if eps <= 0:
+        raise ValueError(f"eps: expected a positive number, got {eps}")
+    if weight is None:
+        return 0, 0, eps
+    if weight.dtype not in _KV_DTYPES:
+        raise ValueError(f"{what}: expected bfloat16, float16 or float32, got {weight.dtype}")
+    return _addr(weight, weight.dtype, (D,), what, dev), _KV_DTYPES[weight.dtype], eps
+
+
+def _heads_fields(x, out, shape, weight, eps, what: str, dev: int) -> tuple:
+    """The fields of an sv_heads: x [B][T][heads][D] into out."""
+    if x is None:
+        return _NO_HEADS
+    p, *strides = _rows4(x, shape, what, dev)
+    o, *out_strides = _rows4(out, shape, what + "_out", dev)
+    return (p, o, shape[2], _KV_DTYPES[out.dtype], *strides, *out_strides,
+            *_norm_fields(weight, eps, shape[3], what + "_weight", dev))
+
+
+def sv_rotate(q, q_out, workspace, k=None, k_out=None, start=None, num=None, offset=None,
+              rope=None, q_weight=None, k_weight=None, eps=None, stream=None) -> None:
+    """Enqueue sv_rotate: norms and rotations of q and k [B][T][heads][D] into
+    q_out and k_out."""
+    B, T, _, D = q.shape
+    dev = workspace.get_device()
+    qf = _heads_fields(q, q_out, q.shape, q_weight, eps, "q", dev)
+    if k is not None:
+        if k.dim() != 4 or k.shape[0] != B or k.shape[1] != T or k.shape[3] != D \
+                or k.dtype != q.dtype:
+            raise ValueError(f"k: expected [{B}][{T}][heads][{D}] of q's dtype, got {k.dtype} "
+                             f"{tuple(k.shape)}")
+        kf = _heads_fields(k, k_out, k.shape, k_weight, eps, "k", dev)
+    else:
+        kf = _NO_HEADS
+    _kv_call("sv_rotate", _pack_rotate(
+        B, T, D, _KV_DTYPES[q.dtype], *qf, *kf, _addr(start, torch.int32, (B,), "start", dev),
+        _addr(num, torch.int32, (B,), "num", dev),
+        _addr(offset, torch.int32, (B, T), "offset", dev), *_rope_fields(rope, dev)),
+        workspace, dev, stream)
+
+
+def sv_kv_append(cache: dict, page_table, kv_len, k_new, v_new, workspace, q=None, q_out=None,
+                 num_new=None, offset=None, rope=None, q_weight=None, k_weight=None, eps=None,
+                 stream=None) -> None:
+    """Enqueue sv_kv_append: keys normed, rotated and, with the values,
+    quantised into the cache; queries normed and rotated into q_out."""
+    B, T = k_new.shape[:2]
+    dev = workspace.get_device()
+    c = _kv_cache(cache, page_table, B, dev)
+    shape = (B, T, c[2], c[3])
+    k, *k_strides = _rows4(k_new, shape, "k_new", dev)
+    v, *v_strides = _rows4(v_new, shape, "v_new", dev)
+    if v_new.dtype != k_new.dtype:
+        raise ValueError("v_new: expected k_new's dtype")
+    qf = _NO_HEADS
+    if q is not None:
+        if q.dtype != k_new.dtype or q.dim() != 4:
+            raise ValueError(f"q: expected [{B}][{T}][heads][{c[3]}] of k_new's dtype, got "
+                             f"{q.dtype} {tuple(q.shape)}")
+        qf = _heads_fields(q, q_out, (B, T, q.shape[2], c[3]), q_weight, eps, "q", dev)
+    _kv_call("sv_kv_append", _pack_append(
+        *c, B, T, _KV_DTYPES[k_new.dtype], *qf, k, v, *k_strides, *v_strides,
+        *_norm_fields(k_weight, eps, c[3], "k_weight", dev),
+        _addr(kv_len, torch.int32, (B,), "kv_len", dev),
+        _addr(num_new, torch.int32, (B,), "num_new", dev),
+        _addr(offset, torch.int32, (B, T), "offset", dev), *_rope_fields(rope, dev)),
+        workspace, dev, stream)
+
+
+def sv_token_logprobs(logits, workspace, R: int, tokens=None, num_rows=None, rows=None,
+                      temperature=None, top: int = 0, logprobs=None, entropy=None,
+                      top_tokens=None, top_logprobs=None, stream=None) -> None:
+    """Enqueue sv_token_logprobs on logits [B][N][V]: tokens and logprobs
+    [B][R] or [B][R][M], entropy [B][R], top_tokens and top_logprobs
+    [B][R][top]."""
+    if logits.dim() != 3 or (logits.shape[2] > 1 and logits.stride(2) != 1):
+        raise ValueError("logits: expected [B][N][V] with contiguous rows")
+    B, N, V = logits.shape
+    dev = workspace.get_device()
+    if logits.get_device() != dev:
+        _wrong_device(logits, dev)
+    M = 0
+    if tokens is not None:
+        if tokens.dim() not in (2, 3):
+            raise ValueError("tokens: expected [B][R] or [B][R][M]")
+        M = tokens.shape[2] if tokens.dim() == 3 else 1
+    shape = (B, R) if tokens is None else (B, R, *tokens.shape[2:])
+    batch, row, _ = logits.stride()
+    _kv_call("sv_token_logprobs", _pack_logprobs(
+        B, N, R, M, V, _dtype_code(logits), logits.data_ptr(), batch if B > 1 else 0,
+        row if N > 1 else 0, _addr(tokens, torch.int32, shape, "tokens", dev),
+        _addr(num_rows, torch.int32, (B,), "num_rows", dev),
+        _addr(rows, torch.int32, (B, R), "rows", dev),
+        _addr(temperature, torch.float32, (B,), "temperature", dev), top,
+        _addr(logprobs, torch.float32, shape, "logprobs", dev),
+        _addr(entropy, torch.float32, (B, R), "entropy", dev),
+        _addr(top_tokens, torch.int32, (B, R, top), "top_tokens", dev),
+        _addr(top_logprobs, torch.float32, (B, R, top), "top_logprobs", dev)),
+        workspace, dev, stream)

@@ -1,0 +1,172 @@
+// rotate.cu -- C ABI of the norms and rotations of queries and keys (see
+// include/specverify.h): argument checks and launches.
+#include <algorithm>
+
+#include "sv_host.cuh"
+#include "sv_rotate.cuh"
+
+namespace {
+
+using namespace sv;
+
+bool dtype_ok(int d) { return d == SV_BF16 || d == SV_FP16 || d == SV_FP32; }
+
+bool norm_ok(const sv_head_norm& n) {
+  if (n.eps == 0.f) return n.weight == nullptr;
+  if (!(n.eps >= 1e-30f) || !(n.eps - n.eps == 0.f)) return false;
+  return n.weight == nullptr ||
+         (dtype_ok(n.weight_dtype) &&
+          aligned(n.weight, static_cast<size_t>(dtype_bytes(n.weight_dtype))));
+}
+
+bool rope_ok(const sv_rope& r, int D) {
+  if (r.dim < 0 || r.dim > D || r.dim % 16 != 0) return false;
+  return r.dim == 0 || (r.freq != nullptr && aligned(r.freq, 16) && r.scale - r.scale == 0.f);
+}
+
+bool heads_ok(const sv_heads& h, sv_dtype dtype) {
+  if (h.heads < 0 || h.heads > SV_MAX_KV_HEADS) return false;
+  if (h.heads == 0) return true;
+  const size_t es = static_cast<size_t>(dtype_bytes(dtype));
+  return dtype_ok(h.out_dtype) && h.x != nullptr && h.out != nullptr && aligned(h.x, es) &&
+         aligned(h.out, static_cast<size_t>(dtype_bytes(h.out_dtype))) && norm_ok(h.norm) &&
+         (h.x != h.out ||
+          (h.out_dtype == dtype && h.batch_stride == h.out_batch_stride &&
+           h.token_stride == h.out_token_stride && h.head_stride == h.out_head_stride));
+}
+
+HeadNorm norm_view(const sv_head_norm& n) { return HeadNorm{n.weight, n.weight_dtype, n.eps}; }
+
+Rope rope_view(const sv_rope& r) {
+  return Rope{r.dim, r.interleaved, r.scale, reinterpret_cast<const unsigned long long*>(r.freq)};
+}
+
+// A kind of heads for blocks of `threads` threads; B requests of T tokens of
+// `lanes` lanes.  A thread takes several heads of its token, which share sines
+// and cosines, once that leaves the GPU full.
+Heads heads_view(const sv_heads& h, sv_dtype dtype, int B, int T, int lanes, int threads, int sms) {
+  Heads v = {};
+  if (h.heads == 0) return v;
+  v.x = h.x;
+  v.out = h.out;
+  v.heads = h.heads;
+  v.out_dtype = h.out_dtype;
+  v.batch = h.batch_stride;
+  v.token = h.token_stride;
+  v.head = h.head_stride;
+  v.out_batch = h.out_batch_stride;
+  v.out_token = h.out_token_stride;
+  v.out_head = h.out_head_stride;
+  v.x_vec = rows_aligned(h.x, dtype_bytes(dtype), 16, v.batch, v.token, v.head);
+  v.out_vec = rows_aligned(h.out, dtype_bytes(h.out_dtype), 16, v.out_batch, v.out_token, v.out_head);
+  v.norm = norm_view(h.norm);
+  const int64_t one = static_cast<int64_t>(B) * T * lanes;  // threads of a head
+  v.per = 8;
+  while (v.per > 1 && one * ((h.heads + v.per - 1) / v.per) < int64_t{1024} * sms) v.per /= 2;
+  const int64_t mine = static_cast<int64_t>(T) * lanes * ((h.heads + v.per - 1) / v.per);
+  v.blocks = static_cast<int>((mine + threads - 1) / threads);
+  return v;
+}
+
+}  // namespace
+
+extern "C" {
+
+sv_status sv_rotate(const sv_rotate_args* a, void* workspace, size_t ws_bytes,
+                    sv_stream_t stream) {
+  SV_RANGE("sv_rotate");
+  if (a == nullptr) return SV_EINVAL;
+  if (a->B < 0 || a->B > SV_MAX_B || a->T < 1 || a->T > SV_MAX_KV_T || a->D < 16 ||
+      a->D > SV_MAX_ROTATE_D || a->D % 16 != 0 || !dtype_ok(a->dtype))
+    return SV_EINVAL;
+  if (a->B == 0) return SV_OK;
+  if (!rope_ok(a->rope, a->D) || !heads_ok(a->q, a->dtype) || !heads_ok(a->k, a->dtype))
+    return SV_EINVAL;
+  if (a->q.heads + a->k.heads == 0) return SV_OK;
+  const sv_status wst = workspace_ok(workspace, ws_bytes, SV_MIN_WORKSPACE_BYTES);
+  if (wst != SV_OK) return wst;
+  Device dev;
+  const sv_status ds = device(dev);
+  if (ds != SV_OK) return ds;
+
+  RotateProblem p;
+  p.B = a->B;
+  p.T = a->T;
+  p.D = a->D;
+  p.lane_shift = 0;
+  while ((16 << p.lane_shift) < a->D) ++p.lane_shift;
+  p.lanes = 1 << p.lane_shift;
+  p.q = heads_view(a->q, a->dtype, a->B, a->T, p.lanes, kRotateThreads, dev.sms);
+  p.k = heads_view(a->k, a->dtype, a->B, a->T, p.lanes, kRotateThreads, dev.sms);
+  p.rope = rope_view(a->rope);
+  p.start = a->start;
+  p.num = a->num;
+  p.offset = a->offset;
+  p.err = error_word(workspace);
+  const dim3 grid(static_cast<unsigned>(p.q.blocks + p.k.blocks), static_cast<unsigned>(a->B));
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  switch (a->dtype) {
+    case SV_BF16: return launch(rotate_kernel<__nv_bfloat16>, p, grid, kRotateThreads, 0, st);
+    case SV_FP16: return launch(rotate_kernel<__half>, p, grid, kRotateThreads, 0, st);
+    default: return launch(rotate_kernel<float>, p, grid, kRotateThreads, 0, st);
+  }
+}
+
+sv_status sv_kv_append(const sv_kv_append_args* a, void* workspace, size_t ws_bytes,
+                       sv_stream_t stream) {
+  SV_RANGE("sv_kv_append");
+  if (a == nullptr) return SV_EINVAL;
+  if (a->B < 0 || a->B > SV_MAX_B || a->T < 1 || a->T > SV_MAX_KV_T || !dtype_ok(a->dtype))
+    return SV_EINVAL;
+  if (a->B == 0) return SV_OK;
+  if (!cache_ok(a->cache) || a->k_new == nullptr || a->v_new == nullptr || a->kv_len == nullptr ||
+      !rope_ok(a->rope, a->cache.D) || !heads_ok(a->q, a->dtype) || !norm_ok(a->k_norm))
+    return SV_EINVAL;
+  const int es = dtype_bytes(a->dtype);
+  if (!aligned(a->k_new, static_cast<size_t>(es)) || !aligned(a->v_new, static_cast<size_t>(es)))
+    return SV_EINVAL;
+  const sv_status wst = workspace_ok(workspace, ws_bytes, SV_MIN_WORKSPACE_BYTES);
+  if (wst != SV_OK) return wst;
+  Device dev;
+  const sv_status ds = device(dev);
+  if (ds != SV_OK) return ds;
+
+  KvAppendProblem p;
+  p.c = cache_view(a->cache);
+  p.B = a->B;
+  p.T = a->T;
+  p.pages = (a->T + p.c.page_size - 2) / p.c.page_size + 1;
+  p.k_new = a->k_new;
+  p.v_new = a->v_new;
+  p.k_batch = a->k_batch_stride;
+  p.k_token = a->k_token_stride;
+  p.k_head = a->k_head_stride;
+  p.v_batch = a->v_batch_stride;
+  p.v_token = a->v_token_stride;
+  p.v_head = a->v_head_stride;
+  p.k_vec = rows_aligned(a->k_new, es, 16, p.k_batch, p.k_token, p.k_head);
+  p.v_vec = rows_aligned(a->v_new, es, 16, p.v_batch, p.v_token, p.v_head);
+  p.k_norm = norm_view(a->k_norm);
+  p.rope = rope_view(a->rope);
+  p.kv_len = a->kv_len;
+  p.num_new = a->num_new;
+  p.offset = a->offset;
+  p.err = error_word(workspace);
+  p.q = heads_view(a->q, a->dtype, a->B, a->T, p.c.D / 16, kAppendThreads, dev.sms);
+  // a thread for every kAppendChunks chunks of sixteen values of a (page, head, side)
+  const int chunks = std::min(a->T, p.c.page_size) * (p.c.D / 16);
+  p.group = 32;
+  while (p.group * kAppendChunks < chunks) p.group *= 2;
+  static_assert(128 * 128 / 16 <= kAppendThreads * kAppendChunks, "a page fits one block");
+  const int64_t threads = static_cast<int64_t>(p.pages) * 2 * p.c.Hkv * p.group;
+  p.blocks = static_cast<int>((threads + kAppendThreads - 1) / kAppendThreads);
+  const dim3 grid(static_cast<unsigned>(p.blocks + p.q.blocks), static_cast<unsigned>(a->B));
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  switch (a->dtype) {
+    case SV_BF16: return launch(kv_append_kernel<__nv_bfloat16>, p, grid, kAppendThreads, 0, st);
+    case SV_FP16: return launch(kv_append_kernel<__half>, p, grid, kAppendThreads, 0, st);
+    default: return launch(kv_append_kernel<float>, p, grid, kAppendThreads, 0, st);
+  }
+}
+
+}  // extern "C"

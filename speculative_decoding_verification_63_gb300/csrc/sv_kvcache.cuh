@@ -149,6 +149,23 @@ struct KvWriteProblem {
   int* err;
 };
 
+// The tokens that stay in a page whose scale grows, at the larger scale (f: the
+// old by the new), by a group of GT threads: chunks of sixteen codes.
+__device__ __forceinline__ void rescale_kept(unsigned char* dst, int chunks, int gl, int GT,
+                                             float f) {
+  for (int c = gl; c < chunks; c += GT) {
+    uint4* p = reinterpret_cast<uint4*>(dst + static_cast<long long>(c) * 16);
+    uint4 v = *p;
+    unsigned* w = reinterpret_cast<unsigned*>(&v);
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const float2 lo = float2_of_half2(half2_lo(w[q])), hi = float2_of_half2(half2_hi(w[q]));
+      w[q] = e4m3x4(lo.x * f, lo.y * f, hi.x * f, hi.y * f);
+    }
+    *p = v;
+  }
+}
+
 // One thread group per (request, page of the round, side, head): it takes
 // the largest |x| of the page's new tokens, settles the scale, and converts
 // from registers, so each new value is read once and each code written once
@@ -260,21 +277,7 @@ __global__ void __launch_bounds__(kKvThreads) kv_write_kernel(const KvWriteProbl
           make_uint4(w[0], w[1], w[2], w[3]);
     }
   }
-  if (kept > 0 && e > before) {
-    // the tokens that stay, at the larger scale
-    const float f = pow2f(before - e);
-    for (int c = gl; c < kept << pshift; c += GT) {
-      uint4* p = reinterpret_cast<uint4*>(dst + static_cast<long long>(c) * 16);
-      uint4 v = *p;
-      unsigned* w = reinterpret_cast<unsigned*>(&v);
-#pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const float2 lo = float2_of_half2(half2_lo(w[q])), hi = float2_of_half2(half2_hi(w[q]));
-        w[q] = e4m3x4(lo.x * f, lo.y * f, hi.x * f, hi.y * f);
-      }
-      *p = v;
-    }
-  }
+  if (kept > 0 && e > before) rescale_kept(dst, kept << pshift, gl, GT, pow2f(before - e));
   if (gl == 0) {
     if (kept == 0 || e > before) *scale = pow2f(e);
     if (stored != scale_value(stored)) record_error(a.err, SV_DERR_ARG);

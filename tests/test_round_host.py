@@ -1,0 +1,401 @@
+"""Norms and rotations of queries and keys and log probabilities without a GPU:
+struct layouts, refusals before any device work, the binding's checks, the
+frequencies, and the plain implementations' own pins."""
+import ctypes
+import math
+import os
+import re
+import subprocess
+
+import numpy as np
+import pytest
+import torch
+
+import round_util as ru
+import speculative_decoding_verification_63_gb300 as sv
+from speculative_decoding_verification_63_gb300 import _build
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+FAKE, WS = 0x100000, ctypes.c_void_p(0x200000)
+BIG = 1 << 30
+
+
+@pytest.fixture(scope="module")
+def b():
+    from speculative_decoding_verification_63_gb300 import _binding
+    _build.build_library()
+    _binding.lib()
+    return _binding
+
+
+def test_struct_layout_matches_binding(tmp_path, b):
+    lines = ['#include "specverify.h"', "#include <stdio.h>", "#include <stddef.h>",
+             "int main(void) {"]
+    expect = []
+    for cname, cls in [("sv_rope", b.SvRope), ("sv_head_norm", b.SvHeadNorm),
+                       ("sv_heads", b.SvHeads), ("sv_rotate_args", b.SvRotateArgs),
+                       ("sv_kv_append_args", b.SvKvAppendArgs),
+                       ("sv_token_logprobs_args", b.SvTokenLogprobsArgs)]:
+        lines.append(f'printf("%zu\\n", sizeof({cname}));')
+        expect.append(ctypes.sizeof(cls))
+        for f, _ in cls._fields_:
+            lines.append(f'printf("%zu\\n", offsetof({cname}, {f}));')
+            expect.append(getattr(cls, f).offset)
+    c = tmp_path / "layout.c"
+    c.write_text("\n".join(lines + ["return 0; }"]))
+    exe = tmp_path / "layout"
+    subprocess.run(["gcc", "-std=c11", f"-I{os.path.join(ROOT, 'include')}", "-o", str(exe),
+                    str(c)], check=True)
+    got = subprocess.run([str(exe)], capture_output=True, text=True, check=True).stdout
+    assert [int(x) for x in got.split()] == expect
+
+
+# ---------------------------------------------------------------- refusals
+
+def _heads(h, heads=4, D=64, **kw):
+    h.x, h.out, h.heads = FAKE, FAKE + (1 << 16), heads
+    h.batch_stride = h.out_batch_stride = 1 << 12
+    h.token_stride = h.out_token_stride = heads * D
+    h.head_stride = h.out_head_stride = D
+    for k, v in kw.items():
+        if k in ("weight", "weight_dtype", "eps"):
+            setattr(h.norm, k, v)
+        else:
+            setattr(h, k, v)
+
+
+def _rope(r, **kw):
+    r.dim, r.interleaved, r.scale, r.freq = 64, 0, 1.0, FAKE
+    for k, v in kw.items():
+        setattr(r, k, v)
+
+
+def _rotate(b, q=None, k=None, rope=None, **kw):
+    a = b.SvRotateArgs()
+    a.B, a.T, a.D, a.dtype = 2, 4, 64, b.SV_BF16
+    _heads(a.q, **(q or {}))
+    if k is not None:
+        _heads(a.k, **k)
+    _rope(a.rope, **(rope or {}))
+    for name, v in kw.items():
+        setattr(a, name, v)
+    return a
+
+
+def _append(b, cache=None, q=None, rope=None, norm=None, **kw):
+    a = b.SvKvAppendArgs()
+    c = a.cache
+    c.num_pages, c.page_size, c.Hkv, c.D, c.slots = 8, 16, 2, 64, 4
+    c.k = c.v = c.k_scale = c.v_scale = c.page_table = FAKE
+    c.head_stride, c.page_stride = 16 * 64, 2 * 16 * 64
+    for name, v in (cache or {}).items():
+        setattr(c, name, v)
+    a.B, a.T, a.dtype = 2, 4, b.SV_BF16
+    a.k_new = a.v_new = a.kv_len = FAKE
+    _heads(a.q, **(q or {}))
+    _rope(a.rope, **(rope or {}))
+    for name, v in (norm or {}).items():
+        setattr(a.k_norm, name, v)
+    for name, v in kw.items():
+        setattr(a, name, v)
+    return a
+
+
+def _logprobs(b, **kw):
+    a = b.SvTokenLogprobsArgs()
+    a.B, a.N, a.R, a.M, a.V, a.dtype, a.top = 2, 4, 4, 1, 1000, b.SV_BF16, 3
+    a.batch_stride, a.row_stride = 4000, 1000
+    for f in ("logits", "tokens", "logprob", "entropy", "top_token", "top_logprob"):
+        setattr(a, f, FAKE)
+    for name, v in kw.items():
+        setattr(a, name, v)
+    return a
+
+
+def _call(b, name, a, ws=WS, n=BIG):
+    return getattr(b.lib(), name)(bytes(a), ws, n, None)
+
+
+CALLS = [("sv_rotate", _rotate), ("sv_kv_append", _append), ("sv_token_logprobs", _logprobs)]
+
+
+@pytest.mark.parametrize("name,make", CALLS)
+def test_refusals_of_all(b, name, make):
+    assert getattr(b.lib(), name)(None, WS, BIG, None) == b.SV_EINVAL
+    assert _call(b, name, make(b, B=0)) == b.SV_OK
+    for kw in [dict(B=-1), dict(B=b.SV_MAX_B + 1), dict(dtype=3), dict(dtype=-1)]:
+        assert _call(b, name, make(b, **kw)) == b.SV_EINVAL, kw
+    ok = make(b)
+    assert _call(b, name, ok, ws=ctypes.c_void_p(0)) == b.SV_EWORKSPACE
+    assert _call(b, name, ok, ws=ctypes.c_void_p(0x200010)) == b.SV_EWORKSPACE
+    assert _call(b, name, ok, n=b.SV_MIN_WORKSPACE_BYTES - 1) == b.SV_EWORKSPACE
+
+
+BAD_ROPES = [dict(dim=-16), dict(dim=8), dict(dim=40), dict(dim=80), dict(freq=None),
+             dict(freq=FAKE + 8), dict(scale=math.nan), dict(scale=math.inf)]
+BAD_HEADS = [dict(heads=-1), dict(heads=257), dict(x=None), dict(out=None), dict(x=FAKE + 1),
+             dict(out=FAKE + 1), dict(out_dtype=3), dict(out=FAKE, out_dtype=1),
+             dict(out=FAKE, out_token_stride=64), dict(eps=-1e-6), dict(eps=1e-31),
+             dict(eps=math.inf), dict(eps=math.nan), dict(weight=FAKE),
+             dict(weight=FAKE, eps=1e-6, weight_dtype=3), dict(weight=FAKE + 1, eps=1e-6)]
+
+
+@pytest.mark.parametrize("name,make", CALLS[:2])
+def test_refusals_of_rotations(b, name, make):
+    for kw in [dict(T=0), dict(T=b.SV_MAX_KV_T + 1)] + [dict(rope=r) for r in BAD_ROPES] + [
+            dict(q=h) for h in BAD_HEADS]:
+        assert _call(b, name, make(b, **kw)) == b.SV_EINVAL, kw
+    if name == "sv_rotate":
+        for kw in [dict(D=8), dict(D=72), dict(D=272), dict(D=0)] + [dict(k=h) for h in BAD_HEADS]:
+            assert _call(b, name, make(b, **kw)) == b.SV_EINVAL, kw
+        assert _call(b, name, make(b, q=dict(heads=0))) == b.SV_OK
+    else:
+        for kw in [dict(cache=dict(D=80)), dict(cache=dict(page_size=48)), dict(cache=dict(k=None)),
+                   dict(k_new=None), dict(v_new=None), dict(kv_len=None), dict(k_new=FAKE + 1),
+                   dict(v_new=FAKE + 1), dict(norm=dict(weight=FAKE)), dict(norm=dict(eps=-1.0))]:
+            assert _call(b, name, make(b, **kw)) == b.SV_EINVAL, kw
+
+
+def test_refusals_of_log_probabilities(b):
+    for kw in [dict(N=0), dict(N=65537), dict(R=0), dict(R=65537), dict(R=5), dict(M=-1),
+               dict(M=b.SV_MAX_GIVEN + 1), dict(V=0), dict(V=b.SV_MAX_V + 1), dict(top=-1),
+               dict(top=b.SV_MAX_TOPK + 1), dict(dtype=b.SV_FP16), dict(logits=None),
+               dict(logits=FAKE + 1), dict(tokens=None), dict(logprob=None), dict(top_token=None),
+               dict(top_logprob=None), dict(batch_stride=-1), dict(row_stride=-1)]:
+        assert _call(b, "sv_token_logprobs", _logprobs(b, **kw)) == b.SV_EINVAL, kw
+
+
+# ----------------------------------------------------------------- binding
+
+class OnDevice:
+    """A CPU tensor that says it lives on a GPU."""
+
+    def __init__(self, t, index=0):
+        self.t, self.index = t, index
+
+    def __getattr__(self, name):
+        return getattr(self.t, name)
+
+    def get_device(self):
+        return self.index
+
+    @property
+    def device(self):
+        return torch.device("cuda", self.index) if self.index >= 0 else torch.device("cpu")
+
+
+class Launches(list):
+    def __getattr__(self, name):
+        return lambda *args: (self.append((name, args[0])), 0)[1]
+
+
+@pytest.fixture
+def launches(b, monkeypatch):
+    got = Launches()
+    monkeypatch.setattr(b, "_lib_handle", got)
+    monkeypatch.setattr(b, "_current_device", lambda: 0)
+    monkeypatch.setattr(b, "current_raw_stream", lambda dev: 0)
+    return got
+
+
+def tensors(op):
+    i32 = lambda *s: torch.zeros(s, dtype=torch.int32)  # noqa: E731
+    x = lambda h: torch.zeros((2, 3, h, 64), dtype=torch.bfloat16)  # noqa: E731
+    codes = lambda: torch.zeros((4, 2, 16, 64), dtype=torch.uint8).view(  # noqa: E731
+        torch.float8_e4m3fn)
+    ws = torch.zeros(8192, dtype=torch.uint8)
+    rope = dict(sv.rope(64, device="cpu"), freq=OnDevice(sv.rope(64, device="cpu")["freq"]))
+    if op == "logprobs":
+        d = dict(logits=torch.zeros(2, 3, 50), workspace=ws, tokens=i32(2, 3), num_rows=i32(2),
+                 rows=i32(2, 3), temperature=torch.ones(2), logprobs=torch.zeros(2, 3),
+                 entropy=torch.zeros(2, 3), top_tokens=i32(2, 3, 4),
+                 top_logprobs=torch.zeros(2, 3, 4))
+        return {k: OnDevice(v) for k, v in d.items()} | dict(R=3, top=4)
+    w = torch.ones(64, dtype=torch.bfloat16)
+    d = dict(q=x(4), q_out=x(4), workspace=ws, offset=i32(2, 3), q_weight=w, k_weight=w.clone())
+    if op == "rotate":
+        d |= dict(k=x(2), k_out=x(2), start=i32(2), num=i32(2))
+        return {k: OnDevice(v) for k, v in d.items()} | dict(rope=rope, eps=1e-6)
+    d |= dict(page_table=i32(2, 2), kv_len=i32(2), num_new=i32(2), k_new=x(2), v_new=x(2))
+    cache = dict(k=codes(), v=codes(), k_scale=torch.ones(4, 2), v_scale=torch.ones(4, 2))
+    return ({k: OnDevice(v) for k, v in d.items()} |
+            dict(rope=rope, eps=1e-6, cache={k: OnDevice(v) for k, v in cache.items()}))
+
+
+FUNCS = {"rotate": "sv_rotate", "append": "sv_kv_append", "logprobs": "sv_token_logprobs"}
+
+
+@pytest.mark.parametrize("op", list(FUNCS))
+def test_packed_arguments(b, launches, op):
+    """What the binding packs is the structure's fields."""
+    a = tensors(op)
+    getattr(b, FUNCS[op])(**a)
+    [(name, packed)] = launches
+    assert name == FUNCS[op]
+    cls = {"rotate": b.SvRotateArgs, "append": b.SvKvAppendArgs,
+           "logprobs": b.SvTokenLogprobsArgs}[op]
+    s = cls.from_buffer_copy(packed)
+    if op == "logprobs":
+        assert (s.B, s.N, s.R, s.M, s.V, s.top, s.dtype) == (2, 3, 3, 1, 50, 4, b.SV_FP32)
+        assert (s.batch_stride, s.row_stride) == (150, 50)
+        for f, t in [("logits", "logits"), ("tokens", "tokens"), ("rows", "rows"),
+                     ("num_rows", "num_rows"), ("temperature", "temperature"),
+                     ("logprob", "logprobs"), ("entropy", "entropy"), ("top_token", "top_tokens"),
+                     ("top_logprob", "top_logprobs")]:
+            assert getattr(s, f) == a[t].data_ptr(), f
+        return
+    assert (s.B, s.T, s.dtype, s.q.heads, s.q.out_dtype) == (2, 3, b.SV_BF16, 4, b.SV_BF16)
+    assert (s.q.x, s.q.out) == (a["q"].data_ptr(), a["q_out"].data_ptr())
+    assert (s.q.batch_stride, s.q.token_stride, s.q.out_head_stride) == (768, 256, 64)
+    assert s.q.norm.weight == a["q_weight"].data_ptr() and abs(s.q.norm.eps - 1e-6) < 1e-12
+    assert (s.rope.dim, s.rope.interleaved, s.rope.scale) == (64, 0, 1.0)
+    assert s.rope.freq == a["rope"]["freq"].data_ptr() and s.offset == a["offset"].data_ptr()
+    k = s.k.norm if op == "rotate" else s.k_norm
+    assert k.weight == a["k_weight"].data_ptr() and k.weight_dtype == b.SV_BF16
+    if op == "rotate":
+        assert (s.k.heads, s.start, s.num) == (2, a["start"].data_ptr(), a["num"].data_ptr())
+    else:
+        assert (s.k_new, s.v_token_stride) == (a["k_new"].data_ptr(), 128)
+        assert (s.kv_len, s.num_new) == (a["kv_len"].data_ptr(), a["num_new"].data_ptr())
+
+
+@pytest.mark.parametrize("op", list(FUNCS))
+def test_tensors_of_another_device_are_refused(b, launches, op):
+    ok = tensors(op)
+    for name, t in ok.items():
+        for bad in (1, -1):
+            if isinstance(t, OnDevice):
+                wrong = OnDevice(t.t, bad)
+            elif name == "rope":
+                wrong = dict(t, freq=OnDevice(t["freq"].t, bad))
+            elif name == "cache":
+                wrong = dict(t, v_scale=OnDevice(t["v_scale"].t, bad))
+            else:
+                continue
+            with pytest.raises(ValueError):
+                getattr(b, FUNCS[op])(**(ok | {name: wrong}))
+    assert launches == []
+
+
+WRONG = {
+    "rotate": [dict(k=torch.zeros(2, 3, 2, 64)), dict(k=torch.zeros(2, 4, 2, 64).bfloat16()),
+               dict(q_out=torch.zeros(2, 3, 5, 64).bfloat16()), dict(eps=None), dict(eps=0.0),
+               dict(q_weight=torch.ones(32)), dict(q_weight=torch.ones(64, dtype=torch.int32)),
+               dict(start=torch.zeros(2)), dict(num=torch.zeros(3, dtype=torch.int32)),
+               dict(offset=torch.zeros(3, 2, dtype=torch.int32))],
+    "append": [dict(q=torch.zeros(2, 3, 4, 64)), dict(q=torch.zeros(2, 3, 4, 128).bfloat16()),
+               dict(v_new=torch.zeros(2, 3, 2, 64)), dict(eps=None), dict(eps=-1.0),
+               dict(kv_len=torch.zeros(2, dtype=torch.int64)),
+               dict(k_weight=torch.ones(128)), dict(offset=torch.zeros(2, dtype=torch.int32))],
+    "logprobs": [dict(logits=torch.zeros(2, 3, 50).half()), dict(logits=torch.zeros(2, 150)),
+                 dict(logits=torch.zeros(2, 50, 3).transpose(1, 2)),
+                 dict(tokens=torch.zeros(2, 4, dtype=torch.int32)),
+                 dict(tokens=torch.zeros(2, dtype=torch.int32)),
+                 dict(logprobs=torch.zeros(2, 3, 1)), dict(top_tokens=torch.zeros(2, 3, 4)),
+                 dict(temperature=torch.ones(3)), dict(rows=torch.zeros(2, 2, dtype=torch.int32))],
+}
+
+
+@pytest.mark.parametrize("op", list(FUNCS))
+def test_wrong_types_and_shapes_are_refused(b, launches, op):
+    ok = tensors(op)
+    for kw in WRONG[op]:
+        kw = {k: OnDevice(v) if isinstance(v, torch.Tensor) else v for k, v in kw.items()}
+        with pytest.raises(ValueError):
+            getattr(b, FUNCS[op])(**(ok | kw))
+    if op != "logprobs":
+        rope = ok["rope"]
+        for bad in (dict(rope, dim=32), dict(rope, freq=OnDevice(torch.zeros(32)))):
+            with pytest.raises(ValueError):
+                getattr(b, FUNCS[op])(**(ok | dict(rope=bad)))
+    assert launches == []
+
+
+# -------------------------------------------------------------------- rope
+
+def test_frequencies():
+    """Each kind of scaling at the pairs where its value is known."""
+    radians = lambda r: [x % (1 << 64) / 2.0 ** 64 * 2 * math.pi  # noqa: E731
+                         for x in r["freq"].tolist()]
+    rope = lambda **kw: sv.rope(128, 5e5, device="cpu", **kw)  # noqa: E731
+    plain = radians(rope())
+    assert plain == pytest.approx([5e5 ** (-c / 64) for c in range(64)], rel=1e-14)
+    assert radians(rope(scaling=dict(type="linear", factor=4))) == pytest.approx(
+        [x / 4 for x in plain], rel=1e-14)
+    ntk = radians(rope(scaling=dict(type="ntk", factor=4)))
+    assert ntk[0] == 1 and ntk[63] == pytest.approx(plain[63] / 4, rel=1e-12)
+    yarn = rope(scaling=dict(type="yarn", factor=8, context=8192))
+    assert yarn["scale"] == pytest.approx(0.1 * math.log(8) + 1)
+    y = [a / b for a, b in zip(radians(yarn), plain)]
+    turns = [8192 * x / (2 * math.pi) for x in plain]
+    for ratio, n in zip(y, turns):
+        assert 1 / 8 - 1e-9 <= ratio <= 1 + 1e-9
+        if n > 40:
+            assert ratio == pytest.approx(1)
+        if n < 0.8:
+            assert ratio == pytest.approx(1 / 8)
+    assert all(a >= c - 1e-9 for a, c in zip(y, y[1:]))
+    wave = [a / b for a, b in zip(radians(rope(scaling=dict(
+        type="wavelength", factor=8, context=8192, low=1, high=4))), plain)]
+    for ratio, n in zip(wave, turns):
+        want = 1 if n >= 4 else 1 / 8 if n <= 1 else (n - 1) / 3 + (1 - (n - 1) / 3) / 8
+        assert ratio == pytest.approx(want, rel=1e-9)
+    f = radians(rope(scaling=dict(type="factors", factors=[2.0] * 32 + [5.0] * 32)))
+    assert f[0] == pytest.approx(0.5) and f[63] == pytest.approx(plain[63] / 5)
+    # above half a turn, and backwards: the same angles
+    r = dict(freq=sv.rope_turns([5.0, -1.0], "cpu"))
+    assert radians(r) == pytest.approx([5.0, 2 * math.pi - 1])
+    for bad in (dict(dim=24), dict(dim=0), dict(dim=272), dict(base=0.0), dict(base=math.inf),
+                dict(scaling=dict(type="other")), dict(scaling=dict(type="factors", factors=[1]))):
+        with pytest.raises(ValueError):
+            sv.rope(**(dict(dim=64, device="cpu") | bad))
+
+
+# --------------------------------------------- the plain implementations' pins
+
+def test_plain_rotation():
+    """A quarter turn, norms that survive turning, and positions that only matter
+    by their differences."""
+    rope = dict(freq=torch.tensor([1 << 62] * 8), dim=16, interleaved=False, scale=1.0)
+    x = np.arange(16.0).reshape(1, 1, 1, 16)
+    y, _ = ru.rotated(x, [[1]], rope)
+    assert np.allclose(y[0, 0, 0], np.concatenate([-np.arange(8, 16), np.arange(8)]))
+    y, _ = ru.rotated(x, [[1]], dict(rope, interleaved=True))
+    assert np.allclose(y[0, 0, 0, :4], [-1, 0, -3, 2])
+    rng = np.random.default_rng(1)
+    rope = sv.rope(64, device="cpu", interleaved=True)
+    q, k = rng.normal(size=(2, 1, 1, 1, 64))
+    dots = [np.vdot(ru.rotated(q, [[a]], rope)[0], ru.rotated(k, [[c]], rope)[0])
+            for a, c in ((5, 2), (1000003, 1000000), (0, -3))]
+    assert np.allclose(dots, dots[0], atol=1e-9)
+    y, _ = ru.rotated(q, [[9]], None, None, 1e-9)
+    assert np.isclose((y ** 2).mean(), 1)
+
+
+def test_plain_log_probabilities():
+    row = ru.Row(np.log(np.array([0.5, 0.25, 0.125, 0.125])) + 3.0)
+    assert np.allclose(np.exp(row.lp), [0.5, 0.25, 0.125, 0.125])
+    assert np.isclose(row.entropy, 1.75 * math.log(2))
+    assert row.top(3).tolist() == [0, 1, 2]
+    row = ru.Row(np.array([1.0, -np.inf, 1.0, 1.0]), 0.5)
+    assert np.isclose(row.entropy, math.log(3)) and row.top(9).tolist() == [0, 2, 3]
+    assert (np.isfinite(row.bounds()[0])).all()
+
+
+# ------------------------------------------------------------------ builds
+
+def preprocessed(name, **kw):
+    flags = [f for f in _build.compile_flags(**kw) if f.startswith(("-I", "-D", "-std"))]
+    return subprocess.run([_build.nvcc(), "-E", "-x", "cu", *flags,
+                           os.path.join(_build.CSRC, name)], capture_output=True, text=True,
+                          check=True).stdout
+
+
+def test_nvtx_build_opens_a_range_per_call():
+    for unit, names in (("rotate.cu", ("sv_rotate", "sv_kv_append")),
+                        ("logprobs.cu", ("sv_token_logprobs",))):
+        out = preprocessed(unit, nvtx=True)
+        for name in names:
+            assert re.search(r"sv_status\s+" + name + r"\s*\([^{]*\{\s*const\s+SvKvRange\s+sv_range_"
+                             r"\s*\(\s*\"" + name + r"\"\s*\)", out), name
+        assert "SvKvRange" not in preprocessed(unit)
