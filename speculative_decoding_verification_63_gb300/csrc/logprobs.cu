@@ -67,7 +67,7 @@ sv_status sv_token_logprobs(const sv_token_logprobs_args* a, void* workspace, si
   const int64_t rows = static_cast<int64_t>(a->B) * a->R;
   const int groups = (a->V + 32 / es - 1 + kLpGroup - 1) / kLpGroup;
   p.cluster = 1;
-  while (p.cluster < kLpMaxCluster && rows * p.cluster < 8 * dev.sms &&
+  while (p.cluster < kLpMaxCluster && rows * p.cluster * 2 <= 4 * dev.sms &&
          groups > p.cluster * kLpThreads)
     p.cluster *= 2;
   // a map fits its CTA

@@ -61,7 +61,7 @@ Heads heads_view(const sv_heads& h, sv_dtype dtype, int B, int T, int lanes, int
   v.out_vec = rows_aligned(h.out, dtype_bytes(h.out_dtype), 16, v.out_batch, v.out_token, v.out_head);
   v.norm = norm_view(h.norm);
   const int64_t one = static_cast<int64_t>(B) * T * lanes;  // threads of a head
-  v.per = 8;
+  v.per = 16;
   while (v.per > 1 && one * ((h.heads + v.per - 1) / v.per) < int64_t{1024} * sms) v.per /= 2;
   const int64_t mine = static_cast<int64_t>(T) * lanes * ((h.heads + v.per - 1) / v.per);
   v.blocks = static_cast<int>((mine + threads - 1) / threads);
@@ -95,9 +95,8 @@ sv_status sv_rotate(const sv_rotate_args* a, void* workspace, size_t ws_bytes,
   p.D = a->D;
   p.lane_shift = 0;
   while ((16 << p.lane_shift) < a->D) ++p.lane_shift;
-  p.lanes = 1 << p.lane_shift;
-  p.q = heads_view(a->q, a->dtype, a->B, a->T, p.lanes, kRotateThreads, dev.sms);
-  p.k = heads_view(a->k, a->dtype, a->B, a->T, p.lanes, kRotateThreads, dev.sms);
+  p.q = heads_view(a->q, a->dtype, a->B, a->T, 1 << p.lane_shift, kRotateThreads, dev.sms);
+  p.k = heads_view(a->k, a->dtype, a->B, a->T, 1 << p.lane_shift, kRotateThreads, dev.sms);
   p.rope = rope_view(a->rope);
   p.start = a->start;
   p.num = a->num;
@@ -152,20 +151,27 @@ sv_status sv_kv_append(const sv_kv_append_args* a, void* workspace, size_t ws_by
   p.num_new = a->num_new;
   p.offset = a->offset;
   p.err = error_word(workspace);
-  p.q = heads_view(a->q, a->dtype, a->B, a->T, p.c.D / 16, kAppendThreads, dev.sms);
-  // a thread for every kAppendChunks chunks of sixteen values of a (page, head, side)
+  // a thread for every chunk of sixteen values of a (page, head, side), or for two
   const int chunks = std::min(a->T, p.c.page_size) * (p.c.D / 16);
+  const int block = chunks > 512 ? 512 : 256, each = chunks > 256 ? 2 : 1;
+  static_assert(128 * 128 / 16 <= 512 * 2, "a page fits one block");
+  p.q = heads_view(a->q, a->dtype, a->B, a->T, p.c.D / 16, block, dev.sms);
   p.group = 32;
-  while (p.group * kAppendChunks < chunks) p.group *= 2;
-  static_assert(128 * 128 / 16 <= kAppendThreads * kAppendChunks, "a page fits one block");
+  while (p.group * each < chunks) p.group *= 2;
   const int64_t threads = static_cast<int64_t>(p.pages) * 2 * p.c.Hkv * p.group;
-  p.blocks = static_cast<int>((threads + kAppendThreads - 1) / kAppendThreads);
+  p.blocks = static_cast<int>((threads + block - 1) / block);
   const dim3 grid(static_cast<unsigned>(p.blocks + p.q.blocks), static_cast<unsigned>(a->B));
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  auto run = [&](auto t) {
+    using T = decltype(t);
+    return block == 512 ? launch(kv_append_kernel<T, 512, 2>, p, grid, block, 0, st)
+           : each == 2  ? launch(kv_append_kernel<T, 256, 2>, p, grid, block, 0, st)
+                        : launch(kv_append_kernel<T, 256, 1>, p, grid, block, 0, st);
+  };
   switch (a->dtype) {
-    case SV_BF16: return launch(kv_append_kernel<__nv_bfloat16>, p, grid, kAppendThreads, 0, st);
-    case SV_FP16: return launch(kv_append_kernel<__half>, p, grid, kAppendThreads, 0, st);
-    default: return launch(kv_append_kernel<float>, p, grid, kAppendThreads, 0, st);
+    case SV_BF16: return run(__nv_bfloat16());
+    case SV_FP16: return run(__half());
+    default: return run(float());
   }
 }
 

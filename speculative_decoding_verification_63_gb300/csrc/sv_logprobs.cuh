@@ -53,30 +53,6 @@ struct LogprobProblem {
   int* err;
 };
 
-__device__ __forceinline__ float2 lp_add(float2 a, float2 b) {
-  float2 d;
-  asm("{\n\t.reg .b64 a, b, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
-      "add.rn.f32x2 d, a, b;\n\tmov.b64 {%0, %1}, d;\n\t}"
-      : "=f"(d.x), "=f"(d.y)
-      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
-  return d;
-}
-__device__ __forceinline__ float2 lp_mul(float2 a, float2 b) {
-  float2 d;
-  asm("{\n\t.reg .b64 a, b, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
-      "mul.rn.f32x2 d, a, b;\n\tmov.b64 {%0, %1}, d;\n\t}"
-      : "=f"(d.x), "=f"(d.y)
-      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
-  return d;
-}
-__device__ __forceinline__ float2 lp_fma(float2 a, float2 b, float2 c) {
-  float2 d;
-  asm("{\n\t.reg .b64 a, b, c, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
-      "mov.b64 c, {%6, %7};\n\tfma.rn.f32x2 d, a, b, c;\n\tmov.b64 {%0, %1}, d;\n\t}"
-      : "=f"(d.x), "=f"(d.y)
-      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
-  return d;
-}
 __device__ __forceinline__ float max_nan(float a, float b) {
   float d;
   asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
@@ -454,12 +430,12 @@ __global__ void __launch_bounds__(kLpThreads, 4) logprob_kernel(const LogprobPro
         for (int u = 0; u < U; ++u)
 #pragma unroll
           for (int i = 0; i < kLpGroup / 2; ++i) {
-            float2 e = lp_mul(lp_add(lp_pair(raw[u], i), ref), c2);
+            float2 e = x2_mul(x2_add(lp_pair(raw[u], i), ref), c2);
             e.x = fmaxf(e.x, -1000.f);
             e.y = fmaxf(e.y, -1000.f);
             const float2 f = make_float2(fast_exp2(e.x), fast_exp2(e.y));
-            z = lp_add(z, f);
-            w = lp_fma(f, e, w);
+            z = x2_add(z, f);
+            w = x2_fma(f, e, w);
           }
         s.z += z.x + z.y;
         s.a += w.x + w.y;
