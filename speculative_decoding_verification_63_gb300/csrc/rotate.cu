@@ -1,6 +1,7 @@
 // rotate.cu -- C ABI of the norms and rotations of queries and keys (see
 // include/specverify.h): argument checks and launches.
 #include <algorithm>
+#include <type_traits>
 
 #include "sv_host.cuh"
 #include "sv_rotate.cuh"
@@ -41,9 +42,18 @@ Rope rope_view(const sv_rope& r) {
   return Rope{r.dim, r.interleaved, r.scale, reinterpret_cast<const unsigned long long*>(r.freq)};
 }
 
+// Heads that a thread takes: they share sines and cosines, and their loads
+// follow one another without a pause.  As many as leave this many threads an SM
+// (16384 tokens: 16 heads 54 us, 8 heads 54; 1024 tokens of 40 heads, by threads an SM:
+// 1024 10.0 us, 256 8.1, 128 7.7; 448 tokens 6.0, 5.1, 5.1).
+constexpr int kRotatePer = 16, kRotateFill = 128;
+// The same for the groups that write the cache, whose threads hold a page's
+// values (prompts of 4 x 8190 tokens, 8 heads: 8 at a time 130 us, 4 145, 2 148; 8 x
+// 512 tokens, by threads an SM: 1024 30 us, 512 25, 256 22, 128 26).
+constexpr int kAppendPer = 8, kAppendFill = 256;
+
 // A kind of heads for blocks of `threads` threads; B requests of T tokens of
-// `lanes` lanes.  A thread takes several heads of its token, which share sines
-// and cosines, once that leaves the GPU full.
+// `lanes` lanes.
 Heads heads_view(const sv_heads& h, sv_dtype dtype, int B, int T, int lanes, int threads, int sms) {
   Heads v = {};
   if (h.heads == 0) return v;
@@ -58,14 +68,29 @@ Heads heads_view(const sv_heads& h, sv_dtype dtype, int B, int T, int lanes, int
   v.out_token = h.out_token_stride;
   v.out_head = h.out_head_stride;
   v.x_vec = rows_aligned(h.x, dtype_bytes(dtype), 16, v.batch, v.token, v.head);
-  v.out_vec = rows_aligned(h.out, dtype_bytes(h.out_dtype), 16, v.out_batch, v.out_token, v.out_head);
+  const int oes = dtype_bytes(h.out_dtype);
+  v.out_vec = rows_aligned(h.out, oes, 32, v.out_batch, v.out_token, v.out_head)   ? 32
+              : rows_aligned(h.out, oes, 16, v.out_batch, v.out_token, v.out_head) ? 16
+                                                                                   : 0;
   v.norm = norm_view(h.norm);
   const int64_t one = static_cast<int64_t>(B) * T * lanes;  // threads of a head
-  v.per = 16;
-  while (v.per > 1 && one * ((h.heads + v.per - 1) / v.per) < int64_t{1024} * sms) v.per /= 2;
+  v.per = std::min(kRotatePer, h.heads);
+  while (v.per > 1 && one * ((h.heads + v.per - 1) / v.per) < int64_t{kRotateFill} * sms)
+    v.per = (v.per + 1) / 2;
   const int64_t mine = static_cast<int64_t>(T) * lanes * ((h.heads + v.per - 1) / v.per);
   v.blocks = static_cast<int>((mine + threads - 1) / threads);
   return v;
+}
+
+template <class T, bool NEAR, int THREADS, int CH>
+sv_status run_append(const KvAppendProblem& p, dim3 grid, cudaStream_t stream) {
+  constexpr size_t smem = sizeof(AppendFeed<T, THREADS, CH>);
+  const auto kernel = kv_append_kernel<T, NEAR, THREADS, CH>;
+  if (smem > 48 * 1024 &&
+      cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                           static_cast<int>(smem)) != cudaSuccess)
+    return SV_ECUDA;
+  return launch(kernel, p, grid, THREADS, smem, stream);
 }
 
 }  // namespace
@@ -104,10 +129,15 @@ sv_status sv_rotate(const sv_rotate_args* a, void* workspace, size_t ws_bytes,
   p.err = error_word(workspace);
   const dim3 grid(static_cast<unsigned>(p.q.blocks + p.k.blocks), static_cast<unsigned>(a->B));
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  auto run = [&](auto t) {
+    using T = decltype(t);
+    return p.rope.interleaved ? launch(rotate_kernel<T, true>, p, grid, kRotateThreads, 0, st)
+                              : launch(rotate_kernel<T, false>, p, grid, kRotateThreads, 0, st);
+  };
   switch (a->dtype) {
-    case SV_BF16: return launch(rotate_kernel<__nv_bfloat16>, p, grid, kRotateThreads, 0, st);
-    case SV_FP16: return launch(rotate_kernel<__half>, p, grid, kRotateThreads, 0, st);
-    default: return launch(rotate_kernel<float>, p, grid, kRotateThreads, 0, st);
+    case SV_BF16: return run(__nv_bfloat16());
+    case SV_FP16: return run(__half());
+    default: return run(float());
   }
 }
 
@@ -158,20 +188,30 @@ sv_status sv_kv_append(const sv_kv_append_args* a, void* workspace, size_t ws_by
   p.q = heads_view(a->q, a->dtype, a->B, a->T, p.c.D / 16, block, dev.sms);
   p.group = 32;
   while (p.group * each < chunks) p.group *= 2;
-  const int64_t threads = static_cast<int64_t>(p.pages) * 2 * p.c.Hkv * p.group;
+  // heads a group takes: sines and cosines are shared, once that leaves the GPU full
+  p.per = std::min(kAppendPer, p.c.Hkv);
+  while (p.per > 1 && static_cast<int64_t>(a->B) * p.pages * 2 * p.group *
+                              ((p.c.Hkv + p.per - 1) / p.per) < int64_t{kAppendFill} * dev.sms)
+    p.per = (p.per + 1) / 2;
+  p.chunks = (p.c.Hkv + p.per - 1) / p.per;
+  const int64_t threads = static_cast<int64_t>(p.pages) * 2 * p.chunks * p.group;
   p.blocks = static_cast<int>((threads + block - 1) / block);
   const dim3 grid(static_cast<unsigned>(p.blocks + p.q.blocks), static_cast<unsigned>(a->B));
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  auto run = [&](auto t) {
+  auto run = [&](auto t, auto near) {
     using T = decltype(t);
-    return block == 512 ? launch(kv_append_kernel<T, 512, 2>, p, grid, block, 0, st)
-           : each == 2  ? launch(kv_append_kernel<T, 256, 2>, p, grid, block, 0, st)
-                        : launch(kv_append_kernel<T, 256, 1>, p, grid, block, 0, st);
+    constexpr bool N = decltype(near)::value;
+    return block == 512 ? run_append<T, N, 512, 2>(p, grid, st)
+           : each == 2  ? run_append<T, N, 256, 2>(p, grid, st)
+                        : run_append<T, N, 256, 1>(p, grid, st);
+  };
+  auto pairs = [&](auto t) {
+    return p.rope.interleaved ? run(t, std::true_type()) : run(t, std::false_type());
   };
   switch (a->dtype) {
-    case SV_BF16: return run(__nv_bfloat16());
-    case SV_FP16: return run(__half());
-    default: return run(float());
+    case SV_BF16: return pairs(__nv_bfloat16());
+    case SV_FP16: return pairs(__half());
+    default: return pairs(float());
   }
 }
 

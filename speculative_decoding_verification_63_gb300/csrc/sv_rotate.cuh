@@ -41,7 +41,8 @@ struct Heads {
   const void* x;
   void* out;
   int heads, out_dtype;
-  bool x_vec, out_vec;  // 16-byte accesses
+  bool x_vec;   // 16-byte loads
+  int out_vec;  // bytes that stores may have at once: 0 (elements), 16 or 32
   long long batch, token, head, out_batch, out_token, out_head;
   HeadNorm norm;
   int per;     // heads a thread takes
@@ -53,20 +54,20 @@ struct Pairs {
   float2 u[4], v[4];
 };
 
-// Where it lies: channels a .. a + 7 and b .. b + 7, in memory.
+// Where it lies in memory: channels a .. a + 7 and b .. b + 7.  NEAR (pairs of
+// neighbours): u the even ones of the sixteen, v the odd ones; else u those of a,
+// v those of b.
 struct Place {
   int a, b;
-  bool on;    // its channels turn
-  bool near;  // pairs are neighbours: u the even channels, v the odd ones
+  bool on;  // its channels turn
 };
 
+template <bool NEAR>
 __device__ __forceinline__ Place place_of(const Rope& r, int j) {
   Place t;
   t.on = 16 * j < r.dim;
-  t.near = t.on && r.interleaved != 0;
-  const bool far = t.on && r.interleaved == 0;
-  t.a = far ? 8 * j : 16 * j;
-  t.b = far ? r.dim / 2 + 8 * j : 16 * j + 8;
+  t.a = !NEAR && t.on ? 8 * j : 16 * j;
+  t.b = !NEAR && t.on ? r.dim / 2 + 8 * j : 16 * j + 8;
   return t;
 }
 
@@ -95,70 +96,133 @@ __device__ __forceinline__ void load_pairs(RawPairs<T>& r, const T* p, const Pla
   }
 }
 
+// Loads some heads ahead, through shared memory: each thread copies its own
+// pieces asynchronously into slots of its own and reads them when their turn has
+// come, so nothing is shared and no thread waits for another, and what is under
+// way takes no registers.  Pieces that are not on a 16-byte boundary are loaded
+// when they are needed.
+template <class T, int THREADS, int CH>
+struct Ahead {
+  static constexpr int kPieces = static_cast<int>(sizeof(T)) * CH;  // of 16 bytes a head
+  static constexpr int kStages = 8 / kPieces > 1 ? 8 / kPieces : 2;
+  uint4 slot[kStages][kPieces][THREADS];
+
+  template <bool NEAR>
+  __device__ __forceinline__ void ask(int i, int chunk, const T* p, const Place& at, bool vec) {
+    constexpr int H = static_cast<int>(sizeof(T)) / 2;
+    uint4(*to)[THREADS] = &slot[i % kStages][chunk * 2 * H];
+    if (vec) {
+#pragma unroll
+      for (int k = 0; k < H; ++k) {
+        copy<NEAR>(&to[k][threadIdx.x], reinterpret_cast<const uint4*>(p + at.a) + k);
+        copy<NEAR>(&to[H + k][threadIdx.x], reinterpret_cast<const uint4*>(p + at.b) + k);
+      }
+    }
+  }
+  // (Two pieces that make one 32-byte sector come through L1, so that the sector
+  // is fetched once; others past it.)
+  template <bool NEAR>
+  static __device__ __forceinline__ void copy(uint4* to, const uint4* from) {
+    if (NEAR || sizeof(T) == 4)
+      asm volatile("cp.async.ca.shared.global [%0], [%1], 16;" ::"r"(smem_u32(to)), "l"(from)
+                   : "memory");
+    else
+      asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(to)), "l"(from)
+                   : "memory");
+  }
+  // a head's copies are a group; the oldest of kStages - 1 groups is done
+  static __device__ __forceinline__ void commit() {
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  }
+  static __device__ __forceinline__ void wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 2) : "memory");
+  }
+  __device__ __forceinline__ void take(RawPairs<T>& r, int i, int chunk, const T* p,
+                                       const Place& at, bool vec) const {
+    if (vec) {
+#pragma unroll
+      for (int k = 0; k < static_cast<int>(sizeof(T)); ++k)
+        r.w[k] = slot[i % kStages][chunk * sizeof(T) + k][threadIdx.x];
+    } else {
+      load_pairs(r, p, at, false);
+    }
+  }
+};
+
 __device__ __forceinline__ float2 two_of(unsigned w, __nv_bfloat16) {
   return make_float2(bf16lo(w), bf16hi(w));
 }
 __device__ __forceinline__ float2 two_of(unsigned w, __half) { return float2_of_half2(w); }
 
-template <class T>
-__device__ __forceinline__ Pairs pairs_of(const RawPairs<T>& r, bool near) {
+template <bool NEAR, class T>
+__device__ __forceinline__ Pairs pairs_of(const RawPairs<T>& r) {
   const unsigned* w = reinterpret_cast<const unsigned*>(r.w);
+  float f[16];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    if constexpr (sizeof(T) == 4) {
+      f[2 * i] = __uint_as_float(w[2 * i]);
+      f[2 * i + 1] = __uint_as_float(w[2 * i + 1]);
+    } else {
+      const float2 t = two_of(w[i], T());
+      f[2 * i] = t.x;
+      f[2 * i + 1] = t.y;
+    }
+  }
   Pairs y;
-  if constexpr (sizeof(T) == 4) {
-    const float* f = reinterpret_cast<const float*>(r.w);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      y.u[i] = near ? make_float2(f[4 * i], f[4 * i + 2]) : make_float2(f[2 * i], f[2 * i + 1]);
-      y.v[i] = near ? make_float2(f[4 * i + 1], f[4 * i + 3])
-                    : make_float2(f[8 + 2 * i], f[9 + 2 * i]);
-    }
-  } else {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const unsigned p = near ? __byte_perm(w[2 * i], w[2 * i + 1], 0x5410) : w[i];
-      const unsigned q = near ? __byte_perm(w[2 * i], w[2 * i + 1], 0x7632) : w[4 + i];
-      y.u[i] = two_of(p, T());
-      y.v[i] = two_of(q, T());
-    }
+  for (int i = 0; i < 4; ++i) {
+    y.u[i] = NEAR ? make_float2(f[4 * i], f[4 * i + 2]) : make_float2(f[2 * i], f[2 * i + 1]);
+    y.v[i] = NEAR ? make_float2(f[4 * i + 1], f[4 * i + 3]) : make_float2(f[8 + 2 * i], f[9 + 2 * i]);
   }
   return y;
 }
 
-__device__ __forceinline__ unsigned word_of(float2 x, __nv_bfloat16) {
-  const __nv_bfloat162 h = __floats2bfloat162_rn(x.x, x.y);
+__device__ __forceinline__ unsigned word_of(float x, float y, __nv_bfloat16) {
+  const __nv_bfloat162 h = __floats2bfloat162_rn(x, y);
   return *reinterpret_cast<const unsigned*>(&h);
 }
-__device__ __forceinline__ unsigned word_of(float2 x, __half) {
-  const __half2 h = __floats2half2_rn(x.x, x.y);
+__device__ __forceinline__ unsigned word_of(float x, float y, __half) {
+  const __half2 h = __floats2half2_rn(x, y);
   return *reinterpret_cast<const unsigned*>(&h);
 }
 
-// Rounded once, to type T.
-template <class T>
-__device__ __forceinline__ void store_pairs_as(T* p, const Pairs& y, const Place& at, bool vec) {
+__device__ __forceinline__ void store32(void* p, const unsigned* w) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(w[0]),
+               "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+               : "memory");
+}
+
+// Rounded once, to type T; vec: bytes on whose boundaries the pieces lie, 0, 16 or
+// 32 (with 32, stores fill whole sectors).
+template <bool NEAR, class T>
+__device__ __forceinline__ void store_pairs_as(T* p, const Pairs& y, const Place& at, int vec) {
   RawPairs<T> r;
   unsigned* w = reinterpret_cast<unsigned*>(r.w);
+  float f[16];  // in the order of memory
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
+    f[NEAR ? 4 * i : 2 * i] = y.u[i].x;
+    f[NEAR ? 4 * i + 2 : 2 * i + 1] = y.u[i].y;
+    f[NEAR ? 4 * i + 1 : 8 + 2 * i] = y.v[i].x;
+    f[NEAR ? 4 * i + 3 : 9 + 2 * i] = y.v[i].y;
+  }
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
     if constexpr (sizeof(T) == 4) {
-      float* f = reinterpret_cast<float*>(r.w);
-      f[2 * i] = at.near ? (i & 1 ? y.u[i / 2].y : y.u[i / 2].x) : y.u[i].x;
-      f[2 * i + 1] = at.near ? (i & 1 ? y.v[i / 2].y : y.v[i / 2].x) : y.u[i].y;
-      f[8 + 2 * i] = at.near ? (i & 1 ? y.u[2 + i / 2].y : y.u[2 + i / 2].x) : y.v[i].x;
-      f[9 + 2 * i] = at.near ? (i & 1 ? y.v[2 + i / 2].y : y.v[2 + i / 2].x) : y.v[i].y;
+      w[2 * i] = __float_as_uint(f[2 * i]);
+      w[2 * i + 1] = __float_as_uint(f[2 * i + 1]);
     } else {
-      const unsigned u = word_of(y.u[i], T()), v = word_of(y.v[i], T());
-      if (at.near) {
-        w[2 * i] = __byte_perm(u, v, 0x5410);
-        w[2 * i + 1] = __byte_perm(u, v, 0x7632);
-      } else {
-        w[i] = u;
-        w[4 + i] = v;
-      }
+      w[i] = word_of(f[2 * i], f[2 * i + 1], T());
     }
   }
   constexpr int H = static_cast<int>(sizeof(T)) / 2;
-  if (vec) {
+  if (vec == 32 && sizeof(T) == 4) {
+    store32(p + at.a, w);
+    store32(p + at.b, w + 8);
+  } else if (vec == 32 && NEAR) {
+    store32(p + at.a, w);
+  } else if (vec) {
 #pragma unroll
     for (int i = 0; i < H; ++i) {
       reinterpret_cast<uint4*>(p + at.a)[i] = r.w[i];
@@ -173,38 +237,30 @@ __device__ __forceinline__ void store_pairs_as(T* p, const Pairs& y, const Place
     }
   }
 }
-__device__ __forceinline__ void store_pairs(void* out, int dtype, long long at, const Pairs& y,
-                                            const Place& p, bool vec) {
+template <bool NEAR>
+__device__ __forceinline__ void store_pairs(void* out, int dtype, const Pairs& y, const Place& p,
+                                            int vec) {
   if (dtype == SV_BF16)
-    store_pairs_as(static_cast<__nv_bfloat16*>(out) + at, y, p, vec);
+    store_pairs_as<NEAR>(static_cast<__nv_bfloat16*>(out), y, p, vec);
   else if (dtype == SV_FP16)
-    store_pairs_as(static_cast<__half*>(out) + at, y, p, vec);
+    store_pairs_as<NEAR>(static_cast<__half*>(out), y, p, vec);
   else
-    store_pairs_as(static_cast<float*>(out) + at, y, p, vec);
+    store_pairs_as<NEAR>(static_cast<float*>(out), y, p, vec);
 }
 
 // The norm's weights of the lane's pairs.
+template <bool NEAR, class T>
+__device__ __forceinline__ Pairs weights_as(const T* w, const Place& at) {
+  RawPairs<T> r;
+  load_pairs(r, w, at, (reinterpret_cast<uintptr_t>(w) & 15) == 0);
+  return pairs_of<NEAR>(r);
+}
+template <bool NEAR>
 __device__ __forceinline__ Pairs weights_of(const HeadNorm& n, const Place& at) {
-  Pairs w;
-  if (n.weight == nullptr) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) w.u[i] = w.v[i] = x2_of(1.f);
-    return w;
-  }
-  const bool vec = (reinterpret_cast<uintptr_t>(n.weight) & 15) == 0;
-  if (n.weight_dtype == SV_BF16) {
-    RawPairs<__nv_bfloat16> r;
-    load_pairs(r, static_cast<const __nv_bfloat16*>(n.weight), at, vec);
-    return pairs_of(r, at.near);
-  }
-  if (n.weight_dtype == SV_FP16) {
-    RawPairs<__half> r;
-    load_pairs(r, static_cast<const __half*>(n.weight), at, vec);
-    return pairs_of(r, at.near);
-  }
-  RawPairs<float> r;
-  load_pairs(r, static_cast<const float*>(n.weight), at, vec);
-  return pairs_of(r, at.near);
+  if (n.weight_dtype == SV_BF16)
+    return weights_as<NEAR>(static_cast<const __nv_bfloat16*>(n.weight), at);
+  if (n.weight_dtype == SV_FP16) return weights_as<NEAR>(static_cast<const __half*>(n.weight), at);
+  return weights_as<NEAR>(static_cast<const float*>(n.weight), at);
 }
 
 // Cosine and sine of turns / 2^32 of a turn, for two at once.  The nearest
@@ -234,26 +290,15 @@ __device__ __forceinline__ void cos_sin(unsigned t0, unsigned t1, float2& c, flo
                   __uint_as_float(__float_as_uint(s1) ^ (q1 << 30 & 0x80000000u)));
 }
 
-// The frequencies of the lane's pairs, and their cosines and sines (with the
-// rope's scale) at a position.
-struct Freq {
-  ulonglong2 f[4];
-};
-__device__ __forceinline__ Freq freq_of(const Rope& r, int j, const Place& at) {
-  Freq w;
-#pragma unroll
-  for (int i = 0; i < 4; ++i)
-    w.f[i] = at.on ? __ldg(reinterpret_cast<const ulonglong2*>(r.freq + 8 * j) + i)
-                   : make_ulonglong2(0, 0);
-  return w;
-}
-__device__ __forceinline__ void turn_at(const Freq& w, const Rope& r, long long pos, float2 (&c)[4],
+// Cosines and sines of the lane's pairs, times the rope's scale, at a position.
+__device__ __forceinline__ void turn_at(const Rope& r, int j, long long pos, float2 (&c)[4],
                                         float2 (&s)[4]) {
   const unsigned long long p = static_cast<unsigned long long>(pos);
+  const ulonglong2* f = reinterpret_cast<const ulonglong2*>(r.freq + 8 * j);
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    cos_sin(static_cast<unsigned>(p * w.f[i].x >> 32), static_cast<unsigned>(p * w.f[i].y >> 32),
-            c[i], s[i]);
+    const ulonglong2 w = __ldg(f + i);
+    cos_sin(static_cast<unsigned>(p * w.x >> 32), static_cast<unsigned>(p * w.y >> 32), c[i], s[i]);
     c[i] = x2_mul(c[i], x2_of(r.scale));
     s[i] = x2_mul(s[i], x2_of(r.scale));
   }
@@ -266,7 +311,7 @@ __device__ __forceinline__ void scale_pairs(Pairs& y, float f) {
     y.v[i] = x2_mul(y.v[i], x2_of(f));
   }
 }
-__device__ __forceinline__ float square_sum(const Pairs& y, int lanes) {
+__device__ __forceinline__ float square_sum(const Pairs& y, int lane_shift) {
   float2 a = x2_mul(y.u[0], y.u[0]), b = x2_mul(y.v[0], y.v[0]);
 #pragma unroll
   for (int i = 1; i < 4; ++i) {
@@ -275,19 +320,22 @@ __device__ __forceinline__ float square_sum(const Pairs& y, int lanes) {
   }
   a = x2_add(a, b);
   float ss = a.x + a.y;
-  for (int o = 1; o < lanes; o <<= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+#pragma unroll
+  for (int k = 0; k < 4; ++k)
+    if (k < lane_shift) ss += __shfl_xor_sync(0xffffffffu, ss, 1 << k);
   return ss;
 }
-// What a head over `lanes` lanes (a power of two; whole warps call this; lanes
-// without channels hold zeros) is to be multiplied by.  Where the squares pass the
+// What a head over 2^lane_shift lanes (whole warps call this; lanes without
+// channels hold zeros) is to be multiplied by.  Where the squares pass the
 // range of fp32 they are taken again of values 2^-70 as large, which the head
 // then is; eps is nothing beside them.
-__device__ __forceinline__ float norm_of(Pairs& y, float eps, float inv_d, int lanes) {
-  float ss = square_sum(y, lanes);
+__device__ __forceinline__ float norm_of(Pairs& y, float eps, float inv_d,
+                                         int lane_shift) {
+  float ss = square_sum(y, lane_shift);
   if (__builtin_expect(__any_sync(0xffffffffu, !(ss < kPosInf)), 0)) {
     const bool large = !(ss < kPosInf);
     if (large) scale_pairs(y, 0x1p-70f);
-    const float again = square_sum(y, lanes);
+    const float again = square_sum(y, lane_shift);
     if (large) {
       ss = again;
       eps = 0.f;
@@ -305,41 +353,46 @@ __device__ __forceinline__ long long position_of(const int* start, const int* of
 // Norm and rotation of one kind of heads of request b, by the threads of
 // `h.blocks` blocks: a thread takes one token, one lane's channels and h.per
 // heads, for which sines, cosines and weights are the same.
-template <class T>
+template <class T, bool NEAR, class Feed>
 __device__ __forceinline__ void rotate_heads(const Heads& h, const Rope& rope, int b, int n, int T_,
                                              const int* start, const int* offset, int D,
-                                             int lane_shift, int thread) {
+                                             int lane_shift, int thread, Feed& feed) {
   // (at most 2^16 tokens of 16 lanes, 256 heads and a block's rounding: 32 bits)
   const int per_chunk = T_ << lane_shift, lanes = 1 << lane_shift;
   const int chunk = thread / per_chunk, rest = thread - chunk * per_chunk;
   const int t = rest >> lane_shift, j = rest & (lanes - 1);
   const int h0 = chunk * h.per;
   const int heads = 16 * j < D && h0 < h.heads ? min(h.per, h.heads - h0) : 0;
-  const int live = t < n ? heads : 0;
-  const Place at = place_of(rope, j);
+  const int all = __reduce_max_sync(0xffffffffu, heads);  // of the warp
+  const bool live = t < n && heads > 0;
+  const Place at = place_of<NEAR>(rope, j);
   const T* x = static_cast<const T*>(h.x) + b * h.batch + t * h.token + h0 * h.head;
-  RawPairs<T> next = {};
-  if (live > 0) load_pairs(next, x, at, h.x_vec);
+  const T* ask = x;
+#pragma unroll
+  for (int i = 0; i < Feed::kStages - 1; ++i, ask += h.head) {
+    if (live && i < heads) feed.template ask<NEAR>(i, 0, ask, at, h.x_vec);
+    Feed::commit();
+  }
 
   // u' = u a - v d, v' = v b + u c with a = w_u cos, b = w_v cos, c = w_u sin, d = w_v sin
   Pairs cs, sn;  // (a, b), (c, -d)
   const bool norm = h.norm.eps > 0.f;
-  if (live > 0) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    cs.u[i] = cs.v[i] = x2_of(1.f);
+    sn.u[i] = sn.v[i] = x2_of(0.f);
+  }
+  if (live) {
     if (at.on) {
-      float2 c[4], s[4];
-      turn_at(freq_of(rope, j, at), rope, position_of(start, offset, T_, b, t), c, s);
+      turn_at(rope, j, position_of(start, offset, T_, b, t), cs.u, sn.u);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        cs.u[i] = cs.v[i] = c[i];
-        sn.u[i] = s[i];
-        sn.v[i] = make_float2(-s[i].x, -s[i].y);
+        cs.v[i] = cs.u[i];
+        sn.v[i] = make_float2(-sn.u[i].x, -sn.u[i].y);
       }
-    } else {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) cs.u[i] = cs.v[i] = x2_of(1.f);
     }
     if (norm && h.norm.weight != nullptr) {
-      const Pairs w = weights_of(h.norm, at);
+      const Pairs w = weights_of<NEAR>(h.norm, at);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         cs.u[i] = x2_mul(cs.u[i], w.u[i]);
@@ -349,15 +402,24 @@ __device__ __forceinline__ void rotate_heads(const Heads& h, const Rope& rope, i
       }
     }
   }
-  const long long out = b * h.out_batch + t * h.out_token + h0 * h.out_head;
+  const int es = h.out_dtype == SV_FP32 ? 4 : 2;
+  char* out = static_cast<char*>(h.out) + (b * h.out_batch + t * h.out_token + h0 * h.out_head) * es;
+  const long long step = h.out_head * es;
   const float inv_d = 1.f / static_cast<float>(D);
 #pragma unroll 1
-  for (int i = 0; i < h.per; ++i) {  // (the same for all threads)
-    Pairs y = pairs_of(next, at.near);
-    if (i + 1 < live) load_pairs(next, x + (i + 1) * h.head, at, h.x_vec);
+  for (int i = 0; i < all; ++i) {
+    Feed::wait();
+    RawPairs<T> raw = {};
+    if (live && i < heads) feed.take(raw, i, 0, x, at, h.x_vec);
+    x += h.head;
+    if (live && i + Feed::kStages - 1 < heads)
+      feed.template ask<NEAR>(i + Feed::kStages - 1, 0, ask, at, h.x_vec);
+    ask += h.head;
+    Feed::commit();
+    Pairs y = pairs_of<NEAR>(raw);
     float f = 1.f;
-    if (norm) f = norm_of(y, h.norm.eps, inv_d, lanes);
-    if (i < live) {
+    if (norm) f = norm_of(y, h.norm.eps, inv_d, lane_shift);
+    if (live) {
       if (at.on) {
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
@@ -373,11 +435,9 @@ __device__ __forceinline__ void rotate_heads(const Heads& h, const Rope& rope, i
         }
       }
       if (norm) scale_pairs(y, f);
-    } else {  // behind the request's last token
-#pragma unroll
-      for (int k = 0; k < 4; ++k) y.u[k] = y.v[k] = x2_of(0.f);
-    }
-    if (i < heads) store_pairs(h.out, h.out_dtype, out + i * h.out_head, y, at, h.out_vec);
+    }  // (zeros behind the request's last token)
+    if (i < heads) store_pairs<NEAR>(out, h.out_dtype, y, at, h.out_vec);
+    out += step;
   }
 }
 
@@ -391,8 +451,9 @@ struct RotateProblem {
 
 constexpr int kRotateThreads = 256;
 
-template <class T>
+template <class T, bool NEAR>
 __global__ void __launch_bounds__(kRotateThreads, 3) rotate_kernel(const RotateProblem a) {
+  __shared__ Ahead<T, kRotateThreads, 1> feed;
   grid_dependency_wait();
   const int b = static_cast<int>(blockIdx.y);
   int block = static_cast<int>(blockIdx.x);
@@ -403,8 +464,8 @@ __global__ void __launch_bounds__(kRotateThreads, 3) rotate_kernel(const RotateP
   }
   const bool keys = block >= a.q.blocks;
   if (keys) block -= a.q.blocks;
-  rotate_heads<T>(keys ? a.k : a.q, a.rope, b, n, a.T, a.start, a.offset, a.D, a.lane_shift,
-                  block * kRotateThreads + static_cast<int>(threadIdx.x));
+  rotate_heads<T, NEAR>(keys ? a.k : a.q, a.rope, b, n, a.T, a.start, a.offset, a.D, a.lane_shift,
+                  block * kRotateThreads + static_cast<int>(threadIdx.x), feed);
 }
 
 // ------------------------------------------------------------------ append
@@ -412,7 +473,9 @@ __global__ void __launch_bounds__(kRotateThreads, 3) rotate_kernel(const RotateP
 struct KvAppendProblem {
   KvCache c;
   int B, T, pages;  // pages a request can touch
-  int group;        // threads of one (page, head, side): 32 .. all
+  int group;        // threads of one (page, side): 32 .. all
+  int per;          // heads a group takes, one after the other
+  int chunks;       // groups of a (page, side): Hkv / per
   int blocks;       // blocks of a request that write the cache; then q.blocks
   Heads q;
   const void *k_new, *v_new;
@@ -425,180 +488,226 @@ struct KvAppendProblem {
 };
 
 // As kv_write_kernel: a thread group for each (request, page of the round,
-// side, head), which holds the page's new values in registers, CH chunks of
-// sixteen a thread, from the load to the codes.
-template <class T, int THREADS, int CH>
-__global__ void __launch_bounds__(THREADS, THREADS == 256 ? 3 : 1)
-    kv_append_kernel(const KvAppendProblem a) {
-  __shared__ float red[THREADS / 32];
-  grid_dependency_wait();
+// side, heads), which holds a head's new values of the page in registers, CH
+// chunks of sixteen a thread, until their codes are written.  Sines and cosines
+// serve all its heads.
+template <class T, bool NEAR, int THREADS, int CH, class Feed>
+__device__ __forceinline__ void append_pages(const KvAppendProblem& a, int b, int len, int n,
+                                             bool ok, float (*red)[THREADS / 32], Feed& feed) {
   const int tid = static_cast<int>(threadIdx.x);
   const int Hkv = a.c.Hkv, D = a.c.D, P = a.c.page_size;
+  const int pshift = D == 64 ? 2 : 3, parts = 1 << pshift;  // lanes of a head
+  const int GT = a.group, gl = tid & (GT - 1);
+  const int task = static_cast<int>(blockIdx.x) * (THREADS / GT) + tid / GT;
+  const int is = task / a.chunks, h0 = (task - is * a.chunks) * a.per;
+  const int side = is & 1, i = is >> 1;
+  // The page's new tokens.  (Their values are asked for before the page's id is
+  // there: a trip to memory less.)
+  int kept = 0, first = 0, count = 0, slot = 0, row0 = 0;
+  if (i < a.pages && ok && n > 0) {
+    slot = (len >> a.c.page_shift) + i;
+    const int from = max(len, slot << a.c.page_shift);
+    const long long to =
+        min(static_cast<long long>(len) + n, (static_cast<long long>(slot) + 1) << a.c.page_shift);
+    if (from < to) {
+      kept = i == 0 ? len & (P - 1) : 0;
+      first = from - len;
+      count = static_cast<int>(to - from);
+      row0 = from & (P - 1);
+      if (!SV_CHECK(slot >= 0 && slot < a.c.slots && row0 + count <= P &&
+                        first + count <= a.T && first >= 0 && count * (D / 16) <= GT * CH,
+                    a.err))
+        count = 0;
+    }
+  }
+  int heads = count > 0 ? min(a.per, Hkv - h0) : 0;
+  const int j = gl & (parts - 1);  // the same for all of a thread's chunks
+  const int chunks = count << pshift;
+  Place at = place_of<NEAR>(a.rope, j);
+  if (side) at = Place{16 * j, 16 * j + 8, false};  // values stay where they are
+  const long long head = side ? a.v_head : a.k_head;
+  const bool vec = side ? a.v_vec : a.k_vec;
+  const T* src[CH];
+#pragma unroll
+  for (int k = 0; k < CH; ++k) {
+    const int c = gl + k * GT;
+    src[k] = static_cast<const T*>(side ? a.v_new : a.k_new) +
+             (side ? b * a.v_batch + h0 * a.v_head + (first + (c >> pshift)) * a.v_token
+                   : b * a.k_batch + h0 * a.k_head + (first + (c >> pshift)) * a.k_token);
+  }
+  const int stages = Feed::kStages - 1;  // heads asked for ahead
+#pragma unroll
+  for (int i = 0; i < Feed::kStages - 1; ++i) {
+#pragma unroll
+    for (int k = 0; k < CH; ++k)
+      if (i < heads && gl + k * GT < chunks) feed.template ask<NEAR>(i, k, src[k] + i * head, at, vec);
+    Feed::commit();
+  }
+  const bool reports = h0 == 0 && side == 0 && gl == 0;
+  if (!ok && i == 0 && reports) record_error(a.err, SV_DERR_ARG);
+  int page = 0;
+  if (count > 0) {
+    page = a.c.page_table[static_cast<long long>(b) * a.c.slots + slot];
+    if (page < 0 || page >= a.c.num_pages) {
+      if (reports) record_error(a.err, SV_DERR_PAGE);
+      page = heads = 0;
+    }
+  }
+  const bool norm = side == 0 && a.k_norm.eps > 0.f;
+  const bool weighted = norm && a.k_norm.weight != nullptr && gl < chunks;
+  Pairs w;
+  if (weighted) w = weights_of<NEAR>(a.k_norm, at);
+  float2 cs[CH][4], sn[CH][4];
+  if (side == 0 && at.on)
+#pragma unroll
+    for (int k = 0; k < CH; ++k) {
+      const int c = gl + k * GT;
+      if (c < chunks)
+        turn_at(a.rope, j, position_of(a.kv_len, a.offset, a.T, b, first + (c >> pshift)), cs[k],
+                sn[k]);
+    }
+  unsigned char* dst = (side ? a.c.v : a.c.k) + page * a.c.page_stride + h0 * a.c.head_stride;
+  float* scale = (side ? a.c.v_scale : a.c.k_scale) + static_cast<long long>(page) * Hkv + h0;
+
+#pragma unroll 1
+  for (int hh = 0; hh < a.per; ++hh) {  // (the same for all threads of the block)
+    const bool here = hh < heads;
+    Pairs y[CH];
+    Feed::wait();
+#pragma unroll
+    for (int k = 0; k < CH; ++k) {
+      RawPairs<T> raw = {};
+      if (here && gl + k * GT < chunks) feed.take(raw, hh, k, src[k], at, vec);
+      if (hh + stages < heads && gl + k * GT < chunks)
+        feed.template ask<NEAR>(hh + stages, k, src[k] + stages * head, at, vec);
+      src[k] += head;
+      y[k] = pairs_of<NEAR>(raw);
+    }
+    Feed::commit();
+    float stored = 0x1p-48f;
+    if (here && kept > 0) stored = *scale;
+    if (side == 0) {  // (a warp has one side)
+#pragma unroll
+      for (int k = 0; k < CH; ++k) {
+        if (norm) {
+          const float f = norm_of(y[k], a.k_norm.eps, 1.f / static_cast<float>(D), pshift);
+          scale_pairs(y[k], f);
+          if (weighted)
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+              y[k].u[q] = x2_mul(y[k].u[q], w.u[q]);
+              y[k].v[q] = x2_mul(y[k].v[q], w.v[q]);
+            }
+        }
+        if (at.on && gl + k * GT < chunks) {
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            const float2 u = y[k].u[q], v = y[k].v[q];
+            y[k].u[q] = x2_fma(u, cs[k][q], x2_mul(v, make_float2(-sn[k][q].x, -sn[k][q].y)));
+            y[k].v[q] = x2_fma(v, cs[k][q], x2_mul(u, sn[k][q]));
+          }
+        }
+      }
+    }
+    unsigned bits = 0;  // magnitudes order as their bits do
+#pragma unroll
+    for (int k = 0; k < CH; ++k)
+      if (here && gl + k * GT < chunks)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          bits = max(max(bits, __float_as_uint(y[k].u[q].x) & 0x7fffffffu),
+                     __float_as_uint(y[k].u[q].y) & 0x7fffffffu);
+          bits = max(max(bits, __float_as_uint(y[k].v[q].x) & 0x7fffffffu),
+                     __float_as_uint(y[k].v[q].y) & 0x7fffffffu);
+        }
+    if (__builtin_expect(bits >= 0x7f800000u, 0)) {
+      // the finite ones only
+      record_error(a.err, SV_DERR_NONFINITE);
+      bits = 0;
+      auto finite = [&](float x) {
+        const unsigned m = __float_as_uint(x) & 0x7fffffffu;
+        bits = max(bits, m < 0x7f800000u ? m : 0u);
+      };
+#pragma unroll
+      for (int k = 0; k < CH; ++k)
+        if (gl + k * GT < chunks)
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            finite(y[k].u[q].x);
+            finite(y[k].u[q].y);
+            finite(y[k].v[q].x);
+            finite(y[k].v[q].y);
+          }
+    }
+    float amax = __uint_as_float(__reduce_max_sync(0xffffffffu, bits));
+    // (two rows of `red` in turns: a row's readers are past the barrier of the
+    // other before it is written again)
+    if ((tid & 31) == 0) red[hh & 1][tid >> 5] = amax;
+    __syncthreads();  // every thread has read the old scale, too
+    const int w0 = (tid / GT) * (GT / 32);
+    for (int k = 0; k < GT / 32; ++k) amax = fmaxf(amax, red[hh & 1][w0 + k]);
+    if (here) {
+      const int before = scale_exp(stored), e = max(needed_exp(amax), before);
+      const float2 inv = x2_of(pow2f(-e));
+#pragma unroll
+      for (int k = 0; k < CH; ++k) {
+        const int c = gl + k * GT;
+        if (c < chunks) {
+          unsigned char* row = dst + (row0 + (c >> pshift)) * D;
+          unsigned o[4];
+#pragma unroll
+          for (int q = 0; q < 2; ++q) {
+            const float2 u0 = x2_mul(y[k].u[2 * q], inv), u1 = x2_mul(y[k].u[2 * q + 1], inv);
+            const float2 v0 = x2_mul(y[k].v[2 * q], inv), v1 = x2_mul(y[k].v[2 * q + 1], inv);
+            if (NEAR) {
+              o[2 * q] = e4m3x4(u0.x, v0.x, u0.y, v0.y);
+              o[2 * q + 1] = e4m3x4(u1.x, v1.x, u1.y, v1.y);
+            } else {
+              o[q] = e4m3x4(u0.x, u0.y, u1.x, u1.y);
+              o[2 + q] = e4m3x4(v0.x, v0.y, v1.x, v1.y);
+            }
+          }
+          *reinterpret_cast<uint2*>(row + at.a) = make_uint2(o[0], o[1]);
+          *reinterpret_cast<uint2*>(row + at.b) = make_uint2(o[2], o[3]);
+        }
+      }
+      if (kept > 0 && e > before) rescale_kept(dst, kept << pshift, gl, GT, pow2f(before - e));
+      if (gl == 0) {
+        if (kept == 0 || e > before) *scale = pow2f(e);
+        if (stored != scale_value(stored)) record_error(a.err, SV_DERR_ARG);
+      }
+    }
+    dst += a.c.head_stride;
+    ++scale;
+  }
+}
+
+template <class T, int THREADS, int CH>
+union AppendFeed {
+  Ahead<T, THREADS, 1> q;
+  Ahead<T, THREADS, CH> kv;
+};
+
+template <class T, bool NEAR, int THREADS, int CH>
+__global__ void __launch_bounds__(THREADS, THREADS == 256 ? (CH == 1 ? 3 : 2) : 1)
+    kv_append_kernel(const KvAppendProblem a) {
+  __shared__ float red[2][THREADS / 32];
+  extern __shared__ __align__(16) unsigned char append_feed[];
+  AppendFeed<T, THREADS, CH>& feed = *reinterpret_cast<AppendFeed<T, THREADS, CH>*>(append_feed);
+  grid_dependency_wait();
   const int b = static_cast<int>(blockIdx.y);
   const int len = a.kv_len[b];
   const int n = a.num_new ? a.num_new[b] : a.T;
   const bool ok = len >= 0 && n >= 0 && n <= a.T &&
-                  (n == 0 ||
-                   static_cast<long long>(len) + n <= static_cast<long long>(a.c.slots) * P);
-  const int pshift = D == 64 ? 2 : 3, parts = 1 << pshift;  // lanes of a head
-
-  if (static_cast<int>(blockIdx.x) >= a.blocks) {
-    rotate_heads<T>(a.q, a.rope, b, ok ? n : 0, a.T, a.kv_len, a.offset, D, pshift,
-                    (static_cast<int>(blockIdx.x) - a.blocks) * THREADS + tid);
-    return;
-  }
-
-  const int GT = a.group, gl = tid & (GT - 1);
-  const int task = static_cast<int>(blockIdx.x) * (THREADS / GT) + tid / GT;
-  const int is = task / Hkv, h = task - is * Hkv;
-  const int side = is & 1, i = is >> 1;
-  int kept = 0, first = 0, count = 0, page = 0, row0 = 0;
-  bool active = false;
-  if (i < a.pages) {
-    const bool reports = h == 0 && side == 0 && gl == 0;
-    if (!ok) {
-      if (i == 0 && reports) record_error(a.err, SV_DERR_ARG);
-    } else if (n > 0) {
-      const int slot = (len >> a.c.page_shift) + i;
-      const int from = max(len, slot << a.c.page_shift);
-      const long long to =
-          min(static_cast<long long>(len) + n, (static_cast<long long>(slot) + 1) << a.c.page_shift);
-      if (from < to && SV_CHECK(slot >= 0 && slot < a.c.slots, a.err)) {
-        page = a.c.page_table[static_cast<long long>(b) * a.c.slots + slot];
-        if (page < 0 || page >= a.c.num_pages) {
-          if (reports) record_error(a.err, SV_DERR_PAGE);
-        } else {
-          kept = i == 0 ? len & (P - 1) : 0;
-          first = from - len;
-          count = static_cast<int>(to - from);
-          row0 = from & (P - 1);
-          active = SV_CHECK(row0 + count <= P && first + count <= a.T && first >= 0 &&
-                                count * (D / 16) <= GT * CH,
-                            a.err);
-        }
-      }
-    }
-  }
-
-  const int j = gl & (parts - 1);  // the same for all of a thread's chunks
-  const int chunks = active ? count << pshift : 0;
-  Place at = place_of(a.rope, j);
-  if (side) at = Place{16 * j, 16 * j + 8, false, false};  // values stay where they are
-  Pairs y[CH];
-  {
-    const T* src = static_cast<const T*>(side ? a.v_new : a.k_new) +
-                   (side ? b * a.v_batch + h * a.v_head : b * a.k_batch + h * a.k_head);
-    const long long tstride = side ? a.v_token : a.k_token;
-    const bool vec = side ? a.v_vec : a.k_vec;
-    RawPairs<T> raw[CH] = {};
-#pragma unroll
-    for (int k = 0; k < CH; ++k) {
-      const int c = gl + k * GT;
-      if (c < chunks) load_pairs(raw[k], src + (first + (c >> pshift)) * tstride, at, vec);
-    }
-#pragma unroll
-    for (int k = 0; k < CH; ++k) y[k] = pairs_of(raw[k], at.near);
-  }
-  if (side == 0) {  // (a warp has one side)
-    Freq freq = {};
-    if (gl < chunks) freq = freq_of(a.rope, j, at);
-    const bool norm = a.k_norm.eps > 0.f;
-#pragma unroll
-    for (int k = 0; k < CH; ++k) {
-      const int c = gl + k * GT;
-      const bool here = c < chunks;
-      if (norm) {
-        const float f = norm_of(y[k], a.k_norm.eps, 1.f / static_cast<float>(D), parts);
-        scale_pairs(y[k], f);
-        if (here && a.k_norm.weight != nullptr) {
-          const Pairs w = weights_of(a.k_norm, at);
-#pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            y[k].u[q] = x2_mul(y[k].u[q], w.u[q]);
-            y[k].v[q] = x2_mul(y[k].v[q], w.v[q]);
-          }
-        }
-      }
-      if (here && at.on) {
-        float2 cs[4], sn[4];
-        turn_at(freq, a.rope, position_of(a.kv_len, a.offset, a.T, b, first + (c >> pshift)), cs,
-                sn);
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          const float2 u = y[k].u[q], v = y[k].v[q];
-          y[k].u[q] = x2_fma(u, cs[q], x2_mul(v, make_float2(-sn[q].x, -sn[q].y)));
-          y[k].v[q] = x2_fma(v, cs[q], x2_mul(u, sn[q]));
-        }
-      }
-    }
-  }
-  float amax = 0.f;
-  {
-    unsigned bits = 0;  // magnitudes order as their bits do (chunks that are none hold zeros)
-#pragma unroll
-    for (int k = 0; k < CH; ++k)
-#pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        bits = max(max(bits, __float_as_uint(y[k].u[q].x) & 0x7fffffffu),
-                   __float_as_uint(y[k].u[q].y) & 0x7fffffffu);
-        bits = max(max(bits, __float_as_uint(y[k].v[q].x) & 0x7fffffffu),
-                   __float_as_uint(y[k].v[q].y) & 0x7fffffffu);
-      }
-    amax = __uint_as_float(bits);
-  }
-  if (__builtin_expect(!(amax < kPosInf), 0)) {
-    // the finite ones only
-    record_error(a.err, SV_DERR_NONFINITE);
-    amax = 0.f;
-    auto finite = [&](float x) {
-      const float m = fabsf(x);
-      amax = fmaxf(amax, m < kPosInf ? m : 0.f);
-    };
-#pragma unroll
-    for (int k = 0; k < CH; ++k)
-#pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        finite(y[k].u[q].x);
-        finite(y[k].u[q].y);
-        finite(y[k].v[q].x);
-        finite(y[k].v[q].y);
-      }
-  }
-  amax = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(amax)));
-  float* scale = (side ? a.c.v_scale : a.c.k_scale) + static_cast<long long>(page) * Hkv + h;
-  float stored = 0x1p-48f;
-  if (active && kept > 0) stored = *scale;
-  if ((tid & 31) == 0) red[tid >> 5] = amax;
-  __syncthreads();  // every thread has read the old scale
-  const int w0 = (tid / GT) * (GT / 32);
-  for (int w = 0; w < GT / 32; ++w) amax = fmaxf(amax, red[w0 + w]);
-  if (!active) return;
-  const int before = scale_exp(stored), e = max(needed_exp(amax), before);
-  const float inv = pow2f(-e);
-  unsigned char* dst = (side ? a.c.v : a.c.k) + page * a.c.page_stride + h * a.c.head_stride;
-#pragma unroll
-  for (int k = 0; k < CH; ++k) {
-    const int c = gl + k * GT;
-    if (c < chunks) {
-      unsigned char* row = dst + (row0 + (c >> pshift)) * D;
-      unsigned w[4];
-#pragma unroll
-      for (int q = 0; q < 2; ++q) {
-        const float2 u0 = x2_mul(y[k].u[2 * q], x2_of(inv)), u1 = x2_mul(y[k].u[2 * q + 1], x2_of(inv));
-        const float2 v0 = x2_mul(y[k].v[2 * q], x2_of(inv)), v1 = x2_mul(y[k].v[2 * q + 1], x2_of(inv));
-        const unsigned u = e4m3x4(u0.x, u0.y, u1.x, u1.y), v = e4m3x4(v0.x, v0.y, v1.x, v1.y);
-        w[at.near ? 2 * q : q] = at.near ? __byte_perm(u, v, 0x5140) : u;
-        w[at.near ? 2 * q + 1 : 2 + q] = at.near ? __byte_perm(u, v, 0x7362) : v;
-      }
-      *reinterpret_cast<uint2*>(row + at.a) = make_uint2(w[0], w[1]);
-      *reinterpret_cast<uint2*>(row + at.b) = make_uint2(w[2], w[3]);
-    }
-  }
-  if (kept > 0 && e > before) rescale_kept(dst, kept << pshift, gl, GT, pow2f(before - e));
-  if (gl == 0) {
-    if (kept == 0 || e > before) *scale = pow2f(e);
-    if (stored != scale_value(stored)) record_error(a.err, SV_DERR_ARG);
-  }
+                  (n == 0 || static_cast<long long>(len) + n <=
+                                 static_cast<long long>(a.c.slots) * a.c.page_size);
+  if (static_cast<int>(blockIdx.x) >= a.blocks)
+    rotate_heads<T, NEAR>(a.q, a.rope, b, ok ? n : 0, a.T, a.kv_len, a.offset, a.c.D,
+                          a.c.D == 64 ? 2 : 3,
+                          (static_cast<int>(blockIdx.x) - a.blocks) * THREADS +
+                              static_cast<int>(threadIdx.x), feed.q);
+  else
+    append_pages<T, NEAR, THREADS, CH>(a, b, len, n, ok, red, feed.kv);
 }
 
 }  // namespace sv
