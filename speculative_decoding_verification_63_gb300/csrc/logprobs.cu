@@ -10,10 +10,12 @@ namespace {
 using namespace sv;
 
 template <class T, bool TOP>
-sv_status run(const LogprobProblem& p, cudaStream_t stream) {
-  const size_t map = TOP ? static_cast<size_t>(p.share) * sizeof(typename LpKey<T>::Map) : 0;
-  static_assert(4 * (sizeof(LpShared) + kLpMapBytes + 1024) <= 227 * 1024, "four CTAs an SM");
-  if (map + sizeof(LpShared) > 48 * 1024) return SV_EINVAL;  // (never: share is chosen for it)
+sv_status run(const LogprobProblem& p, size_t map, cudaStream_t stream) {
+  static_assert(kLpCtasPerSm * (sizeof(LpShared) + kLpMapBytes + 1024) <= 227 * 1024, "four CTAs an SM");
+  if (map + sizeof(LpShared) > 48 * 1024 &&
+      cudaFuncSetAttribute(logprob_kernel<T, TOP>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                           kLpMapBytes) != cudaSuccess)
+    return SV_ECUDA;
   const dim3 grid(static_cast<unsigned>(p.B) * static_cast<unsigned>(p.R) *
                   static_cast<unsigned>(p.cluster));
   return launch(logprob_kernel<T, TOP>, p, grid, kLpThreads, map, stream, p.cluster);
@@ -64,24 +66,35 @@ sv_status sv_token_logprobs(const sv_token_logprobs_args* a, void* workspace, si
   p.top_logprob = a->top_logprob;
   p.err = error_word(workspace);
   // Groups of a row that begins anywhere within 32 bytes.
-  const int64_t rows = static_cast<int64_t>(a->B) * a->R;
   const int groups = (a->V + 32 / es - 1 + kLpGroup - 1) / kLpGroup;
+  // CTAs of a row: as long as they all run at once (four an SM) and have a turn
+  // of groups each, up to four, whose barriers are still cheap; eight for a
+  // handful of rows.  (256 rows of 152064, top 20: 1 25.5 us, 2 23.0; 64 rows of
+  // 128256, top 5: 1 16.8, 2 11.9, 4 9.7, 8 10.7; 1 row: 4 10.2, 8 7.0.  448 rows:
+  // 1 25.3, 2 32; with num_rows, where half of the rows are there, 1 22.0, 2 18.9.)
+  int64_t rows = static_cast<int64_t>(a->B) * a->R;
+  if (a->num_rows != nullptr && a->R > 1) rows = rows * 5 / 8;
   p.cluster = 1;
-  while (p.cluster < kLpMaxCluster && rows * p.cluster * 2 <= 4 * dev.sms &&
+  while (p.cluster < 4 && rows * p.cluster * 2 <= kLpCtasPerSm * dev.sms &&
          groups > p.cluster * kLpThreads)
     p.cluster *= 2;
-  // a map fits its CTA
-  while (a->top > 0 && static_cast<int64_t>((groups + p.cluster - 1) / p.cluster) *
-                               (es == 2 ? 2 : 4) > kLpMapBytes)
-    p.cluster *= 2;
-  p.share = (groups + p.cluster - 1) / p.cluster;
-  // of each warp, so that there are about twice as many as asked for
+  if (p.cluster == 4 && rows * 8 <= dev.sms && groups > 4 * kLpThreads) p.cluster = 8;
+  // a map fits its CTA (whole 32s of groups)
+  auto share = [&] { return ((groups + 31) / 32 + p.cluster - 1) / p.cluster * 32; };
+  while (a->top > 0 && share() * es > kLpMapBytes) p.cluster *= 2;
+  const size_t map = a->top > 0 ? static_cast<size_t>(share()) * es : 0;
+  // Maxima of each warp that make the bound: somewhat more in all than are asked
+  // for (the likeliest tokens are often neighbours, in the hands of one warp), a
+  // power of two.
   const int warps = p.cluster * kLpWarps;
-  p.published = std::min(kLpPublished / warps, std::max(2, (2 * a->top + warps - 1) / warps));
+  p.published = 1;
+  while (p.published * warps < std::max(64, 5 * a->top / 4)) p.published *= 2;
+  p.all_shift = 0;
+  while ((1 << p.all_shift) < p.published * warps) ++p.all_shift;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   if (a->dtype == SV_BF16)
-    return a->top > 0 ? run<__nv_bfloat16, true>(p, st) : run<__nv_bfloat16, false>(p, st);
-  return a->top > 0 ? run<float, true>(p, st) : run<float, false>(p, st);
+    return a->top > 0 ? run<__nv_bfloat16, true>(p, map, st) : run<__nv_bfloat16, false>(p, map, st);
+  return a->top > 0 ? run<float, true>(p, map, st) : run<float, false>(p, map, st);
 }
 
 }  // extern "C"

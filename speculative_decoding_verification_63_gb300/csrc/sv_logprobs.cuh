@@ -19,12 +19,12 @@
 // its maximum, as an order-preserving key, in a map in shared memory.  The `top`
 // largest logits lie in the `top` groups of largest maxima (equal ones: the
 // first): each group left out is outranked by a logit of each of those.  A
-// bound below the top-th largest maximum comes from the threads' own maxima
-// (they are maxima of disjoint sets of groups), so only a few groups are looked
-// at; where too many reach it (equal maxima all over a row, as under a mask of
-// the type's lowest value), the bound is raised by bisection.  The chosen
-// groups are read again, and the logits that reach the last of their maxima are
-// ranked by counting.
+// bound at or below the top-th largest maximum comes from the threads' own
+// maxima (they are maxima of disjoint sets of groups).  The few groups that reach
+// it are read again by the threads that met them, and the logits that reach it are
+// ranked by counting.  Where too many do (equal logits all over a row, as under a
+// mask of the type's lowest value), the `top` groups are found first, by bisection
+// on the keys in the map.
 #pragma once
 
 #include "sv_cluster.cuh"
@@ -33,17 +33,19 @@
 namespace sv {
 
 constexpr int kLpThreads = 256, kLpWarps = kLpThreads / 32;
+constexpr int kLpCtasPerSm = 4;
 constexpr int kLpGroup = 16;       // logits of a group
 constexpr int kLpMaxCluster = 8;
 constexpr int kLpMapBytes = 34816; // most that a CTA's map holds
-constexpr int kLpList = 512;       // groups that are ranked by counting
+constexpr int kLpList = SV_MAX_TOPK * kLpGroup;  // items that are ranked by counting
+constexpr int kLpGroups = 512;     // groups that a CTA reads again
 constexpr int kLpPublished = 256;  // maxima that make the bound
 
 struct LogprobProblem {
   int B, N, R, M, V, top;
   int cluster;     // CTAs of a row
-  int share;       // groups of a CTA
-  int published;   // maxima of each warp that make the bound
+  int published;   // maxima of each warp that make the bound: 2^all_shift in all
+  int all_shift;
   const void* logits;
   long long batch, row;
   const int *tokens, *num_rows, *rows;
@@ -63,29 +65,30 @@ __device__ __forceinline__ unsigned warp_max_u32(unsigned v) {
   asm volatile("redux.sync.max.u32 %0, %1, 0xffffffff;" : "=r"(m) : "r"(v));
   return m;
 }
-__device__ __forceinline__ void cl_st_u32(uint32_t addr, uint32_t v) {
-  asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
-}
-__device__ __forceinline__ void cl_st_u64(uint32_t addr, uint64_t v) {
-  asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(addr), "l"(v) : "memory");
-}
-__device__ __forceinline__ uint32_t cl_atomic_add(uint32_t addr, uint32_t v) {
-  uint32_t old;
-  asm volatile("atom.relaxed.cluster.shared::cluster.add.u32 %0, [%1], %2;"
-               : "=r"(old)
-               : "r"(addr), "r"(v)
-               : "memory");
-  return old;
+// The address of `p` (in this CTA's shared memory) in the CTA `rank` of the
+// cluster; itself where that is this one.
+template <class P>
+__device__ __forceinline__ P* cl_at(P* p, int rank) {
+  P* q;
+  asm("mapa.u64 %0, %1, %2;" : "=l"(q) : "l"(p), "r"(rank));
+  return q;
 }
 
 // Keys that order as the logits do (-0 as +0), and the logit of a key.  No key
-// is 0; a key above LpKey::kNone is that of a logit above -inf.
+// is 0; a key above LpKey::kNone is that of a logit above -inf.  Maps hold the
+// logits' own bits, which cost the stream less.
 template <class T>
 struct LpKey;
 template <>
 struct LpKey<__nv_bfloat16> {
   using Map = unsigned short;
   static constexpr unsigned kNone = 0x007fu;  // of -inf
+  static __device__ __forceinline__ Map map(float x) {
+    return static_cast<Map>(__float_as_uint(x) >> 16);
+  }
+  static __device__ __forceinline__ unsigned of_map(Map m) {
+    return of(__uint_as_float(static_cast<unsigned>(m) << 16));
+  }
   static __device__ __forceinline__ unsigned of(float x) {
     const unsigned u = __float_as_uint(x + 0.f) >> 16;
     return (u & 0x8000u) ? u ^ 0xffffu : u | 0x8000u;
@@ -98,6 +101,8 @@ template <>
 struct LpKey<float> {
   using Map = unsigned;
   static constexpr unsigned kNone = 0x007fffffu;
+  static __device__ __forceinline__ Map map(float x) { return __float_as_uint(x); }
+  static __device__ __forceinline__ unsigned of_map(Map m) { return of(__uint_as_float(m)); }
   static __device__ __forceinline__ unsigned of(float x) {
     const unsigned u = __float_as_uint(x + 0.f);
     return (u & 0x80000000u) ? ~u : u | 0x80000000u;
@@ -112,10 +117,15 @@ __device__ __forceinline__ unsigned long long lp_item(unsigned key, int index) {
   return static_cast<unsigned long long>(key) << 32 | ~static_cast<unsigned>(index);
 }
 
-// The cluster barrier behind code in which a warp's lanes may have parted.
-__device__ __forceinline__ void lp_sync() {
-  __syncwarp();
-  cl_sync();
+// The cluster's barrier (a block's, where that is all) behind code in which a
+// warp's lanes may have parted.
+__device__ __forceinline__ void lp_sync(int cluster) {
+  if (cluster == 1) {
+    __syncthreads();
+  } else {
+    __syncwarp();
+    cl_sync();
+  }
 }
 
 // Sixteen logits as loaded.
@@ -151,6 +161,24 @@ struct LpRow {
   }
 };
 
+// A CTA's share of a row: every `cluster`-th 32 groups, so that the likeliest
+// tokens, often neighbours, are spread over the CTAs.  Its i-th group:
+struct LpShare {
+  int cluster, rank;
+  __device__ __forceinline__ int group(int i) const {
+    return (((i >> 5) * cluster + rank) << 5) + (i & 31);
+  }
+  // the place of group g, and whose it is
+  __device__ __forceinline__ int owner(int g) const { return (g >> 5) % cluster; }
+  __device__ __forceinline__ int place(int g) const { return ((g >> 5) / cluster << 5) + (g & 31); }
+  // groups of a row of `all` that are this CTA's: whole 32s but for the row's last
+  __device__ __forceinline__ int count(int all) const {
+    const int blocks = all >> 5, rest = all & 31;
+    const int mine = blocks / cluster + (rank < blocks % cluster);
+    return (mine << 5) + (rank == blocks % cluster ? rest : 0);
+  }
+};
+
 template <class T>
 __device__ __forceinline__ float2 lp_pair(const LpRaw<T>& r, int i) {
   if constexpr (sizeof(T) == 2) return make_float2(bf16lo(r.w[i]), bf16hi(r.w[i]));
@@ -172,14 +200,33 @@ __device__ __forceinline__ float lp_max(const LpRaw<T>& r) {
   }
 }
 
-// Reference, sum and sum of weight x exponent (binary units).
+// What has been summed: the largest logit m, and relative to 2^k, k = m c rounded
+// to fp32 (a reference of its own, which takes one instruction an exponent),
+// z = sum 2^(x c - k) and a = sum 2^(x c - k) (x c - k).  Where m c is so large
+// that k could be off it by more than 2^-9 (logits in the thousands; a row of the
+// type's lowest values; temperatures near 0), the reference is m c itself and
+// exponents are (x - m) c.
 struct LpSum {
   float m, z, a;
 };
-// 2^((from - to) c) and the exponent, of a partial sum whose reference rises.
+constexpr float kLpWide = 65536.f;
+__device__ __forceinline__ bool lp_wide(float m, float c) { return !(fabsf(m * c) < kLpWide); }
+// m c less the reference.
+__device__ __forceinline__ float lp_off(float m, float c) {
+  return lp_wide(m, c) ? 0.f : fmaf(m, c, -(m * c));
+}
+// The exponent of logit x against reference m, at least -1000.
+__device__ __forceinline__ float lp_exponent(float x, float m, float c) {
+  return fmaxf(lp_wide(m, c) ? (x - m) * c : fmaf(x, c, -(m * c)), -1000.f);
+}
+// From reference `from` to `to`, in exponents.
+__device__ __forceinline__ float lp_shift(float from, float to, float c) {
+  return fmaxf((from - to) * c + (lp_off(to, c) - lp_off(from, c)), -1000.f);
+}
+// A partial sum whose reference rises.
 __device__ __forceinline__ void lp_raise(LpSum& s, float to, float c) {
   if (s.m > kNegInf) {
-    const float d = fmaxf((s.m - to) * c, -1000.f), f = fast_exp2(d);
+    const float d = lp_shift(s.m, to, c), f = fast_exp2(d);
     s.a = f * fmaf(d, s.z, s.a);
     s.z *= f;
   }
@@ -198,149 +245,170 @@ __device__ __forceinline__ LpSum lp_warp_sum(LpSum s, float c) {
   return s;
 }
 
+// Sixteen logits, NG groups of them, into z and a.  FAST: m c is not wide and,
+// for bf16, logits below -2^100 may count as -2^100: their weights are zero and
+// their exponents finite (m > -2^90, 2^-60 < c < 2^26).
+template <class T, bool FAST, int NG>
+__device__ __forceinline__ void lp_accumulate(LpSum& s, const LpRaw<T> (&raw)[NG], float c) {
+  const float2 c2 = x2_of(c), k2 = x2_of(-(s.m * c)), m2 = x2_of(-s.m);
+  float2 z = x2_of(0.f), a = x2_of(0.f);
+#pragma unroll
+  for (int u = 0; u < NG; ++u)
+#pragma unroll
+    for (int i = 0; i < kLpGroup / 2; ++i) {
+      float2 e;
+      if constexpr (FAST && sizeof(T) == 2) {
+        unsigned w = raw[u].w[i];
+        asm("max.bf16x2 %0, %1, %2;" : "=r"(w) : "r"(w), "r"(0xf180f180u));  // -2^100
+        e = x2_fma(make_float2(bf16lo(w), bf16hi(w)), c2, k2);
+      } else {
+        const float2 x = lp_pair(raw[u], i);
+        e = FAST ? x2_fma(x, c2, k2) : x2_mul(x2_add(x, m2), c2);
+        e.x = fmaxf(e.x, -1000.f);
+        e.y = fmaxf(e.y, -1000.f);
+      }
+      const float2 f = make_float2(fast_exp2(e.x), fast_exp2(e.y));
+      z = x2_add(z, f);
+      a = x2_fma(f, e, a);
+    }
+  s.z += z.x + z.y;
+  s.a += a.x + a.y;
+}
+
+// The same for references of any size: one that is not wide has exponents x c - k.
+template <class T, int NG>
+__device__ __forceinline__ void lp_slow(LpSum& s, const LpRaw<T> (&raw)[NG], float c) {
+  if (lp_wide(s.m, c)) {
+    lp_accumulate<T, false>(s, raw, c);
+    return;
+  }
+#pragma unroll
+  for (int u = 0; u < NG; ++u)
+#pragma unroll
+    for (int i = 0; i < kLpGroup / 2; ++i) {
+      const float2 x = lp_pair(raw[u], i);
+      const float e0 = lp_exponent(x.x, s.m, c), e1 = lp_exponent(x.y, s.m, c);
+      const float f0 = fast_exp2(e0), f1 = fast_exp2(e1);
+      s.z += f0 + f1;
+      s.a = fmaf(f1, e1, fmaf(f0, e0, s.a));
+    }
+}
+
+// What the first CTA of a cluster collects, and what every CTA holds.
 struct LpShared {
-  float4 part[kLpMaxCluster * kLpWarps];  // the warps' sums
-  unsigned published[kLpPublished];       // the warps' largest maxima (first CTA)
-  union {
-    unsigned long long list[kLpList];                        // key << 32 | ~group
-    unsigned long long logit[SV_MAX_TOPK * kLpGroup];        // key << 32 | ~token
-  };
-  int group[SV_MAX_TOPK];     // the chosen groups
-  unsigned count[40];         // of the list, and of the bisection's steps
-  unsigned equal[kLpMaxCluster];
-  unsigned bound, last;       // keys: of the first scan; of the last chosen group
-  unsigned logits;            // listed
+  float4 part[kLpMaxCluster * kLpWarps];         // first: the warps' sums
+  alignas(16) unsigned long long item[kLpList];  // first: key << 32 | ~token (or ~group)
+  alignas(16) unsigned published[kLpPublished];  // every: the warps' largest maxima,
+  unsigned larger[kLpPublished];                 // how many are larger, and the bound
+  int group[kLpGroups];                          // every: groups that are read again
+  unsigned groups;
+  unsigned bound;
+  unsigned count[64];  // first: items; the bisections' steps (at most 2 + 32 + 25)
   float m, log_z, entropy;
 };
 
-// The number of this CTA's groups whose key is at least k, over all threads of
-// the cluster, into *counter of the first CTA.
-template <class Map>
-__device__ __forceinline__ void lp_count(const Map* map, int groups, unsigned k, uint32_t counter) {
-  unsigned c = 0;
-  for (int i = static_cast<int>(threadIdx.x); i < groups; i += kLpThreads) c += map[i] >= k;
-  c = __reduce_add_sync(0xffffffffu, c);
-  if ((threadIdx.x & 31) == 0 && c) cl_atomic_add(counter, c);
+__device__ __forceinline__ void lp_push(LpShared* first, unsigned long long v) {
+  const unsigned at = atomicAdd(&first->count[0], 1u);
+  if (at < kLpList) first->item[at] = v;
 }
 
-// Chooses the row's top groups: their indices in sh.group of the first CTA, the
-// smallest chosen key in sh.last, their number returned there.  `mine`: the
-// thread's largest key, map the CTA's keys (thread i wrote i, i + 256 ..), g0
-// its first group.  Every thread of the cluster calls this.
+// The logits of the listed groups that reach `bound`, as items of the first CTA.
 template <class T>
-__device__ __forceinline__ int lp_choose(const LogprobProblem& a, LpShared& sh,
-                                         const typename LpKey<T>::Map* map, int g0, int groups,
-                                         unsigned mine, int rank) {
-  const int tid = static_cast<int>(threadIdx.x), lane = tid & 31, warp = tid >> 5;
-  const int n = a.top;
-  const uint32_t count = cl_map(sh.count, 0), list = cl_map(sh.list, 0);
-  // the bound: the n-th largest of what the warps published
-  const int all = a.cluster * kLpWarps * a.published;
-  if (rank == 0 && tid < all) {
-    const unsigned v = sh.published[tid];
-    int before = 0;
-    for (int i = 0; i < all; ++i) {
-      const unsigned o = sh.published[i];
-      before += o > v || (o == v && i < tid);
+__device__ __forceinline__ void lp_read_groups(const LpRow<T>& in, const int* group, int groups,
+                                               unsigned bound, LpShared* first) {
+  constexpr int N = 4;  // loads under way together
+#pragma unroll 1
+  for (int e0 = static_cast<int>(threadIdx.x); e0 < groups * kLpGroup; e0 += N * kLpThreads) {
+    int id[N];
+    float v[N];
+#pragma unroll
+    for (int q = 0; q < N; ++q) {
+      const int e = e0 + q * kLpThreads;
+      v[q] = kNegInf;
+      id[q] = -1;
+      if (e < groups * kLpGroup) id[q] = group[e / kLpGroup] * kLpGroup + e % kLpGroup - in.off;
+      if (id[q] >= 0 && id[q] < in.V) v[q] = lp_value(in.x + id[q]);
     }
-    if (before == n - 1) {
-      const unsigned bound = max(v, LpKey<T>::kNone + 1);
-      for (int r = 0; r < a.cluster; ++r) cl_st_u32(cl_map(&sh.bound, r), bound);
+#pragma unroll
+    for (int q = 0; q < N; ++q) {
+      const unsigned k = LpKey<T>::of(v[q]);
+      if (k >= bound) lp_push(first, lp_item(k, id[q]));
     }
   }
-  lp_sync();
-  const unsigned bound = sh.bound;
-  if (mine >= bound)
-    for (int i = tid; i < groups; i += kLpThreads) {
-      const unsigned k = map[i];
-      if (k >= bound) {
-        const unsigned at = cl_atomic_add(count, 1u);
-        if (at < kLpList)
-          cl_st_u64(list + 8 * at, lp_item(k, g0 + i));
-      }
-    }
-  lp_sync();
-  unsigned found = cl_ld_u32(count);
-  if (__builtin_expect(found > kLpList, 0)) {
-    // lo: at least n (and too many) groups reach it; hi: fewer than n do.  Equal
-    // maxima are the likely reason, so the first step tries lo + 1.
-    unsigned lo = bound, hi = sizeof(typename LpKey<T>::Map) == 2 ? 0x10000u : 0xffffffffu;
-    unsigned above = 0;  // groups that reach hi
-    bool fits = false;
-    for (int step = 1; hi - lo > 1 && !fits; ++step) {
-      const unsigned mid = step == 1 ? lo + 1 : lo + (hi - lo) / 2;
-      lp_count(map, groups, mid, count + 4 * step);
-      lp_sync();
-      const unsigned c = cl_ld_u32(count + 4 * step);
-      if (c >= static_cast<unsigned>(n)) {
-        lo = mid;
-        fits = c <= kLpList;
-      } else {
-        hi = mid;
-        above = c;
-      }
-    }
-    // All that reach lo if they fit; else all that reach hi = lo + 1 and, of
-    // those equal to lo, the first ones, up to n.
-    lp_sync();  // every CTA has read the counts
-    if (rank == 0 && tid == 0) sh.count[0] = 0;
-    unsigned c = 0;
-    for (int i = tid; i < groups; i += kLpThreads) c += map[i] == lo;
-    c = __reduce_add_sync(0xffffffffu, c);
-    if (lane == 0 && c)
-      for (int r = 0; r < a.cluster; ++r) cl_atomic_add(cl_map(&sh.equal[rank], r), c);
-    lp_sync();
-    const unsigned from = fits ? lo : hi;
-    for (int i = tid; i < groups; i += kLpThreads) {
-      const unsigned k = map[i];
-      if (k >= from) {
-        const unsigned at = cl_atomic_add(count, 1u);
-        if (at < kLpList)
-          cl_st_u64(list + 8 * at, lp_item(k, g0 + i));
-      }
-    }
-    if (!fits && warp == 0) {
-      int wanted = n - static_cast<int>(above);
-      for (int r = 0; r < rank; ++r) wanted -= static_cast<int>(min(sh.equal[r], 1u << 20));
-      for (int i0 = 0; i0 < groups && wanted > 0; i0 += 32) {
-        const bool is = i0 + lane < groups && map[i0 + lane] == lo;
-        const unsigned who = __ballot_sync(0xffffffffu, is);
-        if (is && __popc(who & ((1u << lane) - 1)) < wanted) {
-          const unsigned at = cl_atomic_add(count, 1u);
-          if (at < kLpList)
-            cl_st_u64(list + 8 * at, lp_item(lo, g0 + i0 + lane));
-        }
-        wanted -= __popc(who);
-      }
-    }
-    lp_sync();
-    found = cl_ld_u32(count);
-  }
-  // The first CTA stays until the others have read its count; it waits at its
-  // end.
-  __syncwarp();
-  cl_arrive();
-  if (rank != 0) {
-    cl_wait();
-    return 0;
-  }
-  // the n best of the list, by key, then by group
-  found = min(found, static_cast<unsigned>(kLpList));
-  const int chosen = min(static_cast<int>(found), n);
-  for (unsigned i = tid; i < found; i += kLpThreads) {
-    const unsigned long long v = sh.list[i];
-    int before = 0;
-    for (unsigned k = 0; k < found; ++k) before += sh.list[k] > v;
-    if (before < chosen) sh.group[before] = static_cast<int>(~static_cast<unsigned>(v));
-    if (before == chosen - 1) sh.last = static_cast<unsigned>(v >> 32);
-  }
-  if (tid == 0) sh.logits = 0;
-  __syncthreads();
-  return chosen;
 }
 
+// Too many logits reach the bound: finds the row's n groups of largest maxima
+// (equal ones: the first) and collects the logits that reach the last of them, at
+// most kLpList.  Every thread of the cluster calls this.
+template <class T>
+__device__ __noinline__ void lp_choose(const LogprobProblem& a, LpShared& sh,
+                                       const typename LpKey<T>::Map* map, LpRow<T> in,
+                                       LpShare share, int groups, unsigned bound) {
+  const int tid = static_cast<int>(threadIdx.x), lane = tid & 31;
+  const unsigned n = static_cast<unsigned>(a.top);
+  LpShared* const first = cl_at(&sh, 0);
+  int step = 1;
+  // how many groups of the row satisfy `is` (key, index)
+  auto count = [&](auto is) {
+    unsigned c = 0;
+    for (int i = tid; i < groups; i += kLpThreads)
+      c += is(LpKey<T>::of_map(map[i]), share.group(i));
+    c = __reduce_add_sync(0xffffffffu, c);
+    if (lane == 0 && c) atomicAdd(&first->count[step], c);
+    lp_sync(a.cluster);
+    return *static_cast<volatile unsigned*>(&first->count[step++]);
+  };
+  // lo: at least n groups reach it; hi: fewer than n do, `above`.  Equal maxima are the
+  // likely reason to be here, so lo + 1 is tried first.
+  unsigned lo = bound, hi = 0xffffffffu, above = 0;
+  const bool enough = count([&](unsigned k, int) { return k >= lo; }) >= n;
+  while (enough && hi - lo > 1) {
+    const unsigned mid = step == 2 ? lo + 1 : lo + (hi - lo) / 2;
+    const unsigned c = count([&](unsigned k, int) { return k >= mid; });
+    if (c >= n) {
+      lo = mid;
+    } else {
+      hi = mid;
+      above = c;
+    }
+  }
+  // of the groups equal to lo those before `end`: at most as many as are left
+  int end = 0, past = 1 << 24;
+  while (enough && past - end > 1) {
+    const int mid = end + (past - end) / 2;
+    if (count([&](unsigned k, int g) { return k == lo && g < mid; }) <= n - above)
+      end = mid;
+    else
+      past = mid;
+  }
+  lp_sync(a.cluster);  // every CTA has read the counts
+  if (share.rank == 0 && tid == 0) sh.count[0] = 0;
+  lp_sync(a.cluster);
+  for (int i = tid; i < groups; i += kLpThreads) {
+    const unsigned k = LpKey<T>::of_map(map[i]);
+    const int g = share.group(i);
+    if (enough ? k >= hi || (k == lo && g < end) : k >= lo) lp_push(first, lp_item(k, g));
+  }
+  lp_sync(a.cluster);
+  if (share.rank != 0) return;
+  // the chosen groups' logits (n groups at most, so they all fit)
+  const int chosen = min(static_cast<int>(sh.count[0]), SV_MAX_TOPK);
+  if (tid < chosen) sh.group[tid] = static_cast<int>(~static_cast<unsigned>(sh.item[tid]));
+  __syncthreads();
+  if (tid == 0) sh.count[0] = 0;
+  __syncthreads();
+  lp_read_groups(in, sh.group, chosen, lo, &sh);
+  __syncthreads();
+}
+
+// Bound: HBM for many rows (2047 rows of 128256 bf16 logits without likeliest
+// tokens 86 us, 90 % of the copy bandwidth; with 5 of them 95 us); for few rows the way
+// from one trip to memory to the next (launch, what the row is, its logits) and,
+// for the likeliest tokens, five barriers and a second look at memory, some 4 us.
+// Four groups a thread in flight and four CTAs an SM: two groups and five CTAs
+// took 88 and 98 us, eight groups and three CTAs 98 and 109.
 template <class T, bool TOP>
-__global__ void __launch_bounds__(kLpThreads, 4) logprob_kernel(const LogprobProblem a) {
+__global__ void __launch_bounds__(kLpThreads, kLpCtasPerSm) logprob_kernel(const LogprobProblem a) {
   using Key = LpKey<T>;
   using Map = typename Key::Map;
   constexpr int U = sizeof(T) == 2 ? 4 : 2;  // groups whose loads are under way together
@@ -348,231 +416,262 @@ __global__ void __launch_bounds__(kLpThreads, 4) logprob_kernel(const LogprobPro
   __shared__ LpShared sh;
   const int tid = static_cast<int>(threadIdx.x), lane = tid & 31, warp = tid >> 5;
   const int rank = static_cast<int>(cl_rank());
-  grid_dependency_wait();
   const int out = static_cast<int>(cl_id());
   const int b = out / a.R, r = out - b * a.R;
+  const long long orow = out;
   const float nan = __int_as_float(0x7fc00000);
+  if (TOP) {
+    if (tid < 64) sh.count[tid] = 0;
+    if (tid < kLpPublished) sh.larger[tid] = 0;
+    if (tid == 0) sh.groups = 0;
+  }
+  if (a.cluster > 1) {
+    __syncwarp();
+    cl_arrive();
+  }
+  grid_dependency_wait();
 
-  // what the row is (the same for all threads of the cluster)
+  // What the row is (the same for all threads of the cluster): one trip to memory.
   const int n = a.num_rows ? a.num_rows[b] : a.R;
   float t = a.temperature ? a.temperature[b] : 1.f;
+  const int row = a.rows ? a.rows[orow] : r;
+  int token = rank == 0 && tid < a.M ? a.tokens[orow * a.M + tid] : -1;
   int flag = n < 0 || n > a.R || !(t >= 0.f && t < kPosInf) ? SV_DERR_ARG : 0;
   bool live = flag == 0 && r < n;
-  int row = r;
-  if (live && a.rows) {
-    row = a.rows[static_cast<long long>(b) * a.R + r];
-    if (row < 0 || row >= a.N) {
-      flag = SV_DERR_ARG;
-      live = false;
-    }
+  if (live && (row < 0 || row >= a.N)) {
+    flag = SV_DERR_ARG;
+    live = false;
   }
   if (flag && rank == 0 && tid == 0) record_error(a.err, flag);
   if (t == 0.f) t = 1.f;
-  const long long orow = out;
+  if (a.cluster > 1) cl_wait();  // the first CTA is there
 
-  if (live) {
-    const T* x = static_cast<const T*>(a.logits) + b * a.batch + row * a.row;
-    LpRow<T> in;
-    in.x = x;
-    in.off = static_cast<int>(reinterpret_cast<uintptr_t>(x) & 31) / static_cast<int>(sizeof(T));
-    in.V = a.V;
-    const int all = (a.V + in.off + kLpGroup - 1) / kLpGroup;
-    const int g0 = rank * a.share, groups = max(0, min(all - g0, a.share));
-    const float c = fminf(1.44269504f / t, 3e38f), inv_t = fminf(1.f / t, 3e38f);
-    Map* const map = reinterpret_cast<Map*>(lp_map);
-
-    // the given token's logit, for the end
-    int token = -1;
-    float given = 0.f;
-    if (rank == 0 && tid < a.M) {
-      token = a.tokens[orow * a.M + tid];
-      if (token >= 0 && token < a.V) given = lp_value(x + token);
-    }
-    if (TOP && tid < 40) sh.count[tid] = 0;
-    if (TOP && tid < kLpMaxCluster) sh.equal[tid] = 0;
-    if (TOP && tid == 0) sh.bound = 0;
-    __syncwarp();
-    cl_arrive();
-
-    LpSum s{kNegInf, 0.f, 0.f};
-    unsigned mine = 0;
-#pragma unroll 1
-    for (int i0 = tid; i0 < groups; i0 += U * kLpThreads) {
-      LpRaw<T> raw[U];
-      bool here[U];
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-        here[u] = i0 + u * kLpThreads < groups && in.whole(g0 + i0 + u * kLpThreads);
-        if (here[u]) {
-          in.load(raw[u], g0 + i0 + u * kLpThreads);
-        } else {
-#pragma unroll
-          for (int i = 0; i < static_cast<int>(sizeof(raw[u].w)) / 4; ++i)
-            raw[u].w[i] = sizeof(T) == 2 ? 0xff80ff80u : 0xff800000u;
-        }
-      }
-      float m = kNegInf;
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const float gm = lp_max(raw[u]);
-        m = max_nan(m, gm);
-        if (TOP && here[u]) {
-          const unsigned k = Key::of(gm);
-          map[i0 + u * kLpThreads] = static_cast<Map>(k);
-          mine = max(mine, k);
-        }
-      }
-      if (!(m <= s.m)) lp_raise(s, m, c);
-      if (s.m > kNegInf) {
-        const float2 ref = make_float2(-s.m, -s.m), c2 = make_float2(c, c);
-        float2 z = make_float2(0.f, 0.f), w = make_float2(0.f, 0.f);
-#pragma unroll
-        for (int u = 0; u < U; ++u)
-#pragma unroll
-          for (int i = 0; i < kLpGroup / 2; ++i) {
-            float2 e = x2_mul(x2_add(lp_pair(raw[u], i), ref), c2);
-            e.x = fmaxf(e.x, -1000.f);
-            e.y = fmaxf(e.y, -1000.f);
-            const float2 f = make_float2(fast_exp2(e.x), fast_exp2(e.y));
-            z = x2_add(z, f);
-            w = x2_fma(f, e, w);
-          }
-        s.z += z.x + z.y;
-        s.a += w.x + w.y;
-      }
-    }
-
-    // The first and the last group, where they are not all the row's: a logit a
-    // lane, by the warp of the thread whose turn the group was.
-#pragma unroll 1
-    for (int e = 0; e < 2; ++e) {
-      const int i = (e ? all - 1 : 0) - g0;
-      if (i < 0 || i >= groups || in.whole(g0 + i) || (e && all == 1)) continue;
-      if ((i & (kLpThreads - 1)) >> 5 != warp) continue;
-      const int id = (g0 + i) * kLpGroup - in.off + lane;
-      float v = kNegInf;
-      if (lane < kLpGroup && id >= 0 && id < a.V) v = lp_value(x + id);
-      if (!(v <= s.m)) lp_raise(s, v, c);
-      if (s.m > kNegInf) {
-        const float d = fmaxf((v - s.m) * c, -1000.f), f = fast_exp2(d);
-        s.z += f;
-        s.a = fmaf(f, d, s.a);
-      }
-      if (TOP) {
-        const unsigned k = warp_max_u32(Key::of(v));
-        if (lane == (i & 31)) {
-          map[i] = static_cast<Map>(k);
-          mine = max(mine, k);
-        }
-      }
-    }
-
-    s = lp_warp_sum(s, c);
-    __syncwarp();
-    cl_wait();  // the first CTA is there
-    if (lane == 0) {
-      const uint32_t p = cl_map(&sh.part[rank * kLpWarps + warp], 0);
-      cl_st_u64(p, static_cast<uint64_t>(__float_as_uint(s.z)) << 32 | __float_as_uint(s.m));
-      cl_st_u32(p + 8, __float_as_uint(s.a));
-    }
-    if (TOP) {
-      unsigned left = mine;
-      for (int i = 0; i < a.published; ++i) {
-        const unsigned v = warp_max_u32(left);
-        if (lane == __ffs(__ballot_sync(0xffffffffu, left == v)) - 1) {
-          cl_st_u32(cl_map(&sh.published[(rank * kLpWarps + warp) * a.published + i], 0), v);
-          left = 0;
-        }
-      }
-    }
-    lp_sync();
-    if (rank == 0 && warp == kLpWarps - 1) {
-      // the row's sums
-      LpSum q{kNegInf, 0.f, 0.f};
-      for (int i = lane; i < a.cluster * kLpWarps; i += 32) {
-        const float4 p = sh.part[i];
-        LpSum o{p.x, p.y, p.z};
-        const float m = max_nan(q.m, o.m);
-        lp_raise(q, m, c);
-        lp_raise(o, m, c);
-        q.z += o.z;
-        q.a += o.a;
-      }
-      q = lp_warp_sum(q, c);
-      if (lane == 0) {
-        int bad = 0;
-        if (!(q.m < kPosInf)) bad = SV_DERR_NONFINITE;
-        else if (!(q.m > kNegInf)) bad = SV_DERR_MASS;
-        if (bad) record_error(a.err, bad);
-        sh.m = bad ? nan : q.m;
-        sh.log_z = logf(q.z);
-        sh.entropy = bad ? nan : sh.log_z - q.a / q.z * 0.69314718055994531f;
-      }
-    }
-    int chosen = 0;
-    if (TOP) chosen = lp_choose<T>(a, sh, map, g0, groups, mine, rank);
+  if (!live) {
+    // nothing to report
     if (rank != 0) return;
-    __syncthreads();
-    const float m = sh.m, log_z = sh.log_z;
-    auto logprob = [&](float v) { return (v - m) * inv_t - log_z; };
-    if (tid == 0 && a.entropy) a.entropy[orow] = sh.entropy;
-    for (int i = tid; i < a.M; i += kLpThreads) {
-      if (i >= kLpThreads) {
-        token = a.tokens[orow * a.M + i];
-        if (token >= 0 && token < a.V) given = lp_value(x + token);
-      }
-      const bool there = token >= 0 && token < a.V;
-      if (!there && token != -1) record_error(a.err, SV_DERR_TOKEN);
-      a.logprob[orow * a.M + i] = there ? logprob(given) : nan;
-    }
-    if (TOP) {
-      if (!(m < kPosInf)) {  // NaN: a row with an error
-        for (int i = tid; i < a.top; i += kLpThreads) {
-          a.top_token[orow * a.top + i] = -1;
-          a.top_logprob[orow * a.top + i] = nan;
-        }
-        __syncwarp();
-        cl_wait();
-        return;
-      }
-      const unsigned last = chosen == a.top ? sh.last : Key::kNone + 1;
-      for (int e = tid; e < chosen * kLpGroup; e += kLpThreads) {
-        const int id = sh.group[e / kLpGroup] * kLpGroup + e % kLpGroup - in.off;
-        if (id < 0 || id >= a.V) continue;
-        const unsigned k = Key::of(lp_value(x + id));
-        if (k >= last)
-          sh.logit[atomicAdd(&sh.logits, 1u)] =
-              lp_item(k, id);
-      }
-      __syncthreads();
-      const int found = static_cast<int>(sh.logits);
-      for (int i = tid; i < found; i += kLpThreads) {
-        const unsigned long long v = sh.logit[i];
-        int before = 0;
-        for (int k = 0; k < found; ++k) before += sh.logit[k] > v;
-        if (before < a.top) {
-          a.top_token[orow * a.top + before] = static_cast<int>(~static_cast<unsigned>(v));
-          a.top_logprob[orow * a.top + before] =
-              logprob(Key::value(static_cast<unsigned>(v >> 32)));
-        }
-      }
-      for (int i = found + tid; i < a.top; i += kLpThreads) {
-        a.top_token[orow * a.top + i] = -1;
-        a.top_logprob[orow * a.top + i] = kNegInf;
-      }
-      __syncwarp();
-      cl_wait();  // (lp_choose)
+    if (tid == 0 && a.entropy) a.entropy[orow] = nan;
+    for (int i = tid; i < a.M; i += kLpThreads) a.logprob[orow * a.M + i] = nan;
+    for (int i = tid; i < a.top; i += kLpThreads) {
+      a.top_token[orow * a.top + i] = -1;
+      a.top_logprob[orow * a.top + i] = nan;
     }
     return;
   }
 
-  // a row that has nothing to report
-  if (rank != 0) return;
-  if (tid == 0 && a.entropy) a.entropy[orow] = nan;
-  for (int i = tid; i < a.M; i += kLpThreads) a.logprob[orow * a.M + i] = nan;
-  for (int i = tid; i < a.top; i += kLpThreads) {
-    a.top_token[orow * a.top + i] = -1;
-    a.top_logprob[orow * a.top + i] = nan;
+  const T* x = static_cast<const T*>(a.logits) + b * a.batch + row * a.row;
+  LpRow<T> in;
+  in.x = x;
+  in.off = static_cast<int>(reinterpret_cast<uintptr_t>(x) & 31) / static_cast<int>(sizeof(T));
+  in.V = a.V;
+  const int all = (a.V + in.off + kLpGroup - 1) / kLpGroup;
+  const LpShare share{a.cluster, rank};
+  const int groups = share.count(all);
+  const float c = fminf(1.44269504f / t, 3e38f), inv_t = fminf(1.f / t, 3e38f);
+  Map* const map = reinterpret_cast<Map*>(lp_map);
+  float given = 0.f;  // the given token's logit, for the end
+  if (token >= 0 && token < a.V) given = lp_value(x + token);
+
+  const bool fast = sizeof(T) == 4 || (c > 0x1p-60f && c < 0x1p26f);
+  LpSum s{kNegInf, 0.f, 0.f};
+  // the largest logit of the thread's best turn of U groups and of the next best,
+  // and where the best begins
+  float mine = kNegInf, second = kNegInf;
+  int at = tid;
+#pragma unroll 1
+  for (int i0 = tid; i0 < groups; i0 += U * kLpThreads) {
+    LpRaw<T> raw[U];
+    bool here[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int g = share.group(i0 + u * kLpThreads);
+      here[u] = i0 + u * kLpThreads < groups && in.whole(g);
+      if (here[u]) {
+        in.load(raw[u], g);
+      } else {
+#pragma unroll
+        for (int i = 0; i < static_cast<int>(sizeof(raw[u].w)) / 4; ++i)
+          raw[u].w[i] = sizeof(T) == 2 ? 0xff80ff80u : 0xff800000u;
+      }
+    }
+    float m = kNegInf;
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const float gm = lp_max(raw[u]);
+      m = max_nan(m, gm);
+      if (TOP && here[u]) map[i0 + u * kLpThreads] = Key::map(gm);
+    }
+    if (TOP) {
+      second = fmaxf(second, fminf(mine, m));
+      at = m > mine ? i0 : at;
+      mine = fmaxf(mine, m);
+    }
+    if (!(m <= s.m)) lp_raise(s, m, c);
+    if (fast && s.m > (sizeof(T) == 2 ? -0x1p90f : kNegInf) && !lp_wide(s.m, c))
+      lp_accumulate<T, true>(s, raw, c);
+    else if (s.m > kNegInf)
+      lp_slow<T>(s, raw, c);
+  }
+
+  // The first and the last group, where they are not all the row's: a logit a
+  // lane, by the warp of the thread whose turn the group was.
+#pragma unroll 1
+  for (int e = 0; e < 2; ++e) {
+    const int g = e ? all - 1 : 0, i = share.place(g);
+    if (share.owner(g) != rank || in.whole(g) || (e && all == 1)) continue;
+    if ((i & (kLpThreads - 1)) >> 5 != warp) continue;
+    const int id = g * kLpGroup - in.off + lane;
+    float v = kNegInf;
+    if (lane < kLpGroup && id >= 0 && id < a.V) v = lp_value(x + id);
+    if (!(v <= s.m)) lp_raise(s, v, c);
+    if (s.m > kNegInf) {
+      const float d = lp_exponent(v, s.m, c), f = fast_exp2(d);
+      s.z += f;
+      s.a = fmaf(f, d, s.a);
+    }
+    if (TOP) {
+      const float gm = Key::value(warp_max_u32(Key::of(v)));
+      if (lane == (i & 31)) {
+        map[i] = Key::map(gm);
+        second = fmaxf(second, fminf(mine, gm));
+        at = gm > mine ? i - (i - tid) % (U * kLpThreads) : at;
+        mine = fmaxf(mine, gm);
+      }
+    }
+  }
+
+  LpShared* const first = cl_at(&sh, 0);
+  s = lp_warp_sum(s, c);
+  if (lane == 0) first->part[rank * kLpWarps + warp] = make_float4(s.m, s.z, s.a, 0.f);
+  if (TOP) {
+    // the warp's largest maxima, to every CTA
+    unsigned* const to = cl_at(&sh, lane < a.cluster ? lane : 0)->published +
+                         (rank * kLpWarps + warp) * a.published;
+    unsigned left = Key::of(mine);
+#pragma unroll 1
+    for (int i = 0; i < a.published; ++i) {
+      const unsigned v = warp_max_u32(left);
+      if (lane < a.cluster) to[i] = v;
+      if (lane == __ffs(__ballot_sync(0xffffffffu, left == v)) - 1) left = 0;
+    }
+  }
+  lp_sync(a.cluster);
+  if (!TOP && rank != 0) return;
+  if (rank == 0 && warp == kLpWarps - 1) {
+    // the row's sums
+    LpSum q{kNegInf, 0.f, 0.f};
+    for (int i = lane; i < a.cluster * kLpWarps; i += 32) {
+      const float4 p = sh.part[i];
+      LpSum o{p.x, p.y, p.z};
+      const float m = max_nan(q.m, o.m);
+      lp_raise(q, m, c);
+      lp_raise(o, m, c);
+      q.z += o.z;
+      q.a += o.a;
+    }
+    q = lp_warp_sum(q, c);
+    if (lane == 0) {
+      int bad = 0;
+      if (!(q.m < kPosInf)) bad = SV_DERR_NONFINITE;
+      else if (!(q.m > kNegInf)) bad = SV_DERR_MASS;
+      if (bad) record_error(a.err, bad);
+      const float ln2 = 0.69314718055994531f, z = log2f(q.z);
+      sh.m = bad ? nan : q.m;
+      sh.log_z = (z - lp_off(q.m, c)) * ln2;  // relative to m itself
+      sh.entropy = bad ? nan : (z - q.a / q.z) * ln2;
+    }
+  }
+  bool leave = false;
+  if (TOP) {
+    // The bound: the top-th largest of what was published.  A thread compares one
+    // of the keys with a share of them.
+    {
+      const int v = tid & ((1 << a.all_shift) - 1), each = (1 << 2 * a.all_shift) / kLpThreads;
+      const int i0 = (tid >> a.all_shift) * each;
+      const unsigned k = sh.published[v];
+      unsigned larger = 0;
+#pragma unroll 4
+      for (int i = i0; i < i0 + each; i += 4) {
+        const uint4 o = *reinterpret_cast<const uint4*>(&sh.published[i]);
+        larger += (o.x > k || (o.x == k && i < v)) + (o.y > k || (o.y == k && i + 1 < v)) +
+                  (o.z > k || (o.z == k && i + 2 < v)) + (o.w > k || (o.w == k && i + 3 < v));
+      }
+      atomicAdd(&sh.larger[v], larger);
+      __syncthreads();
+      // (no logit of -inf is listed)
+      if (i0 == 0 && sh.larger[v] == static_cast<unsigned>(a.top - 1))
+        sh.bound = max(k, Key::kNone + 1);
+      __syncthreads();
+    }
+    const unsigned bound = sh.bound;
+    if (Key::of(mine) >= bound) {
+      // the thread's groups that reach it: of its best turn, rarely of others too
+      const bool one = Key::of(second) < bound;
+      const int end = one ? min(groups, at + U * kLpThreads) : groups;
+#pragma unroll 1
+      for (int i = one ? at : tid; i < end; i += kLpThreads)
+        if (Key::of_map(map[i]) >= bound) {
+          const unsigned to = atomicAdd(&sh.groups, 1u);
+          if (to < kLpGroups) sh.group[to] = share.group(i);
+        }
+    }
+    __syncthreads();
+    if (sh.groups <= kLpGroups)
+      lp_read_groups(in, sh.group, static_cast<int>(sh.groups), bound, first);
+    else if (tid == 0)
+      atomicAdd(&first->count[0], kLpList + 1u);
+    lp_sync(a.cluster);
+    if (__builtin_expect(*static_cast<volatile unsigned*>(&first->count[0]) > kLpList, 0)) {
+      lp_choose<T>(a, sh, map, in, share, groups, bound);
+    } else if (a.cluster > 1) {
+      // The first CTA stays until the others have read its count; it waits at its
+      // end.  (lp_choose ends with a barrier of its own.)
+      __syncwarp();
+      cl_arrive();
+      leave = true;
+      if (rank != 0) cl_wait();
+    }
+    if (rank != 0) return;
+  } else {
+    __syncthreads();
+  }
+  const float m = sh.m, log_z = sh.log_z;
+  auto logprob = [&](float v) { return (v - m) * inv_t - log_z; };
+  if (tid == 0 && a.entropy) a.entropy[orow] = sh.entropy;
+  for (int i = tid; i < a.M; i += kLpThreads) {
+    if (i >= kLpThreads) {
+      token = a.tokens[orow * a.M + i];
+      if (token >= 0 && token < a.V) given = lp_value(x + token);
+    }
+    const bool there = token >= 0 && token < a.V;
+    if (!there && token != -1) record_error(a.err, SV_DERR_TOKEN);
+    a.logprob[orow * a.M + i] = there ? logprob(given) : nan;
+  }
+  if (TOP) {
+    const bool bad = !(m < kPosInf);  // NaN: a row with an error
+    const int found = bad ? 0 : min(static_cast<int>(sh.count[0]), kLpList);
+    // four lanes an item, whose rank is the number of larger ones
+#pragma unroll 1
+    for (int i0 = 0; i0 < found; i0 += kLpThreads / 4) {
+      const int i = i0 + tid / 4;
+      const unsigned long long v = i < found ? sh.item[i] : ~0ull;
+      int before = 0;
+#pragma unroll 4
+      for (int k = tid & 3; k < found; k += 4) before += sh.item[k] > v;
+      before += __shfl_xor_sync(0xffffffffu, before, 1);
+      before += __shfl_xor_sync(0xffffffffu, before, 2);
+      if (i < found && before < a.top && (tid & 3) == 0) {
+        a.top_token[orow * a.top + before] = static_cast<int>(~static_cast<unsigned>(v));
+        a.top_logprob[orow * a.top + before] = logprob(Key::value(static_cast<unsigned>(v >> 32)));
+      }
+    }
+    for (int i = found + tid; i < a.top; i += kLpThreads) {
+      a.top_token[orow * a.top + i] = -1;
+      a.top_logprob[orow * a.top + i] = bad ? nan : kNegInf;
+    }
+    if (leave) {
+      __syncwarp();
+      cl_wait();
+    }
   }
 }
 
