@@ -373,14 +373,11 @@ def rotate(q, k=None, start=None, num=None, offset=None, rope=None, q_weight=Non
     depths); later rows become zero.  rope: rope()'s dict, None for norms
     alone; eps None: no norm.  Returns q and k (device tensors), which are the
     arguments themselves when inplace."""
-    out = dict(q=q if inplace else torch.empty_like(q, memory_format=torch.contiguous_format))
-    if k is not None:
-        out["k"] = k if inplace else torch.empty_like(k, memory_format=torch.contiguous_format)
     if ws is None:
         ws = workspace(SV_MIN_WORKSPACE_BYTES, q.device, "kv")
-    sv_rotate(q, out["q"], ws, k=k, k_out=out.get("k"), start=start, num=num, offset=offset,
-              rope=rope, q_weight=q_weight, k_weight=k_weight, eps=eps)
-    return out
+    out = ... if inplace else None
+    q, k = sv_rotate(q, out, ws, k, out, start, num, offset, rope, q_weight, k_weight, eps)
+    return dict(q=q) if k is None else dict(q=q, k=k)
 
 
 def kv_append(cache: dict, page_table, kv_len, q, k_new, v_new, num_new=None, offset=None,
@@ -393,15 +390,11 @@ def kv_append(cache: dict, page_table, kv_len, q, k_new, v_new, num_new=None, of
     kv_len[b] + t of request b and has position kv_len[b] + t, or kv_len[b] +
     offset[b][t] (tree_mask's depths).  Returns q (q_dtype, its own by
     default; rows behind the last token zero)."""
-    out = {}
-    if q is not None:
-        out["q"] = torch.empty_like(q, dtype=q_dtype, memory_format=torch.contiguous_format)
     if ws is None:
         ws = workspace(SV_MIN_WORKSPACE_BYTES, k_new.device, "kv")
-    sv_kv_append(cache, page_table, kv_len, k_new, v_new, ws, q=q, q_out=out.get("q"),
-                 num_new=num_new, offset=offset, rope=rope, q_weight=q_weight, k_weight=k_weight,
-                 eps=eps)
-    return out
+    q, = sv_kv_append(cache, page_table, kv_len, k_new, v_new, ws, q, None, num_new, offset, rope,
+                      q_weight, k_weight, eps, None, q_dtype)
+    return {} if q is None else dict(q=q)
 
 
 def token_logprobs(logits, tokens=None, num_rows=None, rows=None, R: int | None = None,
@@ -417,20 +410,15 @@ def token_logprobs(logits, tokens=None, num_rows=None, rows=None, R: int | None 
     logprobs (tokens' shape), top_tokens and top_logprobs [B][R][top] (device
     tensors): equal logits list the lower token first, tokens of logit -inf are
     not listed (-1, -inf), and rows from num_rows on are NaN and -1."""
-    B, N = logits.shape[:2]
-    dev = logits.device
-    if R is None:
-        R = tokens.shape[1] if tokens is not None else rows.shape[1] if rows is not None else N
-    out = dict(entropy=torch.empty((B, R), dtype=torch.float32, device=dev))
-    if tokens is not None:
-        out["logprobs"] = torch.empty(tokens.shape, dtype=torch.float32, device=dev)
-    if top > 0:
-        out["top_tokens"] = torch.empty((B, R, top), dtype=torch.int32, device=dev)
-        out["top_logprobs"] = torch.empty((B, R, top), dtype=torch.float32, device=dev)
     if ws is None:
-        ws = workspace(SV_MIN_WORKSPACE_BYTES, dev, "kv")
-    sv_token_logprobs(logits, ws, R, tokens=tokens, num_rows=num_rows, rows=rows,
-                      temperature=temperature, top=top, **out)
+        ws = workspace(SV_MIN_WORKSPACE_BYTES, logits.device, "kv")
+    lp, entropy, ids, best = sv_token_logprobs(
+        logits, ws, R, tokens, num_rows, rows, temperature, top, None, None, None, None, None, True)
+    out = dict(entropy=entropy)
+    if lp is not None:
+        out["logprobs"] = lp
+    if ids is not None:
+        out["top_tokens"], out["top_logprobs"] = ids, best
     return out
 
 

@@ -670,125 +670,80 @@ def sv_kv_attention(q, cache: dict, page_table, kv_len, out, workspace, scale: f
 
 
 # --------------------- norms and positions of queries and keys, log probabilities
+#
+# A model makes these calls in every layer or step and they take a dozen tensors
+# each, so their marshalling is compiled (csrc/native.cpp).  Results that are not
+# given are allocated there.
 
-_pack_rotate, _pack_append = _packer(SvRotateArgs).pack, _packer(SvKvAppendArgs).pack
-_pack_logprobs = _packer(SvTokenLogprobsArgs).pack
-_NO_NORM = (0, 0, 0.0)
-_NO_HEADS = (0, 0, 0, 0, 0, 0, 0, 0, 0, 0) + _NO_NORM
-_NO_ROPE = (0, 0, 1.0, 0)
-
-
-def _rope_fields(rope, dev: int) -> tuple:
-    """The fields of an sv_rope, from the dict that rope() makes."""
-    if rope is None:
-        return _NO_ROPE
-    dim = rope["dim"]
-    return (dim, 1 if rope["interleaved"] else 0, rope["scale"],
-            _addr(rope["freq"], torch.int64, (dim // 2,), "rope freq", dev))
+_native_module = None
+_entries: dict = {}
 
 
-def _norm_fields(weight, eps, D: int, what: str, dev: int) -> tuple:
-    """The fields of an sv_head_norm: none without eps."""
-    if eps is None:
-        if weight is not None:
-            raise ValueError(f"{what}: a norm's weight, but no eps")
-        return _NO_NORM
-    if eps <= 0:
-        raise ValueError(f"eps: expected a positive number, got {eps}")
-    if weight is None:
-        return 0, 0, eps
-    if weight.dtype not in _KV_DTYPES:
-        raise ValueError(f"{what}: expected bfloat16, float16 or float32, got {weight.dtype}")
-    return _addr(weight, weight.dtype, (D,), what, dev), _KV_DTYPES[weight.dtype], eps
+def _native():
+    global _native_module
+    if _native_module is None:
+        try:
+            from . import _native as module
+        except ImportError as e:
+            raise RuntimeError("the compiled binding is missing: build it with "
+                               "__graft_entry__.build()") from e
+        _native_module = module
+    return _native_module
 
 
-def _heads_fields(x, out, shape, weight, eps, what: str, dev: int) -> tuple:
-    """The fields of an sv_heads: x [B][T][heads][D] into out."""
-    if x is None:
-        return _NO_HEADS
-    p, *strides = _rows4(x, shape, what, dev)
-    o, *out_strides = _rows4(out, shape, what + "_out", dev)
-    return (p, o, shape[2], _KV_DTYPES[out.dtype], *strides, *out_strides,
-            *_norm_fields(weight, eps, shape[3], what + "_weight", dev))
+def _entry(name: str) -> int:
+    """The address of an entry point of the loaded library."""
+    h = _lib_handle or lib()
+    known = _entries.get(name)
+    if known is None or known[0] is not h:
+        known = _entries[name] = (h, ctypes.cast(getattr(h, name), ctypes.c_void_p).value)
+    return known[1]
+
+
+def _launched(name: str, result):
+    if result.__class__ is int:
+        raise SpecVerifyError(result, name)
+    return result
+
+
+def _raw_stream(stream):
+    return stream.cuda_stream if hasattr(stream, "cuda_stream") else stream
 
 
 def sv_rotate(q, q_out, workspace, k=None, k_out=None, start=None, num=None, offset=None,
-              rope=None, q_weight=None, k_weight=None, eps=None, stream=None) -> None:
+              rope=None, q_weight=None, k_weight=None, eps=None, stream=None) -> tuple:
     """Enqueue sv_rotate: norms and rotations of q and k [B][T][heads][D] into
-    q_out and k_out."""
-    B, T, _, D = q.shape
-    dev = workspace.get_device()
-    qf = _heads_fields(q, q_out, q.shape, q_weight, eps, "q", dev)
-    if k is not None:
-        if k.dim() != 4 or k.shape[0] != B or k.shape[1] != T or k.shape[3] != D \
-                or k.dtype != q.dtype:
-            raise ValueError(f"k: expected [{B}][{T}][heads][{D}] of q's dtype, got {k.dtype} "
-                             f"{tuple(k.shape)}")
-        kf = _heads_fields(k, k_out, k.shape, k_weight, eps, "k", dev)
-    else:
-        kf = _NO_HEADS
-    _kv_call("sv_rotate", _pack_rotate(
-        B, T, D, _KV_DTYPES[q.dtype], *qf, *kf, _addr(start, torch.int32, (B,), "start", dev),
-        _addr(num, torch.int32, (B,), "num", dev),
-        _addr(offset, torch.int32, (B, T), "offset", dev), *_rope_fields(rope, dev)),
-        workspace, dev, stream)
+    q_out and k_out (None: new tensors; Ellipsis: in place).  Returns both."""
+    if stream is not None:
+        stream = _raw_stream(stream)
+    return _launched("sv_rotate", (_native_module or _native()).rotate(
+        _entry("sv_rotate"), workspace, stream, q, q_out, k, k_out, start, num, offset, rope,
+        q_weight, k_weight, eps))
 
 
 def sv_kv_append(cache: dict, page_table, kv_len, k_new, v_new, workspace, q=None, q_out=None,
                  num_new=None, offset=None, rope=None, q_weight=None, k_weight=None, eps=None,
-                 stream=None) -> None:
+                 stream=None, q_dtype=None) -> tuple:
     """Enqueue sv_kv_append: keys normed, rotated and, with the values,
-    quantised into the cache; queries normed and rotated into q_out."""
-    B, T = k_new.shape[:2]
-    dev = workspace.get_device()
-    c = _kv_cache(cache, page_table, B, dev)
-    shape = (B, T, c[2], c[3])
-    k, *k_strides = _rows4(k_new, shape, "k_new", dev)
-    v, *v_strides = _rows4(v_new, shape, "v_new", dev)
-    if v_new.dtype != k_new.dtype:
-        raise ValueError("v_new: expected k_new's dtype")
-    qf = _NO_HEADS
-    if q is not None:
-        if q.dtype != k_new.dtype or q.dim() != 4:
-            raise ValueError(f"q: expected [{B}][{T}][heads][{c[3]}] of k_new's dtype, got "
-                             f"{q.dtype} {tuple(q.shape)}")
-        qf = _heads_fields(q, q_out, (B, T, q.shape[2], c[3]), q_weight, eps, "q", dev)
-    _kv_call("sv_kv_append", _pack_append(
-        *c, B, T, _KV_DTYPES[k_new.dtype], *qf, k, v, *k_strides, *v_strides,
-        *_norm_fields(k_weight, eps, c[3], "k_weight", dev),
-        _addr(kv_len, torch.int32, (B,), "kv_len", dev),
-        _addr(num_new, torch.int32, (B,), "num_new", dev),
-        _addr(offset, torch.int32, (B, T), "offset", dev), *_rope_fields(rope, dev)),
-        workspace, dev, stream)
+    quantised into the cache; queries normed and rotated into q_out (None: a new
+    tensor of q_dtype, q's own by default).  Returns (q_out,)."""
+    if stream is not None:
+        stream = _raw_stream(stream)
+    return _launched("sv_kv_append", (_native_module or _native()).kv_append(
+        _entry("sv_kv_append"), workspace, stream, cache, page_table, kv_len, q, q_out, q_dtype,
+        k_new, v_new, num_new, offset, rope, q_weight, k_weight, eps))
 
 
-def sv_token_logprobs(logits, workspace, R: int, tokens=None, num_rows=None, rows=None,
+def sv_token_logprobs(logits, workspace, R=None, tokens=None, num_rows=None, rows=None,
                       temperature=None, top: int = 0, logprobs=None, entropy=None,
-                      top_tokens=None, top_logprobs=None, stream=None) -> None:
+                      top_tokens=None, top_logprobs=None, stream=None,
+                      allocate: bool = False) -> tuple:
     """Enqueue sv_token_logprobs on logits [B][N][V]: tokens and logprobs
     [B][R] or [B][R][M], entropy [B][R], top_tokens and top_logprobs
-    [B][R][top]."""
-    if logits.dim() != 3 or (logits.shape[2] > 1 and logits.stride(2) != 1):
-        raise ValueError("logits: expected [B][N][V] with contiguous rows")
-    B, N, V = logits.shape
-    dev = workspace.get_device()
-    if logits.get_device() != dev:
-        _wrong_device(logits, dev)
-    M = 0
-    if tokens is not None:
-        if tokens.dim() not in (2, 3):
-            raise ValueError("tokens: expected [B][R] or [B][R][M]")
-        M = tokens.shape[2] if tokens.dim() == 3 else 1
-    shape = (B, R) if tokens is None else (B, R, *tokens.shape[2:])
-    batch, row, _ = logits.stride()
-    _kv_call("sv_token_logprobs", _pack_logprobs(
-        B, N, R, M, V, _dtype_code(logits), logits.data_ptr(), batch if B > 1 else 0,
-        row if N > 1 else 0, _addr(tokens, torch.int32, shape, "tokens", dev),
-        _addr(num_rows, torch.int32, (B,), "num_rows", dev),
-        _addr(rows, torch.int32, (B, R), "rows", dev),
-        _addr(temperature, torch.float32, (B,), "temperature", dev), top,
-        _addr(logprobs, torch.float32, shape, "logprobs", dev),
-        _addr(entropy, torch.float32, (B, R), "entropy", dev),
-        _addr(top_tokens, torch.int32, (B, R, top), "top_tokens", dev),
-        _addr(top_logprobs, torch.float32, (B, R, top), "top_logprobs", dev)),
-        workspace, dev, stream)
+    [B][R][top] (allocate: new tensors for all that is asked for).  Returns
+    logprobs, entropy, top_tokens and top_logprobs."""
+    if stream is not None:
+        stream = _raw_stream(stream)
+    return _launched("sv_token_logprobs", (_native_module or _native()).token_logprobs(
+        _entry("sv_token_logprobs"), workspace, stream, logits, R, tokens, num_rows, rows,
+        temperature, top, allocate, logprobs, entropy, top_tokens, top_logprobs))

@@ -5,6 +5,7 @@ import concurrent.futures
 import os
 import shutil
 import subprocess
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -13,6 +14,8 @@ INCLUDE = os.path.join(ROOT, "include")
 LIBRARY = os.path.join(PKG, "libspecverify.so")
 # the debug build: device-side bounds and alignment checks (-DSV_CHECKS)
 LIBRARY_CHECKS = os.path.join(PKG, "libspecverify_checks.so")
+# the compiled part of the Python binding
+NATIVE = os.path.join(PKG, "_native.so")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 
@@ -77,3 +80,45 @@ def build_library(force: bool = False, verbose: bool = False, extra_flags=(),
     with open(stamp, "w") as f:
         f.write(" ".join(flags))
     return out
+
+
+def native_command(out: str) -> list[str]:
+    """The host compiler's call for the compiled part of the binding (csrc/native.cpp
+    against torch's headers)."""
+    import torch
+    gxx = shutil.which("g++") or shutil.which("c++")
+    if gxx is None:
+        raise RuntimeError("g++ not found: needed for the compiled part of the binding")
+    root = os.path.dirname(torch.__file__)
+    abi = int(torch._C._GLIBCXX_USE_CXX11_ABI)
+    return [gxx, "-O2", "-std=c++17", "-fPIC", "-shared", f"-D_GLIBCXX_USE_CXX11_ABI={abi}",
+            f"-I{INCLUDE}", f"-I{root}/include", f"-I{root}/include/torch/csrc/api/include",
+            f"-I{sysconfig.get_path('include')}", f"-I{cuda_home()}/include",
+            os.path.join(CSRC, "native.cpp"), "-o", out, f"-L{root}/lib", "-ltorch_python",
+            "-ltorch_cpu", "-lc10", "-lc10_cuda"]
+
+
+def cuda_home() -> str:
+    return os.path.dirname(os.path.dirname(os.path.realpath(nvcc())))
+
+
+def build_native(force: bool = False) -> str:
+    """Compile csrc/native.cpp into _native.so, for this torch and Python."""
+    import torch
+    source = os.path.join(CSRC, "native.cpp")
+    stamp = NATIVE + ".flags"
+    flags = " ".join([torch.__version__, sysconfig.get_python_version(), *native_command(NATIVE)])
+    newest = max(os.path.getmtime(p) for p in (source, os.path.join(INCLUDE, "specverify.h")))
+    if (not force and os.path.exists(stamp) and open(stamp).read() == flags
+            and os.path.exists(NATIVE) and os.path.getmtime(NATIVE) >= newest):
+        return NATIVE
+    tmp = NATIVE + f".tmp{os.getpid()}"
+    try:
+        subprocess.run(native_command(tmp), check=True)
+        os.replace(tmp, NATIVE)
+    finally:
+        if os.path.exists(tmp):
+            os.remove(tmp)
+    with open(stamp, "w") as f:
+        f.write(flags)
+    return NATIVE

@@ -167,75 +167,52 @@ def test_refusals_of_log_probabilities(b):
 
 # ----------------------------------------------------------------- binding
 
-class OnDevice:
-    """A CPU tensor that says it lives on a GPU."""
-
-    def __init__(self, t, index=0):
-        self.t, self.index = t, index
-
-    def __getattr__(self, name):
-        return getattr(self.t, name)
-
-    def get_device(self):
-        return self.index
-
-    @property
-    def device(self):
-        return torch.device("cuda", self.index) if self.index >= 0 else torch.device("cpu")
-
-
-class Launches(list):
-    def __getattr__(self, name):
-        return lambda *args: (self.append((name, args[0])), 0)[1]
-
-
-@pytest.fixture
-def launches(b, monkeypatch):
-    got = Launches()
-    monkeypatch.setattr(b, "_lib_handle", got)
-    monkeypatch.setattr(b, "_current_device", lambda: 0)
-    monkeypatch.setattr(b, "current_raw_stream", lambda dev: 0)
-    return got
+@pytest.fixture(scope="module")
+def native(b):
+    _build.build_native()
+    return b._native()
 
 
 def tensors(op):
+    """Arguments of the compiled binding, in its order, on the CPU; entry 0 gives the
+    packed structure back."""
     i32 = lambda *s: torch.zeros(s, dtype=torch.int32)  # noqa: E731
     x = lambda h: torch.zeros((2, 3, h, 64), dtype=torch.bfloat16)  # noqa: E731
     codes = lambda: torch.zeros((4, 2, 16, 64), dtype=torch.uint8).view(  # noqa: E731
         torch.float8_e4m3fn)
-    ws = torch.zeros(8192, dtype=torch.uint8)
-    rope = dict(sv.rope(64, device="cpu"), freq=OnDevice(sv.rope(64, device="cpu")["freq"]))
-    if op == "logprobs":
-        d = dict(logits=torch.zeros(2, 3, 50), workspace=ws, tokens=i32(2, 3), num_rows=i32(2),
-                 rows=i32(2, 3), temperature=torch.ones(2), logprobs=torch.zeros(2, 3),
-                 entropy=torch.zeros(2, 3), top_tokens=i32(2, 3, 4),
-                 top_logprobs=torch.zeros(2, 3, 4))
-        return {k: OnDevice(v) for k, v in d.items()} | dict(R=3, top=4)
+    a = dict(entry=0, workspace=torch.zeros(8192, dtype=torch.uint8), stream=None)
+    if op == "token_logprobs":
+        return a | dict(logits=torch.zeros(2, 3, 50), R=None, tokens=i32(2, 3), num_rows=i32(2),
+                        rows=i32(2, 3), temperature=torch.ones(2), top=4, allocate=False,
+                        logprobs=torch.zeros(2, 3), entropy=torch.zeros(2, 3),
+                        top_tokens=i32(2, 3, 4), top_logprobs=torch.zeros(2, 3, 4))
     w = torch.ones(64, dtype=torch.bfloat16)
-    d = dict(q=x(4), q_out=x(4), workspace=ws, offset=i32(2, 3), q_weight=w, k_weight=w.clone())
+    tail = dict(offset=i32(2, 3), rope=sv.rope(64, device="cpu"), q_weight=w, k_weight=w.clone(),
+                eps=1e-6)
     if op == "rotate":
-        d |= dict(k=x(2), k_out=x(2), start=i32(2), num=i32(2))
-        return {k: OnDevice(v) for k, v in d.items()} | dict(rope=rope, eps=1e-6)
-    d |= dict(page_table=i32(2, 2), kv_len=i32(2), num_new=i32(2), k_new=x(2), v_new=x(2))
+        return a | dict(q=x(4), q_out=x(4), k=x(2), k_out=x(2), start=i32(2), num=i32(2)) | tail
     cache = dict(k=codes(), v=codes(), k_scale=torch.ones(4, 2), v_scale=torch.ones(4, 2))
-    return ({k: OnDevice(v) for k, v in d.items()} |
-            dict(rope=rope, eps=1e-6, cache={k: OnDevice(v) for k, v in cache.items()}))
+    return a | dict(cache=cache, page_table=i32(2, 2), kv_len=i32(2), q=x(4), q_out=x(4),
+                    q_dtype=None, k_new=x(2), v_new=x(2), num_new=i32(2)) | tail
 
 
-FUNCS = {"rotate": "sv_rotate", "append": "sv_kv_append", "logprobs": "sv_token_logprobs"}
+OPS = ["rotate", "kv_append", "token_logprobs"]
 
 
-@pytest.mark.parametrize("op", list(FUNCS))
-def test_packed_arguments(b, launches, op):
+def packed(b, native, op, a):
+    cls = {"rotate": b.SvRotateArgs, "kv_append": b.SvKvAppendArgs,
+           "token_logprobs": b.SvTokenLogprobsArgs}[op]
+    raw = getattr(native, op)(*a.values())
+    assert len(raw) == ctypes.sizeof(cls)
+    return cls.from_buffer_copy(raw)
+
+
+@pytest.mark.parametrize("op", OPS)
+def test_packed_arguments(b, native, op):
     """What the binding packs is the structure's fields."""
     a = tensors(op)
-    getattr(b, FUNCS[op])(**a)
-    [(name, packed)] = launches
-    assert name == FUNCS[op]
-    cls = {"rotate": b.SvRotateArgs, "append": b.SvKvAppendArgs,
-           "logprobs": b.SvTokenLogprobsArgs}[op]
-    s = cls.from_buffer_copy(packed)
-    if op == "logprobs":
+    s = packed(b, native, op, a)
+    if op == "token_logprobs":
         assert (s.B, s.N, s.R, s.M, s.V, s.top, s.dtype) == (2, 3, 3, 1, 50, 4, b.SV_FP32)
         assert (s.batch_stride, s.row_stride) == (150, 50)
         for f, t in [("logits", "logits"), ("tokens", "tokens"), ("rows", "rows"),
@@ -253,62 +230,124 @@ def test_packed_arguments(b, launches, op):
     k = s.k.norm if op == "rotate" else s.k_norm
     assert k.weight == a["k_weight"].data_ptr() and k.weight_dtype == b.SV_BF16
     if op == "rotate":
-        assert (s.k.heads, s.start, s.num) == (2, a["start"].data_ptr(), a["num"].data_ptr())
+        assert (s.D, s.k.heads, s.start, s.num) == (64, 2, a["start"].data_ptr(),
+                                                    a["num"].data_ptr())
     else:
+        c = s.cache
+        assert (c.num_pages, c.page_size, c.Hkv, c.D, c.slots) == (4, 16, 2, 64, 2)
+        assert (c.page_stride, c.head_stride, c.k) == (2048, 1024, a["cache"]["k"].data_ptr())
+        assert (c.v_scale, c.page_table) == (a["cache"]["v_scale"].data_ptr(),
+                                             a["page_table"].data_ptr())
         assert (s.k_new, s.v_token_stride) == (a["k_new"].data_ptr(), 128)
         assert (s.kv_len, s.num_new) == (a["kv_len"].data_ptr(), a["num_new"].data_ptr())
 
 
-@pytest.mark.parametrize("op", list(FUNCS))
-def test_tensors_of_another_device_are_refused(b, launches, op):
+def test_packed_strides_and_options(b, native):
+    """Slices of a projection, dimensions of size one, in place, no norm, no rope, no
+    keys; tokens [B][R][M]; what is not asked for."""
+    x = torch.zeros(2, 3, 8, 64, dtype=torch.float16)
+    a = tensors("rotate") | dict(q=x[:, :, 2:6], q_out=..., k=None, k_out=None, rope=None,
+                                 q_weight=None, k_weight=None, eps=None, start=None)
+    s = packed(b, native, "rotate", a)
+    assert (s.q.x, s.q.out, s.q.heads) == (x.data_ptr() + 2 * 64 * 2, x.data_ptr() + 2 * 64 * 2, 4)
+    assert (s.q.token_stride, s.q.out_token_stride) == (512, 512)
+    assert (s.k.heads, s.q.norm.eps, s.rope.dim, s.rope.scale, s.start) == (0, 0.0, 0, 1.0, None)
+    one = torch.zeros(1, 1, 1, 64).as_strided((1, 1, 1, 64), (7, 9, 11, 1))
+    a = tensors("rotate") | dict(q=one, q_out=None, k=None, k_out=None, num=None, offset=None,
+                                 start=None, q_weight=None, k_weight=None)
+    s = packed(b, native, "rotate", a)
+    assert (s.q.batch_stride, s.q.token_stride, s.q.head_stride) == (0, 0, 0)
+    assert s.q.out not in (None, s.q.x)
+    a = tensors("kv_append") | dict(q_out=None, q_dtype=torch.float16)
+    assert packed(b, native, "kv_append", a).q.out_dtype == b.SV_FP16
+    a = tensors("kv_append") | dict(q=None, q_out=None, q_weight=None)
+    assert packed(b, native, "kv_append", a).q.heads == 0
+    a = tensors("token_logprobs") | dict(tokens=torch.zeros(2, 2, 5, dtype=torch.int32),
+                                         logprobs=None, entropy=None, rows=None, top=0,
+                                         top_tokens=None, top_logprobs=None)
+    s = packed(b, native, "token_logprobs", a)
+    assert (s.R, s.M, s.logprob, s.top_token) == (2, 5, None, None)
+    s = packed(b, native, "token_logprobs", a | dict(allocate=True, top=3))
+    assert s.logprob and s.entropy and s.top_token and s.top_logprob
+
+
+@pytest.mark.parametrize("op", OPS)
+def test_tensors_of_another_device_are_refused(native, op):
     ok = tensors(op)
     for name, t in ok.items():
-        for bad in (1, -1):
-            if isinstance(t, OnDevice):
-                wrong = OnDevice(t.t, bad)
-            elif name == "rope":
-                wrong = dict(t, freq=OnDevice(t["freq"].t, bad))
-            elif name == "cache":
-                wrong = dict(t, v_scale=OnDevice(t["v_scale"].t, bad))
-            else:
-                continue
-            with pytest.raises(ValueError):
-                getattr(b, FUNCS[op])(**(ok | {name: wrong}))
-    assert launches == []
+        if isinstance(t, torch.Tensor):
+            wrong = torch.empty_strided(t.shape, t.stride(), dtype=t.dtype, device="meta")
+        elif name == "rope":
+            wrong = dict(t, freq=t["freq"].to("meta"))
+        elif name == "cache":
+            wrong = dict(t, v_scale=t["v_scale"].to("meta"))
+        else:
+            continue
+        with pytest.raises(ValueError):
+            getattr(native, op)(*(ok | {name: wrong}).values())
+
+
+@pytest.mark.parametrize("op", OPS)
+def test_tensors_of_the_cpu_are_refused(b, native, op):
+    """... by a call that is not asked for its structure."""
+    a = tensors(op) | dict(entry=b._entry({"rotate": "sv_rotate", "kv_append": "sv_kv_append",
+                                           "token_logprobs": "sv_token_logprobs"}[op]))
+    with pytest.raises(ValueError, match="device tensors"):
+        getattr(native, op)(*a.values())
 
 
 WRONG = {
     "rotate": [dict(k=torch.zeros(2, 3, 2, 64)), dict(k=torch.zeros(2, 4, 2, 64).bfloat16()),
                dict(q_out=torch.zeros(2, 3, 5, 64).bfloat16()), dict(eps=None), dict(eps=0.0),
+               dict(eps=math.nan), dict(k=None, k_out=None), dict(q=torch.zeros(2, 3, 64)),
+               dict(q=torch.zeros(2, 3, 64, 4).bfloat16().transpose(2, 3)),
+               dict(q=torch.zeros(2, 3, 4, 64, dtype=torch.int32)), dict(q=None), dict(q=3),
                dict(q_weight=torch.ones(32)), dict(q_weight=torch.ones(64, dtype=torch.int32)),
                dict(start=torch.zeros(2)), dict(num=torch.zeros(3, dtype=torch.int32)),
-               dict(offset=torch.zeros(3, 2, dtype=torch.int32))],
-    "append": [dict(q=torch.zeros(2, 3, 4, 64)), dict(q=torch.zeros(2, 3, 4, 128).bfloat16()),
-               dict(v_new=torch.zeros(2, 3, 2, 64)), dict(eps=None), dict(eps=-1.0),
-               dict(kv_len=torch.zeros(2, dtype=torch.int64)),
-               dict(k_weight=torch.ones(128)), dict(offset=torch.zeros(2, dtype=torch.int32))],
-    "logprobs": [dict(logits=torch.zeros(2, 3, 50).half()), dict(logits=torch.zeros(2, 150)),
-                 dict(logits=torch.zeros(2, 50, 3).transpose(1, 2)),
-                 dict(tokens=torch.zeros(2, 4, dtype=torch.int32)),
-                 dict(tokens=torch.zeros(2, dtype=torch.int32)),
-                 dict(logprobs=torch.zeros(2, 3, 1)), dict(top_tokens=torch.zeros(2, 3, 4)),
-                 dict(temperature=torch.ones(3)), dict(rows=torch.zeros(2, 2, dtype=torch.int32))],
+               dict(offset=torch.zeros(3, 2, dtype=torch.int32)), dict(rope=5), dict(rope={})],
+    "kv_append": [dict(q=torch.zeros(2, 3, 4, 64)), dict(q=torch.zeros(2, 3, 4, 128).bfloat16()),
+                  dict(v_new=torch.zeros(2, 3, 2, 64)), dict(eps=None), dict(eps=-1.0),
+                  dict(kv_len=torch.zeros(2, dtype=torch.int64)), dict(q_dtype=3),
+                  dict(k_new=torch.zeros(2, 3, 3, 64).bfloat16()), dict(cache={}), dict(cache=1),
+                  dict(page_table=torch.zeros(4, dtype=torch.int32)), dict(q=None, q_out=None),
+                  dict(k_weight=torch.ones(128)), dict(offset=torch.zeros(2, dtype=torch.int32))],
+    "token_logprobs": [dict(logits=torch.zeros(2, 3, 50).half()), dict(logits=torch.zeros(2, 150)),
+                       dict(logits=torch.zeros(2, 50, 3).transpose(1, 2)), dict(R=4),
+                       dict(tokens=torch.zeros(2, 4, dtype=torch.int32)),
+                       dict(tokens=torch.zeros(2, dtype=torch.int32)), dict(top=65), dict(top=-1),
+                       dict(logprobs=torch.zeros(2, 3, 1)), dict(top_tokens=torch.zeros(2, 3, 4)),
+                       dict(temperature=torch.ones(3)), dict(R=-1, allocate=True),
+                       dict(rows=torch.zeros(2, 2, dtype=torch.int32))],
 }
 
 
-@pytest.mark.parametrize("op", list(FUNCS))
-def test_wrong_types_and_shapes_are_refused(b, launches, op):
+@pytest.mark.parametrize("op", OPS)
+def test_wrong_types_and_shapes_are_refused(native, op):
     ok = tensors(op)
     for kw in WRONG[op]:
-        kw = {k: OnDevice(v) if isinstance(v, torch.Tensor) else v for k, v in kw.items()}
         with pytest.raises(ValueError):
-            getattr(b, FUNCS[op])(**(ok | kw))
-    if op != "logprobs":
+            getattr(native, op)(*(ok | kw).values())
+    if op != "token_logprobs":
         rope = ok["rope"]
-        for bad in (dict(rope, dim=32), dict(rope, freq=OnDevice(torch.zeros(32)))):
+        for bad in (dict(rope, dim=32), dict(rope, freq=torch.zeros(32))):
             with pytest.raises(ValueError):
-                getattr(b, FUNCS[op])(**(ok | dict(rope=bad)))
-    assert launches == []
+                getattr(native, op)(*(ok | dict(rope=bad)).values())
+    if op == "kv_append":
+        for bad in (dict(v=torch.zeros(4, 2, 16, 64)), dict(k_scale=torch.ones(4, 3)),
+                    dict(k=torch.zeros(4, 2, 16, 64)), dict(v_scale=torch.ones(4, 2).double())):
+            with pytest.raises(ValueError):
+                native.kv_append(*(ok | dict(cache=ok["cache"] | bad)).values())
+    for n in (0, 3, 40):
+        with pytest.raises(TypeError):
+            getattr(native, op)(*[None] * n)
+
+
+def test_a_missing_build_is_reported(b, monkeypatch):
+    monkeypatch.setattr(b, "_native_module", None)
+    monkeypatch.setitem(__import__("sys").modules, b.__package__ + "._native", None)
+    monkeypatch.delattr(sv, "_native", raising=False)
+    with pytest.raises(RuntimeError, match="build"):
+        b._native()
 
 
 # -------------------------------------------------------------------- rope
