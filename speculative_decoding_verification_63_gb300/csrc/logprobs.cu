@@ -82,7 +82,8 @@ sv_status sv_token_logprobs(const sv_token_logprobs_args* a, void* workspace, si
   // a map fits its CTA (whole 32s of groups)
   auto share = [&] { return ((groups + 31) / 32 + p.cluster - 1) / p.cluster * 32; };
   while (a->top > 0 && share() * es > kLpMapBytes) p.cluster *= 2;
-  const size_t map = a->top > 0 ? static_cast<size_t>(share()) * es : 0;
+  p.share = share();
+  const size_t map = a->top > 0 ? static_cast<size_t>(p.share) * es : 0;
   // Maxima of each warp that make the bound: somewhat more in all than are asked
   // for (the likeliest tokens are often neighbours, in the hands of one warp), a
   // power of two.

@@ -140,10 +140,16 @@ Tensor empty(IntArrayRef shape, ScalarType dtype, const Place& p) {
   return at::empty(shape, at::TensorOptions().dtype(dtype).device(p.device));
 }
 
+// New tensors belong to the current stream: a call on another one is given its
+// results.
+void own(PyObject* stream, const char* what) {
+  if (given(stream)) refuse(std::string(what) + ": a call on a given stream needs its results");
+}
+
 // One kind of heads; `out` (kept in `keep`) is given, or allocated as `dtype`, or, for
 // Ellipsis, x itself.
 void heads(sv_heads& h, PyObject* x, PyObject* out, ScalarType dtype, PyObject* weight,
-           PyObject* eps, const char* what, const Place& p, Tensor& keep) {
+           PyObject* eps, PyObject* stream, const char* what, const Place& p, Tensor& keep) {
   const Tensor& t = tensor(x, what);
   const IntArrayRef shape = t.sizes();
   h.heads = static_cast<int>(shape[2]);
@@ -160,6 +166,7 @@ void heads(sv_heads& h, PyObject* x, PyObject* out, ScalarType dtype, PyObject* 
     keep = tensor(out, what);
     rows(keep, shape, what, p, s);
   } else {
+    own(stream, what);
     keep = empty(shape, dtype, p);
     for (int i = 0; i < 3; ++i) s[i] = shape[i] > 1 ? keep.stride(i) : 0;
   }
@@ -245,7 +252,7 @@ PyObject* rotate(PyObject*, PyObject* const* v, Py_ssize_t nv) {
     a.D = small(D, "q");
     a.dtype = dtype_of(q, "q");
     Tensor q_out, k_out;
-    heads(a.q, v[3], v[4], q.scalar_type(), v[11], v[13], "q", p, q_out);
+    heads(a.q, v[3], v[4], q.scalar_type(), v[11], v[13], v[2], "q", p, q_out);
     if (given(v[5])) {
       const Tensor& k = tensor(v[5], "k");
       four(k, "k");
@@ -253,7 +260,7 @@ PyObject* rotate(PyObject*, PyObject* const* v, Py_ssize_t nv) {
         refuse("k: expected [" + std::to_string(B) + "][" + std::to_string(T) + "][heads][" +
                std::to_string(D) + "] of q's dtype, got " + c10::toString(k.scalar_type()) + " " +
                text(k.sizes()));
-      heads(a.k, v[5], v[6], k.scalar_type(), v[12], v[13], "k", p, k_out);
+      heads(a.k, v[5], v[6], k.scalar_type(), v[12], v[13], v[2], "k", p, k_out);
     } else if (given(v[12])) {
       refuse("k_weight: a norm's weight, but no k");
     }
@@ -346,7 +353,7 @@ PyObject* kv_append(PyObject*, PyObject* const* v, Py_ssize_t nv) {
         if (!THPDtype_Check(v[8])) refuse("q_dtype: expected a dtype");
         dtype = reinterpret_cast<THPDtype*>(v[8])->scalar_type;
       }
-      heads(a.q, v[6], v[7], dtype, v[14], v[16], "q", p, q_out);
+      heads(a.q, v[6], v[7], dtype, v[14], v[16], v[2], "q", p, q_out);
     } else if (given(v[14])) {
       refuse("q_weight: a norm's weight, but no q");
     }
@@ -414,6 +421,7 @@ PyObject* token_logprobs(PyObject*, PyObject* const* v, Py_ssize_t nv) {
         static_cast<const float*>(address(v[8], ScalarType::Float, {B}, "temperature", p));
     Tensor out[4];
     if (PyObject_IsTrue(v[10])) {
+      own(v[2], "logits");
       if (R < 0) refuse("R: out of range");
       if (given(v[5])) out[0] = empty(asked, ScalarType::Float, p);
       out[1] = empty(one, ScalarType::Float, p);

@@ -44,6 +44,7 @@ constexpr int kLpPublished = 256;  // maxima that make the bound
 struct LogprobProblem {
   int B, N, R, M, V, top;
   int cluster;     // CTAs of a row
+  int share;       // groups that a CTA's map has room for
   int published;   // maxima of each warp that make the bound: 2^all_shift in all
   int all_shift;
   const void* logits;
@@ -153,6 +154,9 @@ struct LpRow {
   __device__ __forceinline__ bool whole(int g) const {
     const int first = g * kLpGroup - off;
     return first >= 0 && first + kLpGroup <= V;
+  }
+  __device__ __forceinline__ bool aligned(int g) const {
+    return (reinterpret_cast<uintptr_t>(x + (g * kLpGroup - off)) & 31) == 0;
   }
   __device__ __forceinline__ void load(LpRaw<T>& r, int g) const {
     const char* p = reinterpret_cast<const char*>(x + (g * kLpGroup - off));
@@ -327,7 +331,7 @@ __device__ __forceinline__ void lp_read_groups(const LpRow<T>& in, const int* gr
       v[q] = kNegInf;
       id[q] = -1;
       if (e < groups * kLpGroup) id[q] = group[e / kLpGroup] * kLpGroup + e % kLpGroup - in.off;
-      if (id[q] >= 0 && id[q] < in.V) v[q] = lp_value(in.x + id[q]);
+      if (id[q] >= 0 && id[q] < in.V) v[q] = lp_value(in.x + id[q]);  // (an edge's rest is none)
     }
 #pragma unroll
     for (int q = 0; q < N; ++q) {
@@ -465,7 +469,8 @@ __global__ void __launch_bounds__(kLpThreads, kLpCtasPerSm) logprob_kernel(const
   in.V = a.V;
   const int all = (a.V + in.off + kLpGroup - 1) / kLpGroup;
   const LpShare share{a.cluster, rank};
-  const int groups = share.count(all);
+  int groups = share.count(all);
+  if (TOP && !SV_CHECK(groups <= a.share, a.err)) groups = 0;  // the map's size
   const float c = fminf(1.44269504f / t, 3e38f), inv_t = fminf(1.f / t, 3e38f);
   Map* const map = reinterpret_cast<Map*>(lp_map);
   float given = 0.f;  // the given token's logit, for the end
@@ -485,7 +490,7 @@ __global__ void __launch_bounds__(kLpThreads, kLpCtasPerSm) logprob_kernel(const
     for (int u = 0; u < U; ++u) {
       const int g = share.group(i0 + u * kLpThreads);
       here[u] = i0 + u * kLpThreads < groups && in.whole(g);
-      if (here[u]) {
+      if (here[u] && SV_CHECK(in.aligned(g), a.err)) {
         in.load(raw[u], g);
       } else {
 #pragma unroll

@@ -108,10 +108,14 @@ struct Ahead {
   uint4 slot[kStages][kPieces][THREADS];
 
   template <bool NEAR>
-  __device__ __forceinline__ void ask(int i, int chunk, const T* p, const Place& at, bool vec) {
+  __device__ __forceinline__ void ask(int i, int chunk, const T* p, const Place& at, bool vec,
+                                      int* err) {
     constexpr int H = static_cast<int>(sizeof(T)) / 2;
     uint4(*to)[THREADS] = &slot[i % kStages][chunk * 2 * H];
-    if (vec) {
+    if (vec && SV_CHECK(((reinterpret_cast<uintptr_t>(p + at.a) |
+                          reinterpret_cast<uintptr_t>(p + at.b)) & 15) == 0 &&
+                            chunk * 2 * H + 2 * H <= kPieces,
+                        err)) {
 #pragma unroll
       for (int k = 0; k < H; ++k) {
         copy<NEAR>(&to[k][threadIdx.x], reinterpret_cast<const uint4*>(p + at.a) + k);
@@ -356,7 +360,7 @@ __device__ __forceinline__ long long position_of(const int* start, const int* of
 template <class T, bool NEAR, class Feed>
 __device__ __forceinline__ void rotate_heads(const Heads& h, const Rope& rope, int b, int n, int T_,
                                              const int* start, const int* offset, int D,
-                                             int lane_shift, int thread, Feed& feed) {
+                                             int lane_shift, int thread, Feed& feed, int* err) {
   // (at most 2^16 tokens of 16 lanes, 256 heads and a block's rounding: 32 bits)
   const int per_chunk = T_ << lane_shift, lanes = 1 << lane_shift;
   const int chunk = thread / per_chunk, rest = thread - chunk * per_chunk;
@@ -370,7 +374,7 @@ __device__ __forceinline__ void rotate_heads(const Heads& h, const Rope& rope, i
   const T* ask = x;
 #pragma unroll
   for (int i = 0; i < Feed::kStages - 1; ++i, ask += h.head) {
-    if (live && i < heads) feed.template ask<NEAR>(i, 0, ask, at, h.x_vec);
+    if (live && i < heads) feed.template ask<NEAR>(i, 0, ask, at, h.x_vec, err);
     Feed::commit();
   }
 
@@ -413,7 +417,7 @@ __device__ __forceinline__ void rotate_heads(const Heads& h, const Rope& rope, i
     if (live && i < heads) feed.take(raw, i, 0, x, at, h.x_vec);
     x += h.head;
     if (live && i + Feed::kStages - 1 < heads)
-      feed.template ask<NEAR>(i + Feed::kStages - 1, 0, ask, at, h.x_vec);
+      feed.template ask<NEAR>(i + Feed::kStages - 1, 0, ask, at, h.x_vec, err);
     ask += h.head;
     Feed::commit();
     Pairs y = pairs_of<NEAR>(raw);
@@ -465,7 +469,7 @@ __global__ void __launch_bounds__(kRotateThreads, 3) rotate_kernel(const RotateP
   const bool keys = block >= a.q.blocks;
   if (keys) block -= a.q.blocks;
   rotate_heads<T, NEAR>(keys ? a.k : a.q, a.rope, b, n, a.T, a.start, a.offset, a.D, a.lane_shift,
-                  block * kRotateThreads + static_cast<int>(threadIdx.x), feed);
+                  block * kRotateThreads + static_cast<int>(threadIdx.x), feed, a.err);
 }
 
 // ------------------------------------------------------------------ append
@@ -540,7 +544,8 @@ __device__ __forceinline__ void append_pages(const KvAppendProblem& a, int b, in
   for (int i = 0; i < Feed::kStages - 1; ++i) {
 #pragma unroll
     for (int k = 0; k < CH; ++k)
-      if (i < heads && gl + k * GT < chunks) feed.template ask<NEAR>(i, k, src[k] + i * head, at, vec);
+      if (i < heads && gl + k * GT < chunks) 
+        feed.template ask<NEAR>(i, k, src[k] + i * head, at, vec, a.err);
     Feed::commit();
   }
   const bool reports = h0 == 0 && side == 0 && gl == 0;
@@ -579,7 +584,7 @@ __device__ __forceinline__ void append_pages(const KvAppendProblem& a, int b, in
       RawPairs<T> raw = {};
       if (here && gl + k * GT < chunks) feed.take(raw, hh, k, src[k], at, vec);
       if (hh + stages < heads && gl + k * GT < chunks)
-        feed.template ask<NEAR>(hh + stages, k, src[k] + stages * head, at, vec);
+        feed.template ask<NEAR>(hh + stages, k, src[k] + stages * head, at, vec, a.err);
       src[k] += head;
       y[k] = pairs_of<NEAR>(raw);
     }
@@ -705,7 +710,7 @@ __global__ void __launch_bounds__(THREADS, THREADS == 256 ? (CH == 1 ? 3 : 2) : 
     rotate_heads<T, NEAR>(a.q, a.rope, b, ok ? n : 0, a.T, a.kv_len, a.offset, a.c.D,
                           a.c.D == 64 ? 2 : 3,
                           (static_cast<int>(blockIdx.x) - a.blocks) * THREADS +
-                              static_cast<int>(threadIdx.x), feed.q);
+                              static_cast<int>(threadIdx.x), feed.q, a.err);
   else
     append_pages<T, NEAR, THREADS, CH>(a, b, len, n, ok, red, feed.kv);
 }

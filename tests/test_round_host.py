@@ -337,6 +337,12 @@ def test_wrong_types_and_shapes_are_refused(native, op):
                     dict(k=torch.zeros(4, 2, 16, 64)), dict(v_scale=torch.ones(4, 2).double())):
             with pytest.raises(ValueError):
                 native.kv_append(*(ok | dict(cache=ok["cache"] | bad)).values())
+    # new tensors belong to the current stream
+    own = {"rotate": dict(k_out=None), "kv_append": dict(q_out=None),
+           "token_logprobs": dict(allocate=True)}[op]
+    getattr(native, op)(*(ok | own).values())
+    with pytest.raises(ValueError, match="stream"):
+        getattr(native, op)(*(ok | own | dict(stream=7)).values())
     for n in (0, 3, 40):
         with pytest.raises(TypeError):
             getattr(native, op)(*[None] * n)
