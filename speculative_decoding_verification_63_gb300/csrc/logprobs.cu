@@ -89,7 +89,8 @@ sv_status sv_token_logprobs(const sv_token_logprobs_args* a, void* workspace, si
   // power of two.
   const int warps = p.cluster * kLpWarps;
   p.published = 1;
-  while (p.published * warps < std::max(64, 5 * a->top / 4)) p.published *= 2;
+  while (p.published * warps < std::min(kLpPublished, std::max(kLpLeast, 3 * a->top / 2)))
+    p.published *= 2;
   p.all_shift = 0;
   while ((1 << p.all_shift) < p.published * warps) ++p.all_shift;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);

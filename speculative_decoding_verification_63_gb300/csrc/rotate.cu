@@ -52,6 +52,12 @@ constexpr int kRotatePer = 16, kRotateFill = 128;
 // 512 tokens, by threads an SM: 1024 30 us, 512 25, 256 22, 128 26).
 constexpr int kAppendPer = 8, kAppendFill = 256;
 
+// `heads` in as many parts as `per` at a time make, of even sizes.
+int even(int heads, int per) {
+  const int parts = (heads + per - 1) / per;
+  return (heads + parts - 1) / parts;
+}
+
 // A kind of heads for blocks of `threads` threads; B requests of T tokens of
 // `lanes` lanes.
 Heads heads_view(const sv_heads& h, sv_dtype dtype, int B, int T, int lanes, int threads, int sms) {
@@ -77,6 +83,7 @@ Heads heads_view(const sv_heads& h, sv_dtype dtype, int B, int T, int lanes, int
   v.per = std::min(kRotatePer, h.heads);
   while (v.per > 1 && one * ((h.heads + v.per - 1) / v.per) < int64_t{kRotateFill} * sms)
     v.per = (v.per + 1) / 2;
+  v.per = even(h.heads, v.per);
   const int64_t mine = static_cast<int64_t>(T) * lanes * ((h.heads + v.per - 1) / v.per);
   v.blocks = static_cast<int>((mine + threads - 1) / threads);
   return v;
@@ -193,6 +200,7 @@ sv_status sv_kv_append(const sv_kv_append_args* a, void* workspace, size_t ws_by
   while (p.per > 1 && static_cast<int64_t>(a->B) * p.pages * 2 * p.group *
                               ((p.c.Hkv + p.per - 1) / p.per) < int64_t{kAppendFill} * dev.sms)
     p.per = (p.per + 1) / 2;
+  p.per = even(p.c.Hkv, p.per);
   p.chunks = (p.c.Hkv + p.per - 1) / p.per;
   const int64_t threads = static_cast<int64_t>(p.pages) * 2 * p.chunks * p.group;
   p.blocks = static_cast<int>((threads + block - 1) / block);

@@ -39,7 +39,10 @@ constexpr int kLpMaxCluster = 8;
 constexpr int kLpMapBytes = 34816; // most that a CTA's map holds
 constexpr int kLpList = SV_MAX_TOPK * kLpGroup;  // items that are ranked by counting
 constexpr int kLpGroups = 512;     // groups that a CTA reads again
-constexpr int kLpPublished = 256;  // maxima that make the bound
+constexpr int kLpPublished = 128;  // maxima that make the bound, at most
+constexpr int kLpLeast = 32;       // and at least: a thread's share of them is whole uint4s
+static_assert(kLpLeast * kLpLeast / kLpThreads % 4 == 0 && kLpMaxCluster * kLpWarps <= kLpPublished,
+              "shares of the published maxima");
 
 struct LogprobProblem {
   int B, N, R, M, V, top;
@@ -60,6 +63,11 @@ __device__ __forceinline__ float max_nan(float a, float b) {
   float d;
   asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
   return d;
+}
+__device__ __forceinline__ float warp_max_nan(float v) {
+  float m;
+  asm volatile("redux.sync.max.NaN.f32 %0, %1, 0xffffffff;" : "=f"(m) : "f"(v));
+  return m;
 }
 __device__ __forceinline__ unsigned warp_max_u32(unsigned v) {
   unsigned m;
@@ -237,10 +245,7 @@ __device__ __forceinline__ void lp_raise(LpSum& s, float to, float c) {
   s.m = to;
 }
 __device__ __forceinline__ LpSum lp_warp_sum(LpSum s, float c) {
-  float m = s.m;
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
-  lp_raise(s, m, c);
+  lp_raise(s, warp_max_nan(s.m), c);
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) {
     s.z += __shfl_xor_sync(0xffffffffu, s.z, o);
@@ -303,10 +308,9 @@ struct LpShared {
   float4 part[kLpMaxCluster * kLpWarps];         // first: the warps' sums
   alignas(16) unsigned long long item[kLpList];  // first: key << 32 | ~token (or ~group)
   alignas(16) unsigned published[kLpPublished];  // every: the warps' largest maxima,
-  unsigned larger[kLpPublished];                 // how many are larger, and the bound
+  unsigned larger[kLpPublished];                 // and how many are larger
   int group[kLpGroups];                          // every: groups that are read again
   unsigned groups;
-  unsigned bound;
   unsigned count[64];  // first: items; the bisections' steps (at most 2 + 32 + 25)
   float m, log_z, entropy;
 };
@@ -406,9 +410,9 @@ __device__ __noinline__ void lp_choose(const LogprobProblem& a, LpShared& sh,
 }
 
 // Bound: HBM for many rows (2047 rows of 128256 bf16 logits without likeliest
-// tokens 86 us, 90 % of the copy bandwidth; with 5 of them 95 us); for few rows the way
+// tokens 86 us, 90 % of the copy bandwidth; with 5 of them 94 us); for few rows the way
 // from one trip to memory to the next (launch, what the row is, its logits) and,
-// for the likeliest tokens, five barriers and a second look at memory, some 4 us.
+// for the likeliest tokens, four barriers and a second look at memory, some 4 us.
 // Four groups a thread in flight and four CTAs an SM: two groups and five CTAs
 // took 88 and 98 us, eight groups and three CTAs 98 and 109.
 template <class T, bool TOP>
@@ -588,7 +592,9 @@ __global__ void __launch_bounds__(kLpThreads, kLpCtasPerSm) logprob_kernel(const
   bool leave = false;
   if (TOP) {
     // The bound: the top-th largest of what was published.  A thread compares one
-    // of the keys with a share of them.
+    // of the keys with a share of them; a warp looks for the one with top - 1
+    // larger ones.
+    unsigned bound = Key::kNone + 1;  // (no logit of -inf is listed)
     {
       const int v = tid & ((1 << a.all_shift) - 1), each = (1 << 2 * a.all_shift) / kLpThreads;
       const int i0 = (tid >> a.all_shift) * each;
@@ -602,12 +608,11 @@ __global__ void __launch_bounds__(kLpThreads, kLpCtasPerSm) logprob_kernel(const
       }
       atomicAdd(&sh.larger[v], larger);
       __syncthreads();
-      // (no logit of -inf is listed)
-      if (i0 == 0 && sh.larger[v] == static_cast<unsigned>(a.top - 1))
-        sh.bound = max(k, Key::kNone + 1);
-      __syncthreads();
+#pragma unroll 1
+      for (int i = lane; i < 1 << a.all_shift; i += 32)
+        if (sh.larger[i] == static_cast<unsigned>(a.top - 1)) bound = max(bound, sh.published[i]);
+      bound = warp_max_u32(bound);
     }
-    const unsigned bound = sh.bound;
     if (Key::of(mine) >= bound) {
       // the thread's groups that reach it: of its best turn, rarely of others too
       const bool one = Key::of(second) < bound;

@@ -525,6 +525,9 @@ __device__ __forceinline__ void append_pages(const KvAppendProblem& a, int b, in
     }
   }
   int heads = count > 0 ? min(a.per, Hkv - h0) : 0;
+  const bool reports = h0 == 0 && side == 0 && gl == 0;
+  if (!ok && i == 0 && reports) record_error(a.err, SV_DERR_ARG);
+  if (!__syncthreads_or(heads > 0)) return;  // no page of the round here
   const int j = gl & (parts - 1);  // the same for all of a thread's chunks
   const int chunks = count << pshift;
   Place at = place_of<NEAR>(a.rope, j);
@@ -548,8 +551,6 @@ __device__ __forceinline__ void append_pages(const KvAppendProblem& a, int b, in
         feed.template ask<NEAR>(i, k, src[k] + i * head, at, vec, a.err);
     Feed::commit();
   }
-  const bool reports = h0 == 0 && side == 0 && gl == 0;
-  if (!ok && i == 0 && reports) record_error(a.err, SV_DERR_ARG);
   int page = 0;
   if (count > 0) {
     page = a.c.page_table[static_cast<long long>(b) * a.c.slots + slot];
