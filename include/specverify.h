@@ -487,7 +487,8 @@ typedef struct {
 } sv_head_norm;
 
 /* Heads of one kind, in and out: element (b, t, h, i) at b * batch_stride + t *
-   token_stride + h * head_stride + i. */
+   token_stride + h * head_stride + i.  No two elements of out share a place
+   (SV_EINVAL for a stride of 0 along more than one). */
 typedef struct {
   const void* x;
   void* out;               /* x itself (the same strides and type) or apart from it */

@@ -319,38 +319,51 @@ def rope(dim: int, base: float = 10000.0, interleaved: bool = False, scaling: di
     if not (base > 0 and math.isfinite(base)):
         raise ValueError(f"rope: base must be a positive number, got {base}")
     how = dict(scaling or {"type": "none"})
-    kind = how.pop("type", None)
-    pairs = dim // 2
+    kind, pairs, scale = how.pop("type", None), dim // 2, 1.0
+
+    def take(name, default=None):
+        x = how.pop(name, default)
+        if x is None:
+            raise ValueError(f"rope: {kind} scaling needs {name!r}")
+        if not (x > 0 and math.isfinite(x)):
+            raise ValueError(f"rope: {name} must be a positive number, got {x}")
+        return x
+
     if kind == "ntk":
-        if dim <= 2:
-            raise ValueError("rope: ntk scaling needs more than one pair")
-        base *= how["factor"] ** (dim / (dim - 2))
+        base *= take("factor") ** (dim / (dim - 2))
     f = [base ** (-2.0 * c / dim) for c in range(pairs)]
-    scale = 1.0
     if kind == "linear":
-        f = [x / how["factor"] for x in f]
+        s = take("factor")
+        f = [x / s for x in f]
     elif kind == "yarn":
-        s, context = how["factor"], how["context"]
+        s, context = take("factor"), take("context")
+        fast, slow = take("fast", 32.0), take("slow", 1.0)
+        if base <= 1:
+            raise ValueError(f"rope: yarn scaling needs a base above 1, got {base}")
 
         def pair(turns):  # the pair that turns so often over the trained context
             return dim * math.log(context / (turns * 2 * math.pi)) / (2 * math.log(base))
-        lo = max(math.floor(pair(how.get("fast", 32.0))), 0)
-        hi = min(math.ceil(pair(how.get("slow", 1.0))), dim - 1)
+        lo, hi = max(math.floor(pair(fast)), 0), min(math.ceil(pair(slow)), dim - 1)
         ramp = [min(1.0, max(0.0, (c - lo) / max(hi - lo, 1e-3))) for c in range(pairs)]
         f = [x * (1 - r) + x / s * r for x, r in zip(f, ramp)]
-        scale = how.get("attention", 0.1 * math.log(s) + 1.0 if s > 1 else 1.0)
+        scale = take("attention", 0.1 * math.log(s) + 1.0 if s > 1 else 1.0)
     elif kind == "wavelength":
-        s, context = how["factor"], how["context"]
-        low, high = how.get("low", 1.0), how.get("high", 4.0)
+        s, context = take("factor"), take("context")
+        low, high = take("low", 1.0), take("high", 4.0)
+        if low >= high:
+            raise ValueError("rope: wavelength scaling needs low < high")
         keep = [min(1.0, max(0.0, (context * x / (2 * math.pi) - low) / (high - low))) for x in f]
         f = [x * k + x / s * (1 - k) for x, k in zip(f, keep)]
     elif kind == "factors":
-        if len(how["factors"]) != pairs:
-            raise ValueError(f"rope: expected {pairs} factors, got {len(how['factors'])}")
-        f = [x / y for x, y in zip(f, how["factors"])]
-        scale = how.get("attention", 1.0)
+        factors = how.pop("factors", ())
+        if len(factors) != pairs or not all(x > 0 and math.isfinite(x) for x in factors):
+            raise ValueError(f"rope: expected {pairs} positive factors")
+        f = [x / y for x, y in zip(f, factors)]
+        scale = take("attention", 1.0)
     elif kind not in ("none", "ntk"):
         raise ValueError(f"rope: no scaling of type {kind!r}")
+    if how:
+        raise ValueError(f"rope: {kind} scaling does not take {', '.join(map(repr, how))}")
     return dict(freq=rope_turns(f, device), dim=dim, interleaved=bool(interleaved),
                 scale=float(scale))
 

@@ -81,6 +81,8 @@ sv_status sv_token_logprobs(const sv_token_logprobs_args* a, void* workspace, si
   if (p.cluster == 4 && rows * 8 <= dev.sms && groups > 4 * kLpThreads) p.cluster = 8;
   // a map fits its CTA (whole 32s of groups)
   auto share = [&] { return ((groups + 31) / 32 + p.cluster - 1) / p.cluster * 32; };
+  static_assert(((SV_MAX_V + 7 + 15) / 16 + 31) / 32 / kLpMaxCluster * 32 * 4 + 128 <= kLpMapBytes,
+                "the largest vocabulary");
   while (a->top > 0 && share() * es > kLpMapBytes) p.cluster *= 2;
   p.share = share();
   const size_t map = a->top > 0 ? static_cast<size_t>(p.share) * es : 0;
@@ -89,7 +91,7 @@ sv_status sv_token_logprobs(const sv_token_logprobs_args* a, void* workspace, si
   // power of two.
   const int warps = p.cluster * kLpWarps;
   p.published = 1;
-  while (p.published * warps < std::min(kLpPublished, std::max(kLpLeast, 3 * a->top / 2)))
+  while (p.published * warps < std::min(kLpPublished, std::max(kLpLeast, 5 * a->top / 2)))
     p.published *= 2;
   p.all_shift = 0;
   while ((1 << p.all_shift) < p.published * warps) ++p.all_shift;

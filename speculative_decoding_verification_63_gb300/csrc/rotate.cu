@@ -25,12 +25,15 @@ bool rope_ok(const sv_rope& r, int D) {
   return r.dim == 0 || (r.freq != nullptr && aligned(r.freq, 16) && r.scale - r.scale == 0.f);
 }
 
-bool heads_ok(const sv_heads& h, sv_dtype dtype) {
+bool heads_ok(const sv_heads& h, sv_dtype dtype, int B, int T) {
   if (h.heads < 0 || h.heads > SV_MAX_KV_HEADS) return false;
   if (h.heads == 0) return true;
   const size_t es = static_cast<size_t>(dtype_bytes(dtype));
   return dtype_ok(h.out_dtype) && h.x != nullptr && h.out != nullptr && aligned(h.x, es) &&
          aligned(h.out, static_cast<size_t>(dtype_bytes(h.out_dtype))) && norm_ok(h.norm) &&
+         // (results that share their places would be written by several threads)
+         (B <= 1 || h.out_batch_stride != 0) && (T <= 1 || h.out_token_stride != 0) &&
+         (h.heads <= 1 || h.out_head_stride != 0) &&
          (h.x != h.out ||
           (h.out_dtype == dtype && h.batch_stride == h.out_batch_stride &&
            h.token_stride == h.out_token_stride && h.head_stride == h.out_head_stride));
@@ -112,7 +115,8 @@ sv_status sv_rotate(const sv_rotate_args* a, void* workspace, size_t ws_bytes,
       a->D > SV_MAX_ROTATE_D || a->D % 16 != 0 || !dtype_ok(a->dtype))
     return SV_EINVAL;
   if (a->B == 0) return SV_OK;
-  if (!rope_ok(a->rope, a->D) || !heads_ok(a->q, a->dtype) || !heads_ok(a->k, a->dtype))
+  if (!rope_ok(a->rope, a->D) || !heads_ok(a->q, a->dtype, a->B, a->T) ||
+      !heads_ok(a->k, a->dtype, a->B, a->T))
     return SV_EINVAL;
   if (a->q.heads + a->k.heads == 0) return SV_OK;
   const sv_status wst = workspace_ok(workspace, ws_bytes, SV_MIN_WORKSPACE_BYTES);
@@ -156,7 +160,7 @@ sv_status sv_kv_append(const sv_kv_append_args* a, void* workspace, size_t ws_by
     return SV_EINVAL;
   if (a->B == 0) return SV_OK;
   if (!cache_ok(a->cache) || a->k_new == nullptr || a->v_new == nullptr || a->kv_len == nullptr ||
-      !rope_ok(a->rope, a->cache.D) || !heads_ok(a->q, a->dtype) || !norm_ok(a->k_norm))
+      !rope_ok(a->rope, a->cache.D) || !heads_ok(a->q, a->dtype, a->B, a->T) || !norm_ok(a->k_norm))
     return SV_EINVAL;
   const int es = dtype_bytes(a->dtype);
   if (!aligned(a->k_new, static_cast<size_t>(es)) || !aligned(a->v_new, static_cast<size_t>(es)))

@@ -37,8 +37,9 @@ constexpr int kLpCtasPerSm = 4;
 constexpr int kLpGroup = 16;       // logits of a group
 constexpr int kLpMaxCluster = 8;
 constexpr int kLpMapBytes = 34816; // most that a CTA's map holds
-constexpr int kLpList = SV_MAX_TOPK * kLpGroup;  // items that are ranked by counting
-constexpr int kLpGroups = 512;     // groups that a CTA reads again
+constexpr int kLpList = SV_MAX_TOPK * kLpGroup;  // items that there is room for
+constexpr int kLpCounted = 128;    // items that are ranked by counting; more are sorted
+constexpr int kLpGroups = 256;     // groups that a CTA reads again
 constexpr int kLpPublished = 128;  // maxima that make the bound, at most
 constexpr int kLpLeast = 32;       // and at least: a thread's share of them is whole uint4s
 static_assert(kLpLeast * kLpLeast / kLpThreads % 4 == 0 && kLpMaxCluster * kLpWarps <= kLpPublished,
@@ -311,13 +312,19 @@ struct LpShared {
   unsigned larger[kLpPublished];                 // and how many are larger
   int group[kLpGroups];                          // every: groups that are read again
   unsigned groups;
-  unsigned count[64];  // first: items; the bisections' steps (at most 2 + 32 + 25)
+  unsigned count[64];  // first: items; three for each step of lp_choose
   float m, log_z, entropy;
 };
 
-__device__ __forceinline__ void lp_push(LpShared* first, unsigned long long v) {
-  const unsigned at = atomicAdd(&first->count[0], 1u);
-  if (at < kLpList) first->item[at] = v;
+// Items of the lanes that have one, by a whole warp: one addition for all of them.
+__device__ __forceinline__ void lp_push(LpShared* first, bool is, unsigned long long v) {
+  const unsigned who = __ballot_sync(0xffffffffu, is);
+  if (who == 0) return;
+  const int lane = static_cast<int>(threadIdx.x) & 31, leader = __ffs(who) - 1;
+  unsigned at = 0;
+  if (lane == leader) at = atomicAdd(&first->count[0], static_cast<unsigned>(__popc(who)));
+  at = __shfl_sync(0xffffffffu, at, leader) + __popc(who & ((1u << lane) - 1));
+  if (is && at < kLpList) first->item[at] = v;
 }
 
 // The logits of the listed groups that reach `bound`, as items of the first CTA.
@@ -326,7 +333,8 @@ __device__ __forceinline__ void lp_read_groups(const LpRow<T>& in, const int* gr
                                                unsigned bound, LpShared* first) {
   constexpr int N = 4;  // loads under way together
 #pragma unroll 1
-  for (int e0 = static_cast<int>(threadIdx.x); e0 < groups * kLpGroup; e0 += N * kLpThreads) {
+  for (int e0 = static_cast<int>(threadIdx.x); (e0 & ~31) < groups * kLpGroup;
+       e0 += N * kLpThreads) {  // (whole warps)
     int id[N];
     float v[N];
 #pragma unroll
@@ -340,9 +348,31 @@ __device__ __forceinline__ void lp_read_groups(const LpRow<T>& in, const int* gr
 #pragma unroll
     for (int q = 0; q < N; ++q) {
       const unsigned k = LpKey<T>::of(v[q]);
-      if (k >= bound) lp_push(first, lp_item(k, id[q]));
+      lp_push(first, k >= bound, lp_item(k, id[q]));
     }
   }
+}
+
+// Sorts items by falling value, by all threads of the block (bitonic; room up to the
+// next power of two is used).
+__device__ __noinline__ void lp_sort(unsigned long long* v, int n) {
+  const int tid = static_cast<int>(threadIdx.x);
+  int size = 2;
+  while (size < n) size *= 2;
+  for (int i = n + tid; i < size; i += kLpThreads) v[i] = 0;
+  __syncthreads();
+  for (int k = 2; k <= size; k *= 2)
+    for (int j = k / 2; j > 0; j /= 2) {
+      for (int i = tid; i < size / 2; i += kLpThreads) {
+        const int lo = 2 * i - (i & (j - 1)), hi = lo + j;
+        const unsigned long long x = v[lo], y = v[hi];
+        if ((x < y) == ((lo & k) == 0)) {
+          v[lo] = y;
+          v[hi] = x;
+        }
+      }
+      __syncthreads();
+    }
 }
 
 // Too many logits reach the bound: finds the row's n groups of largest maxima
@@ -355,57 +385,73 @@ __device__ __noinline__ void lp_choose(const LogprobProblem& a, LpShared& sh,
   const int tid = static_cast<int>(threadIdx.x), lane = tid & 31;
   const unsigned n = static_cast<unsigned>(a.top);
   LpShared* const first = cl_at(&sh, 0);
-  int step = 1;
-  // how many groups of the row satisfy `is` (key, index)
-  auto count = [&](auto is) {
-    unsigned c = 0;
-    for (int i = tid; i < groups; i += kLpThreads)
-      c += is(LpKey<T>::of_map(map[i]), share.group(i));
-    c = __reduce_add_sync(0xffffffffu, c);
-    if (lane == 0 && c) atomicAdd(&first->count[step], c);
-    lp_sync(a.cluster);
-    return *static_cast<volatile unsigned*>(&first->count[step++]);
-  };
-  // lo: at least n groups reach it; hi: fewer than n do, `above`.  Equal maxima are the
-  // likely reason to be here, so lo + 1 is tried first.
-  unsigned lo = bound, hi = 0xffffffffu, above = 0;
-  const bool enough = count([&](unsigned k, int) { return k >= lo; }) >= n;
-  while (enough && hi - lo > 1) {
-    const unsigned mid = step == 2 ? lo + 1 : lo + (hi - lo) / 2;
-    const unsigned c = count([&](unsigned k, int) { return k >= mid; });
-    if (c >= n) {
-      lo = mid;
-    } else {
-      hi = mid;
-      above = c;
+  // lo: at least n groups of the row reach it; hi: fewer than n do, `above`.  Each step
+  // counts what reaches three keys between them; the first begins with lo and lo + 1,
+  // since equal maxima are the likely reason to be here.
+  unsigned lo = bound, hi = sizeof(typename LpKey<T>::Map) == 2 ? 0x10000u : 0xffffffffu;
+  unsigned above = 0;
+  bool enough = true;
+  // (at most 18 steps for keys of 32 bits)
+  for (int step = 0; step < 20 && enough && (step == 0 || hi - lo > 1); ++step) {
+    const unsigned part = (hi - lo) / 4;
+    const unsigned at[3] = {step == 0 ? lo : lo + max(part, 1u),
+                            step == 0 ? lo + 1 : lo + max(2 * part, 1u),
+                            step == 0 ? lo + 2 * part : lo + max(3 * part, 1u)};
+    unsigned c[3] = {0, 0, 0};
+    for (int i = tid; i < groups; i += kLpThreads) {
+      const unsigned k = LpKey<T>::of_map(map[i]);
+#pragma unroll
+      for (int q = 0; q < 3; ++q) c[q] += k >= at[q];
     }
-  }
-  // of the groups equal to lo those before `end`: at most as many as are left
-  int end = 0, past = 1 << 24;
-  while (enough && past - end > 1) {
-    const int mid = end + (past - end) / 2;
-    if (count([&](unsigned k, int g) { return k == lo && g < mid; }) <= n - above)
-      end = mid;
-    else
-      past = mid;
+#pragma unroll
+    for (int q = 0; q < 3; ++q) {
+      c[q] = __reduce_add_sync(0xffffffffu, c[q]);
+      if (lane == 0 && c[q]) atomicAdd(&first->count[1 + 3 * step + q], c[q]);
+    }
+    lp_sync(a.cluster);
+#pragma unroll
+    for (int q = 2; q >= 0; --q) {  // from the largest key down
+      const unsigned all = *static_cast<volatile unsigned*>(&first->count[1 + 3 * step + q]);
+      if (all < n) {
+        hi = at[q];
+        above = all;
+      }
+    }
+    enough = hi != lo;  // (else fewer groups have a logit above -inf: all of them)
+#pragma unroll
+    for (int q = 0; q < 3; ++q)
+      if (at[q] < hi && at[q] > lo) lo = at[q];
   }
   lp_sync(a.cluster);  // every CTA has read the counts
   if (share.rank == 0 && tid == 0) sh.count[0] = 0;
   lp_sync(a.cluster);
-  for (int i = tid; i < groups; i += kLpThreads) {
-    const unsigned k = LpKey<T>::of_map(map[i]);
-    const int g = share.group(i);
-    if (enough ? k >= hi || (k == lo && g < end) : k >= lo) lp_push(first, lp_item(k, g));
+  // the groups that reach hi (or all, where there are fewer than n), and of each
+  // CTA the first of those equal to lo, as many as are missing
+  const unsigned from = enough ? hi : bound;
+  for (int i = tid; (i & ~31) < groups; i += kLpThreads) {
+    const unsigned k = i < groups ? LpKey<T>::of_map(map[i]) : 0;
+    lp_push(first, i < groups && k >= from, lp_item(k, share.group(i)));
+  }
+  if (enough && tid < 32) {
+    int wanted = static_cast<int>(n - above);
+    for (int i = lane; (i & ~31) < groups && wanted > 0; i += 32) {
+      bool is = i < groups && LpKey<T>::of_map(map[i]) == lo;
+      const unsigned who = __ballot_sync(0xffffffffu, is);
+      is = is && __popc(who & ((1u << lane) - 1)) < wanted;
+      lp_push(first, is, lp_item(lo, share.group(i)));
+      wanted -= __popc(who);
+    }
   }
   lp_sync(a.cluster);
   if (share.rank != 0) return;
-  // the chosen groups' logits (n groups at most, so they all fit)
-  const int chosen = min(static_cast<int>(sh.count[0]), SV_MAX_TOPK);
+  // the best n of them (fewer than n, and n of each CTA, were put down)
+  static_assert((kLpMaxCluster + 1) * SV_MAX_TOPK <= kLpList, "items");
+  const int found = min(static_cast<int>(sh.count[0]), kLpList), chosen = min(found, a.top);
+  lp_sort(sh.item, found);
   if (tid < chosen) sh.group[tid] = static_cast<int>(~static_cast<unsigned>(sh.item[tid]));
-  __syncthreads();
   if (tid == 0) sh.count[0] = 0;
   __syncthreads();
-  lp_read_groups(in, sh.group, chosen, lo, &sh);
+  lp_read_groups(in, sh.group, chosen, enough ? lo : bound, &sh);
   __syncthreads();
 }
 
@@ -621,7 +667,8 @@ __global__ void __launch_bounds__(kLpThreads, kLpCtasPerSm) logprob_kernel(const
       for (int i = one ? at : tid; i < end; i += kLpThreads)
         if (Key::of_map(map[i]) >= bound) {
           const unsigned to = atomicAdd(&sh.groups, 1u);
-          if (to < kLpGroups) sh.group[to] = share.group(i);
+          if (to >= kLpGroups) break;  // too many: lp_choose
+          sh.group[to] = share.group(i);
         }
     }
     __syncthreads();
@@ -659,6 +706,14 @@ __global__ void __launch_bounds__(kLpThreads, kLpCtasPerSm) logprob_kernel(const
   if (TOP) {
     const bool bad = !(m < kPosInf);  // NaN: a row with an error
     const int found = bad ? 0 : min(static_cast<int>(sh.count[0]), kLpList);
+    if (found > kLpCounted) {
+      lp_sort(sh.item, found);
+      for (int i = tid; i < min(found, a.top); i += kLpThreads) {
+        const unsigned long long v = sh.item[i];
+        a.top_token[orow * a.top + i] = static_cast<int>(~static_cast<unsigned>(v));
+        a.top_logprob[orow * a.top + i] = logprob(Key::value(static_cast<unsigned>(v >> 32)));
+      }
+    } else
     // four lanes an item, whose rank is the number of larger ones
 #pragma unroll 1
     for (int i0 = 0; i0 < found; i0 += kLpThreads / 4) {

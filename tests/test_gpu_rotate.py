@@ -146,6 +146,27 @@ def test_norm_extremes(dtype):
     assert torch.isnan(got[5, 0, 0]).sum() == 2 and torch.isnan(got[6, 0, 1]).all()
 
 
+def test_rows_past_32_bits():
+    """Tokens more than 2^31 values apart, in place and on their way into the cache."""
+    rng = np.random.default_rng(8)
+    stride, T, H, D = (1 << 31) + 128, 3, 2, 64
+    buf = torch.zeros((T - 1) * stride + H * D, dtype=torch.bfloat16, device="cuda")
+    view = buf.as_strided((1, T, H, D), (0, stride, D, 1))
+    x, x64 = as_type(rng.normal(size=(1, T, H, D)), "bf16")
+    view.copy_(x)
+    rope, pos = sv.rope(64), [[5, 6, 7]]
+    ref = ku.random_cache(rng, 2, H, 16, D)
+    dev = ku.to_device(ref)
+    q = sv.kv_append(dev, i32([[1]]), i32([5]), view, view, view, rope=rope, eps=1e-6)["q"]
+    y, size = ru.rotated(x64, pos, rope, None, 1e-6)
+    near(q, y, size, "bf16")
+    ref.write(np.array([[1]]), [5], [T], y, x64)
+    _, v, ks, vs = ku.from_device(dev)
+    assert np.array_equal(v, ref.v) and np.array_equal(ks, ref.ks) and np.array_equal(vs, ref.vs)
+    sv.rotate(view, start=i32([5]), rope=rope, eps=1e-6, inplace=True)
+    assert torch.equal(view, q)
+
+
 def test_rotate_bad_num_and_empty():
     x = torch.ones(3, 4, 2, 64, device="cuda", dtype=torch.bfloat16)
     ws = new_ws()

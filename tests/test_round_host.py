@@ -135,7 +135,8 @@ BAD_ROPES = [dict(dim=-16), dict(dim=8), dict(dim=40), dict(dim=80), dict(freq=N
              dict(freq=FAKE + 8), dict(scale=math.nan), dict(scale=math.inf)]
 BAD_HEADS = [dict(heads=-1), dict(heads=257), dict(x=None), dict(out=None), dict(x=FAKE + 1),
              dict(out=FAKE + 1), dict(out_dtype=3), dict(out=FAKE, out_dtype=1),
-             dict(out=FAKE, out_token_stride=64), dict(eps=-1e-6), dict(eps=1e-31),
+             dict(out=FAKE, out_token_stride=64), dict(out_batch_stride=0),
+             dict(out_token_stride=0), dict(out_head_stride=0), dict(eps=-1e-6), dict(eps=1e-31),
              dict(eps=math.inf), dict(eps=math.nan), dict(weight=FAKE),
              dict(weight=FAKE, eps=1e-6, weight_dtype=3), dict(weight=FAKE + 1, eps=1e-6)]
 
@@ -391,7 +392,13 @@ def test_frequencies():
     r = dict(freq=sv.rope_turns([5.0, -1.0], "cpu"))
     assert radians(r) == pytest.approx([5.0, 2 * math.pi - 1])
     for bad in (dict(dim=24), dict(dim=0), dict(dim=272), dict(base=0.0), dict(base=math.inf),
-                dict(scaling=dict(type="other")), dict(scaling=dict(type="factors", factors=[1]))):
+                dict(scaling=dict(type="other")), dict(scaling=dict(type="factors", factors=[1])),
+                dict(scaling=dict(type="factors", factors=[0.0] * 32)), dict(scaling={}, dim=8),
+                dict(scaling=dict(factor=2)), dict(scaling=dict(type="linear")),
+                dict(scaling=dict(type="linear", factor=0)), dict(scaling=dict(type="yarn", factor=2)),
+                dict(scaling=dict(type="yarn", factor=2, context=8192), base=1.0),
+                dict(scaling=dict(type="linear", factor=2, context=8192)),
+                dict(scaling=dict(type="wavelength", factor=2, context=8192, low=4, high=4))):
         with pytest.raises(ValueError):
             sv.rope(**(dict(dim=64, device="cpu") | bad))
 
@@ -444,3 +451,65 @@ def test_nvtx_build_opens_a_range_per_call():
             assert re.search(r"sv_status\s+" + name + r"\s*\([^{]*\{\s*const\s+SvKvRange\s+sv_range_"
                              r"\s*\(\s*\"" + name + r"\"\s*\)", out), name
         assert "SvKvRange" not in preprocessed(unit)
+
+
+# ------------------------------------------------------- the likeliest tokens
+
+def search(keys, n, bound, top):
+    """The steps in which the kernel looks for the n-th largest of `keys` (at least
+    n of them, or not, reach `bound`): (it, the next key up, how many reach that)."""
+    lo, hi, above, enough, step = bound, top, 0, True, 0
+    while step < 20 and enough and (step == 0 or hi - lo > 1):
+        part = (hi - lo) // 4
+        at = ([lo, lo + 1, lo + 2 * part] if step == 0 else
+              [lo + max(part, 1), lo + max(2 * part, 1), lo + max(3 * part, 1)])
+        count = [int((keys >= x).sum()) for x in at]
+        for q in (2, 1, 0):
+            if count[q] < n:
+                hi, above = at[q], count[q]
+        enough = hi != lo
+        for x in at:
+            if lo < x < hi:
+                lo = x
+        step += 1
+    return (lo, hi, above) if enough else None
+
+
+def test_the_search_finds_the_last_group():
+    rng = np.random.default_rng(2)
+    for trial in range(2000):
+        top = 0x10000 if trial % 2 else 0xffffffff
+        span = int(rng.choice([1, 2, 5, 100, 5000, top - 300]))
+        base = int(rng.integers(129, top - 100 - span)) if span < top - 300 else 129
+        keys = np.minimum(base + rng.integers(0, span + 1, rng.integers(1, 200)), top - 1)
+        n = int(rng.integers(1, 65))
+        bound = int(rng.choice([keys.min(), 128]))
+        got = search(keys, n, bound, top)
+        if len(keys) < n:
+            assert got is None
+        else:
+            last = int(np.sort(keys)[-n])
+            assert got == (last, last + 1, int((keys > last).sum()))
+
+
+def test_the_best_groups_hold_the_likeliest_tokens():
+    """The n largest logits (lower ids first among equal ones) lie in the n groups of
+    largest maxima (lower groups first), and reach the last of these maxima; a bound
+    from maxima of disjoint sets of groups leaves none of them out."""
+    rng = np.random.default_rng(3)
+    for trial in range(300):
+        V, n = int(rng.integers(1, 900)), int(rng.integers(1, 65))
+        kind = trial % 4
+        x = (rng.normal(size=V) if kind == 0 else rng.integers(0, 3, V).astype(float) if kind == 1
+             else np.zeros(V) if kind == 2 else np.sort(rng.normal(size=V)))
+        want = ru.Row(x).top(n)
+        padded = np.append(x, np.full(-V % 16, -np.inf)).reshape(-1, 16)
+        groups = padded.max(1)
+        best = np.lexsort((np.arange(len(groups)), -groups))[:n]
+        assert set(want // 16) <= set(best)
+        if len(groups) >= n:
+            assert (x[want] >= groups[best[-1]]).all()
+        sets = [groups[i::7].max() for i in range(7) if i < len(groups)]
+        if len(sets) >= n:
+            bound = np.sort(sets)[-n]
+            assert (groups >= bound).sum() >= n and (x[want] >= bound).all()
