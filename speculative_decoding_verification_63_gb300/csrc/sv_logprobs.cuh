@@ -29,6 +29,7 @@
 
 #include "sv_cluster.cuh"
 #include "sv_device.cuh"
+#include "sv_pairs.cuh"
 
 namespace sv {
 

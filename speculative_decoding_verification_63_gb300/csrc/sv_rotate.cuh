@@ -22,6 +22,7 @@
 #pragma once
 
 #include "sv_kvcache.cuh"
+#include "sv_pairs.cuh"
 
 namespace sv {
 
