@@ -10,21 +10,20 @@
 //
 // A row belongs to a cluster of 1 to 8 CTAs, each of which streams a share of it
 // from memory straight into registers, 32 bytes a thread and load (rows need no
-// alignment: a share begins on a 32-byte boundary at or before the row, and what
-// is not the row's counts as -inf).  Statistics and candidates meet in the
-// shared memory of the cluster's first CTA, so nothing goes through global
-// memory and no order of arrival matters.
+// alignment: groups of sixteen logits begin on 32-byte boundaries, the first one at
+// or before the row, and what is not the row's counts as -inf).  Statistics and
+// candidates meet in the shared memory of the cluster's first CTA, so nothing goes
+// through global memory and no order of arrival matters.
 //
-// The likeliest tokens.  While streaming, each group of sixteen logits leaves
-// its maximum, as an order-preserving key, in a map in shared memory.  The `top`
-// largest logits lie in the `top` groups of largest maxima (equal ones: the
-// first): each group left out is outranked by a logit of each of those.  A
-// bound at or below the top-th largest maximum comes from the threads' own
-// maxima (they are maxima of disjoint sets of groups).  The few groups that reach
-// it are read again by the threads that met them, and the logits that reach it are
-// ranked by counting.  Where too many do (equal logits all over a row, as under a
-// mask of the type's lowest value), the `top` groups are found first, by bisection
-// on the keys in the map.
+// The likeliest tokens.  While streaming, each group leaves its maximum in a map in
+// shared memory.  The `top` largest logits lie in the `top` groups of largest maxima
+// (equal ones: the first): each group left out is outranked by a logit of each of
+// those.  A bound at or below the top-th largest maximum comes from the warps'
+// largest thread maxima (they are maxima of disjoint sets of groups).  The few
+// groups that reach it are read again, and their logits that reach it are ranked by
+// counting.  Where too many do (equal logits all over a row, as under a mask of the
+// type's lowest value), the `top` groups are found first, by a search on the keys in
+// the map.
 #pragma once
 
 #include "sv_cluster.cuh"
@@ -707,27 +706,25 @@ __global__ void __launch_bounds__(kLpThreads, kLpCtasPerSm) logprob_kernel(const
   if (TOP) {
     const bool bad = !(m < kPosInf);  // NaN: a row with an error
     const int found = bad ? 0 : min(static_cast<int>(sh.count[0]), kLpList);
+    auto put = [&](int place, unsigned long long v) {
+      a.top_token[orow * a.top + place] = static_cast<int>(~static_cast<unsigned>(v));
+      a.top_logprob[orow * a.top + place] = logprob(Key::value(static_cast<unsigned>(v >> 32)));
+    };
     if (found > kLpCounted) {
       lp_sort(sh.item, found);
-      for (int i = tid; i < min(found, a.top); i += kLpThreads) {
-        const unsigned long long v = sh.item[i];
-        a.top_token[orow * a.top + i] = static_cast<int>(~static_cast<unsigned>(v));
-        a.top_logprob[orow * a.top + i] = logprob(Key::value(static_cast<unsigned>(v >> 32)));
-      }
-    } else
-    // four lanes an item, whose rank is the number of larger ones
+      for (int i = tid; i < min(found, a.top); i += kLpThreads) put(i, sh.item[i]);
+    } else {
+      // four lanes an item, whose place is the number of larger ones
 #pragma unroll 1
-    for (int i0 = 0; i0 < found; i0 += kLpThreads / 4) {
-      const int i = i0 + tid / 4;
-      const unsigned long long v = i < found ? sh.item[i] : ~0ull;
-      int before = 0;
+      for (int i0 = 0; i0 < found; i0 += kLpThreads / 4) {
+        const int i = i0 + tid / 4;
+        const unsigned long long v = i < found ? sh.item[i] : ~0ull;
+        int before = 0;
 #pragma unroll 4
-      for (int k = tid & 3; k < found; k += 4) before += sh.item[k] > v;
-      before += __shfl_xor_sync(0xffffffffu, before, 1);
-      before += __shfl_xor_sync(0xffffffffu, before, 2);
-      if (i < found && before < a.top && (tid & 3) == 0) {
-        a.top_token[orow * a.top + before] = static_cast<int>(~static_cast<unsigned>(v));
-        a.top_logprob[orow * a.top + before] = logprob(Key::value(static_cast<unsigned>(v >> 32)));
+        for (int k = tid & 3; k < found; k += 4) before += sh.item[k] > v;
+        before += __shfl_xor_sync(0xffffffffu, before, 1);
+        before += __shfl_xor_sync(0xffffffffu, before, 2);
+        if (i < found && before < a.top && (tid & 3) == 0) put(before, v);
       }
     }
     for (int i = found + tid; i < a.top; i += kLpThreads) {

@@ -456,6 +456,10 @@ struct RotateProblem {
 
 constexpr int kRotateThreads = 256;
 
+// Bound: HBM (2 prompts of 8190 tokens, 40 heads of 128, 335 MB: 53.6 us, 92 % of the
+// copy bandwidth; pairs of neighbours 55, fp32 56 for half as many tokens; loads into
+// registers a head ahead 67.7; two blocks an SM 76 and four 70 at that time).  Small
+// calls: the launch (2.8 us for one token of 64 requests).
 template <class T, bool NEAR>
 __global__ void __launch_bounds__(kRotateThreads, 3) rotate_kernel(const RotateProblem a) {
   __shared__ Ahead<T, kRotateThreads, 1> feed;
@@ -695,6 +699,12 @@ union AppendFeed {
   Ahead<T, THREADS, CH> kv;
 };
 
+// Blocks of 256 threads with one chunk a thread for up to 256 chunks a page and head (a
+// page's, or the round's), with two up to 512; of 512 threads above.  Bound: HBM, at 84 %
+// of the copy bandwidth, with the fixed latencies of the norm's and rotation's
+// arithmetic close behind (4 prompts of 8190 tokens, 32 query and 8 key heads of 128,
+// 738 MB: 130 us; 126 registers, so two blocks an SM; a third, with the sines in
+// shared memory, 139; the queries in a launch of their own 141).
 template <class T, bool NEAR, int THREADS, int CH>
 __global__ void __launch_bounds__(THREADS, THREADS == 256 ? (CH == 1 ? 3 : 2) : 1)
     kv_append_kernel(const KvAppendProblem a) {

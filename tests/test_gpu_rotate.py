@@ -354,3 +354,57 @@ def test_calls_in_a_graph_and_on_a_side_stream():
         assert torch.equal(got["q"], want["q"]) and torch.equal(again["q"], turned["q"])
         for n in eager:
             assert torch.equal(eager[n].view(torch.uint8), replayed[n].view(torch.uint8))
+
+
+def test_many_requests_and_none():
+    """1024 requests with a token each or none; a round without tokens leaves the cache
+    as it is."""
+    rng = np.random.default_rng(17)
+    B, H, P, D = 1024, 1, 16, 64
+    lens, new = rng.integers(0, 16, B), rng.integers(0, 2, B)
+    lens = np.minimum(lens, 15)
+    ref = ku.random_cache(rng, B, H, P, D)
+    table = np.arange(B, dtype=np.int32)[rng.permutation(B)].reshape(B, 1)
+    dev, ws = ku.to_device(ref), new_ws()
+    x, x64 = as_type(rng.normal(size=(B, 1, 3, D)), "bf16")
+    rope = sv.rope(64)
+    zero = i32(np.zeros(B))
+    got = sv.kv_append(dev, i32(table), i32(lens), x[:, :, :1], x[:, :, 1:2], x[:, :, 2:],
+                       num_new=zero, rope=rope, eps=1e-6, ws=ws)
+    assert not got["q"].any()
+    gk, gv, ks, vs = ku.from_device(dev)
+    assert np.array_equal(gk, ref.k) and np.array_equal(gv, ref.v) and np.array_equal(ks, ref.ks)
+    pos = ru.positions(lens, None, B, 1)
+    y, size = ru.rotated(x64, pos, rope, None, 1e-6)
+    got = sv.kv_append(dev, i32(table), i32(lens), x[:, :, :1], x[:, :, 1:2], x[:, :, 2:],
+                       num_new=i32(new), rope=rope, eps=1e-6, ws=ws)
+    ref.write(table, lens, new, y[:, :, 1:2], x64[:, :, 2:])
+    gk, gv, ks, vs = ku.from_device(dev)
+    assert np.array_equal(gv, ref.v) and np.array_equal(ks, ref.ks) and np.array_equal(vs, ref.vs)
+    y[new == 0] = size[new == 0] = 0
+    near(got["q"], y[:, :, :1], size[:, :, :1], "bf16")
+    turned = sv.rotate(x, start=i32(lens), num=i32(new), rope=rope, eps=1e-6, ws=ws)["q"]
+    assert torch.equal(turned[:, :, :1], got["q"])
+    assert flags(ws) == (sv.SV_OK, 0)
+
+
+def test_two_streams_at_once():
+    """Calls of two streams share nothing but the error word."""
+    rng = np.random.default_rng(18)
+    x, _ = as_type(rng.normal(size=(4, 600, 12, 128)), "bf16")
+    rope, start = sv.rope(128), i32([0, 5, 9, 1000])
+    want = sv.rotate(x, start=start, rope=rope, eps=1e-6)["q"]
+    logits, _ = as_type(rng.normal(size=(2, 100, 32000)), "bf16")
+    said = sv.token_logprobs(logits, top=5)
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    got = [[], []]
+    for _ in range(5):
+        for i, s in enumerate(streams):
+            with torch.cuda.stream(s):
+                got[i].append((sv.rotate(x, start=start, rope=rope, eps=1e-6)["q"],
+                               sv.token_logprobs(logits, top=5)))
+    torch.cuda.synchronize()
+    for q, lp in got[0] + got[1]:
+        assert torch.equal(q, want)
+        assert all(torch.equal(lp[n], said[n]) for n in said)
