@@ -560,7 +560,7 @@ __global__ void __launch_bounds__(kLpThreads, kLpCtasPerSm) logprob_kernel(const
       at = m > mine ? i0 : at;
       mine = fmaxf(mine, m);
     }
-    if (!(m <= s.m)) lp_raise(s, m, c);
+    if (!(m <= s.m)) lp_raise(s, max_nan(s.m, m), c);  // (a NaN stays one)
     if (fast && s.m > (sizeof(T) == 2 ? -0x1p90f : kNegInf) && !lp_wide(s.m, c))
       lp_accumulate<T, true>(s, raw, c);
     else if (s.m > kNegInf)
@@ -577,7 +577,7 @@ __global__ void __launch_bounds__(kLpThreads, kLpCtasPerSm) logprob_kernel(const
     const int id = g * kLpGroup - in.off + lane;
     float v = kNegInf;
     if (lane < kLpGroup && id >= 0 && id < a.V) v = lp_value(x + id);
-    if (!(v <= s.m)) lp_raise(s, v, c);
+    if (!(v <= s.m)) lp_raise(s, max_nan(s.m, v), c);
     if (s.m > kNegInf) {
       const float d = lp_exponent(v, s.m, c), f = fast_exp2(d);
       s.z += f;

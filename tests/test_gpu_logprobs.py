@@ -263,3 +263,30 @@ def test_in_a_graph_and_on_a_side_stream():
         torch.cuda.synchronize()
         for n in want:
             assert same(got[n], want[n]) and same(other[n], want[n]), n
+
+
+@pytest.mark.parametrize("top", [0, 5])
+@pytest.mark.parametrize("B,N,V,dtype", [(5, 128, 40003, "bf16"), (5, 128, 20003, "fp32"),
+                                         (1, 40, 300001, "bf16"), (1, 9, 300001, "fp32"),
+                                         (2, 17, 41, "bf16"), (2, 17, 1003, "fp32")])
+def test_one_bad_logit_anywhere(B, N, V, dtype, top):
+    """A NaN or +inf at the row's ends and all over it, before and behind ordinary
+    logits of the same thread, at the first, the next turn or in an edge's group:
+    the row is without values and its neighbours keep theirs."""
+    rng = np.random.default_rng(V + N)
+    x, _ = as_type(rng.normal(size=(B, N, V)), dtype)
+    at = np.linspace(0, V - 1, B * N).astype(int).reshape(B, N)
+    for value in (np.nan, np.inf):
+        bad = x.clone()
+        for b in range(B):
+            for r in range(0, N, 2):
+                bad[b, r, at[b, r]] = value
+        ws = new_ws()
+        got = sv.token_logprobs(bad, i32(np.zeros((B, N))), top=top, ws=ws)
+        assert flags(ws) == (sv.SV_EDATA, sv.SV_DERR_NONFINITE)
+        for name in ("entropy", "logprobs") + (("top_logprobs",) if top else ()):
+            gone = torch.isnan(got[name]).cpu().numpy().reshape(B, N, -1)
+            assert gone[:, ::2].all(), (name, value, np.argwhere(~gone[:, ::2]).tolist()[:4])
+            assert not gone[:, 1::2].any()
+        if top:
+            assert (got["top_tokens"][:, ::2] == -1).all()
