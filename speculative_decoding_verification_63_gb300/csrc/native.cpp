@@ -136,6 +136,11 @@ void norm(sv_head_norm& n, PyObject* weight, PyObject* eps, int64_t D, const cha
   n.weight = address(weight, w.scalar_type(), {D}, what, p);
 }
 
+int small(int64_t n, const char* what) {
+  if (n > INT32_MAX) refuse(std::string(what) + ": out of range");
+  return static_cast<int>(n);
+}
+
 Tensor empty(IntArrayRef shape, ScalarType dtype, const Place& p) {
   return at::empty(shape, at::TensorOptions().dtype(dtype).device(p.device));
 }
@@ -152,7 +157,7 @@ void heads(sv_heads& h, PyObject* x, PyObject* out, ScalarType dtype, PyObject* 
            PyObject* eps, PyObject* stream, const char* what, const Place& p, Tensor& keep) {
   const Tensor& t = tensor(x, what);
   const IntArrayRef shape = t.sizes();
-  h.heads = static_cast<int>(shape[2]);
+  h.heads = small(shape[2], what);
   int64_t s[3];
   rows(t, shape, what, p, s);
   dtype_of(t, what);
@@ -180,11 +185,6 @@ void heads(sv_heads& h, PyObject* x, PyObject* out, ScalarType dtype, PyObject* 
 
 void four(const Tensor& t, const char* what) {
   if (t.dim() != 4) refuse(std::string(what) + ": expected [B][T][heads][D], got " + text(t.sizes()));
-}
-
-int small(int64_t n, const char* what) {
-  if (n > INT32_MAX) refuse(std::string(what) + ": out of range");
-  return static_cast<int>(n);
 }
 
 // The packed structure for entry 0, else the call's results or status.
@@ -430,6 +430,7 @@ PyObject* token_logprobs(PyObject*, PyObject* const* v, Py_ssize_t nv) {
         out[3] = empty(top, ScalarType::Float, p);
       }
     } else {
+      if (given(v[11]) && !given(v[5])) refuse("logprobs: given, but no tokens");
       address(v[11], ScalarType::Float, asked, "logprobs", p);
       address(v[12], ScalarType::Float, one, "entropy", p);
       address(v[13], ScalarType::Int, top, "top_tokens", p);

@@ -513,3 +513,13 @@ def test_the_best_groups_hold_the_likeliest_tokens():
         if len(sets) >= n:
             bound = np.sort(sets)[-n]
             assert (groups >= bound).sum() >= n and (x[want] >= bound).all()
+
+
+def test_results_without_tokens_and_head_counts_past_32_bits_are_refused(native):
+    a = tensors("token_logprobs")
+    with pytest.raises(ValueError, match="no tokens"):
+        native.token_logprobs(*(a | dict(tokens=None)).values())
+    native.token_logprobs(*(a | dict(tokens=None, logprobs=None)).values())
+    many = torch.zeros(64, dtype=torch.bfloat16).as_strided((2, 3, (1 << 32) + 4, 64), (0, 0, 0, 1))
+    with pytest.raises(ValueError, match="out of range"):
+        native.rotate(*(tensors("rotate") | dict(q=many, q_out=...)).values())
