@@ -45,15 +45,22 @@ Rope rope_view(const sv_rope& r) {
   return Rope{r.dim, r.interleaved, r.scale, reinterpret_cast<const unsigned long long*>(r.freq)};
 }
 
-// Heads that a thread takes: they share sines and cosines, and their loads
-// follow one another without a pause.  As many as leave this many threads an SM
-// (16384 tokens: 16 heads 54 us, 8 heads 54; 1024 tokens of 40 heads, by threads an SM:
-// 1024 10.0 us, 256 8.1, 128 7.7; 448 tokens 6.0, 5.1, 5.1).
-constexpr int kRotatePer = 16, kRotateFill = 128;
+// Heads that a thread takes: they share sines and cosines, and their loads follow one
+// another without a pause.  Where 16 make fewer than two thirds of the threads that run
+// at once, half as many heads each, as long as all threads still run at once (40
+// requests of 64 tokens, 20 heads: 16 heads a thread 8.8 us, 4 5.9; 128 of 4 tokens, 72
+// heads of 256: 16 heads 11.6, 2 8.9).  Where even 16 make more than run at once, 8,
+// and blocks of the same tokens follow one another, so that what is read together lies
+// together (16384 tokens of 40 heads: 52.7 us; 16 heads 56.1, 4 59.8; blocks of the same
+// heads one after the other, 16 heads 54.5, 8 54.1).
+constexpr int kRotatePer = 16, kRotateMany = 8;
 // The same for the groups that write the cache, whose threads hold a page's
 // values (prompts of 4 x 8190 tokens, 8 heads: 8 at a time 130 us, 4 145, 2 148; 8 x
-// 512 tokens, by threads an SM: 1024 30 us, 512 25, 256 22, 128 26).
+// 512 tokens, by threads an SM: 600 26 us, 400 22, 256 22, 128 26).
 constexpr int kAppendPer = 8, kAppendFill = 256;
+// Threads of an SM that run at once: three blocks of rotations or of appends with one
+// chunk a thread, two of those with two.
+constexpr int kThreadsOf3 = 3 * 256, kThreadsOf2 = 2 * 256;
 
 // `heads` in as many parts as `per` at a time make, of even sizes.
 int even(int heads, int per) {
@@ -61,9 +68,8 @@ int even(int heads, int per) {
   return (heads + parts - 1) / parts;
 }
 
-// A kind of heads for blocks of `threads` threads; B requests of T tokens of
-// `lanes` lanes.
-Heads heads_view(const sv_heads& h, sv_dtype dtype, int B, int T, int lanes, int threads, int sms) {
+// A kind of heads, of which a thread takes up to `per`.
+Heads heads_view(const sv_heads& h, sv_dtype dtype, int per) {
   Heads v = {};
   if (h.heads == 0) return v;
   v.x = h.x;
@@ -82,25 +88,34 @@ Heads heads_view(const sv_heads& h, sv_dtype dtype, int B, int T, int lanes, int
               : rows_aligned(h.out, oes, 16, v.out_batch, v.out_token, v.out_head) ? 16
                                                                                    : 0;
   v.norm = norm_view(h.norm);
-  const int64_t one = static_cast<int64_t>(B) * T * lanes;  // threads of a head
-  v.per = std::min(kRotatePer, h.heads);
-  while (v.per > 1 && one * ((h.heads + v.per - 1) / v.per) < int64_t{kRotateFill} * sms)
-    v.per = (v.per + 1) / 2;
+  v.per = std::min(per, h.heads);
   v.per = even(h.heads, v.per);
-  const int64_t mine = static_cast<int64_t>(T) * lanes * ((h.heads + v.per - 1) / v.per);
-  v.blocks = static_cast<int>((mine + threads - 1) / threads);
+  v.parts = (h.heads + v.per - 1) / v.per;
   return v;
 }
 
+// How many heads a thread takes, for `one` lanes of tokens and room for `room` threads
+// at once; `most` where there are more.
+int heads_per_thread(const sv_heads& q, const sv_heads& k, int64_t one, int64_t room, int most) {
+  auto threads = [&](int per) {
+    return one * ((q.heads + per - 1) / per + (k.heads + per - 1) / per);
+  };
+  int per = kRotatePer;
+  if (threads(per) > room) return most;
+  while (per > 1 && threads(per) * 3 < room * 2 && threads(per / 2) <= room) per /= 2;
+  return per;
+}
+
 template <class T, bool NEAR, int THREADS, int CH>
-sv_status run_append(const KvAppendProblem& p, dim3 grid, cudaStream_t stream) {
-  constexpr size_t smem = sizeof(AppendFeed<T, THREADS, CH>);
+sv_status run_append(const KvAppendProblem& p, dim3 grid, int block, cudaStream_t stream) {
+  const size_t smem = sizeof(uint4) * kAppendSlots<T, CH> * block;
   const auto kernel = kv_append_kernel<T, NEAR, THREADS, CH>;
-  if (smem > 48 * 1024 &&
+  constexpr int most = static_cast<int>(sizeof(uint4)) * kAppendSlots<T, CH> * THREADS;
+  if (most > 48 * 1024 &&
       cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                           static_cast<int>(smem)) != cudaSuccess)
+                           most) != cudaSuccess)
     return SV_ECUDA;
-  return launch(kernel, p, grid, THREADS, smem, stream);
+  return launch(kernel, p, grid, block, smem, stream);
 }
 
 }  // namespace
@@ -131,19 +146,29 @@ sv_status sv_rotate(const sv_rotate_args* a, void* workspace, size_t ws_bytes,
   p.D = a->D;
   p.lane_shift = 0;
   while ((16 << p.lane_shift) < a->D) ++p.lane_shift;
-  p.q = heads_view(a->q, a->dtype, a->B, a->T, 1 << p.lane_shift, kRotateThreads, dev.sms);
-  p.k = heads_view(a->k, a->dtype, a->B, a->T, 1 << p.lane_shift, kRotateThreads, dev.sms);
+  p.of_t = a->T == 1 ? 0 : ~uint64_t{0} / static_cast<unsigned>(a->T) + 1;
+  const int64_t one = (static_cast<int64_t>(a->B) * a->T) << p.lane_shift;
+  const int64_t room = int64_t{kThreadsOf3} * dev.sms;
+  const int per = heads_per_thread(a->q, a->k, one, room, kRotateMany);
+  p.q = heads_view(a->q, a->dtype, per);
+  p.k = heads_view(a->k, a->dtype, per);
+  const int parts = p.q.parts + p.k.parts;
+  p.parts_first = one * parts > room;
+  int block = kRotateThreads;
+  while (block > 64 && one * parts < static_cast<int64_t>(block) * dev.sms) block /= 2;
   p.rope = rope_view(a->rope);
   p.start = a->start;
   p.num = a->num;
   p.offset = a->offset;
   p.err = error_word(workspace);
-  const dim3 grid(static_cast<unsigned>(p.q.blocks + p.k.blocks), static_cast<unsigned>(a->B));
+  const int64_t columns = (one + block - 1) / block;
+  const dim3 grid(static_cast<unsigned>(p.parts_first ? columns * parts : columns),
+                  static_cast<unsigned>(p.parts_first ? 1 : parts));
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   auto run = [&](auto t) {
     using T = decltype(t);
-    return p.rope.interleaved ? launch(rotate_kernel<T, true>, p, grid, kRotateThreads, 0, st)
-                              : launch(rotate_kernel<T, false>, p, grid, kRotateThreads, 0, st);
+    return p.rope.interleaved ? launch(rotate_kernel<T, true>, p, grid, block, 0, st)
+                              : launch(rotate_kernel<T, false>, p, grid, block, 0, st);
   };
   switch (a->dtype) {
     case SV_BF16: return run(__nv_bfloat16());
@@ -194,28 +219,35 @@ sv_status sv_kv_append(const sv_kv_append_args* a, void* workspace, size_t ws_by
   p.err = error_word(workspace);
   // a thread for every chunk of sixteen values of a (page, head, side), or for two
   const int chunks = std::min(a->T, p.c.page_size) * (p.c.D / 16);
-  const int block = chunks > 512 ? 512 : 256, each = chunks > 256 ? 2 : 1;
+  const int most = chunks > 512 ? 512 : 256, each = chunks > 256 ? 2 : 1;
   static_assert(128 * 128 / 16 <= 512 * 2, "a page fits one block");
-  p.q = heads_view(a->q, a->dtype, a->B, a->T, p.c.D / 16, block, dev.sms);
-  p.group = 32;
-  while (p.group * each < chunks) p.group *= 2;
+  const int group = (chunks + 32 * each - 1) / (32 * each) * 32;
   // heads a group takes: sines and cosines are shared, once that leaves the GPU full
-  p.per = std::min(kAppendPer, p.c.Hkv);
-  while (p.per > 1 && static_cast<int64_t>(a->B) * p.pages * 2 * p.group *
-                              ((p.c.Hkv + p.per - 1) / p.per) < int64_t{kAppendFill} * dev.sms)
-    p.per = (p.per + 1) / 2;
-  p.per = even(p.c.Hkv, p.per);
-  p.chunks = (p.c.Hkv + p.per - 1) / p.per;
-  const int64_t threads = static_cast<int64_t>(p.pages) * 2 * p.chunks * p.group;
-  p.blocks = static_cast<int>((threads + block - 1) / block);
-  const dim3 grid(static_cast<unsigned>(p.blocks + p.q.blocks), static_cast<unsigned>(a->B));
+  int per = kAppendPer;
+  while (per > 1 && static_cast<int64_t>(a->B) * p.pages * 2 * group *
+                            ((p.c.Hkv + per - 1) / per) < int64_t{kAppendFill} * dev.sms)
+    per /= 2;
+  const int groups = std::min(most / group, std::max((p.c.Hkv + per - 1) / per, 64 / group));
+  const int block = each == 2 ? most : group * groups;
+  p.set = even(p.c.Hkv, per * groups);
+  p.sets = (p.c.Hkv + p.set - 1) / p.set;
+  p.blocks = p.pages * 2 * p.sets;
+  const int64_t lanes = static_cast<int64_t>(a->T) * (p.c.D / 16);
+  // (queries beside the blocks of the pages that a round fills at least)
+  const int64_t busy = static_cast<int64_t>(a->B) * ((a->T + p.c.page_size - 1) / p.c.page_size) * 2 *
+                       p.sets * block;
+  const int64_t room = int64_t{each == 2 ? kThreadsOf2 : kThreadsOf3} * dev.sms - busy;
+  p.q = heads_view(a->q, a->dtype,
+                   heads_per_thread(a->q, sv_heads{}, a->B * lanes, room, kRotatePer));
+  const dim3 grid(static_cast<unsigned>(p.blocks + (lanes * p.q.parts + block - 1) / block),
+                  static_cast<unsigned>(a->B));
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   auto run = [&](auto t, auto near) {
     using T = decltype(t);
     constexpr bool N = decltype(near)::value;
-    return block == 512 ? run_append<T, N, 512, 2>(p, grid, st)
-           : each == 2  ? run_append<T, N, 256, 2>(p, grid, st)
-                        : run_append<T, N, 256, 1>(p, grid, st);
+    return most == 512 ? run_append<T, N, 512, 2>(p, grid, block, st)
+           : each == 2  ? run_append<T, N, 256, 2>(p, grid, block, st)
+                        : run_append<T, N, 256, 1>(p, grid, block, st);
   };
   auto pairs = [&](auto t) {
     return p.rope.interleaved ? run(t, std::true_type()) : run(t, std::false_type());

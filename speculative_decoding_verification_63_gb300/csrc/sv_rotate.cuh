@@ -47,7 +47,7 @@ struct Heads {
   long long batch, token, head, out_batch, out_token, out_head;
   HeadNorm norm;
   int per;     // heads a thread takes
-  int blocks;  // blocks of a request
+  int parts;   // parts that makes of them
 };
 
 // What a lane holds of a head: its pairs.
@@ -102,25 +102,29 @@ __device__ __forceinline__ void load_pairs(RawPairs<T>& r, const T* p, const Pla
 // come, so nothing is shared and no thread waits for another, and what is under
 // way takes no registers.  Pieces that are not on a 16-byte boundary are loaded
 // when they are needed.
-template <class T, int THREADS, int CH>
+template <class T, int CH, int STRIDE>
 struct Ahead {
   static constexpr int kPieces = static_cast<int>(sizeof(T)) * CH;  // of 16 bytes a head
   static constexpr int kStages = 8 / kPieces > 1 ? 8 / kPieces : 2;
-  uint4 slot[kStages][kPieces][THREADS];
+  static constexpr int kSlots = kStages * kPieces;  // of a thread
+  uint4* mine;  // the thread's first slot; the next one is STRIDE (the block's threads)
+  int stride;   // further, or `stride` where that is 0
+  __device__ __forceinline__ uint4* slot(int i, int piece) const {
+    return mine + (i % kStages * kPieces + piece) * (STRIDE ? STRIDE : stride);
+  }
 
   template <bool NEAR>
   __device__ __forceinline__ void ask(int i, int chunk, const T* p, const Place& at, bool vec,
-                                      int* err) {
+                                      int* err) const {
     constexpr int H = static_cast<int>(sizeof(T)) / 2;
-    uint4(*to)[THREADS] = &slot[i % kStages][chunk * 2 * H];
     if (vec && SV_CHECK(((reinterpret_cast<uintptr_t>(p + at.a) |
                           reinterpret_cast<uintptr_t>(p + at.b)) & 15) == 0 &&
                             chunk * 2 * H + 2 * H <= kPieces,
                         err)) {
 #pragma unroll
       for (int k = 0; k < H; ++k) {
-        copy<NEAR>(&to[k][threadIdx.x], reinterpret_cast<const uint4*>(p + at.a) + k);
-        copy<NEAR>(&to[H + k][threadIdx.x], reinterpret_cast<const uint4*>(p + at.b) + k);
+        copy<NEAR>(slot(i, chunk * 2 * H + k), reinterpret_cast<const uint4*>(p + at.a) + k);
+        copy<NEAR>(slot(i, chunk * 2 * H + H + k), reinterpret_cast<const uint4*>(p + at.b) + k);
       }
     }
   }
@@ -147,7 +151,7 @@ struct Ahead {
     if (vec) {
 #pragma unroll
       for (int k = 0; k < static_cast<int>(sizeof(T)); ++k)
-        r.w[k] = slot[i % kStages][chunk * sizeof(T) + k][threadIdx.x];
+        r.w[k] = *slot(i, chunk * static_cast<int>(sizeof(T)) + k);
     } else {
       load_pairs(r, p, at, false);
     }
@@ -355,21 +359,23 @@ __device__ __forceinline__ long long position_of(const int* start, const int* of
          (offset ? offset[static_cast<long long>(b) * T + t] : t);
 }
 
-// Norm and rotation of one kind of heads of request b, by the threads of
-// `h.blocks` blocks: a thread takes one token, one lane's channels and h.per
-// heads, for which sines, cosines and weights are the same.
+// Where a thread works: token t of request b, which has n tokens, and lane j of it.
+struct Spot {
+  bool on;
+  int b, t, j, n;
+};
+
+// Norm and rotation of heads h0 .. of one kind at a thread's spot: one lane's channels
+// of up to h.per heads, for which sines, cosines and weights are the same.  Whole warps
+// call this.
 template <class T, bool NEAR, class Feed>
-__device__ __forceinline__ void rotate_heads(const Heads& h, const Rope& rope, int b, int n, int T_,
+__device__ __forceinline__ void rotate_heads(const Heads& h, const Rope& rope, const Spot& spot, int T_,
                                              const int* start, const int* offset, int D,
-                                             int lane_shift, int thread, Feed& feed, int* err) {
-  // (at most 2^16 tokens of 16 lanes, 256 heads and a block's rounding: 32 bits)
-  const int per_chunk = T_ << lane_shift, lanes = 1 << lane_shift;
-  const int chunk = thread / per_chunk, rest = thread - chunk * per_chunk;
-  const int t = rest >> lane_shift, j = rest & (lanes - 1);
-  const int h0 = chunk * h.per;
-  const int heads = 16 * j < D && h0 < h.heads ? min(h.per, h.heads - h0) : 0;
+                                             int lane_shift, int h0, const Feed& feed, int* err) {
+  const int b = spot.b, t = spot.t, j = spot.j;
+  const int heads = spot.on && 16 * j < D && h0 < h.heads ? min(h.per, h.heads - h0) : 0;
   const int all = __reduce_max_sync(0xffffffffu, heads);  // of the warp
-  const bool live = t < n && heads > 0;
+  const bool live = t < spot.n && heads > 0;
   const Place at = place_of<NEAR>(rope, j);
   const T* x = static_cast<const T*>(h.x) + b * h.batch + t * h.token + h0 * h.head;
   const T* ask = x;
@@ -448,33 +454,54 @@ __device__ __forceinline__ void rotate_heads(const Heads& h, const Rope& rope, i
 
 struct RotateProblem {
   int B, T, D, lane_shift;
+  unsigned long long of_t;  // 2^64 / T, rounded up; 0: T is 1
+  bool parts_first;         // blocks of the same tokens follow one another, not those of
+                            // the same part of the heads (blockIdx.y)
   Heads q, k;
   Rope rope;
   const int *start, *num, *offset;
   int* err;
 };
 
+// At most; small calls are spread over more blocks.
 constexpr int kRotateThreads = 256;
 
-// Bound: HBM (2 prompts of 8190 tokens, 40 heads of 128, 335 MB: 53.6 us, 92 % of the
-// copy bandwidth; pairs of neighbours 55, fp32 56 for half as many tokens; loads into
-// registers a head ahead 67.7; two blocks an SM 76 and four 70 at that time).  Small
-// calls: the launch (2.8 us for one token of 64 requests).
+// Bound: HBM (2 prompts of 8190 tokens, 40 heads of 128, 335 MB: 52.2 us, 95 % of the
+// copy bandwidth; pairs of neighbours 54, fp32 55 for half as many tokens; before the
+// blocks of the same tokens followed one another 54.5; loads into registers a head
+// ahead 67.7; two blocks an SM 76 and four 70 at that time).  Small calls: the launch
+// (2.7 us for one token of 64 requests).  Tokens lie flat over the requests, so that
+// blocks are full whatever T is (256 requests of one token: 4.3 us, a request a block
+// 5.2; 64 of 7: 4.3 and 5.1).  Sines made together by the parts of a block, through
+// shared memory: 0.1 to 0.4 us more in small calls, 1.3 in prompts.
 template <class T, bool NEAR>
 __global__ void __launch_bounds__(kRotateThreads, 3) rotate_kernel(const RotateProblem a) {
-  __shared__ Ahead<T, kRotateThreads, 1> feed;
+  using Feed = Ahead<T, 1, kRotateThreads>;
+  __shared__ uint4 slots[Feed::kSlots * kRotateThreads];
   grid_dependency_wait();
-  const int b = static_cast<int>(blockIdx.y);
-  int block = static_cast<int>(blockIdx.x);
-  int n = a.num ? a.num[b] : a.T;
-  if (n < 0 || n > a.T) {
-    if (block == 0 && threadIdx.x == 0) record_error(a.err, SV_DERR_ARG);
-    n = 0;
+  // Tokens lie one request behind the other (at most 2^10 requests of 2^16 tokens of
+  // 16 lanes, and a block's rounding: 31 bits).
+  const int parts = a.q.parts + a.k.parts, x = static_cast<int>(blockIdx.x);
+  const int column = a.parts_first ? x / parts : x;
+  const int part = a.parts_first ? x - column * parts : static_cast<int>(blockIdx.y);
+  const int thread = column * static_cast<int>(blockDim.x) + static_cast<int>(threadIdx.x);
+  const int token = thread >> a.lane_shift;
+  Spot spot = {};
+  spot.j = thread & ((1 << a.lane_shift) - 1);
+  if (token < a.B * a.T) {
+    spot.on = true;
+    spot.b = a.of_t ? static_cast<int>(__umul64hi(token, a.of_t)) : token;
+    spot.t = token - spot.b * a.T;
+    spot.n = a.num ? a.num[spot.b] : a.T;
+    if (spot.n < 0 || spot.n > a.T) {
+      if (part == 0 && spot.t == 0 && spot.j == 0) record_error(a.err, SV_DERR_ARG);
+      spot.n = 0;
+    }
   }
-  const bool keys = block >= a.q.blocks;
-  if (keys) block -= a.q.blocks;
-  rotate_heads<T, NEAR>(keys ? a.k : a.q, a.rope, b, n, a.T, a.start, a.offset, a.D, a.lane_shift,
-                  block * kRotateThreads + static_cast<int>(threadIdx.x), feed, a.err);
+  const bool keys = part >= a.q.parts;
+  const Heads& h = keys ? a.k : a.q;
+  rotate_heads<T, NEAR>(h, a.rope, spot, a.T, a.start, a.offset, a.D, a.lane_shift,
+                        (keys ? part - a.q.parts : part) * h.per, Feed{slots + threadIdx.x, 0}, a.err);
 }
 
 // ------------------------------------------------------------------ append
@@ -482,10 +509,9 @@ __global__ void __launch_bounds__(kRotateThreads, 3) rotate_kernel(const RotateP
 struct KvAppendProblem {
   KvCache c;
   int B, T, pages;  // pages a request can touch
-  int group;        // threads of one (page, side): 32 .. all
-  int per;          // heads a group takes, one after the other
-  int chunks;       // groups of a (page, side): Hkv / per
-  int blocks;       // blocks of a request that write the cache; then q.blocks
+  int set;          // heads a block takes
+  int sets;         // blocks of a (page, side)
+  int blocks;       // blocks of a request that write the cache; the others take q
   Heads q;
   const void *k_new, *v_new;
   bool k_vec, v_vec;
@@ -496,56 +522,55 @@ struct KvAppendProblem {
   int* err;
 };
 
-// As kv_write_kernel: a thread group for each (request, page of the round,
-// side, heads), which holds a head's new values of the page in registers, CH
-// chunks of sixteen a thread, until their codes are written.  Sines and cosines
-// serve all its heads.
+// A block takes one (request, page of the round, side) and a set of its heads.  A group
+// of its threads, as many warps as this page's new tokens want, holds a head's new
+// values in registers, CH chunks of sixteen a thread, until their codes are written,
+// and goes on to the next head that is its own.  Sines and cosines serve all of them.
+// (Groups as large as the longest round wants: 240 rounds of up to 47 tokens 75 us
+// instead of 70.)
 template <class T, bool NEAR, int THREADS, int CH, class Feed>
 __device__ __forceinline__ void append_pages(const KvAppendProblem& a, int b, int len, int n,
-                                             bool ok, float (*red)[THREADS / 32], Feed& feed) {
+                                             bool ok, float (*red)[THREADS / 32], const Feed& feed) {
   const int tid = static_cast<int>(threadIdx.x);
   const int Hkv = a.c.Hkv, D = a.c.D, P = a.c.page_size;
   const int pshift = D == 64 ? 2 : 3, parts = 1 << pshift;  // lanes of a head
-  const int GT = a.group, gl = tid & (GT - 1);
-  const int task = static_cast<int>(blockIdx.x) * (THREADS / GT) + tid / GT;
-  const int is = task / a.chunks, h0 = (task - is * a.chunks) * a.per;
+  const int is = static_cast<int>(blockIdx.x) / a.sets;  // (page, side)
+  const int h0 = (static_cast<int>(blockIdx.x) - is * a.sets) * a.set;
   const int side = is & 1, i = is >> 1;
+  const bool reports = h0 == 0 && side == 0 && tid == 0;
+  if (!ok && i == 0 && reports) record_error(a.err, SV_DERR_ARG);
+  if (!ok || n <= 0) return;
   // The page's new tokens.  (Their values are asked for before the page's id is
   // there: a trip to memory less.)
-  int kept = 0, first = 0, count = 0, slot = 0, row0 = 0;
-  if (i < a.pages && ok && n > 0) {
-    slot = (len >> a.c.page_shift) + i;
-    const int from = max(len, slot << a.c.page_shift);
-    const long long to =
-        min(static_cast<long long>(len) + n, (static_cast<long long>(slot) + 1) << a.c.page_shift);
-    if (from < to) {
-      kept = i == 0 ? len & (P - 1) : 0;
-      first = from - len;
-      count = static_cast<int>(to - from);
-      row0 = from & (P - 1);
-      if (!SV_CHECK(slot >= 0 && slot < a.c.slots && row0 + count <= P &&
-                        first + count <= a.T && first >= 0 && count * (D / 16) <= GT * CH,
-                    a.err))
-        count = 0;
-    }
-  }
-  int heads = count > 0 ? min(a.per, Hkv - h0) : 0;
-  const bool reports = h0 == 0 && side == 0 && gl == 0;
-  if (!ok && i == 0 && reports) record_error(a.err, SV_DERR_ARG);
-  if (!__syncthreads_or(heads > 0)) return;  // no page of the round here
-  const int j = gl & (parts - 1);  // the same for all of a thread's chunks
+  const int slot = (len >> a.c.page_shift) + i;
+  const int from = max(len, slot << a.c.page_shift);
+  const int count = static_cast<int>(
+      min(static_cast<long long>(len) + n, (static_cast<long long>(slot) + 1) << a.c.page_shift) - from);
+  if (count <= 0) return;  // no page of the round
+  const int kept = i == 0 ? len & (P - 1) : 0, first = from - len, row0 = from & (P - 1);
   const int chunks = count << pshift;
+  const int warps = static_cast<int>(blockDim.x) >> 5;
+  const int gw = (chunks + 32 * CH - 1) / (32 * CH), groups = warps / gw;  // warps of a group
+  if (!SV_CHECK(slot >= 0 && slot < a.c.slots && row0 + count <= P && first >= 0 &&
+                    first + count <= a.T && groups > 0 && h0 < Hkv,
+                a.err))
+    return;
+  const int g = (tid >> 5) / gw, GT = gw << 5, gl = tid - g * GT;
+  const int set = min(a.set, Hkv - h0), passes = (set + groups - 1) / groups;
+  // the thread's heads: h0 + g, h0 + g + groups ..
+  int heads = g < groups && g < set ? (set - g + groups - 1) / groups : 0;
+  const int j = gl & (parts - 1);  // the same for all of a thread's chunks
   Place at = place_of<NEAR>(a.rope, j);
   if (side) at = Place{16 * j, 16 * j + 8, false};  // values stay where they are
-  const long long head = side ? a.v_head : a.k_head;
+  const long long head = (side ? a.v_head : a.k_head) * groups;
   const bool vec = side ? a.v_vec : a.k_vec;
   const T* src[CH];
 #pragma unroll
   for (int k = 0; k < CH; ++k) {
     const int c = gl + k * GT;
     src[k] = static_cast<const T*>(side ? a.v_new : a.k_new) +
-             (side ? b * a.v_batch + h0 * a.v_head + (first + (c >> pshift)) * a.v_token
-                   : b * a.k_batch + h0 * a.k_head + (first + (c >> pshift)) * a.k_token);
+             (side ? b * a.v_batch + (h0 + g) * a.v_head + (first + (c >> pshift)) * a.v_token
+                   : b * a.k_batch + (h0 + g) * a.k_head + (first + (c >> pshift)) * a.k_token);
   }
   const int stages = Feed::kStages - 1;  // heads asked for ahead
 #pragma unroll
@@ -556,13 +581,10 @@ __device__ __forceinline__ void append_pages(const KvAppendProblem& a, int b, in
         feed.template ask<NEAR>(i, k, src[k] + i * head, at, vec, a.err);
     Feed::commit();
   }
-  int page = 0;
-  if (count > 0) {
-    page = a.c.page_table[static_cast<long long>(b) * a.c.slots + slot];
-    if (page < 0 || page >= a.c.num_pages) {
-      if (reports) record_error(a.err, SV_DERR_PAGE);
-      page = heads = 0;
-    }
+  int page = a.c.page_table[static_cast<long long>(b) * a.c.slots + slot];
+  if (page < 0 || page >= a.c.num_pages) {
+    if (reports) record_error(a.err, SV_DERR_PAGE);
+    page = heads = 0;
   }
   const bool norm = side == 0 && a.k_norm.eps > 0.f;
   const bool weighted = norm && a.k_norm.weight != nullptr && gl < chunks;
@@ -577,11 +599,11 @@ __device__ __forceinline__ void append_pages(const KvAppendProblem& a, int b, in
         turn_at(a.rope, j, position_of(a.kv_len, a.offset, a.T, b, first + (c >> pshift)), cs[k],
                 sn[k]);
     }
-  unsigned char* dst = (side ? a.c.v : a.c.k) + page * a.c.page_stride + h0 * a.c.head_stride;
-  float* scale = (side ? a.c.v_scale : a.c.k_scale) + static_cast<long long>(page) * Hkv + h0;
+  unsigned char* dst = (side ? a.c.v : a.c.k) + page * a.c.page_stride + (h0 + g) * a.c.head_stride;
+  float* scale = (side ? a.c.v_scale : a.c.k_scale) + static_cast<long long>(page) * Hkv + h0 + g;
 
 #pragma unroll 1
-  for (int hh = 0; hh < a.per; ++hh) {  // (the same for all threads of the block)
+  for (int hh = 0; hh < passes; ++hh) {  // (the same for all threads of the block)
     const bool here = hh < heads;
     Pairs y[CH];
     Feed::wait();
@@ -655,9 +677,8 @@ __device__ __forceinline__ void append_pages(const KvAppendProblem& a, int b, in
     // other before it is written again)
     if ((tid & 31) == 0) red[hh & 1][tid >> 5] = amax;
     __syncthreads();  // every thread has read the old scale, too
-    const int w0 = (tid / GT) * (GT / 32);
-    for (int k = 0; k < GT / 32; ++k) amax = fmaxf(amax, red[hh & 1][w0 + k]);
     if (here) {
+      for (int k = 0; k < gw; ++k) amax = fmaxf(amax, red[hh & 1][g * gw + k]);
       const int before = scale_exp(stored), e = max(needed_exp(amax), before);
       const float2 inv = x2_of(pow2f(-e));
 #pragma unroll
@@ -688,19 +709,23 @@ __device__ __forceinline__ void append_pages(const KvAppendProblem& a, int b, in
         if (stored != scale_value(stored)) record_error(a.err, SV_DERR_ARG);
       }
     }
-    dst += a.c.head_stride;
-    ++scale;
+    dst += groups * a.c.head_stride;
+    scale += groups;
   }
 }
 
-template <class T, int THREADS, int CH>
-union AppendFeed {
-  Ahead<T, THREADS, 1> q;
-  Ahead<T, THREADS, CH> kv;
-};
+// Slots of a thread in shared memory.
+template <class T, int CH>
+constexpr int kAppendSlots =
+    Ahead<T, 1, 0>::kSlots > Ahead<T, CH, 0>::kSlots ? Ahead<T, 1, 0>::kSlots
+                                                     : Ahead<T, CH, 0>::kSlots;
 
-// Blocks of 256 threads with one chunk a thread for up to 256 chunks a page and head (a
-// page's, or the round's), with two up to 512; of 512 threads above.  Bound: HBM, at 84 %
+// Up to 256 chunks a page and head (a page's, or the round's): one chunk a thread and
+// blocks no larger than the groups want, since all threads of a block wait for one
+// another at each head (4 prompts of 1356 tokens, pages of 16, heads of 64: blocks of
+// one group of 64 threads 15.3 us, of four 26.2).  Up to 512 chunks two a thread and
+// blocks of 256 threads (smaller ones leave registers of the SM unused: 93 rounds of
+// 44 tokens of fp32, 192 threads 35.8 us, 256 31.2); above, 512.  Bound: HBM, at 84 %
 // of the copy bandwidth, with the fixed latencies of the norm's and rotation's
 // arithmetic close behind (4 prompts of 8190 tokens, 32 query and 8 key heads of 128,
 // 738 MB: 130 us; 126 registers, so two blocks an SM; a third, with the sines in
@@ -709,8 +734,10 @@ template <class T, bool NEAR, int THREADS, int CH>
 __global__ void __launch_bounds__(THREADS, THREADS == 256 ? (CH == 1 ? 3 : 2) : 1)
     kv_append_kernel(const KvAppendProblem a) {
   __shared__ float red[2][THREADS / 32];
-  extern __shared__ __align__(16) unsigned char append_feed[];
-  AppendFeed<T, THREADS, CH>& feed = *reinterpret_cast<AppendFeed<T, THREADS, CH>*>(append_feed);
+  extern __shared__ uint4 append_slots[];
+  uint4* const slots = append_slots + threadIdx.x;
+  constexpr int kStride = CH == 1 ? 0 : THREADS;
+  const int stride = static_cast<int>(blockDim.x);
   grid_dependency_wait();
   const int b = static_cast<int>(blockIdx.y);
   const int len = a.kv_len[b];
@@ -718,13 +745,17 @@ __global__ void __launch_bounds__(THREADS, THREADS == 256 ? (CH == 1 ? 3 : 2) : 
   const bool ok = len >= 0 && n >= 0 && n <= a.T &&
                   (n == 0 || static_cast<long long>(len) + n <=
                                  static_cast<long long>(a.c.slots) * a.c.page_size);
-  if (static_cast<int>(blockIdx.x) >= a.blocks)
-    rotate_heads<T, NEAR>(a.q, a.rope, b, ok ? n : 0, a.T, a.kv_len, a.offset, a.c.D,
-                          a.c.D == 64 ? 2 : 3,
-                          (static_cast<int>(blockIdx.x) - a.blocks) * THREADS +
-                              static_cast<int>(threadIdx.x), feed.q, a.err);
-  else
-    append_pages<T, NEAR, THREADS, CH>(a, b, len, n, ok, red, feed.kv);
+  if (static_cast<int>(blockIdx.x) >= a.blocks) {
+    const int lane_shift = a.c.D == 64 ? 2 : 3, lanes = a.T << lane_shift;
+    const int thread = (static_cast<int>(blockIdx.x) - a.blocks) * static_cast<int>(blockDim.x) +
+                       static_cast<int>(threadIdx.x);
+    const int part = thread / lanes, rest = thread - part * lanes;
+    const Spot spot{true, b, rest >> lane_shift, rest & ((1 << lane_shift) - 1), ok ? n : 0};
+    rotate_heads<T, NEAR>(a.q, a.rope, spot, a.T, a.kv_len, a.offset, a.c.D, lane_shift,
+                          part * a.q.per, Ahead<T, 1, kStride>{slots, stride}, a.err);
+  } else {
+    append_pages<T, NEAR, THREADS, CH>(a, b, len, n, ok, red, Ahead<T, CH, kStride>{slots, stride});
+  }
 }
 
 }  // namespace sv

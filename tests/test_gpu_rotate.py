@@ -408,3 +408,38 @@ def test_two_streams_at_once():
     for q, lp in got[0] + got[1]:
         assert torch.equal(q, want)
         assert all(torch.equal(lp[n], said[n]) for n in said)
+
+
+@pytest.mark.parametrize("Hq,dtype,inter", [(20, "bf16", False), (33, "fp16", True)])
+def test_more_tokens_than_run_at_once(Hq, dtype, inter):
+    """Blocks of the same tokens one behind the other: requests of odd lengths, lanes
+    without channels, parts of different sizes."""
+    rng = np.random.default_rng(Hq)
+    B, T, Hk, D = 3, 2003, 5, 80
+    rope, num = sv.rope(64, 5e5, interleaved=inter), np.array([2003, 0, 1001])
+    first = np.array([0, 7, 90001])
+    x, x64 = as_type(rng.normal(size=(B, T, Hq + Hk, D)), dtype)
+    got = sv.rotate(x[:, :, :Hq], x[:, :, Hq:], start=i32(first), num=i32(num), rope=rope, eps=1e-5)
+    y, size = ru.rotated(x64, ru.positions(first, None, B, T), rope, None, 1e-5)
+    for b in range(B):
+        y[b, num[b]:] = size[b, num[b]:] = 0
+    near(got["q"], y[:, :, :Hq], size[:, :, :Hq], dtype)
+    near(got["k"], y[:, :, Hq:], size[:, :, Hq:], dtype)
+
+
+MIXED = [  # rounds of very different lengths in one call: T, Hq, H, P, D, dtype
+    (47, 10, 5, 64, 128, "bf16"),   # two chunks a thread, one group or several
+    (200, 4, 3, 128, 128, "fp16"),  # blocks of 512 threads
+    (18, 16, 2, 64, 128, "bf16"),   # groups of five warps
+    (100, 24, 12, 16, 64, "fp32"),  # several groups, two sets of heads
+    (27, 7, 7, 32, 128, "bf16"),    # groups of seven warps, heads no group's multiple
+    (2, 1, 1, 16, 64, "fp16"),      # a block of two warps
+]
+
+
+@pytest.mark.parametrize("T,Hq,H,P,D,dtype", MIXED)
+def test_append_rounds_of_mixed_lengths(T, Hq, H, P, D, dtype):
+    rng = np.random.default_rng(T)
+    new = np.array([T, 0, 1, T // 2, T, T // 3, max(T - 1, 1), 1])
+    lens = np.array([P - 1, 5, P, 0, 2 * P - T % P, 3 * P + 1, 1, P - 1])
+    check_append(rng, lens, new, T, Hq, H, P, D, dtype, sv.rope(D // 2, 1e4), 1e-6)
