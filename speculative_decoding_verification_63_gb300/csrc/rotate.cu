@@ -108,10 +108,10 @@ int heads_per_thread(const sv_heads& q, const sv_heads& k, int64_t one, int64_t 
 
 template <class T, bool NEAR, int THREADS, int CH>
 sv_status run_append(const KvAppendProblem& p, dim3 grid, int block, cudaStream_t stream) {
-  const size_t smem = sizeof(uint4) * kAppendSlots<T, CH> * block;
+  const size_t smem = sizeof(uint4) * kSlotsOf<T, CH> * block;
   const auto kernel = kv_append_kernel<T, NEAR, THREADS, CH>;
-  constexpr int most = static_cast<int>(sizeof(uint4)) * kAppendSlots<T, CH> * THREADS;
-  if (most > 48 * 1024 &&
+  constexpr int most = static_cast<int>(sizeof(uint4)) * kSlotsOf<T, CH> * THREADS;
+  if (most + 1024 > 48 * 1024 &&  // (static words count, too)
       cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                            most) != cudaSuccess)
     return SV_ECUDA;

@@ -102,11 +102,20 @@ __device__ __forceinline__ void load_pairs(RawPairs<T>& r, const T* p, const Pla
 // come, so nothing is shared and no thread waits for another, and what is under
 // way takes no registers.  Pieces that are not on a 16-byte boundary are loaded
 // when they are needed.
-template <class T, int CH, int STRIDE>
+//
+// A thread's slots, of 16 bytes: four heads of one chunk of 16-bit values or two of two
+// chunks; three and two of fp32 (2 x 4096 tokens of 40 heads: two heads 55.7 us, three
+// 54.9; appends of 4 x 1356 tokens with pages of 16: 24.3 and 20.4), and four for queries
+// beside two chunks (4 x 4096 tokens: 119 us with two, 110).  Twice as many for 16-bit
+// values: prompts 131 us as before, pages of 64 and 128 tokens 1 to 6 % slower.
+template <class T, int CH>
+constexpr int kSlotsOf = sizeof(T) == 2 ? 8 : CH == 1 ? 12 : 16;
+
+template <class T, int CH, int STRIDE, int SLOTS>
 struct Ahead {
   static constexpr int kPieces = static_cast<int>(sizeof(T)) * CH;  // of 16 bytes a head
-  static constexpr int kStages = 8 / kPieces > 1 ? 8 / kPieces : 2;
-  static constexpr int kSlots = kStages * kPieces;  // of a thread
+  static constexpr int kStages = SLOTS / kPieces;
+  static_assert(kStages > 1, "a head ahead");
   uint4* mine;  // the thread's first slot; the next one is STRIDE (the block's threads)
   int stride;   // further, or `stride` where that is 0
   __device__ __forceinline__ uint4* slot(int i, int piece) const {
@@ -467,7 +476,7 @@ struct RotateProblem {
 constexpr int kRotateThreads = 256;
 
 // Bound: HBM (2 prompts of 8190 tokens, 40 heads of 128, 335 MB: 52.2 us, 95 % of the
-// copy bandwidth; pairs of neighbours 54, fp32 55 for half as many tokens; before the
+// copy bandwidth; pairs of neighbours 54, fp32 54 for half as many tokens; before the
 // blocks of the same tokens followed one another 54.5; loads into registers a head
 // ahead 67.7; two blocks an SM 76 and four 70 at that time).  Small calls: the launch
 // (2.7 us for one token of 64 requests).  Tokens lie flat over the requests, so that
@@ -476,8 +485,9 @@ constexpr int kRotateThreads = 256;
 // shared memory: 0.1 to 0.4 us more in small calls, 1.3 in prompts.
 template <class T, bool NEAR>
 __global__ void __launch_bounds__(kRotateThreads, 3) rotate_kernel(const RotateProblem a) {
-  using Feed = Ahead<T, 1, kRotateThreads>;
-  __shared__ uint4 slots[Feed::kSlots * kRotateThreads];
+  constexpr int kSlots = kSlotsOf<T, 1>;
+  using Feed = Ahead<T, 1, kRotateThreads, kSlots>;
+  __shared__ uint4 slots[kSlots * kRotateThreads];
   grid_dependency_wait();
   // Tokens lie one request behind the other (at most 2^10 requests of 2^16 tokens of
   // 16 lanes, and a block's rounding: 31 bits).
@@ -714,12 +724,6 @@ __device__ __forceinline__ void append_pages(const KvAppendProblem& a, int b, in
   }
 }
 
-// Slots of a thread in shared memory.
-template <class T, int CH>
-constexpr int kAppendSlots =
-    Ahead<T, 1, 0>::kSlots > Ahead<T, CH, 0>::kSlots ? Ahead<T, 1, 0>::kSlots
-                                                     : Ahead<T, CH, 0>::kSlots;
-
 // Up to 256 chunks a page and head (a page's, or the round's): one chunk a thread and
 // blocks no larger than the groups want, since all threads of a block wait for one
 // another at each head (4 prompts of 1356 tokens, pages of 16, heads of 64: blocks of
@@ -728,7 +732,7 @@ constexpr int kAppendSlots =
 // 44 tokens of fp32, 192 threads 35.8 us, 256 31.2); above, 512.  Bound: HBM, at 84 %
 // of the copy bandwidth, with the fixed latencies of the norm's and rotation's
 // arithmetic close behind (4 prompts of 8190 tokens, 32 query and 8 key heads of 128,
-// 738 MB: 130 us; 126 registers, so two blocks an SM; a third, with the sines in
+// 738 MB: 130 us; 128 registers, so two blocks an SM; a third, with the sines in
 // shared memory, 139; the queries in a launch of their own 141).
 template <class T, bool NEAR, int THREADS, int CH>
 __global__ void __launch_bounds__(THREADS, THREADS == 256 ? (CH == 1 ? 3 : 2) : 1)
@@ -752,9 +756,9 @@ __global__ void __launch_bounds__(THREADS, THREADS == 256 ? (CH == 1 ? 3 : 2) : 
     const int part = thread / lanes, rest = thread - part * lanes;
     const Spot spot{true, b, rest >> lane_shift, rest & ((1 << lane_shift) - 1), ok ? n : 0};
     rotate_heads<T, NEAR>(a.q, a.rope, spot, a.T, a.kv_len, a.offset, a.c.D, lane_shift,
-                          part * a.q.per, Ahead<T, 1, kStride>{slots, stride}, a.err);
+                          part * a.q.per, Ahead<T, 1, kStride, kSlotsOf<T, CH>>{slots, stride}, a.err);
   } else {
-    append_pages<T, NEAR, THREADS, CH>(a, b, len, n, ok, red, Ahead<T, CH, kStride>{slots, stride});
+    append_pages<T, NEAR, THREADS, CH>(a, b, len, n, ok, red, Ahead<T, CH, kStride, kSlotsOf<T, CH>>{slots, stride});
   }
 }
 
