@@ -105,6 +105,12 @@ float number(PyObject* o) {
   return static_cast<float>(v);
 }
 
+bool truth(PyObject* o) {
+  const int v = PyObject_IsTrue(o);
+  if (v < 0) throw Refused();  // (an array's, say)
+  return v != 0;
+}
+
 PyObject* field(PyObject* dict, const char* name, const char* what) {
   if (!PyDict_Check(dict)) refuse(std::string(what) + ": expected a dict");
   PyObject* v = PyDict_GetItemString(dict, name);
@@ -116,7 +122,7 @@ void rope(sv_rope& r, PyObject* o, const Place& p) {
   r.scale = 1.f;
   if (!given(o)) return;
   r.dim = whole(field(o, "dim", "rope"), "rope dim");
-  r.interleaved = PyObject_IsTrue(field(o, "interleaved", "rope")) ? 1 : 0;
+  r.interleaved = truth(field(o, "interleaved", "rope")) ? 1 : 0;
   r.scale = number(field(o, "scale", "rope"));
   r.freq = static_cast<const uint64_t*>(
       address(field(o, "freq", "rope"), ScalarType::Long, {r.dim / 2}, "rope freq", p));
@@ -420,7 +426,7 @@ PyObject* token_logprobs(PyObject*, PyObject* const* v, Py_ssize_t nv) {
     a.temperature =
         static_cast<const float*>(address(v[8], ScalarType::Float, {B}, "temperature", p));
     Tensor out[4];
-    if (PyObject_IsTrue(v[10])) {
+    if (truth(v[10])) {
       own(v[2], "logits");
       if (R < 0) refuse("R: out of range");
       if (given(v[5])) out[0] = empty(asked, ScalarType::Float, p);
