@@ -488,7 +488,8 @@ typedef struct {
 
 /* Heads of one kind, in and out: element (b, t, h, i) at b * batch_stride + t *
    token_stride + h * head_stride + i.  No two elements of out share a place
-   (SV_EINVAL for a stride of 0 along more than one). */
+   (SV_EINVAL for a stride of 0 along more than one), and none one with other
+   inputs or results of the call (SV_EINVAL where heads of the first token do). */
 typedef struct {
   const void* x;
   void* out;               /* x itself (the same strides and type) or apart from it */

@@ -385,7 +385,7 @@ def rotate(q, k=None, start=None, num=None, offset=None, rope=None, q_weight=Non
     request b is at start[b] + t, or start[b] + offset[b][t] (tree_mask's
     depths); later rows become zero.  rope: rope()'s dict, None for norms
     alone; eps None: no norm.  Returns q and k (device tensors), which are the
-    arguments themselves when inplace."""
+    arguments themselves when inplace (then no head of q is one of k too)."""
     if ws is None:
         ws = workspace(SV_MIN_WORKSPACE_BYTES, q.device, "kv")
     out = ... if inplace else None

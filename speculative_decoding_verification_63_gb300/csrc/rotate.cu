@@ -39,6 +39,46 @@ bool heads_ok(const sv_heads& h, sv_dtype dtype, int B, int T) {
            h.token_stride == h.out_token_stride && h.head_stride == h.out_head_stride));
 }
 
+// Whether heads of the first token of the first request lie on one another, at a and at b
+// (in bytes: `size` a head, `step` from one to the next).  Calls whose results pass this
+// may still share places at other tokens: those are the caller's to keep apart.
+struct Laid {
+  const void* at;
+  int heads;
+  int64_t step, size;
+};
+bool share(const Laid& a, const Laid& b) {
+  const auto at = [](const Laid& h, int i) {
+    return static_cast<int64_t>(reinterpret_cast<uintptr_t>(h.at)) + i * h.step;
+  };
+  const auto apart = [](int64_t lo, int64_t end, int64_t other, int64_t other_end) {
+    return end <= other || other_end <= lo;
+  };
+  if (a.heads == 0 || b.heads == 0) return false;
+  // (mostly decided here: other buffers, or other heads of one projection)
+  if (apart(std::min(at(a, 0), at(a, a.heads - 1)), std::max(at(a, 0), at(a, a.heads - 1)) + a.size,
+            std::min(at(b, 0), at(b, b.heads - 1)), std::max(at(b, 0), at(b, b.heads - 1)) + b.size))
+    return false;
+  // (of equal steps, as between heads of one projection, only how many lie between counts)
+  const bool equal = a.step == b.step;
+  for (int i = equal ? 1 - b.heads : 0; i < a.heads; ++i)
+    for (int j = 0; j < (equal ? 1 : b.heads); ++j)
+      if (!apart(at(a, i), at(a, i) + a.size, at(b, j), at(b, j) + b.size)) return true;
+  return false;
+}
+Laid read(const sv_heads& h, sv_dtype dtype, int D) {
+  const int es = dtype_bytes(dtype);
+  return Laid{h.x, h.heads, h.head_stride * es, int64_t{D} * es};
+}
+Laid written(const sv_heads& h, int D) {
+  const int es = dtype_bytes(h.out_dtype);
+  return Laid{h.out, h.heads, h.out_head_stride * es, int64_t{D} * es};
+}
+// Results lie apart from what else is read: threads of different blocks would meet there.
+bool apart_from_input(const sv_heads& h, sv_dtype dtype, int D) {
+  return h.x == h.out || !share(written(h, D), read(h, dtype, D));
+}
+
 HeadNorm norm_view(const sv_head_norm& n) { return HeadNorm{n.weight, n.weight_dtype, n.eps}; }
 
 Rope rope_view(const sv_rope& r) {
@@ -134,6 +174,11 @@ sv_status sv_rotate(const sv_rotate_args* a, void* workspace, size_t ws_bytes,
       !heads_ok(a->k, a->dtype, a->B, a->T))
     return SV_EINVAL;
   if (a->q.heads + a->k.heads == 0) return SV_OK;
+  if (!apart_from_input(a->q, a->dtype, a->D) || !apart_from_input(a->k, a->dtype, a->D) ||
+      share(written(a->q, a->D), written(a->k, a->D)) ||
+      share(written(a->q, a->D), read(a->k, a->dtype, a->D)) ||
+      share(written(a->k, a->D), read(a->q, a->dtype, a->D)))
+    return SV_EINVAL;
   const sv_status wst = workspace_ok(workspace, ws_bytes, SV_MIN_WORKSPACE_BYTES);
   if (wst != SV_OK) return wst;
   Device dev;
@@ -189,6 +234,11 @@ sv_status sv_kv_append(const sv_kv_append_args* a, void* workspace, size_t ws_by
     return SV_EINVAL;
   const int es = dtype_bytes(a->dtype);
   if (!aligned(a->k_new, static_cast<size_t>(es)) || !aligned(a->v_new, static_cast<size_t>(es)))
+    return SV_EINVAL;
+  const int D = a->cache.D, Hkv = a->cache.Hkv;
+  if (!apart_from_input(a->q, a->dtype, D) ||
+      share(written(a->q, D), Laid{a->k_new, Hkv, a->k_head_stride * es, int64_t{D} * es}) ||
+      share(written(a->q, D), Laid{a->v_new, Hkv, a->v_head_stride * es, int64_t{D} * es}))
     return SV_EINVAL;
   const sv_status wst = workspace_ok(workspace, ws_bytes, SV_MIN_WORKSPACE_BYTES);
   if (wst != SV_OK) return wst;
