@@ -2,6 +2,7 @@
 import numpy as np
 import pytest
 
+import speculative_decoding_verification_63_gb300 as sv
 from test_round_host import FAKE, _append, _call, _rotate, b, native, tensors  # noqa: F401
 
 
@@ -82,3 +83,13 @@ def test_results_that_share_places_are_refused(b, q, k):  # noqa: F811
     for side in "kv":
         a = _append(b, q=args[0], **far | {side + "_new": args[1]["x"], side + "_head_stride": k[3]})
         assert _call(b, "sv_kv_append", a, n=0) == want, side
+
+
+# -------------------------------------------------------------------- rope
+
+@pytest.mark.parametrize("fast,slow", [(1, 32), (4, 4), (0.5, 1)])
+def test_yarn_bounds_that_contradict_are_refused(fast, slow):
+    """No frequency can be kept as a fast one and stretched as a slow one."""
+    with pytest.raises(ValueError, match="slow < fast"):
+        sv.rope(64, device="cpu", scaling=dict(type="yarn", factor=4, context=8192, fast=fast,
+                                               slow=slow))
