@@ -340,8 +340,8 @@ def rope(dim: int, base: float = 10000.0, interleaved: bool = False, scaling: di
         fast, slow = take("fast", 32.0), take("slow", 1.0)
         if base <= 1:
             raise ValueError(f"rope: yarn scaling needs a base above 1, got {base}")
-        if fast <= slow:
-            raise ValueError("rope: yarn scaling needs slow < fast")
+        if fast < slow:
+            raise ValueError("rope: yarn scaling needs slow <= fast")
 
         def pair(turns):  # the pair that turns so often over the trained context
             return dim * math.log(context / (turns * 2 * math.pi)) / (2 * math.log(base))
