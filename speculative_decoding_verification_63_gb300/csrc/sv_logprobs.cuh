@@ -633,7 +633,7 @@ __global__ void __launch_bounds__(kLpThreads, kLpCtasPerSm) logprob_kernel(const
       const float ln2 = 0.69314718055994531f, z = log2f(q.z);
       sh.m = bad ? nan : q.m;
       sh.log_z = (z - lp_off(q.m, c)) * ln2;  // relative to m itself
-      sh.entropy = bad ? nan : (z - q.a / q.z) * ln2;
+      sh.entropy = bad ? nan : fmaxf((z - q.a / q.z) * ln2, 0.f);
     }
   }
   bool leave = false;
@@ -693,7 +693,13 @@ __global__ void __launch_bounds__(kLpThreads, kLpCtasPerSm) logprob_kernel(const
     __syncthreads();
   }
   const float m = sh.m, log_z = sh.log_z;
-  auto logprob = [&](float v) { return (v - m) * inv_t - log_z; };
+  // Where one token holds everything, the logarithm of its weight relative to the
+  // reference is off what it is taken from by some 1e-7, to either side: no probability
+  // is above 1 (and no entropy below 0).  A NaN stays one.
+  auto logprob = [&](float v) {
+    const float lp = (v - m) * inv_t - log_z;
+    return lp > 0.f ? 0.f : lp;
+  };
   if (tid == 0 && a.entropy) a.entropy[orow] = sh.entropy;
   for (int i = tid; i < a.M; i += kLpThreads) {
     if (i >= kLpThreads) {
