@@ -499,6 +499,7 @@ __global__ void __launch_bounds__(kLpThreads, kLpCtasPerSm) logprob_kernel(const
   }
   if (flag && rank == 0 && tid == 0) record_error(a.err, flag);
   if (t == 0.f) t = 1.f;
+  t = fmaxf(t, 0x1p-126f);  // (below, 1 / t passes the range of fp32)
   if (a.cluster > 1) cl_wait();  // the first CTA is there
 
   if (!live) {
@@ -522,7 +523,7 @@ __global__ void __launch_bounds__(kLpThreads, kLpCtasPerSm) logprob_kernel(const
   const LpShare share{a.cluster, rank};
   int groups = share.count(all);
   if (TOP && !SV_CHECK(groups <= a.share, a.err)) groups = 0;  // the map's size
-  const float c = fminf(1.44269504f / t, 3e38f), inv_t = fminf(1.f / t, 3e38f);
+  const float c = 1.44269504f / t, inv_t = 1.f / t;
   Map* const map = reinterpret_cast<Map*>(lp_map);
   float given = 0.f;  // the given token's logit, for the end
   if (token >= 0 && token < a.V) given = lp_value(x + token);

@@ -53,3 +53,21 @@ def test_rows_without_values_keep_their_nan():
     assert torch.isnan(got["entropy"][0, 1:]).all() and torch.isnan(got["logprobs"][0, 1:]).all()
     assert torch.isnan(got["top_logprobs"][0, 1:]).all()
     assert not torch.isnan(got["entropy"][0, 0])
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_temperatures_at_the_ends_of_fp32(dtype):
+    """Subnormal ones count as the least normal one; the largest ones level the logits."""
+    t = np.array([1e-45, 1e-40, 2.0 ** -127, 2.0 ** -126, 3e-38, 1e38, 3.4e38], np.float32)
+    x = np.tile([0.0, -1e-3, 0.0, -1.0, -2.0 ** -120], (len(t), 1))[:, None]
+    x, x64 = as_type(x, dtype)
+    tokens = i32(np.tile(np.arange(5), (len(t), 1, 1)))
+    ws = new_ws()
+    got = sv.token_logprobs(x, tokens, temperature=f32(t), ws=ws)
+    assert flags(ws) == (sv.SV_OK, 0)
+    for b in range(len(t)):
+        row = ru.Row(x64[b, 0], max(float(t[b]), 2.0 ** -126))
+        lp_off, h_off = row.bounds()
+        lp = got["logprobs"][b, 0].double().cpu().numpy()
+        assert (np.abs(lp - row.lp) <= lp_off).all(), (t[b], lp, row.lp)
+        assert abs(float(got["entropy"][b, 0]) - row.entropy) <= h_off
