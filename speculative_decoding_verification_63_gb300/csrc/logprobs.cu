@@ -12,10 +12,7 @@ using namespace sv;
 template <class T, bool TOP>
 sv_status run(const LogprobProblem& p, size_t map, cudaStream_t stream) {
   static_assert(kLpCtasPerSm * (sizeof(LpShared) + kLpMapBytes + 1024) <= 227 * 1024, "four CTAs an SM");
-  if (map + sizeof(LpShared) > 48 * 1024 &&
-      cudaFuncSetAttribute(logprob_kernel<T, TOP>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                           kLpMapBytes) != cudaSuccess)
-    return SV_ECUDA;
+  static_assert(sizeof(LpShared) + kLpMapBytes <= 48 * 1024, "no opt-in to more shared memory");
   const dim3 grid(static_cast<unsigned>(p.B) * static_cast<unsigned>(p.R) *
                   static_cast<unsigned>(p.cluster));
   return launch(logprob_kernel<T, TOP>, p, grid, kLpThreads, map, stream, p.cluster);
