@@ -377,7 +377,8 @@ __device__ __noinline__ void lp_sort(unsigned long long* v, int n) {
 
 // Too many logits reach the bound: finds the row's n groups of largest maxima
 // (equal ones: the first) and collects the logits that reach the last of them, at
-// most kLpList.  Every thread of the cluster calls this.
+// most kLpList.  There are n groups that reach the bound: more than kLpList logits do,
+// or those of more than kLpGroups groups.  Every thread of the cluster calls this.
 template <class T>
 __device__ __noinline__ void lp_choose(const LogprobProblem& a, LpShared& sh,
                                        const typename LpKey<T>::Map* map, LpRow<T> in,
@@ -390,9 +391,9 @@ __device__ __noinline__ void lp_choose(const LogprobProblem& a, LpShared& sh,
   // since equal maxima are the likely reason to be here.
   unsigned lo = bound, hi = sizeof(typename LpKey<T>::Map) == 2 ? 0x10000u : 0xffffffffu;
   unsigned above = 0;
-  bool enough = true;
+  static_assert(kLpList / kLpGroup >= SV_MAX_TOPK && kLpGroups >= SV_MAX_TOPK, "n groups");
   // (at most 18 steps for keys of 32 bits)
-  for (int step = 0; step < 20 && enough && (step == 0 || hi - lo > 1); ++step) {
+  for (int step = 0; step < 20 && (step == 0 || hi - lo > 1); ++step) {
     const unsigned part = (hi - lo) / 4;
     const unsigned at[3] = {step == 0 ? lo : lo + max(part, 1u),
                             step == 0 ? lo + 1 : lo + max(2 * part, 1u),
@@ -417,7 +418,6 @@ __device__ __noinline__ void lp_choose(const LogprobProblem& a, LpShared& sh,
         above = all;
       }
     }
-    enough = hi != lo;  // (else fewer groups have a logit above -inf: all of them)
 #pragma unroll
     for (int q = 0; q < 3; ++q)
       if (at[q] < hi && at[q] > lo) lo = at[q];
@@ -425,14 +425,13 @@ __device__ __noinline__ void lp_choose(const LogprobProblem& a, LpShared& sh,
   lp_sync(a.cluster);  // every CTA has read the counts
   if (share.rank == 0 && tid == 0) sh.count[0] = 0;
   lp_sync(a.cluster);
-  // the groups that reach hi (or all, where there are fewer than n), and of each
-  // CTA the first of those equal to lo, as many as are missing
-  const unsigned from = enough ? hi : bound;
+  // the groups that reach hi, and of each CTA the first of those equal to lo, as many
+  // as are missing
   for (int i = tid; (i & ~31) < groups; i += kLpThreads) {
     const unsigned k = i < groups ? LpKey<T>::of_map(map[i]) : 0;
-    lp_push(first, i < groups && k >= from, lp_item(k, share.group(i)));
+    lp_push(first, i < groups && k >= hi, lp_item(k, share.group(i)));
   }
-  if (enough && tid < 32) {
+  if (tid < 32) {
     int wanted = static_cast<int>(n - above);
     for (int i = lane; (i & ~31) < groups && wanted > 0; i += 32) {
       bool is = i < groups && LpKey<T>::of_map(map[i]) == lo;
@@ -451,7 +450,7 @@ __device__ __noinline__ void lp_choose(const LogprobProblem& a, LpShared& sh,
   if (tid < chosen) sh.group[tid] = static_cast<int>(~static_cast<unsigned>(sh.item[tid]));
   if (tid == 0) sh.count[0] = 0;
   __syncthreads();
-  lp_read_groups(in, sh.group, chosen, enough ? lo : bound, &sh);
+  lp_read_groups(in, sh.group, chosen, lo, &sh);
   __syncthreads();
 }
 
