@@ -26,6 +26,8 @@
 // the map.
 #pragma once
 
+#include <cuda_bf16.h>
+
 #include "sv_cluster.cuh"
 #include "sv_device.cuh"
 #include "sv_pairs.cuh"
@@ -375,6 +377,37 @@ __device__ __noinline__ void lp_sort(unsigned long long* v, int n) {
     }
 }
 
+// The search for the n-th largest of some keys, n of which reach `lo` and fewer, `above`,
+// reach `hi`.  Each step counts what reaches three keys between them; the first begins
+// with lo and lo + 1, since equal maxima are the likely reason to search.  In the end hi
+// is lo + 1.
+struct LpSearch {
+  unsigned lo, hi, above;
+  static constexpr int kSteps = 20;  // (at most 18 are taken for keys of 32 bits)
+  __host__ __device__ __forceinline__ bool more(int step) const {
+    return step < kSteps && (step == 0 || hi - lo > 1);
+  }
+  __host__ __device__ __forceinline__ void keys(int step, unsigned (&at)[3]) const {
+    const unsigned part = (hi - lo) / 4;
+    at[0] = step == 0 ? lo : lo + (part > 1 ? part : 1);
+    at[1] = step == 0 ? lo + 1 : lo + (2 * part > 1 ? 2 * part : 1);
+    at[2] = step == 0 ? lo + 2 * part : lo + (3 * part > 1 ? 3 * part : 1);
+  }
+  // reach: how many keys reach each of at
+  __host__ __device__ __forceinline__ void narrow(const unsigned (&at)[3],
+                                                  const unsigned (&reach)[3], unsigned n) {
+#pragma unroll
+    for (int q = 2; q >= 0; --q)  // from the largest key down
+      if (reach[q] < n) {
+        hi = at[q];
+        above = reach[q];
+      }
+#pragma unroll
+    for (int q = 0; q < 3; ++q)
+      if (at[q] < hi && at[q] > lo) lo = at[q];
+  }
+};
+
 // Too many logits reach the bound: finds the row's n groups of largest maxima
 // (equal ones: the first) and collects the logits that reach the last of them, at
 // most kLpList.  There are n groups that reach the bound: more than kLpList logits do,
@@ -386,19 +419,12 @@ __device__ __noinline__ void lp_choose(const LogprobProblem& a, LpShared& sh,
   const int tid = static_cast<int>(threadIdx.x), lane = tid & 31;
   const unsigned n = static_cast<unsigned>(a.top);
   LpShared* const first = cl_at(&sh, 0);
-  // lo: at least n groups of the row reach it; hi: fewer than n do, `above`.  Each step
-  // counts what reaches three keys between them; the first begins with lo and lo + 1,
-  // since equal maxima are the likely reason to be here.
-  unsigned lo = bound, hi = sizeof(typename LpKey<T>::Map) == 2 ? 0x10000u : 0xffffffffu;
-  unsigned above = 0;
   static_assert(kLpList / kLpGroup >= SV_MAX_TOPK && kLpGroups >= SV_MAX_TOPK, "n groups");
-  // (at most 18 steps for keys of 32 bits)
-  for (int step = 0; step < 20 && (step == 0 || hi - lo > 1); ++step) {
-    const unsigned part = (hi - lo) / 4;
-    const unsigned at[3] = {step == 0 ? lo : lo + max(part, 1u),
-                            step == 0 ? lo + 1 : lo + max(2 * part, 1u),
-                            step == 0 ? lo + 2 * part : lo + max(3 * part, 1u)};
-    unsigned c[3] = {0, 0, 0};
+  static_assert(1 + 3 * LpSearch::kSteps <= sizeof(sh.count) / sizeof(sh.count[0]), "counts");
+  LpSearch s{bound, sizeof(typename LpKey<T>::Map) == 2 ? 0x10000u : 0xffffffffu, 0};
+  for (int step = 0; s.more(step); ++step) {
+    unsigned at[3], c[3] = {0, 0, 0};
+    s.keys(step, at);
     for (int i = tid; i < groups; i += kLpThreads) {
       const unsigned k = LpKey<T>::of_map(map[i]);
 #pragma unroll
@@ -411,17 +437,11 @@ __device__ __noinline__ void lp_choose(const LogprobProblem& a, LpShared& sh,
     }
     lp_sync(a.cluster);
 #pragma unroll
-    for (int q = 2; q >= 0; --q) {  // from the largest key down
-      const unsigned all = *static_cast<volatile unsigned*>(&first->count[1 + 3 * step + q]);
-      if (all < n) {
-        hi = at[q];
-        above = all;
-      }
-    }
-#pragma unroll
     for (int q = 0; q < 3; ++q)
-      if (at[q] < hi && at[q] > lo) lo = at[q];
+      c[q] = *static_cast<volatile unsigned*>(&first->count[1 + 3 * step + q]);
+    s.narrow(at, c, n);
   }
+  const unsigned lo = s.lo, hi = s.hi;
   lp_sync(a.cluster);  // every CTA has read the counts
   if (share.rank == 0 && tid == 0) sh.count[0] = 0;
   lp_sync(a.cluster);
@@ -432,7 +452,7 @@ __device__ __noinline__ void lp_choose(const LogprobProblem& a, LpShared& sh,
     lp_push(first, i < groups && k >= hi, lp_item(k, share.group(i)));
   }
   if (tid < 32) {
-    int wanted = static_cast<int>(n - above);
+    int wanted = static_cast<int>(n - s.above);
     for (int i = lane; (i & ~31) < groups && wanted > 0; i += 32) {
       bool is = i < groups && LpKey<T>::of_map(map[i]) == lo;
       const unsigned who = __ballot_sync(0xffffffffu, is);
