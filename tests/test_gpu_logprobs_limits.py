@@ -6,8 +6,9 @@ import torch
 
 import round_util as ru
 import speculative_decoding_verification_63_gb300 as sv
+from speculative_decoding_verification_63_gb300 import _binding, _build
 from test_gpu_kvcache import as_type, flags, i32, new_ws
-from test_gpu_logprobs import f32
+from test_gpu_logprobs import check, f32
 
 pytestmark = pytest.mark.gpu
 
@@ -71,3 +72,67 @@ def test_temperatures_at_the_ends_of_fp32(dtype):
         lp = got["logprobs"][b, 0].double().cpu().numpy()
         assert (np.abs(lp - row.lp) <= lp_off).all(), (t[b], lp, row.lp)
         assert abs(float(got["entropy"][b, 0]) - row.entropy) <= h_off
+
+
+# ------------------------------------------- the search for the likeliest groups
+
+def spread_over_a_warp(rng, V, cluster):
+    """Different logits, the largest all in the groups of one warp of one CTA of the row's
+    (every 8 * cluster-th 32 groups): more groups than a CTA reads again reach the bound."""
+    group = np.arange(V) // 16
+    return rng.normal(size=V) + 10.0 * ((group // 32) % (8 * cluster) == 5 * cluster + cluster - 1)
+
+
+SEARCHED = {
+    "constant": lambda rng, V, cluster: np.full(V, -2.5),
+    "two values": lambda rng, V, cluster: np.where(rng.random(V) < 0.02, 2.0, 1.0),
+    "a few above": lambda rng, V, cluster: np.where(rng.random(V) < 30 / V, 2.0, 1.0) +
+    (rng.random(V) < 10 / V),
+    "integers": lambda rng, V, cluster: rng.integers(-3, 4, V).astype(float),
+    "lowest": lambda rng, V, cluster: np.where(rng.random(V) < 1 - 40 / V, -3e38,
+                                               rng.normal(size=V)),
+    "a warp": spread_over_a_warp,
+}
+
+
+@pytest.fixture(params=["release", "debug"])
+def build(request):
+    old = _binding.lib()
+    if request.param == "debug":
+        _binding._lib_handle = _binding.lib(_build.build_library(checks=True))
+    try:
+        yield
+    finally:
+        _binding._lib_handle = old
+
+
+@pytest.mark.parametrize("kind", list(SEARCHED))
+@pytest.mark.parametrize("rows,cluster,dtype,V", [
+    (5, 8, "bf16", 160016), (5, 8, "fp32", 300016), (40, 4, "fp32", 300016), (40, 4, "bf16", 20011),
+    (200, 2, "bf16", 160016), (200, 2, "fp32", 80003), (700, 1, "bf16", 80000),
+    (700, 1, "fp32", 40003)])
+def test_many_logits_reach_the_bound(build, kind, rows, cluster, dtype, V):
+    """A row by 1, 2, 4 and 8 CTAs; two rows by their definition, the others are the same."""
+    rng = np.random.default_rng(V + rows)
+    x, x64 = as_type(np.stack([SEARCHED[kind](rng, V, cluster) for _ in range(2)])[None], dtype)
+    if kind == "lowest":
+        x = torch.where(x < -1e38, torch.finfo(x.dtype).min, x)
+        x64 = x.double().cpu().numpy()
+    many = x.expand(rows // 2 + 1, 2, V).contiguous().view(1, -1, V)[:, :rows]
+    for top in (1, 20, 64):
+        ws = new_ws()
+        got = sv.token_logprobs(many, top=top, ws=ws)
+        assert flags(ws) == (sv.SV_OK, 0)
+        check(x64, {n: t[:, :2] for n, t in got.items()}, top=top)
+        for i in range(2):
+            # (rows that begin at other places of 32 bytes have other groups and orders of
+            # sums: the same tokens, and values that are each within the bounds)
+            lp_off, h_off = ru.Row(x64[0, i]).bounds()
+            ids = got["top_tokens"][0, i::2]
+            assert (ids == ids[:1]).all()
+            there = ids[0].cpu().numpy()
+            off = 2 * torch.from_numpy(np.where(there < 0, 0.0, lp_off[there])).cuda()
+            best, entropy = got["top_logprobs"][0, i::2], got["entropy"][0, i::2]
+            same = best == best[:1]  # (-inf too)
+            assert (same | ((best - best[:1]).abs() <= off)).all()
+            assert ((entropy - entropy[0]).abs() <= 2 * h_off).all()
