@@ -136,3 +136,51 @@ def test_many_logits_reach_the_bound(build, kind, rows, cluster, dtype, V):
             same = best == best[:1]  # (-inf too)
             assert (same | ((best - best[:1]).abs() <= off)).all()
             assert ((entropy - entropy[0]).abs() <= 2 * h_off).all()
+
+
+# ------------------------------------------------------------- long rows
+
+def long_bounds(row, turns, groups):
+    """Of a row's log probabilities and its entropy, for any data, where a thread takes
+    `turns` turns of `groups` groups, in units of 2^-24 of Z.  A weight: ex2 is off by 4;
+    its exponent's roundings (c, the product and sum: 3 of itself) and those of the rises
+    behind it (3 of each, which together are the exponent that is left) are 6 times the
+    mean distance to the maximum.  A rise, at most one a turn and three on the way from
+    thread to row: ex2 (4) and a product (1).  Additions: 8 a group, one for the pair and
+    one a turn, 5 in the warp, 2 and 5 over the warps.  The logarithm, the reference and
+    the differences: 4 of what they are made of (round_util.Row.bounds)."""
+    z = (4 + 5 * (turns + 3) + 8 * groups + 1 + turns + 12 + 6 * row.spread) * 2.0 ** -24
+    with np.errstate(invalid="ignore"):
+        d = np.abs(row.x - row.m) / row.t
+    lp = z + 4 * 2.0 ** -24 * (d + abs(row.log_z))
+    h = z * (1 + 2 * row.spread) + 8 * 2.0 ** -24 * (abs(row.log_z) + row.spread)
+    return np.where(np.isfinite(lp), lp, 0.0), h
+
+
+LONG = {
+    "ascending": lambda rng, V: np.linspace(-20, 20, V),
+    "barely ascending": lambda rng, V: np.linspace(0, 0.01, V),
+    "slowly ascending": lambda rng, V: np.linspace(0, 1, V),
+    "steps": lambda rng, V: np.arange(V) // 8192 * 0.05,
+    "descending": lambda rng, V: np.linspace(20, -20, V),
+    "random": lambda rng, V: rng.normal(size=V),
+}
+
+
+@pytest.mark.parametrize("kind", list(LONG))
+@pytest.mark.parametrize("dtype,groups", [("bf16", 4), ("fp32", 2)])
+@pytest.mark.parametrize("V", [1 << 20, 152064])
+def test_long_rows_by_one_cta(kind, dtype, groups, V):
+    """More rows than run at once, the same one: up to 128 turns a thread, whose reference
+    rises at every one of them."""
+    rng = np.random.default_rng(9)
+    x, x64 = as_type(LONG[kind](rng, V), dtype)
+    row = ru.Row(x64)
+    lp_off, h_off = long_bounds(row, -(-(V // 16) // (256 * groups)), groups)
+    tokens = np.array([0, V // 3, V - 1, int(np.argmax(x64))])
+    ws = new_ws()
+    got = sv.token_logprobs(x.expand(1, 700, V), i32(np.tile(tokens, (1, 700, 1))), ws=ws)
+    assert flags(ws) == (sv.SV_OK, 0)
+    lp = got["logprobs"].double().cpu().numpy()
+    assert (np.abs(lp - row.lp[tokens]) <= lp_off[tokens]).all()
+    assert (np.abs(got["entropy"].double().cpu().numpy() - row.entropy) <= h_off).all()
