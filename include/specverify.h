@@ -560,7 +560,8 @@ sv_status sv_kv_append(const sv_kv_append_args* args, void* workspace, size_t ws
  * of its logits (for a tree: 0, then the accepted nodes).  With x the row, t =
  * temperature[b] (0 and NULL: 1; below 2^-126: 2^-126) and ln p_j = x_j / t -
  * ln sum_k exp(x_k / t):
- *   logprob[b][r][m] = ln p of tokens[b][r][m]; NaN where that is -1;
+ *   logprob[b][r][m] = ln p of tokens[b][r][m], -inf where that passes the range of
+ *     fp32; NaN where the token is -1;
  *   entropy[b][r]    = - sum_j p_j ln p_j (logits of -inf add nothing);
  *   top_token[b][r][], top_logprob[b][r][]: the `top` largest logits, the lower
  *     token first among equal ones; -1 and -inf where fewer than `top` tokens

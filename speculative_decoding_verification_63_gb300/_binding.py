@@ -98,6 +98,8 @@ class SvKvAttentionArgs(ctypes.Structure):
                 ("num_new", _P), ("mask", _P), ("words", _i32), ("scale", ctypes.c_float)]
 
 
+# (the structures of the round's calls, for calling the C ABI by hand: the functions below
+# are given theirs by the compiled binding)
 class SvRope(ctypes.Structure):
     _fields_ = [("dim", _i32), ("interleaved", _i32), ("scale", ctypes.c_float), ("freq", _P)]
 

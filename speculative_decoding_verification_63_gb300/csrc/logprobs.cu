@@ -67,8 +67,13 @@ sv_status sv_token_logprobs(const sv_token_logprobs_args* a, void* workspace, si
   // CTAs of a row: as long as they all run at once (four an SM) and have a turn
   // of groups each, up to four, whose barriers are still cheap; eight for a
   // handful of rows.  (256 rows of 152064, top 20: 1 25.5 us, 2 23.0; 64 rows of
-  // 128256, top 5: 1 16.8, 2 11.9, 4 9.7, 8 10.7; 1 row: 4 10.2, 8 7.0.  448 rows:
-  // 1 25.3, 2 32; with num_rows, where half of the rows are there, 1 22.0, 2 18.9.)
+  // 128256, top 5: 1 16.8, 2 11.9, 4 9.7, 8 10.7; 1 row: 4 10.2, 8 7.0.)
+  // num_rows lies on the device.  Where it is given, 5 of 8 rows are taken to be there:
+  // rounds of accepted tokens that are about half full gain, full ones lose, and a caller
+  // whose rows are all there leaves it out.  (Rows of 128256, top 5, in us with this and
+  // without: 448 rows half there 18.3 and 25.4, all there 31.2 and 27.6; 336 rows 17.1 and
+  // 21.9, 27.8 and 26.8; 238 rows 13.3 and 15.6, 23.1 and 18.2; 182 rows 12.6 and 15.1,
+  // 20.4 and 17.5; up to 152 rows, 244 to 304 and above 486 the same.)
   int64_t rows = static_cast<int64_t>(a->B) * a->R;
   if (a->num_rows != nullptr && a->R > 1) rows = rows * 5 / 8;
   p.cluster = 1;
