@@ -420,8 +420,9 @@ def token_logprobs(logits, tokens=None, num_rows=None, rows=None, R: int | None 
     Row r < num_rows[b] of request b is row r of its logits, or rows[b][r];
     tokens [B][R] or [B][R][M] int32 are the tokens asked of it (-1: none).
     For what verify_chain emitted: tokens=out_tokens, num_rows=out_len; for a
-    tree round also rows = 0, then accepted_nodes.  temperature [B]: as the
-    verification's, but 0 (greedy) counts as 1 and less than 2^-126 as 2^-126.  Returns entropy [B][R],
+    tree round also rows = 0, then accepted_nodes (num_rows None where all rows are
+    there).  temperature [B]: as the verification's, but 0 (greedy) counts as 1 and
+    less than 2^-126 as 2^-126.  Returns entropy [B][R],
     logprobs (tokens' shape), top_tokens and top_logprobs [B][R][top] (device
     tensors): equal logits list the lower token first, tokens of logit -inf are
     not listed (-1, -inf), and rows from num_rows on are NaN and -1."""
